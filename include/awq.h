@@ -57,7 +57,8 @@ typedef enum AWQ_ENUM_INT {
 typedef enum AWQ_ENUM_INT {
     AWQ_F32 = 0,   /* IEEE binary32                      */
     AWQ_BF16 = 1,  /* bfloat16 (1 sign, 8 exp, 7 frac)   */
-    AWQ_F16 = 2    /* IEEE binary16; only for stored steps (awq_w4a16_gemm_ex) */
+    AWQ_F16 = 2    /* IEEE binary16; stored steps (awq_w4a16_gemm_ex) and the key/value
+                      cache (awq_kv_*)                                               */
 } awq_dtype;
 
 /* Largest supported alpha-grid length. */
@@ -493,6 +494,125 @@ awq_status awq_w4a16_gemm_ex(const void *X, int64_t M, int64_t D_in, int64_t D_o
                              const uint32_t *packed, const void *scales, awq_dtype scale_type,
                              const uint8_t *zeros, int group, const float *inv_s, void *Y,
                              awq_dtype yt, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The 4-bit key/value cache: written as tokens arrive, read back, attended to.
+ *
+ * The codes are those of the zero-point quantiser's kind, with a stored lowest
+ * value in the place of a zero point.  For one token's key (or value) row x of
+ * one head, per group of `group` channels, in float32:
+ *   lo   = fp16(min x)
+ *   step = fp16( max(max x - lo, 0) / 15 )
+ *   q    = clamp(round_half_even((x - lo) / step), 0, 15)   (0 where step is 0)
+ * and the cache stands for q*step + lo.  Values below about 2^-24 vanish in the
+ * fp16 step.  A head's token whose key or value row holds a NaN, an infinity or
+ * a value beyond +-32768 is stored as NaN: both rows read back as NaN, and
+ * a query that attends to it gets NaN (one that does not is unaffected).
+ */
+
+/* A pool of pages, in device memory.
+ *   pages        [n_pages] pages, page_stride bytes apart (a multiple of 16, at
+ *                least awq_kv_page_size(...)), 16-byte aligned.  A page holds one
+ *                block for each head, a block `page` tokens:
+ *                  key codes    [page][dim/2] bytes: 32-bit word kb*(dim/32) + j of
+ *                               a token holds channels 32j + 8kb + 0..7 in the
+ *                               nibble order of awq_pack
+ *                  value codes  [page/4][16][dim/32][4] bytes: byte [t/4][m][b][t%4]
+ *                               holds channel 32b + m of token t in its low nibble
+ *                               and channel 32b + 16 + m in its high one
+ *                  key pairs    [page][dim/group][2] fp16: step, lo
+ *                  value pairs  [page][dim/group][2] fp16
+ *   heads        key/value heads, 1..65535.   dim   64, 128 or 256.
+ *   group        32, 64 or 128, at most dim.   page  a power of two, 16..256.
+ */
+typedef struct {
+    void *pages;
+    int64_t n_pages;
+    int64_t page_stride;
+    int64_t heads;
+    int dim, group, page;
+} awq_kv_cache;
+
+/* The sequences of a call and their rows.
+ *   rows         rows of the call's tensors (K, V, Q, O); 0 is allowed.
+ *   batch        number of sequences, >= 1.
+ *   max_pages    columns of block_table.
+ *   row_start    device, [batch + 1] int32, ascending: sequence b has rows
+ *                row_start[b] .. row_start[b+1] - 1; rows from row_start[batch] on
+ *                belong to none and are left as they were.  NULL: rows / batch
+ *                rows for each (rows must be a multiple of batch).
+ *   kv_len       device, [batch] int32: the sequence's length in the cache, its
+ *                rows of this call included; its n rows are the last n positions.
+ *                Rows before position 0 (n > kv_len) have no position.
+ *   block_table  device, [batch, max_pages] int32: position p lies in page
+ *                block_table[b, p / page], slot p % page.
+ * The arrays need 4-byte alignment.  They are read by the kernels (so a captured
+ * graph follows them) and everything taken from them is bounded there: kv_len
+ * to 0 .. max_pages*page, rows to 0 .. rows, and a page number outside
+ * 0 .. n_pages-1 (-1, say, for a page that has been given up) is never
+ * accessed: its positions do not exist.
+ */
+typedef struct {
+    int64_t rows, batch, max_pages;
+    const int32_t *row_start;
+    const int32_t *kv_len;
+    const int32_t *block_table;
+} awq_kv_batch;
+
+/* awq_kv_page_size - bytes of one page, heads * (page*dim + 8*page*(dim/group))
+ * (0 if the arguments are invalid; awq_last_error() says why). */
+size_t awq_kv_page_size(int page, int64_t heads, int dim, int group);
+
+/*
+ * awq_kv_append - quantise the rows' keys and values into the cache.
+ *   K, V      device, [rows, heads, dim] of type t (AWQ_F32, AWQ_BF16 or AWQ_F16),
+ *             rows k_stride / v_stride elements apart (a multiple of 16 bytes, at
+ *             least heads*dim: they may be slices of a fused projection).
+ * Rows without a position and rows whose page does not exist are dropped.
+ * Nothing but the rows' own slots is written.  Two rows of a call must not have
+ * the same slot (what that slot holds is then unspecified).
+ */
+awq_status awq_kv_append(const awq_kv_cache *cache, const awq_kv_batch *batch, const void *K, const void *V,
+                         awq_dtype t, int64_t k_stride, int64_t v_stride, hipStream_t stream);
+
+/*
+ * awq_kv_read - the rows' keys and values as the cache stands for them:
+ * q*step + lo, rounded once to float32 and once to type t.  With all positions
+ * of a sequence as its rows (n = kv_len) this reads the whole sequence back.
+ * Rows without a position, or whose page does not exist, are zero.
+ */
+awq_status awq_kv_read(const awq_kv_cache *cache, const awq_kv_batch *batch, void *K, void *V, awq_dtype t,
+                       int64_t k_stride, int64_t v_stride, hipStream_t stream);
+
+/*
+ * awq_kv_attention - attention of the rows' queries over the cache.
+ *   Q, O      device, [rows, q_heads, dim] of type t (AWQ_BF16 or AWQ_F16), rows
+ *             q_stride / o_stride elements apart.  q_heads is a multiple of the
+ *             cache's heads; query head h reads key/value head h / (q_heads/heads).
+ *   max_rows  an upper bound on any sequence's rows, known on the host; 0 means
+ *             `rows`.  It chooses the kernels: with row_start it should be
+ *             given.  A sequence with more rows gets them unspecified
+ *             (nothing outside O and lse is written).  Ignored without row_start.
+ *   scale     > 0; S = scale * q.k'.
+ *   causal    1: a row at position p sees positions <= p; 0: all of kv_len.
+ *   window    > 0: and only positions > p - window (causal = 1); 0: no window.
+ *   lse       device, [rows, q_heads] float32, the natural logarithm of the sum
+ *             of exp S over what the row sees; may be NULL.
+ * A row that sees nothing (kv_len 0, no position, no page) gets O = 0 and
+ * lse = -inf.  Products and sums are float32; scores enter the second product
+ * as fp16 in units of 2^-11 of themselves, and v' as fp16.  Results are
+ * deterministic.
+ *   workspace device, 16-byte aligned, at least awq_kv_attention_workspace_size(...)
+ *             bytes (0: none needed, or invalid arguments, for which
+ *             awq_last_error() is not empty).  Contents on entry do not matter; calls
+ *             (and captured graphs) that may overlap need workspaces of their own.
+ */
+size_t awq_kv_attention_workspace_size(const awq_kv_cache *cache, const awq_kv_batch *batch, int64_t q_heads,
+                                       int64_t max_rows);
+awq_status awq_kv_attention(const awq_kv_cache *cache, const awq_kv_batch *batch, const void *Q, awq_dtype t,
+                            int64_t q_heads, int64_t q_stride, int64_t max_rows, float scale, int causal,
+                            int64_t window, void *O, int64_t o_stride, float *lse, void *workspace,
+                            size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -33,6 +33,13 @@ __all__ = [
     "w4a16_gemm",
     "w4a16_workspace_size",
     "w4a16_gemm_noalloc",
+    "KvCache",
+    "kv_page_size",
+    "kv_cache",
+    "kv_append",
+    "kv_read",
+    "kv_attention_workspace_size",
+    "kv_attention",
     "AWQ_F32",
     "AWQ_BF16",
 ]
@@ -42,7 +49,7 @@ _LIBNAME = "libawq_mi355x.so"
 
 AWQ_F32 = 0
 AWQ_BF16 = 1
-AWQ_F16 = 2                     # stored steps only
+AWQ_F16 = 2                     # stored steps, and the key/value cache
 AWQ_SEARCH_ZERO_POINT = 1       # awq_search_layer_flags
 AWQ_SEARCH_FP16_STEPS = 2
 AWQ_SEARCH_MATRIX_BF16 = 4      # loss contraction on bf16 matrix cores (with correction rows)
@@ -83,6 +90,22 @@ _int = ctypes.c_int
 _uint = ctypes.c_uint
 _sz = ctypes.c_size_t
 
+
+class _KvCacheC(ctypes.Structure):
+    """awq_kv_cache"""
+    _fields_ = [("pages", _vp), ("n_pages", _i64), ("page_stride", _i64), ("heads", _i64), ("dim", _int),
+                ("group", _int), ("page", _int)]
+
+
+class _KvBatchC(ctypes.Structure):
+    """awq_kv_batch"""
+    _fields_ = [("rows", _i64), ("batch", _i64), ("max_pages", _i64), ("row_start", _vp), ("kv_len", _vp),
+                ("block_table", _vp)]
+
+
+_kvc = ctypes.POINTER(_KvCacheC)
+_kvb = ctypes.POINTER(_KvBatchC)
+
 SIGNATURES = {
     "awq_last_error": (ctypes.c_char_p, []),
     "awq_version": (ctypes.c_char_p, []),
@@ -115,6 +138,12 @@ SIGNATURES = {
     "awq_w4a16_gemm_noalloc": (_int, [_vp, _i64, _i64, _i64, _vp, _vp, _int, _vp, _vp, _int, _vp]),
     "awq_w4a16_gemm_ex": (_int, [_vp, _i64, _i64, _i64, _vp, _vp, _int, _vp, _int, _vp, _vp, _int, _vp, _sz,
                                  _vp]),
+    "awq_kv_page_size": (_sz, [_int, _i64, _int, _int]),
+    "awq_kv_append": (_int, [_kvc, _kvb, _vp, _vp, _int, _i64, _i64, _vp]),
+    "awq_kv_read": (_int, [_kvc, _kvb, _vp, _vp, _int, _i64, _i64, _vp]),
+    "awq_kv_attention_workspace_size": (_sz, [_kvc, _kvb, _i64, _i64]),
+    "awq_kv_attention": (_int, [_kvc, _kvb, _vp, _int, _i64, _i64, _i64, ctypes.c_float, _int, _i64, _vp, _i64, _vp,
+                                _vp, _sz, _vp]),
 }
 
 
@@ -480,6 +509,201 @@ def w4a16_gemm_noalloc(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tens
         _dev(inv_s, "inv_s") if inv_s is not None else None, _dev(out, "Y"), _dtype_code(out.dtype),
         _stream(X.device)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# The 4-bit key/value cache
+
+_KV_TYPES = {torch.float32: AWQ_F32, torch.bfloat16: AWQ_BF16, torch.float16: AWQ_F16}
+
+
+@dataclass(frozen=True)
+class KvCache:
+    """A pool of pages of 4-bit keys and values (include/awq.h: awq_kv_cache).
+
+    ``pages`` is uint8 [n_pages, heads, block]; the pages may lie apart (a slice
+    of a larger pool), each one contiguous.  :func:`kv_cache` makes one.
+    """
+    pages: torch.Tensor
+    dim: int           # channels of a head: 64, 128 or 256
+    group: int = 128   # channels that share a step: 32, 64 or 128
+    page: int = 16     # tokens of a page: 16, 32, 64, 128 or 256
+
+    def __post_init__(self):
+        p = self.pages
+        if p.dtype != torch.uint8 or p.dim() != 3:
+            raise TypeError("pages must be uint8 [n_pages, heads, block]")
+        n, heads, block = p.shape
+        size = kv_page_size(self.page, heads, self.dim, self.group)
+        if heads * block != size:
+            raise ValueError(f"a page must hold {size} bytes (got {heads} x {block})")
+        if p.stride(2) != 1 or p.stride(1) != block:
+            raise ValueError("each page must be contiguous")
+        stride = p.stride(0) if n > 1 else size    # torch gives a single page any stride
+        object.__setattr__(self, "_c", _KvCacheC(p.data_ptr(), n, stride, heads, self.dim, self.group, self.page))
+        object.__setattr__(self, "_device", p.device)
+        object.__setattr__(self, "heads", heads)
+
+
+def kv_page_size(page: int, heads: int, dim: int, group: int = 128) -> int:
+    """Bytes of one page: heads * (page*dim + 8*page*(dim/group))."""
+    lib = load()
+    n = lib.awq_kv_page_size(page, heads, dim, group)
+    if n == 0:
+        raise AwqError(-1, lib.awq_last_error().decode(errors="replace"))
+    return int(n)
+
+
+def kv_cache(n_pages: int, heads: int, dim: int, group: int = 128, page: int = 16, device="cuda") -> KvCache:
+    """A pool of ``n_pages`` pages (all zero, which reads back as zero)."""
+    block = kv_page_size(page, heads, dim, group) // heads
+    return KvCache(torch.zeros(n_pages, heads, block, dtype=torch.uint8, device=device), dim, group, page)
+
+
+def _kv_rows(x: torch.Tensor, name: str, device, shape) -> tuple[int, int]:
+    """Pointer and row stride of a [rows, heads, dim] tensor whose rows may lie apart."""
+    if x.device != device:
+        raise ValueError(f"{name} must be on the cache's GPU")
+    if x.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)} (got {list(x.shape)})")
+    if x.is_contiguous():
+        return x.data_ptr(), shape[1] * shape[2]
+    if x.stride(2) != 1 or (shape[1] > 1 and x.stride(1) != shape[2]):
+        raise ValueError(f"each row of {name} must be contiguous")
+    # torch gives a single row any stride
+    return x.data_ptr(), x.stride(0) if shape[0] > 1 else shape[1] * shape[2]
+
+
+def _kv_batch(device, block_table, kv_len, row_start, rows: int) -> _KvBatchC:
+    if device.type != "cuda":
+        raise ValueError("pages must be a GPU tensor")
+    batch, max_pages = block_table.shape
+    if kv_len.shape != (batch,) or (row_start is not None and row_start.shape != (batch + 1,)):
+        raise ValueError("block_table must be [batch, max_pages], kv_len [batch] and row_start [batch + 1]")
+    for x in (block_table, kv_len) if row_start is None else (block_table, kv_len, row_start):
+        if x.dtype != torch.int32:
+            raise TypeError("block_table, kv_len and row_start must be int32")
+        if x.device != device or not x.is_contiguous():
+            raise ValueError("block_table, kv_len and row_start must be contiguous and on the cache's GPU")
+    return _KvBatchC(rows, batch, max_pages, None if row_start is None else row_start.data_ptr(), kv_len.data_ptr(),
+                     block_table.data_ptr())
+
+
+def _kv_type(t: torch.dtype) -> int:
+    if t not in _KV_TYPES:
+        raise TypeError(f"unsupported dtype {t} (float32, bfloat16 or float16)")
+    return _KV_TYPES[t]
+
+
+def _kv_call(device: torch.device, fn, *args):
+    """fn(*args, current stream of `device`), with that device current."""
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream(device))
+    if status != 0:
+        _check(status)
+
+
+def kv_append(cache: KvCache, K: torch.Tensor, V: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor,
+              row_start: torch.Tensor | None = None) -> None:
+    """Quantise the rows' keys and values [rows, heads, dim] into the cache.
+
+    Sequence b's rows are ``row_start[b] .. row_start[b+1] - 1`` (the same number
+    for each sequence without ``row_start``) and become the last of its ``kv_len[b]``
+    positions; position p lies in page ``block_table[b, p // page]``.
+    """
+    dev = cache._device
+    rows = K.shape[0]
+    shape = (rows, cache.heads, cache.dim)
+    if V.dtype != K.dtype:
+        raise TypeError("K and V must have one dtype")
+    b = _kv_batch(dev, block_table, kv_len, row_start, rows)
+    k, k_stride = _kv_rows(K, "K", dev, shape)
+    v, v_stride = _kv_rows(V, "V", dev, shape)
+    _kv_call(dev, _lib.awq_kv_append, cache._c, b, k, v, _kv_type(K.dtype), k_stride, v_stride)
+
+
+def kv_read(cache: KvCache, block_table: torch.Tensor, kv_len: torch.Tensor, rows: int,
+            row_start: torch.Tensor | None = None, dtype: torch.dtype = torch.bfloat16,
+            out: tuple[torch.Tensor, torch.Tensor] | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The rows' keys and values [rows, heads, dim] as the cache stands for them.
+
+    Rows and positions as in :func:`kv_append`: the last positions of each
+    sequence, all of them where its rows are ``kv_len[b]``.  Rows that belong to
+    no sequence are left as they were in ``out`` (unspecified in new tensors).
+    """
+    dev = cache._device
+    shape = (rows, cache.heads, cache.dim)
+    b = _kv_batch(dev, block_table, kv_len, row_start, rows)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev)
+    K, V = out
+    if V.dtype != K.dtype:
+        raise TypeError("both outputs must have one dtype")
+    k, k_stride = _kv_rows(K, "K", dev, shape)
+    v, v_stride = _kv_rows(V, "V", dev, shape)
+    _kv_call(dev, _lib.awq_kv_read, cache._c, b, k, v, _kv_type(K.dtype), k_stride, v_stride)
+    return K, V
+
+
+def _kv_workspace(cache_c, batch_c, q_heads: int, max_rows: int) -> int:
+    n = _lib.awq_kv_attention_workspace_size(cache_c, batch_c, q_heads, max_rows)
+    if n == 0:
+        msg = _lib.awq_last_error()
+        if msg:
+            raise AwqError(-2, msg.decode(errors="replace"))
+    return n
+
+
+def kv_attention_workspace_size(cache: KvCache, q_heads: int, rows: int, batch: int, max_pages: int,
+                                ragged: bool = False, max_rows: int | None = None) -> int:
+    """Bytes of workspace of a :func:`kv_attention` call (``ragged``: with row_start)."""
+    b = _KvBatchC(rows, batch, max_pages, 4 if ragged else None, None, None)   # only whether it is NULL counts
+    return _kv_workspace(cache._c, b, q_heads, max_rows or 0)
+
+
+def kv_attention(Q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, kv_len: torch.Tensor,
+                 row_start: torch.Tensor | None = None, max_rows: int | None = None, scale: float | None = None,
+                 causal: bool = True, window: int = 0, want_lse: bool = False, out: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None):
+    """Attention of the queries [rows, q_heads, dim] (bf16 or fp16) over the cache.
+
+    Rows and positions as in :func:`kv_append` (append the rows' keys first:
+    a row sees its own position).  ``max_rows``: an upper bound on any
+    sequence's rows, known on the host; give it with ``row_start``.  ``scale``
+    defaults to dim ** -0.5.  ``window`` > 0: only the last ``window`` positions.
+    ``workspace``: uint8 of :func:`kv_attention_workspace_size` bytes (None
+    allocates it).  Returns the output like Q, and with ``want_lse`` also the
+    float32 log-sum-exp [rows, q_heads] (-inf, and output 0, where a row sees
+    nothing).
+    """
+    dev = cache._device
+    rows, q_heads = Q.shape[0], Q.shape[1]
+    shape = (rows, q_heads, cache.dim)
+    dtype = Q.dtype
+    if dtype != torch.bfloat16 and dtype != torch.float16:
+        raise TypeError(f"Q must be bfloat16 or float16 (got {dtype})")
+    q, q_stride = _kv_rows(Q, "Q", dev, shape)
+    b = _kv_batch(dev, block_table, kv_len, row_start, rows)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    elif out.dtype != dtype:
+        raise TypeError("out must have the dtype of Q")
+    o, o_stride = _kv_rows(out, "out", dev, shape)
+    lse = torch.empty((rows, q_heads), dtype=torch.float32, device=dev) if want_lse else None
+    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != dev
+                                  or not workspace.is_contiguous()):
+        raise ValueError("workspace must be contiguous uint8 on the cache's GPU")
+    need = _kv_workspace(cache._c, b, q_heads, max_rows or 0)
+    if need and (workspace is None or workspace.numel() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _kv_call(dev, _lib.awq_kv_attention, cache._c, b, q, _KV_TYPES[dtype], q_heads, q_stride, max_rows or 0,
+             cache.dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, o, o_stride,
+             lse.data_ptr() if want_lse else None, workspace.data_ptr() if need else None,
+             workspace.numel() if need else 0)
+    return (out, lse) if want_lse else out
 
 
 # Load at import time: a missing library is an error, never a silent fallback.

@@ -18,7 +18,8 @@ LIB = os.path.join(PKG, "libawq_mi355x.so")
 CALIB_LIB = os.path.join(PKG, "libawq_calib.so")
 
 SOURCES = ["awq_api.hip", "awq_noalloc.hip", "k_stats.hip", "k_search.hip", "k_pack.hip", "k_decode.hip",
-           "k_prefill.hip", "k_clip.hip"]
+           "k_prefill.hip", "k_clip.hip", "awq_kv.hip", "k_kv.hip", "k_kv_attend_64.hip", "k_kv_attend_128.hip",
+           "k_kv_attend_256.hip"]
 CALIB_SOURCES = ["calib.hip"]
 
 # Packed fp32 VALU forms are disabled (-packed-fp32-ops); no fast-math, no

@@ -1,0 +1,703 @@
+// Attention over the 4-bit key/value cache: the kernels, instantiated per head
+// dimension by k_kv_attend_{64,128,256}.hip.
+//
+//   S[t, i] = scale * sum_c k'[t, c] q[i, c],  k' = step*code + lo per group g
+//           = scale * sum_g ( step[t,g] * sum_{c in g} code[t,c] q[i,c] + lo[t,g] * sum_{c in g} q[i,c] )
+//   O[i]    = sum_t softmax(S[., i])_t v'[t]
+//
+// Both products run on 16x16x32 MFMAs, transposed (keys and values are the A
+// operand, queries and scores the B operand), 32 tokens a step:
+//  - S^T = codes·Q^T.  A code enters as the 16-bit float base + code, made by one
+//    and-or on the packed word (16 + code in bf16, 64 + code in fp16, exact).
+//    The accumulator starts at -base * sum q, so it ends at sum code*q; steps and
+//    lowest values are applied in float32.
+//  - A lane's result rows are tokens 4kb..4kb+3 of one query, which are the
+//    tokens that its B operand of the second product takes: scores stay in
+//    their lane.
+//  - O^T = V'^T·P^T in fp16: codes become fp16 by and-or (1024 + code, 64 + code),
+//    an exact packed subtraction, and one packed fma with (step, lo): v' is
+//    rounded once, to 11 bits.  P = exp2(S - m) <= 2^8 is rounded to 11 bits, too.
+//  - The softmax reference m of a query (shared by its 4 lanes) moves only when
+//    a score exceeds it by 2^8, so most steps need no cross-lane maximum and no
+//    rescaling.  Sums l and m stay in float32.
+//
+// Masked scores are set to -inf after the product, so whatever a masked key holds
+// is dropped; value pairs of tokens that do not exist (behind the length, on a
+// page outside the cache) are zeroed, since 0 * NaN would not vanish.
+#pragma once
+
+#include "kv_internal.h"
+
+namespace awq {
+namespace {
+
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kLagLog2 = 8.0f;   // scores may exceed the reference by this (log2): P <= 2^8 fits fp16
+
+template <typename T>
+struct KvType;
+template <>
+struct KvType<__bf16> {
+    typedef bf16x8 vec8;
+    static constexpr float base = 16.0f;
+    // codes of channels (2i, 2i+1) of a key word, + base.  (Base 128 would save the
+    // shift of i = 0; its sums cancel 8 times as much in float32, which shows in lse.)
+    static __device__ __forceinline__ uint32_t pair(uint32_t w, int i) {
+        const uint32_t x = i == 0 ? w << 3 : w >> (4 * i - 3);
+        return (x & 0x00780078u) | 0x41804180u;
+    }
+    static __device__ __forceinline__ floatx4 mfma(uint4 a, vec8 b, floatx4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(vec8, a), b, c, 0, 0, 0);
+    }
+};
+template <>
+struct KvType<_Float16> {
+    typedef half8 vec8;
+    static constexpr float base = 64.0f;
+    static __device__ __forceinline__ uint32_t pair(uint32_t w, int i) {
+        const uint32_t x = i == 0 ? w << 4 : w >> (4 * (i - 1));
+        return (x & 0x00F000F0u) | 0x54005400u;
+    }
+    static __device__ __forceinline__ floatx4 mfma(uint4 a, vec8 b, floatx4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(vec8, a), b, c, 0, 0, 0);
+    }
+};
+
+__device__ __forceinline__ float half_lo(uint32_t x) {
+    return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(x)));
+}
+__device__ __forceinline__ float half_hi(uint32_t x) {
+    return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(x >> 16)));
+}
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+
+template <typename T>
+__device__ __forceinline__ uint2 pack4(float a, float b, float c, float d) {
+    typedef T vec4 __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(uint2, vec4{static_cast<T>(a), static_cast<T>(b), static_cast<T>(c), static_cast<T>(d)});
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    typedef T vec2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, vec2{static_cast<T>(a), static_cast<T>(b)});
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(const unsigned char *p, uint32_t *w) {
+    if constexpr (N == 1) {
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else if constexpr (N == 2) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+        w[0] = x.x, w[1] = x.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const uint4 x = reinterpret_cast<const uint4 *>(p)[i];
+            w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+        }
+    }
+}
+
+// One step's codes and pairs, as a lane holds them.
+template <int D, int NG>
+struct KvStep {
+    uint32_t k[2][D / 32], v[2][D / 32], kp[2][4 * NG], vp[2][4 * NG];
+    bool ok0, ok1;   // the two 16-token halves exist
+};
+
+// Page of token `tok` (uniform in a wave), -1 where there is none.
+__device__ __forceinline__ int kv_page(const KvAttend &a, const int32_t *table, int tok, int len) {
+    if (tok >= len) return -1;
+    const int id = table[tok >> a.c.page_shift];
+    return id < 0 || id >= a.c.n_pages ? -1 : id;
+}
+
+template <int D, int NG>
+__device__ __forceinline__ void kv_load(const KvAttend &a, int head, int tok, int page0, int page1, int lane,
+                                        KvStep<D, NG> &s) {
+    const int n = lane & 15, kb = lane >> 4, P = 1 << a.c.page_shift;
+    s.ok0 = page0 >= 0;
+    s.ok1 = page1 >= 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int page = h ? page1 : page0;
+        const int slot = (tok + 16 * h) & (P - 1);
+        // a half that does not exist reads page 0, which does, and is masked
+        const unsigned char *b =
+            a.c.pages + (page < 0 ? 0 : page) * a.c.page_stride + head * a.c.block;
+        load_words<D / 32>(b + slot * (D / 2) + (n * (D / 2) + kb * (D / 8)), s.k[h]);
+        load_words<D / 32>(b + P * (D / 2) + slot * (D / 2) + (kb * 16 + n) * (D / 8), s.v[h]);
+        load_words<4 * NG>(b + P * D + slot * (4 * NG) + kb * (16 * NG), s.kp[h]);
+        load_words<4 * NG>(b + P * D + P * (4 * NG) + slot * (4 * NG) + kb * (16 * NG), s.vp[h]);
+    }
+}
+
+// One wave's 16*NT columns: queries, running sums, output.
+template <typename T, int D, int NG, int NT>
+struct KvWave {
+    static constexpr int J = D / 32;
+    typename KvType<T>::vec8 q[NT][J];
+    float qs[NT][NG];                 // sum of q over a group
+    floatx4 o[NT][D / 16];            // channel 16i + 4kb + r of column lane & 15
+    float m[NT], l[NT];               // reference (log2) and this lane's share of the sum
+    int pos[NT], low[NT];             // last and first visible position (pos -1: no such column)
+
+    __device__ __forceinline__ void start(const KvAttend &a, int head, int r0, int n, int len, int col0, int lane) {
+        const int kb = lane >> 4;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int c = col0 + 16 * t + (lane & 15), i = c / a.per;
+            const bool real = i < n;
+            const T *src = static_cast<const T *>(a.Q) + (r0 + (real ? i : 0)) * a.q_stride +
+                           static_cast<int64_t>(head * a.per + (c - i * a.per)) * D + 8 * kb;
+            pos[t] = real ? (a.causal ? len - n + i : len - 1) : -1;
+            low[t] = a.window ? len - n + i - a.window + 1 : 0;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) qs[t][g] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                typename KvType<T>::vec8 x = {};
+                if (real) x = *reinterpret_cast<const typename KvType<T>::vec8 *>(src + 32 * j);
+                q[t][j] = x;
+                float sum = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum += static_cast<float>(x[e]);
+                qs[t][j * NG / J] += sum;
+            }
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                qs[t][g] += __shfl_xor(qs[t][g], 16);
+                qs[t][g] += __shfl_xor(qs[t][g], 32);
+            }
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) o[t][d] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+            m[t] = -INFINITY;
+            l[t] = 0.0f;
+        }
+    }
+
+    // Tokens tok .. tok+31.  edge: some of them may be hidden from some column.
+    __device__ __forceinline__ void step(const KvAttend &a, KvStep<D, NG> &s, int tok, int len, bool edge, int lane) {
+        const int kb = lane >> 4;
+        const float scale = a.scale_log2;
+        floatx4 x[2][NT];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                float step[4], lo[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    step[r] = half_lo(s.kp[h][r * NG + g]) * scale;
+                    lo[r] = half_hi(s.kp[h][r * NG + g]) * scale;
+                }
+                floatx4 acc[NT];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const float c0 = -KvType<T>::base * qs[t][g];
+                    acc[t] = floatx4{c0, c0, c0, c0};
+                }
+#pragma unroll
+                for (int j = g * (J / NG); j < (g + 1) * (J / NG); ++j) {
+                    const uint32_t w = s.k[h][j];
+                    const uint4 f = make_uint4(KvType<T>::pair(w, 0), KvType<T>::pair(w, 1), KvType<T>::pair(w, 2),
+                                               KvType<T>::pair(w, 3));
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) acc[t] = KvType<T>::mfma(f, q[t][j], acc[t]);
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float y = lo[r] * qs[t][g];
+                        x[h][t][r] = fmaf(step[r], acc[t][r], g == 0 ? y : x[h][t][r] + y);
+                    }
+            }
+        }
+        if (edge) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int p = tok + 16 * h + 4 * kb + r;
+                    const bool there = h ? s.ok1 : s.ok0;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        if (!there || p > pos[t] || p < low[t]) x[h][t][r] = -INFINITY;
+                    if (!there || p >= len) {
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) s.vp[h][r * NG + g] = 0;
+                    }
+                }
+        }
+        half8 p[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const float top = fmaxf(fmaxf(fmaxf(x[0][t][0], x[0][t][1]), fmaxf(x[0][t][2], x[0][t][3])),
+                                    fmaxf(fmaxf(x[1][t][0], x[1][t][1]), fmaxf(x[1][t][2], x[1][t][3])));
+            if (__any(top > m[t] + kLagLog2)) {
+                float now = fmaxf(m[t], top);
+                now = fmaxf(now, __shfl_xor(now, 16));
+                now = fmaxf(now, __shfl_xor(now, 32));
+                const float f = m[t] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[t] - now);
+                m[t] = now;
+                l[t] *= f;
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[t][d][r] *= f;
+            }
+            const float ref = m[t] == -INFINITY ? 0.0f : m[t];
+            // operand order of the value bytes: tokens (0, 2), (1, 3) of each half
+            constexpr int kOrder[4] = {0, 2, 1, 3};
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float e = __builtin_amdgcn_exp2f(x[h][t][kOrder[r]] - ref);
+                    l[t] += e;
+                    p[t][4 * h + r] = static_cast<_Float16>(e);
+                }
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            half2v vs[2][2], vl[2][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t p0 = s.vp[h][e * NG + g], p1 = s.vp[h][(e + 2) * NG + g];
+                    vs[h][e] = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(p1, p0, 0x05040100u));
+                    vl[h][e] = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(p1, p0, 0x07060302u));
+                }
+#pragma unroll
+            for (int b = g * (J / NG); b < (g + 1) * (J / NG); ++b) {
+                half2v lo[4], hi[4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t w = s.v[h][b] >> (8 * e);
+                        const half2v cl = __builtin_bit_cast(half2v, (w & 0x000F000Fu) | 0x64006400u) -
+                                          half2v{static_cast<_Float16>(1024), static_cast<_Float16>(1024)};
+                        const half2v ch = __builtin_bit_cast(half2v, (w & 0x00F000F0u) | 0x54005400u) -
+                                          half2v{static_cast<_Float16>(64), static_cast<_Float16>(64)};
+                        lo[2 * h + e] = __builtin_elementwise_fma(cl, vs[h][e], vl[h][e]);
+                        hi[2 * h + e] = __builtin_elementwise_fma(ch, vs[h][e], vl[h][e]);
+                    }
+                half8 fl, fh;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    fl[2 * e] = lo[e][0], fl[2 * e + 1] = lo[e][1];
+                    fh[2 * e] = hi[e][0], fh[2 * e + 1] = hi[e][1];
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    o[t][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fl, p[t], o[t][2 * b], 0, 0, 0);
+                    o[t][2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fh, p[t], o[t][2 * b + 1], 0, 0, 0);
+                }
+            }
+        }
+    }
+
+    // Tokens of tiles t0, t0 + stride, .. < t1 of one sequence and head, the
+    // next tile's loads in flight while one is computed.  minpos / maxlow: the
+    // first last-visible and the last first-visible position of the columns.
+    __device__ __forceinline__ void run(const KvAttend &a, const int32_t *table, int head, int t0, int t1, int stride,
+                                        int len, int minpos, int maxlow, int lane) {
+        if (t0 >= t1) return;
+        KvStep<D, NG> s0, s1;
+        int tok = t0 * kKvTile;
+        const int end = t1 * kKvTile, by = stride * kKvTile;
+        kv_load(a, head, tok, kv_page(a, table, tok, len), kv_page(a, table, tok + 16, len), lane, s0);
+        int p0 = -1, p1 = -1;   // pages of the tile after
+        if (tok + by < end) p0 = kv_page(a, table, tok + by, len), p1 = kv_page(a, table, tok + by + 16, len);
+        while (true) {
+            bool more = tok + by < end;
+            if (more) kv_load(a, head, tok + by, p0, p1, lane, s1);
+            if (tok + 2 * by < end)
+                p0 = kv_page(a, table, tok + 2 * by, len), p1 = kv_page(a, table, tok + 2 * by + 16, len);
+            step(a, s0, tok, len, hides(s0, tok, minpos, maxlow), lane);
+            tok += by;
+            if (!more) return;
+            more = tok + by < end;
+            if (more) kv_load(a, head, tok + by, p0, p1, lane, s0);
+            if (tok + 2 * by < end)
+                p0 = kv_page(a, table, tok + 2 * by, len), p1 = kv_page(a, table, tok + 2 * by + 16, len);
+            step(a, s1, tok, len, hides(s1, tok, minpos, maxlow), lane);
+            tok += by;
+            if (!more) return;
+        }
+    }
+    static __device__ __forceinline__ bool hides(const KvStep<D, NG> &s, int tok, int minpos, int maxlow) {
+        return tok + kKvTile - 1 > minpos || tok < maxlow || !s.ok0 || !s.ok1;   // (minpos < length)
+    }
+};
+
+// ---------------------------------------------------------------------------
+// Split path: sequences with at most 64 columns per key head (decoding).  The
+// tiles of all (sequence, head) items form one line, which the workers
+// (workgroups of 4 waves) share equally, so ragged lengths and few sequences
+// load the GPU evenly.  A worker's waves take its tiles in turn and join in
+// LDS.  An item inside one worker is written directly; the pieces of an item
+// that a boundary cuts go to the workspace and kv_merge_kernel joins them in order.
+// Boundaries within kKvSnap tiles of an item's end move there.
+
+constexpr int kSplitWaves = 4;
+
+__device__ __forceinline__ int kv_first_token(const KvAttend &a, int len, int n) {
+    if (!a.window) return 0;
+    const int low = len - n - a.window + 1;
+    return low > 0 ? low & ~(kKvTile - 1) : 0;
+}
+// Tiles of an item of sequence b; 0: not on the split path.
+__device__ __forceinline__ int kv_item_tiles(const KvAttend &a, int b, int &r0, int &n, int &len) {
+    kv_rows(a.s, b, r0, n);
+    len = kv_length(a.s, b, a.c.page_shift);
+    if (n == 0 || static_cast<int64_t>(n) * a.per > a.split_cols) return 0;
+    const int t = (len - kv_first_token(a, len, n) + kKvTile - 1) / kKvTile;
+    return t > 0 ? t : 1;   // an empty item is visited, too: its output is zero
+}
+
+struct KvItem {
+    int b, head, r0, n, len, tiles, begin;   // begin: its first tile on the line
+};
+
+// before[i]: tiles of one head of the sequences before i*chunk (LDS, 257 entries)
+__device__ __forceinline__ KvItem kv_locate(const KvAttend &a, const int *before, int chunk, int x) {
+    const int H = a.c.heads;
+    int lo = 0, hi = 256;   // the last i with H*before[i] <= x
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (H * before[mid] <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    KvItem it;
+    int b = lo * chunk, sum = before[lo];
+    while (true) {   // x < H*before[lo + 1], so a sequence of this chunk holds it
+        it.tiles = kv_item_tiles(a, b, it.r0, it.n, it.len);
+        if (x < H * (sum + it.tiles) || b + 1 >= a.s.B) break;
+        sum += it.tiles;
+        ++b;
+    }
+    it.b = b;
+    it.tiles = it.tiles > 0 ? it.tiles : 1;
+    it.head = kv_clamp((x - H * sum) / it.tiles, 0, H - 1);
+    it.begin = H * sum + it.head * it.tiles;
+    return it;
+}
+
+__device__ __forceinline__ int kv_snap(const KvItem &it, int x) {
+    if (x - it.begin <= kKvSnap) return it.begin;
+    if (it.begin + it.tiles - x <= kKvSnap) return it.begin + it.tiles;
+    return x;
+}
+
+template <typename T, int D, int NG, int NT>
+__global__ __launch_bounds__(64 * kSplitWaves) void kv_split_kernel(KvAttend a) {
+    constexpr int kThreads = 64 * kSplitWaves, kRow = D + 4;
+    __shared__ int before[257];
+    __shared__ int wave_sum[kSplitWaves];
+    __shared__ float ml[kSplitWaves][16 * NT][2];
+    __shared__ float buf[kSplitWaves][16][kRow];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int H = a.c.heads;
+    const int chunk = (a.s.B + 255) / 256;
+    {   // prefix sums over the sequences: thread i sums its chunk
+        int sum = 0, r0, n, len;
+        for (int b = tid * chunk; b < (tid + 1) * chunk && b < a.s.B; ++b) sum += kv_item_tiles(a, b, r0, n, len);
+        int incl = sum;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int up = __shfl_up(incl, d);
+            if (lane >= d) incl += up;
+        }
+        if (lane == 63) wave_sum[wave] = incl;
+        __syncthreads();
+        int base = 0;
+        for (int w = 0; w < wave; ++w) base += wave_sum[w];
+        before[tid + 1] = base + incl;
+        if (tid == 0) before[0] = 0;
+        __syncthreads();
+    }
+    const int total = H * before[256];
+    int share = (total + a.workers - 1) / a.workers;
+    if (share < kKvMinShare) share = kKvMinShare;
+    const int worker = blockIdx.x;
+    int64_t x0 = static_cast<int64_t>(worker) * share, x1 = x0 + share;
+    if (x0 >= total) return;   // (the whole workgroup)
+    int begin = static_cast<int>(x0), end = x1 < total ? static_cast<int>(x1) : total;
+    KvItem it = kv_locate(a, before, chunk, begin);
+    begin = kv_snap(it, begin);
+    if (end < total) end = kv_snap(kv_locate(a, before, chunk, end), end);
+
+    KvWave<T, D, NG, NT> w;
+    while (begin < end) {
+        it = kv_locate(a, before, chunk, begin);
+        const int item_end = it.begin + it.tiles;
+        const int stop = end < item_end ? end : item_end;
+        const bool starts = begin == it.begin, direct = starts && stop == item_end;
+        const int first = kv_first_token(a, it.len, it.n) / kKvTile;
+        const int p0 = it.len - it.n;   // position of the first row
+        w.start(a, it.head, it.r0, it.n, it.len, 0, lane);
+        const int minpos = a.causal ? p0 : it.len - 1;
+        const int maxlow = a.window ? it.len - a.window : 0;
+        w.run(a, a.s.table + static_cast<int64_t>(it.b) * a.s.max_pages, it.head, first + begin - it.begin + wave,
+              first + stop - it.begin, kSplitWaves, it.len, minpos, maxlow, lane);
+        // join the waves
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            w.l[t] += __shfl_xor(w.l[t], 16);
+            w.l[t] += __shfl_xor(w.l[t], 32);
+            if (lane < 16) ml[wave][16 * t + lane][0] = w.m[t], ml[wave][16 * t + lane][1] = w.l[t];
+        }
+        const int cols = it.n * a.per;
+        const int64_t piece = static_cast<int64_t>(worker) * 2 + (starts ? 1 : 0);
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            {
+                const int c = lane & 15, kb = lane >> 4;
+                float top = ml[0][16 * t + c][0];
+#pragma unroll
+                for (int v = 1; v < kSplitWaves; ++v) top = fmaxf(top, ml[v][16 * t + c][0]);
+                const float f = w.m[t] == top ? 1.0f : __builtin_amdgcn_exp2f(w.m[t] - top);
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d) {
+                    float4 y;
+                    y.x = w.o[t][d][0] * f, y.y = w.o[t][d][1] * f, y.z = w.o[t][d][2] * f, y.w = w.o[t][d][3] * f;
+                    *reinterpret_cast<float4 *>(&buf[wave][c][16 * d + 4 * kb]) = y;
+                }
+            }
+            __syncthreads();
+            for (int e = tid; e < 16 * (D / 4); e += kThreads) {
+                const int c = e / (D / 4), d = 4 * (e % (D / 4)), col = 16 * t + c;
+                if (col >= cols) break;
+                float top = ml[0][col][0], sum = 0.0f;
+#pragma unroll
+                for (int v = 1; v < kSplitWaves; ++v) top = fmaxf(top, ml[v][col][0]);
+                float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int v = 0; v < kSplitWaves; ++v) {
+                    const float mv = ml[v][col][0];
+                    sum += ml[v][col][1] * (mv == top ? 1.0f : __builtin_amdgcn_exp2f(mv - top));
+                    const float4 z = *reinterpret_cast<const float4 *>(&buf[v][c][d]);
+                    y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
+                }
+                if (direct) {
+                    const int i = col / a.per, h = it.head * a.per + col - i * a.per;
+                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    T *dst = static_cast<T *>(a.O) + (it.r0 + i) * a.o_stride + static_cast<int64_t>(h) * D + d;
+                    *reinterpret_cast<uint2 *>(dst) = pack4<T>(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+                    if (a.lse && d == 0)
+                        a.lse[static_cast<int64_t>(it.r0 + i) * a.q_heads + h] =
+                            sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+                } else {
+                    *reinterpret_cast<float4 *>(a.part + (piece * (16 * NT) + col) * D + d) = y;
+                    if (d == 0)
+                        *reinterpret_cast<float2 *>(a.part_ml + (piece * (16 * NT) + col) * 2) = make_float2(top, sum);
+                }
+            }
+            __syncthreads();
+        }
+        if (starts && a.items && tid == 0) {
+            // pieces: this worker's and those of the workers whose start lies inside the item
+            const int last = (item_end - kKvSnap - 1) / share;
+            a.items[it.b * H + it.head] = direct ? make_int2(0, 0) : make_int2(worker, last - worker + 1);
+        }
+        begin = stop;
+    }
+}
+
+// Joins the pieces of one item's column: blockIdx.x = item, blockIdx.y = column.
+template <typename T, int D>
+__global__ __launch_bounds__(D / 2) void kv_merge_kernel(KvAttend a) {
+    const int item = blockIdx.x, col = blockIdx.y;
+    const int b = item / a.c.heads, head = item - b * a.c.heads;
+    int r0, n, len;
+    if (kv_item_tiles(a, b, r0, n, len) == 0 || col >= n * a.per) return;
+    const int2 it = a.items[item];
+    if (it.y == 0) return;
+    const int cols = 16 * a.tiles_col, d = 2 * threadIdx.x;
+    float top = -INFINITY, sum = 0.0f, y0 = 0.0f, y1 = 0.0f;
+    for (int k = 0; k < it.y; ++k) {
+        const int64_t at = (static_cast<int64_t>(it.x + k) * 2 + (k == 0 ? 1 : 0)) * cols + col;
+        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + at * 2);
+        const float2 z = *reinterpret_cast<const float2 *>(a.part + at * D + d);
+        const float now = fmaxf(top, ml.x);
+        const float f0 = top == now ? 1.0f : __builtin_amdgcn_exp2f(top - now);
+        const float f1 = ml.x == now ? 1.0f : __builtin_amdgcn_exp2f(ml.x - now);
+        sum = sum * f0 + ml.y * f1;
+        y0 = y0 * f0 + z.x * f1;
+        y1 = y1 * f0 + z.y * f1;
+        top = now;
+    }
+    const int i = col / a.per, h = head * a.per + col - i * a.per;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    T *dst = static_cast<T *>(a.O) + (r0 + i) * a.o_stride + static_cast<int64_t>(h) * D + d;
+    *reinterpret_cast<uint32_t *>(dst) = pack2<T>(y0 * inv, y1 * inv);
+    if (a.lse && d == 0)
+        a.lse[static_cast<int64_t>(r0 + i) * a.q_heads + h] =
+            sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+// ---------------------------------------------------------------------------
+// Wide path: sequences with more than 64 columns per key head (prompts,
+// chunks).  A workgroup takes 256 columns (rows x query heads of one key head),
+// 64 or 32 a wave, over one of `splits` equal parts of the tokens they see.
+
+template <typename T, int D, int NG>
+__global__ __launch_bounds__(256) void kv_wide_kernel(KvAttend a) {
+    constexpr int NT = 4;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int head = blockIdx.x % a.c.heads;
+    const int u = a.units - 1 - blockIdx.x / a.c.heads;   // the longest first
+    const int split = blockIdx.y;
+    int b, k, r0, n;
+    if (a.s.row_start) {
+        b = kv_unit_sequence(a.s, u, a.per, kKvWideCols, 1);
+        k = u - kv_unit_first(a.s, b, a.per, kKvWideCols, 1);
+    } else {
+        const int each = a.units / a.s.B;
+        b = u / each;
+        k = u - b * each;
+    }
+    kv_rows(a.s, b, r0, n);
+    const int64_t cols = static_cast<int64_t>(n) * a.per;
+    if (cols <= a.split_cols || k < 0 || static_cast<int64_t>(k) * kKvWideCols >= cols) return;
+    const int len = kv_length(a.s, b, a.c.page_shift);
+    const int col0 = k * kKvWideCols + wave * (16 * NT);
+    const int p0 = len - n;
+    // rows of this workgroup and of this wave
+    const int last_col = static_cast<int>(cols) - 1;
+    auto row_of = [&](int c) { return (c < last_col ? c : last_col) / a.per; };
+    const int i0 = row_of(k * kKvWideCols), i1 = row_of(k * kKvWideCols + kKvWideCols - 1);
+    const int wi0 = row_of(col0), wi1 = row_of(col0 + 16 * NT - 1);
+    int lo = a.window ? p0 + i0 - a.window + 1 : 0, hi = a.causal ? p0 + i1 + 1 : len;
+    lo = lo > 0 ? lo / kKvTile : 0;
+    hi = hi > 0 ? (hi + kKvTile - 1) / kKvTile : 0;
+    int t0 = lo, t1 = hi;
+    if (a.splits > 1) {
+        const int part = (hi - lo + a.splits - 1) / a.splits;
+        t0 = lo + split * part;
+        t1 = t0 + part < hi ? t0 + part : hi;
+    }
+    const int wave_hi = a.causal ? (p0 + wi1 + kKvTile) / kKvTile : hi;   // (p0 + wi1 >= 0 or nothing visible)
+    if (p0 + wi1 < 0 && a.causal)
+        t1 = t0;
+    else if (wave_hi < t1)
+        t1 = wave_hi;
+    KvWave<T, D, NG, NT> w;
+    w.start(a, head, r0, n, len, col0, lane);
+    const int minpos = a.causal ? p0 + wi0 : len - 1;
+    const int maxlow = a.window ? p0 + wi1 - a.window + 1 : 0;
+    w.run(a, a.s.table + static_cast<int64_t>(b) * a.s.max_pages, head, t0, t1, 1, len, minpos, maxlow, lane);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int c = col0 + 16 * t + (lane & 15), kb = lane >> 4;
+        w.l[t] += __shfl_xor(w.l[t], 16);
+        w.l[t] += __shfl_xor(w.l[t], 32);
+        if (c > last_col) continue;
+        const int i = c / a.per, h = head * a.per + c - i * a.per;
+        const int64_t out = static_cast<int64_t>(r0 + i) * a.q_heads + h;
+        if (a.splits > 1) {
+            const int64_t at = static_cast<int64_t>(split) * a.s.T * a.q_heads + out;
+            if (kb == 0) *reinterpret_cast<float2 *>(a.wide_ml + at * 2) = make_float2(w.m[t], w.l[t]);
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d)
+                *reinterpret_cast<floatx4 *>(a.wide_part + at * D + 16 * d + 4 * kb) = w.o[t][d];
+        } else {
+            const float inv = w.l[t] == 0.0f ? 0.0f : 1.0f / w.l[t];
+            T *dst = static_cast<T *>(a.O) + (r0 + i) * a.o_stride + static_cast<int64_t>(h) * D + 4 * kb;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d)
+                *reinterpret_cast<uint2 *>(dst + 16 * d) = pack4<T>(w.o[t][d][0] * inv, w.o[t][d][1] * inv,
+                                                                    w.o[t][d][2] * inv, w.o[t][d][3] * inv);
+            if (a.lse && kb == 0)
+                a.lse[out] = w.l[t] == 0.0f ? -INFINITY : (w.m[t] + __builtin_amdgcn_logf(w.l[t])) * kLn2;
+        }
+    }
+}
+
+// Joins the splits of one row and query head (D/2 threads of a block each).
+template <typename T, int D>
+__global__ __launch_bounds__(256) void kv_wide_merge_kernel(KvAttend a) {
+    constexpr int kPer = 256 / (D / 2);
+    const int64_t out = static_cast<int64_t>(blockIdx.x) * kPer + threadIdx.x / (D / 2);
+    const int d = 2 * (threadIdx.x % (D / 2));
+    if (out >= static_cast<int64_t>(a.s.T) * a.q_heads) return;
+    const int row = static_cast<int>(out / a.q_heads), h = static_cast<int>(out - static_cast<int64_t>(row) * a.q_heads);
+    int b, r0, n;
+    if (a.s.row_start) {
+        int lo = 0, hi = a.s.B;   // the last sequence that starts at or before the row
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.s.row_start[mid] <= row)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        b = lo;
+    } else {
+        b = row / a.s.even;
+    }
+    kv_rows(a.s, b, r0, n);
+    if (row < r0 || row >= r0 + n || static_cast<int64_t>(n) * a.per <= a.split_cols) return;
+    float top = -INFINITY, sum = 0.0f, y0 = 0.0f, y1 = 0.0f;
+    for (int k = 0; k < a.splits; ++k) {
+        const int64_t at = static_cast<int64_t>(k) * a.s.T * a.q_heads + out;
+        const float2 ml = *reinterpret_cast<const float2 *>(a.wide_ml + at * 2);
+        const float2 z = *reinterpret_cast<const float2 *>(a.wide_part + at * D + d);
+        const float now = fmaxf(top, ml.x);
+        const float f0 = top == now ? 1.0f : __builtin_amdgcn_exp2f(top - now);
+        const float f1 = ml.x == now ? 1.0f : __builtin_amdgcn_exp2f(ml.x - now);
+        sum = sum * f0 + ml.y * f1;
+        y0 = y0 * f0 + z.x * f1;
+        y1 = y1 * f0 + z.y * f1;
+        top = now;
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    T *dst = static_cast<T *>(a.O) + row * a.o_stride + static_cast<int64_t>(h) * D + d;
+    *reinterpret_cast<uint32_t *>(dst) = pack2<T>(y0 * inv, y1 * inv);
+    if (a.lse && d == 0)
+        a.lse[out] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+// ---------------------------------------------------------------------------
+
+template <typename T, int D, int NG>
+hipError_t kv_attend_typed(const KvAttend &a, bool run_split, bool run_wide, bool merge, hipStream_t st) {
+    if (run_split) {
+        const dim3 grid(static_cast<unsigned>(a.workers)), threads(64 * kSplitWaves);
+        if (a.tiles_col == 1)
+            hipLaunchKernelGGL((kv_split_kernel<T, D, NG, 1>), grid, threads, 0, st, a);
+        else if (a.tiles_col == 2)
+            hipLaunchKernelGGL((kv_split_kernel<T, D, NG, 2>), grid, threads, 0, st, a);
+        else
+            hipLaunchKernelGGL((kv_split_kernel<T, D, NG, 4>), grid, threads, 0, st, a);
+        if (merge)
+            hipLaunchKernelGGL((kv_merge_kernel<T, D>), dim3(a.s.B * a.c.heads, 16 * a.tiles_col), dim3(D / 2), 0, st,
+                               a);
+    }
+    if (run_wide) {
+        hipLaunchKernelGGL((kv_wide_kernel<T, D, NG>), dim3(a.units * a.c.heads, a.splits), dim3(256), 0, st, a);
+        if (a.splits > 1) {
+            const int64_t per = 256 / (D / 2), n = (static_cast<int64_t>(a.s.T) * a.q_heads + per - 1) / per;
+            hipLaunchKernelGGL((kv_wide_merge_kernel<T, D>), dim3(static_cast<unsigned>(n)), dim3(256), 0, st, a);
+        }
+    }
+    return hipGetLastError();
+}
+
+template <int D, int NG>
+hipError_t kv_attend_group(const KvAttend &a, int type, bool run_split, bool run_wide, bool merge, hipStream_t st) {
+    if (type == 1) return kv_attend_typed<__bf16, D, NG>(a, run_split, run_wide, merge, st);
+    return kv_attend_typed<_Float16, D, NG>(a, run_split, run_wide, merge, st);
+}
+
+}  // namespace
+}  // namespace awq

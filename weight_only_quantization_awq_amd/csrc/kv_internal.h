@@ -1,0 +1,117 @@
+// Internal declarations of the 4-bit key/value cache (k_kv.hip, kv_attend.h, awq_kv.hip).
+//
+// One block of bytes per (page, head), blocks of a page in head order, page
+// size P tokens, D channels, groups of `group` channels, NG = D / group:
+//   key codes    [P][D/2]           word kb*(D/32) + j of a token: channels 32j + 8kb + 0..7
+//                                   in the nibble order 0,2,4,6,1,3,5,7 of k_pack.hip
+//   value codes  [P/4][16][D/32][4] byte [t/4][m][b][t%4]: channel 32b + m (low nibble)
+//                                   and 32b + 16 + m (high nibble) of token t
+//   key pairs    [P][NG][2] fp16    (step, lowest value)
+//   value pairs  [P][NG][2] fp16
+//
+// The codes lie as the matrix cores take them.  S^T = K·Q^T: lane (n, kb) of a
+// 16x16x32 MFMA feeds 8 channels of key token n, so a lane's chunk kb of a
+// token (D/32 words) is its operand for all D/32 MFMAs, one wide load.
+// O^T = V^T·P^T: the lane that holds the scores of tokens 4kb..4kb+3 (the
+// result rows of the first product) feeds the same tokens of value channel
+// m, which are the bytes of its chunk [t/4][m]: scores go from the first
+// product to the second without crossing lanes, and every wave load of codes
+// is contiguous.
+#pragma once
+
+#include "awq_internal.h"
+
+namespace awq {
+
+struct KvCache {
+    unsigned char *pages;
+    int64_t page_stride;   // bytes between pages
+    int64_t block;         // bytes of one (page, head)
+    int n_pages, page_shift, heads, dim, group;
+};
+
+// The sequences of a call: sequence b's new rows are row_start[b] ..
+// row_start[b+1] - 1 (b*even .. with row_start NULL), the last of its
+// kv_len[b] positions.
+struct KvBatch {
+    const int32_t *row_start, *kv_len, *table;
+    int B, max_pages, T, even;
+};
+
+constexpr float kKvMaxAbs = 32768.0f;   // larger values (and NaN) are stored as NaN
+
+__device__ __forceinline__ int kv_clamp(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
+
+// First row and number of rows of sequence b, inside [0, T) whatever the table holds.
+__device__ __forceinline__ void kv_rows(const KvBatch &s, int b, int &r0, int &n) {
+    if (!s.row_start) {
+        r0 = b * s.even;
+        n = s.even;
+        return;
+    }
+    r0 = kv_clamp(s.row_start[b], 0, s.T);
+    n = kv_clamp(s.row_start[b + 1], r0, s.T) - r0;
+}
+
+// Tokens of sequence b, inside what its row of the page table holds.
+__device__ __forceinline__ int kv_length(const KvBatch &s, int b, int page_shift) {
+    return kv_clamp(s.kv_len[b], 0, s.max_pages << page_shift);
+}
+
+// Ragged rows in units of `size` (rows, or columns of `per` to a row): sequence
+// b owns units first(b) .. first(b+1) - 1 with first(b) = start(b)*per / size +
+// extra*b, which leaves room for every unit that its rows touch.  Finds the
+// sequence of unit u.
+__device__ __forceinline__ int kv_unit_first(const KvBatch &s, int b, int per, int size, int extra) {
+    return static_cast<int>(static_cast<int64_t>(kv_clamp(s.row_start[b], 0, s.T)) * per / size) + extra * b;
+}
+__device__ __forceinline__ int kv_unit_sequence(const KvBatch &s, int u, int per, int size, int extra) {
+    int lo = 0, hi = s.B;   // the last b in [0, B) with first(b) <= u
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (kv_unit_first(s, mid, per, size, extra) <= u)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+struct KvAttend {
+    KvCache c;
+    KvBatch s;
+    const void *Q;
+    void *O;
+    float *lse;
+    int64_t q_stride, o_stride;   // elements between rows
+    int q_heads, per;             // query heads, and query heads per key head
+    float scale_log2;             // scale * log2(e)
+    int causal, window;
+    int split_cols;               // sequences with at most this many columns take the split path
+    // split path
+    int tiles_col;                // column tiles of 16 per item: 1, 2 or 4
+    int workers;
+    int2 *items;                  // [B*heads]: first worker and number of pieces (0: written already)
+    float *part, *part_ml;        // [workers][2][16*tiles_col][dim] and [..][2]
+    // wide path
+    int splits, units;
+    float *wide_part, *wide_ml;   // [splits][T*q_heads][dim] and [..][2]
+};
+
+// A sequence's columns are its query rows x the query heads of one key head.
+constexpr int kKvSplitCols = 64;   // most columns of the split path (4 column tiles)
+constexpr int kKvWideCols = 256;   // columns of one workgroup of the wide path
+constexpr int kKvTile = 32;        // tokens of one step
+constexpr int kKvMinShare = 16;    // tiles: least share of a worker
+constexpr int kKvSnap = 7;         // tiles: pieces this short are not cut off (2 * snap < least share)
+
+hipError_t launch_kv_append(const KvCache &c, const KvBatch &s, const void *K, const void *V, int type,
+                            int64_t k_stride, int64_t v_stride, hipStream_t st);
+hipError_t launch_kv_read(const KvCache &c, const KvBatch &s, void *K, void *V, int type, int64_t k_stride,
+                          int64_t v_stride, hipStream_t st);
+// run_split / run_wide / merge_*: which launches the call needs (awq_kv.hip)
+hipError_t launch_kv_attend_64(const KvAttend &a, int type, bool run_split, bool run_wide, bool merge, hipStream_t st);
+hipError_t launch_kv_attend_128(const KvAttend &a, int type, bool run_split, bool run_wide, bool merge, hipStream_t st);
+hipError_t launch_kv_attend_256(const KvAttend &a, int type, bool run_split, bool run_wide, bool merge, hipStream_t st);
+
+}  // namespace awq
