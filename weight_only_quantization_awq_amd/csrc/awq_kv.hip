@@ -66,7 +66,7 @@ awq_status check(const awq_kv_cache *cache, const awq_kv_batch *batch, awq::KvCa
     const int64_t tiles = (batch->max_pages * cache->page + awq::kKvTile - 1) / awq::kKvTile;
     // units of the copy kernels and tiles of the attention's line
     if ((batch->rows / 4 + 2 * batch->batch) * cache->heads > kMaxCount || batch->batch * cache->heads > kMaxCount ||
-        batch->batch * cache->heads * tiles > kMaxCount)
+        batch->batch * cache->heads * (tiles + awq::kKvItemCost) > kMaxCount)
         return fail(AWQ_ERR_SHAPE, "batch * heads * max_pages or rows * heads too large for one call");
     int shift = 0;
     while ((1 << shift) < cache->page) ++shift;
@@ -123,12 +123,12 @@ awq_status copy_checks(const awq_kv_cache *cache, const awq_kv_batch *batch, con
 // The launches of one attention call and its workspace (byte offsets).
 struct Plan {
     bool split, wide, merge;
-    int tiles_col, split_cols, workers, splits, units;
+    int tiles_col, split_cols, part_cols, workers, splits, units;
     size_t items, part_ml, part, wide_ml, wide_part, total;
 };
 
-// Workgroups that fill the GPU (256 CUs): two a CU.
-constexpr int kWorkers = 512;
+// 256 CUs: workers of the split path (waves, 2 a SIMD), workgroups of the wide path.
+constexpr int kSplitWorkers = 2048, kWideGroups = 512;
 
 awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, int64_t max_rows, Plan *p) {
     if (q_heads < 1 || q_heads > 65535 || q_heads % c.heads != 0)
@@ -147,16 +147,17 @@ awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, i
     p->split = need <= limit && (!p->wide || s.row_start);
     p->tiles_col = need <= 16 ? 1 : need <= 32 ? 2 : 4;
     p->split_cols = p->split ? 16 * p->tiles_col : 0;
-    const int64_t line = s.B * static_cast<int64_t>(c.heads) * tiles;
+    p->part_cols = static_cast<int>(need < p->split_cols && !p->wide ? need : p->split_cols);
+    const int64_t line = s.B * static_cast<int64_t>(c.heads) * (tiles + awq::kKvItemCost);
     const int64_t useful = (line + awq::kKvMinShare - 1) / awq::kKvMinShare;
-    p->workers = static_cast<int>(useful < kWorkers ? useful : kWorkers);
+    p->workers = static_cast<int>(useful < kSplitWorkers ? useful : kSplitWorkers);
     p->merge = p->split && tiles > 2 * awq::kKvSnap;   // shorter items are never cut
     p->units = static_cast<int>(s.row_start ? s.T * per / awq::kKvWideCols + s.B
                                             : s.B * ((s.even * per + awq::kKvWideCols - 1) / awq::kKvWideCols));
     const int64_t groups = static_cast<int64_t>(p->units) * c.heads;
     p->splits = 1;
-    if (p->wide && groups < kWorkers) {
-        int64_t n = (kWorkers + groups - 1) / groups;
+    if (p->wide && groups < kWideGroups) {
+        int64_t n = (kWideGroups + groups - 1) / groups;
         if (n > 16) n = 16;
         if (n > tiles / 8) n = tiles / 8;
         p->splits = static_cast<int>(n < 1 ? 1 : n);
@@ -168,7 +169,7 @@ awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, i
         return here;
     };
     if (p->merge) {
-        const size_t n = static_cast<size_t>(p->workers) * 2 * 16 * p->tiles_col;
+        const size_t n = static_cast<size_t>(p->workers) * 2 * p->part_cols;
         p->items = take(static_cast<size_t>(s.B) * c.heads * 8);
         p->part_ml = take(n * 8);
         p->part = take(n * c.dim * 4);
@@ -257,6 +258,7 @@ awq_status awq_kv_attention(const awq_kv_cache *cache, const awq_kv_batch *batch
     a.window = window > (int64_t(1) << 30) ? 0 : static_cast<int>(window);   // (no sequence is longer)
     a.split_cols = p.split_cols;
     a.tiles_col = p.tiles_col;
+    a.part_cols = p.part_cols;
     a.workers = p.workers;
     a.splits = p.splits;
     a.units = p.units;

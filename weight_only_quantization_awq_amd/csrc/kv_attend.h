@@ -34,6 +34,15 @@ namespace {
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLagLog2 = 8.0f;   // scores may exceed the reference by this (log2): P <= 2^8 fits fp16
 
+// (x & mask) | bits in one instruction: VOP3 takes no literals, so the empty asm
+// statements keep both constants in registers.  (The instruction itself is the
+// compiler's: it has to see it to space it from MFMAs on the same registers.)
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+    asm("" : "+s"(mask));
+    asm("" : "+v"(bits));
+    return (x & mask) | bits;
+}
+
 template <typename T>
 struct KvType;
 template <>
@@ -44,7 +53,7 @@ struct KvType<__bf16> {
     // shift of i = 0; its sums cancel 8 times as much in float32, which shows in lse.)
     static __device__ __forceinline__ uint32_t pair(uint32_t w, int i) {
         const uint32_t x = i == 0 ? w << 3 : w >> (4 * i - 3);
-        return (x & 0x00780078u) | 0x41804180u;
+        return and_or(x, 0x00780078u, 0x41804180u);
     }
     static __device__ __forceinline__ floatx4 mfma(uint4 a, vec8 b, floatx4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(vec8, a), b, c, 0, 0, 0);
@@ -56,7 +65,7 @@ struct KvType<_Float16> {
     static constexpr float base = 64.0f;
     static __device__ __forceinline__ uint32_t pair(uint32_t w, int i) {
         const uint32_t x = i == 0 ? w << 4 : w >> (4 * (i - 1));
-        return (x & 0x00F000F0u) | 0x54005400u;
+        return and_or(x, 0x00F000F0u, 0x54005400u);
     }
     static __device__ __forceinline__ floatx4 mfma(uint4 a, vec8 b, floatx4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(vec8, a), b, c, 0, 0, 0);
@@ -278,9 +287,9 @@ struct KvWave {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const uint32_t w = s.v[h][b] >> (8 * e);
-                        const half2v cl = __builtin_bit_cast(half2v, (w & 0x000F000Fu) | 0x64006400u) -
+                        const half2v cl = __builtin_bit_cast(half2v, and_or(w, 0x000F000Fu, 0x64006400u)) -
                                           half2v{static_cast<_Float16>(1024), static_cast<_Float16>(1024)};
-                        const half2v ch = __builtin_bit_cast(half2v, (w & 0x00F000F0u) | 0x54005400u) -
+                        const half2v ch = __builtin_bit_cast(half2v, and_or(w, 0x00F000F0u, 0x54005400u)) -
                                           half2v{static_cast<_Float16>(64), static_cast<_Float16>(64)};
                         lo[2 * h + e] = __builtin_elementwise_fma(cl, vs[h][e], vl[h][e]);
                         hi[2 * h + e] = __builtin_elementwise_fma(ch, vs[h][e], vl[h][e]);
@@ -300,50 +309,87 @@ struct KvWave {
         }
     }
 
-    // Tokens of tiles t0, t0 + stride, .. < t1 of one sequence and head, the
-    // next tile's loads in flight while one is computed.  minpos / maxlow: the
-    // first last-visible and the last first-visible position of the columns.
-    __device__ __forceinline__ void run(const KvAttend &a, const int32_t *table, int head, int t0, int t1, int stride,
-                                        int len, int minpos, int maxlow, int lane) {
+    // Tokens of tiles t0 .. t1-1 of one sequence and head, the next tile's loads
+    // in flight while one is computed.  minpos / maxlow: the first last-visible
+    // and the last first-visible position of the columns.
+    __device__ __forceinline__ void run(const KvAttend &a, const int32_t *table, int head, int t0, int t1, int len,
+                                        int minpos, int maxlow, int lane) {
         if (t0 >= t1) return;
         KvStep<D, NG> s0, s1;
         int tok = t0 * kKvTile;
-        const int end = t1 * kKvTile, by = stride * kKvTile;
+        const int end = t1 * kKvTile;
         kv_load(a, head, tok, kv_page(a, table, tok, len), kv_page(a, table, tok + 16, len), lane, s0);
         int p0 = -1, p1 = -1;   // pages of the tile after
-        if (tok + by < end) p0 = kv_page(a, table, tok + by, len), p1 = kv_page(a, table, tok + by + 16, len);
+        if (tok + kKvTile < end) p0 = kv_page(a, table, tok + kKvTile, len), p1 = kv_page(a, table, tok + kKvTile + 16, len);
         while (true) {
-            bool more = tok + by < end;
-            if (more) kv_load(a, head, tok + by, p0, p1, lane, s1);
-            if (tok + 2 * by < end)
-                p0 = kv_page(a, table, tok + 2 * by, len), p1 = kv_page(a, table, tok + 2 * by + 16, len);
+            bool more = tok + kKvTile < end;
+            if (more) kv_load(a, head, tok + kKvTile, p0, p1, lane, s1);
+            if (tok + 2 * kKvTile < end)
+                p0 = kv_page(a, table, tok + 2 * kKvTile, len), p1 = kv_page(a, table, tok + 2 * kKvTile + 16, len);
             step(a, s0, tok, len, hides(s0, tok, minpos, maxlow), lane);
-            tok += by;
+            tok += kKvTile;
             if (!more) return;
-            more = tok + by < end;
-            if (more) kv_load(a, head, tok + by, p0, p1, lane, s0);
-            if (tok + 2 * by < end)
-                p0 = kv_page(a, table, tok + 2 * by, len), p1 = kv_page(a, table, tok + 2 * by + 16, len);
+            more = tok + kKvTile < end;
+            if (more) kv_load(a, head, tok + kKvTile, p0, p1, lane, s0);
+            if (tok + 2 * kKvTile < end)
+                p0 = kv_page(a, table, tok + 2 * kKvTile, len), p1 = kv_page(a, table, tok + 2 * kKvTile + 16, len);
             step(a, s1, tok, len, hides(s1, tok, minpos, maxlow), lane);
-            tok += by;
+            tok += kKvTile;
             if (!more) return;
         }
     }
     static __device__ __forceinline__ bool hides(const KvStep<D, NG> &s, int tok, int minpos, int maxlow) {
         return tok + kKvTile - 1 > minpos || tok < maxlow || !s.ok0 || !s.ok1;   // (minpos < length)
     }
+
+    // Output and lse of the columns col0 .. of a sequence's rows.
+    __device__ __forceinline__ void finish(const KvAttend &a, int head, int r0, int n, int col0, int lane) {
+        const int kb = lane >> 4;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int c = col0 + 16 * t + (lane & 15), i = c / a.per, h = head * a.per + c - i * a.per;
+            l[t] += __shfl_xor(l[t], 16);
+            l[t] += __shfl_xor(l[t], 32);
+            if (i >= n) continue;
+            const float inv = l[t] == 0.0f ? 0.0f : 1.0f / l[t];
+            T *dst = static_cast<T *>(a.O) + (r0 + i) * a.o_stride + static_cast<int64_t>(h) * D + 4 * kb;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d)
+                *reinterpret_cast<uint2 *>(dst + 16 * d) =
+                    pack4<T>(o[t][d][0] * inv, o[t][d][1] * inv, o[t][d][2] * inv, o[t][d][3] * inv);
+            if (a.lse && kb == 0)
+                a.lse[static_cast<int64_t>(r0 + i) * a.q_heads + h] =
+                    l[t] == 0.0f ? -INFINITY : (m[t] + __builtin_amdgcn_logf(l[t])) * kLn2;
+        }
+    }
+
+    // Sums of the columns col0 .. < cols, for a join: ml[c] = (reference, sum), part[c] = output.
+    __device__ __forceinline__ void keep(float *ml, float *part, int cols, int col0, int lane) {
+        const int kb = lane >> 4;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int c = col0 + 16 * t + (lane & 15);
+            l[t] += __shfl_xor(l[t], 16);
+            l[t] += __shfl_xor(l[t], 32);
+            if (c >= cols) continue;
+            if (kb == 0) *reinterpret_cast<float2 *>(ml + 2 * c) = make_float2(m[t], l[t]);
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d)
+                *reinterpret_cast<floatx4 *>(part + static_cast<int64_t>(c) * D + 16 * d + 4 * kb) = o[t][d];
+        }
+    }
 };
 
 // ---------------------------------------------------------------------------
-// Split path: sequences with at most 64 columns per key head (decoding).  The
-// tiles of all (sequence, head) items form one line, which the workers
-// (workgroups of 4 waves) share equally, so ragged lengths and few sequences
-// load the GPU evenly.  A worker's waves take its tiles in turn and join in
-// LDS.  An item inside one worker is written directly; the pieces of an item
-// that a boundary cuts go to the workspace and kv_merge_kernel joins them in order.
-// Boundaries within kKvSnap tiles of an item's end move there.
-
-constexpr int kSplitWaves = 4;
+// Split path: sequences with at most 16*NT columns per key head (decoding).
+//
+// The items (sequence, head) form one line, each kKvItemCost + its tiles long,
+// which the workers (one wave each, 2 to a SIMD) share equally: ragged
+// lengths and few long sequences load the GPU evenly, and nothing but the
+// lengths on the device decides it.  A worker that holds a whole item writes
+// its output; the pieces of an item that a boundary cuts go to the workspace
+// and kv_merge_kernel joins them in order.  Boundaries within kKvSnap tiles of an
+// item's ends move there.
 
 __device__ __forceinline__ int kv_first_token(const KvAttend &a, int len, int n) {
     if (!a.window) return 0;
@@ -359,186 +405,152 @@ __device__ __forceinline__ int kv_item_tiles(const KvAttend &a, int b, int &r0, 
     return t > 0 ? t : 1;   // an empty item is visited, too: its output is zero
 }
 
-struct KvItem {
-    int b, head, r0, n, len, tiles, begin;   // begin: its first tile on the line
+// 64 sequences of the line, one to a lane.
+struct KvLine {
+    int chunk, base;          // sequences 64*chunk ..; where the first one's items begin
+    int length, upto, total;  // of one head: this lane's sequence, up to its end, all 64
+
+    __device__ __forceinline__ void load(const KvAttend &a, int c, int lane) {
+        chunk = c;
+        int r0, n, len;
+        const int b = 64 * c + lane, t = b < a.s.B ? kv_item_tiles(a, b, r0, n, len) : 0;
+        length = t > 0 ? t + kKvItemCost : 0;
+        upto = length;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int up = __shfl_up(upto, d);
+            if (lane >= d) upto += up;
+        }
+        total = __builtin_amdgcn_readlane(upto, 63);
+    }
 };
 
-// before[i]: tiles of one head of the sequences before i*chunk (LDS, 257 entries)
-__device__ __forceinline__ KvItem kv_locate(const KvAttend &a, const int *before, int chunk, int x) {
+struct KvItem {
+    int b, head, r0, n, len, tiles, begin, end;   // begin, end: on the line
+};
+
+// The item at x (0 <= x < the line's length), at or behind the line's present chunk.
+__device__ __forceinline__ KvItem kv_locate(const KvAttend &a, KvLine &line, int x, int lane) {
     const int H = a.c.heads;
-    int lo = 0, hi = 256;   // the last i with H*before[i] <= x
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (H * before[mid] <= x)
-            lo = mid;
-        else
-            hi = mid;
+    while (x >= line.base + H * line.total && 64 * (line.chunk + 1) < a.s.B) {
+        line.base += H * line.total;
+        line.load(a, line.chunk + 1, lane);
     }
+    const int y = x - line.base;
+    const int k = kv_clamp(__popcll(__ballot(H * line.upto <= y)), 0, 63);
+    int length = __builtin_amdgcn_readlane(line.length, k);
+    const int before = H * (__builtin_amdgcn_readlane(line.upto, k) - length);
+    length = length > 0 ? length : 1;
     KvItem it;
-    int b = lo * chunk, sum = before[lo];
-    while (true) {   // x < H*before[lo + 1], so a sequence of this chunk holds it
-        it.tiles = kv_item_tiles(a, b, it.r0, it.n, it.len);
-        if (x < H * (sum + it.tiles) || b + 1 >= a.s.B) break;
-        sum += it.tiles;
-        ++b;
-    }
-    it.b = b;
-    it.tiles = it.tiles > 0 ? it.tiles : 1;
-    it.head = kv_clamp((x - H * sum) / it.tiles, 0, H - 1);
-    it.begin = H * sum + it.head * it.tiles;
+    it.b = 64 * line.chunk + k;
+    it.b = it.b < a.s.B ? it.b : a.s.B - 1;
+    it.head = kv_clamp((y - before) / length, 0, H - 1);
+    it.begin = line.base + before + it.head * length;
+    it.end = it.begin + length;
+    it.tiles = length - kKvItemCost;
+    kv_rows(a.s, it.b, it.r0, it.n);
+    it.len = kv_length(a.s, it.b, a.c.page_shift);
     return it;
 }
 
-__device__ __forceinline__ int kv_snap(const KvItem &it, int x) {
-    if (x - it.begin <= kKvSnap) return it.begin;
-    if (it.begin + it.tiles - x <= kKvSnap) return it.begin + it.tiles;
-    return x;
+// The tile at which a boundary at x cuts an item (0 or tiles: not inside).
+__device__ __forceinline__ int kv_cut(const KvItem &it, int x) {
+    const int t = x - it.begin - kKvItemCost;
+    if (t <= kKvSnap) return 0;
+    return it.tiles - t <= kKvSnap ? it.tiles : t;
 }
 
 template <typename T, int D, int NG, int NT>
-__global__ __launch_bounds__(64 * kSplitWaves) void kv_split_kernel(KvAttend a) {
-    constexpr int kThreads = 64 * kSplitWaves, kRow = D + 4;
-    __shared__ int before[257];
-    __shared__ int wave_sum[kSplitWaves];
-    __shared__ float ml[kSplitWaves][16 * NT][2];
-    __shared__ float buf[kSplitWaves][16][kRow];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int H = a.c.heads;
-    const int chunk = (a.s.B + 255) / 256;
-    {   // prefix sums over the sequences: thread i sums its chunk
-        int sum = 0, r0, n, len;
-        for (int b = tid * chunk; b < (tid + 1) * chunk && b < a.s.B; ++b) sum += kv_item_tiles(a, b, r0, n, len);
-        int incl = sum;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int up = __shfl_up(incl, d);
-            if (lane >= d) incl += up;
-        }
-        if (lane == 63) wave_sum[wave] = incl;
-        __syncthreads();
-        int base = 0;
-        for (int w = 0; w < wave; ++w) base += wave_sum[w];
-        before[tid + 1] = base + incl;
-        if (tid == 0) before[0] = 0;
-        __syncthreads();
+__global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(NT * D <= 256 ? 2 : 1))) void kv_split_kernel(
+    KvAttend a) {
+    const int lane = threadIdx.x;
+    KvLine line;
+    line.base = 0;
+    int total = 0;
+    for (int c = (a.s.B - 1) / 64; c >= 0; --c) {   // (ends with chunk 0 loaded)
+        line.load(a, c, lane);
+        total += line.total;
     }
-    const int total = H * before[256];
+    total *= a.c.heads;
     int share = (total + a.workers - 1) / a.workers;
     if (share < kKvMinShare) share = kKvMinShare;
     const int worker = blockIdx.x;
-    int64_t x0 = static_cast<int64_t>(worker) * share, x1 = x0 + share;
-    if (x0 >= total) return;   // (the whole workgroup)
-    int begin = static_cast<int>(x0), end = x1 < total ? static_cast<int>(x1) : total;
-    KvItem it = kv_locate(a, before, chunk, begin);
-    begin = kv_snap(it, begin);
-    if (end < total) end = kv_snap(kv_locate(a, before, chunk, end), end);
+    if (static_cast<int64_t>(worker) * share >= total) return;
+    const int x0 = worker * share, x1 = share < total - x0 ? x0 + share : total;
 
     KvWave<T, D, NG, NT> w;
-    while (begin < end) {
-        it = kv_locate(a, before, chunk, begin);
-        const int item_end = it.begin + it.tiles;
-        const int stop = end < item_end ? end : item_end;
-        const bool starts = begin == it.begin, direct = starts && stop == item_end;
-        const int first = kv_first_token(a, it.len, it.n) / kKvTile;
-        const int p0 = it.len - it.n;   // position of the first row
-        w.start(a, it.head, it.r0, it.n, it.len, 0, lane);
-        const int minpos = a.causal ? p0 : it.len - 1;
-        const int maxlow = a.window ? it.len - a.window : 0;
-        w.run(a, a.s.table + static_cast<int64_t>(it.b) * a.s.max_pages, it.head, first + begin - it.begin + wave,
-              first + stop - it.begin, kSplitWaves, it.len, minpos, maxlow, lane);
-        // join the waves
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            w.l[t] += __shfl_xor(w.l[t], 16);
-            w.l[t] += __shfl_xor(w.l[t], 32);
-            if (lane < 16) ml[wave][16 * t + lane][0] = w.m[t], ml[wave][16 * t + lane][1] = w.l[t];
-        }
-        const int cols = it.n * a.per;
-        const int64_t piece = static_cast<int64_t>(worker) * 2 + (starts ? 1 : 0);
-        __syncthreads();
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            {
-                const int c = lane & 15, kb = lane >> 4;
-                float top = ml[0][16 * t + c][0];
-#pragma unroll
-                for (int v = 1; v < kSplitWaves; ++v) top = fmaxf(top, ml[v][16 * t + c][0]);
-                const float f = w.m[t] == top ? 1.0f : __builtin_amdgcn_exp2f(w.m[t] - top);
-#pragma unroll
-                for (int d = 0; d < D / 16; ++d) {
-                    float4 y;
-                    y.x = w.o[t][d][0] * f, y.y = w.o[t][d][1] * f, y.z = w.o[t][d][2] * f, y.w = w.o[t][d][3] * f;
-                    *reinterpret_cast<float4 *>(&buf[wave][c][16 * d + 4 * kb]) = y;
-                }
+    KvItem it = kv_locate(a, line, x0, lane);
+    int t0 = x0 == it.begin ? 0 : kv_cut(it, x0);
+    while (true) {
+        const int t1 = x1 >= it.end ? it.tiles : kv_cut(it, x1);
+        if (t0 < t1) {
+            const int first = kv_first_token(a, it.len, it.n) / kKvTile;
+            w.start(a, it.head, it.r0, it.n, it.len, 0, lane);
+            const int minpos = a.causal ? it.len - it.n : it.len - 1;
+            const int maxlow = a.window ? it.len - a.window : 0;
+            w.run(a, a.s.table + static_cast<int64_t>(it.b) * a.s.max_pages, it.head, first + t0, first + t1, it.len,
+                  minpos, maxlow, lane);
+            const bool direct = t0 == 0 && t1 == it.tiles;
+            if (direct) {
+                w.finish(a, it.head, it.r0, it.n, 0, lane);
+            } else {
+                // of a worker's two pieces, the one that begins its item goes second
+                const int64_t at = (static_cast<int64_t>(worker) * 2 + (t0 == 0 ? 1 : 0)) * a.part_cols;
+                w.keep(a.part_ml + 2 * at, a.part + at * D, it.n * a.per, 0, lane);
             }
-            __syncthreads();
-            for (int e = tid; e < 16 * (D / 4); e += kThreads) {
-                const int c = e / (D / 4), d = 4 * (e % (D / 4)), col = 16 * t + c;
-                if (col >= cols) break;
-                float top = ml[0][col][0], sum = 0.0f;
-#pragma unroll
-                for (int v = 1; v < kSplitWaves; ++v) top = fmaxf(top, ml[v][col][0]);
-                float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                for (int v = 0; v < kSplitWaves; ++v) {
-                    const float mv = ml[v][col][0];
-                    sum += ml[v][col][1] * (mv == top ? 1.0f : __builtin_amdgcn_exp2f(mv - top));
-                    const float4 z = *reinterpret_cast<const float4 *>(&buf[v][c][d]);
-                    y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
-                }
-                if (direct) {
-                    const int i = col / a.per, h = it.head * a.per + col - i * a.per;
-                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                    T *dst = static_cast<T *>(a.O) + (it.r0 + i) * a.o_stride + static_cast<int64_t>(h) * D + d;
-                    *reinterpret_cast<uint2 *>(dst) = pack4<T>(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-                    if (a.lse && d == 0)
-                        a.lse[static_cast<int64_t>(it.r0 + i) * a.q_heads + h] =
-                            sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
-                } else {
-                    *reinterpret_cast<float4 *>(a.part + (piece * (16 * NT) + col) * D + d) = y;
-                    if (d == 0)
-                        *reinterpret_cast<float2 *>(a.part_ml + (piece * (16 * NT) + col) * 2) = make_float2(top, sum);
-                }
+            if (t0 == 0 && a.items && lane == 0) {
+                // pieces: this worker's and those of the workers whose start cuts the item
+                const int last = (it.end - kKvSnap - 1) / share;
+                a.items[it.b * a.c.heads + it.head] = direct ? make_int2(0, 0) : make_int2(worker, last - worker + 1);
             }
-            __syncthreads();
         }
-        if (starts && a.items && tid == 0) {
-            // pieces: this worker's and those of the workers whose start lies inside the item
-            const int last = (item_end - kKvSnap - 1) / share;
-            a.items[it.b * H + it.head] = direct ? make_int2(0, 0) : make_int2(worker, last - worker + 1);
-        }
-        begin = stop;
+        if (it.end >= x1) return;
+        it = kv_locate(a, line, it.end, lane);
+        t0 = 0;
     }
 }
 
 // Joins the pieces of one item's column: blockIdx.x = item, blockIdx.y = column.
+// D/4 threads hold its channels, and 1024/D groups of them take every
+// (1024/D)th piece; the groups join in LDS.
 template <typename T, int D>
-__global__ __launch_bounds__(D / 2) void kv_merge_kernel(KvAttend a) {
+__global__ __launch_bounds__(256) void kv_merge_kernel(KvAttend a) {
+    constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
     const int item = blockIdx.x, col = blockIdx.y;
-    const int b = item / a.c.heads, head = item - b * a.c.heads;
-    int r0, n, len;
-    if (kv_item_tiles(a, b, r0, n, len) == 0 || col >= n * a.per) return;
     const int2 it = a.items[item];
     if (it.y == 0) return;
-    const int cols = 16 * a.tiles_col, d = 2 * threadIdx.x;
-    float top = -INFINITY, sum = 0.0f, y0 = 0.0f, y1 = 0.0f;
-    for (int k = 0; k < it.y; ++k) {
-        const int64_t at = (static_cast<int64_t>(it.x + k) * 2 + (k == 0 ? 1 : 0)) * cols + col;
-        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + at * 2);
-        const float2 z = *reinterpret_cast<const float2 *>(a.part + at * D + d);
-        const float now = fmaxf(top, ml.x);
+    const int b = item / a.c.heads, head = item - b * a.c.heads;
+    int r0, n;
+    kv_rows(a.s, b, r0, n);
+    if (n == 0 || static_cast<int64_t>(n) * a.per > a.split_cols || col >= n * a.per) return;
+    const int d = 4 * (threadIdx.x % kLanes), group = threadIdx.x / kLanes;
+    float top = -INFINITY, sum = 0.0f;
+    floatx4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto join = [&](float m, float l, floatx4 z) {
+        const float now = fmaxf(top, m);
         const float f0 = top == now ? 1.0f : __builtin_amdgcn_exp2f(top - now);
-        const float f1 = ml.x == now ? 1.0f : __builtin_amdgcn_exp2f(ml.x - now);
-        sum = sum * f0 + ml.y * f1;
-        y0 = y0 * f0 + z.x * f1;
-        y1 = y1 * f0 + z.y * f1;
+        const float f1 = m == now ? 1.0f : __builtin_amdgcn_exp2f(m - now);
+        sum = sum * f0 + l * f1;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y[r] = y[r] * f0 + z[r] * f1;
         top = now;
+    };
+    for (int k = group; k < it.y; k += kGroups) {
+        const int64_t at = (static_cast<int64_t>(it.x + k) * 2 + (k == 0 ? 1 : 0)) * a.part_cols + col;
+        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + at * 2);
+        join(ml.x, ml.y, *reinterpret_cast<const floatx4 *>(a.part + at * D + d));
     }
+    __shared__ floatx4 ys[kGroups][kLanes];
+    __shared__ float2 mls[kGroups];
+    ys[group][threadIdx.x % kLanes] = y;
+    if (d == 0) mls[group] = make_float2(top, sum);
+    __syncthreads();
+    if (group != 0) return;
+    for (int g = 1; g < kGroups; ++g) join(mls[g].x, mls[g].y, ys[g][threadIdx.x]);
     const int i = col / a.per, h = head * a.per + col - i * a.per;
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     T *dst = static_cast<T *>(a.O) + (r0 + i) * a.o_stride + static_cast<int64_t>(h) * D + d;
-    *reinterpret_cast<uint32_t *>(dst) = pack2<T>(y0 * inv, y1 * inv);
+    *reinterpret_cast<uint2 *>(dst) = pack4<T>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
     if (a.lse && d == 0)
         a.lse[static_cast<int64_t>(r0 + i) * a.q_heads + h] =
             sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
@@ -595,31 +607,12 @@ __global__ __launch_bounds__(256) void kv_wide_kernel(KvAttend a) {
     w.start(a, head, r0, n, len, col0, lane);
     const int minpos = a.causal ? p0 + wi0 : len - 1;
     const int maxlow = a.window ? p0 + wi1 - a.window + 1 : 0;
-    w.run(a, a.s.table + static_cast<int64_t>(b) * a.s.max_pages, head, t0, t1, 1, len, minpos, maxlow, lane);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int c = col0 + 16 * t + (lane & 15), kb = lane >> 4;
-        w.l[t] += __shfl_xor(w.l[t], 16);
-        w.l[t] += __shfl_xor(w.l[t], 32);
-        if (c > last_col) continue;
-        const int i = c / a.per, h = head * a.per + c - i * a.per;
-        const int64_t out = static_cast<int64_t>(r0 + i) * a.q_heads + h;
-        if (a.splits > 1) {
-            const int64_t at = static_cast<int64_t>(split) * a.s.T * a.q_heads + out;
-            if (kb == 0) *reinterpret_cast<float2 *>(a.wide_ml + at * 2) = make_float2(w.m[t], w.l[t]);
-#pragma unroll
-            for (int d = 0; d < D / 16; ++d)
-                *reinterpret_cast<floatx4 *>(a.wide_part + at * D + 16 * d + 4 * kb) = w.o[t][d];
-        } else {
-            const float inv = w.l[t] == 0.0f ? 0.0f : 1.0f / w.l[t];
-            T *dst = static_cast<T *>(a.O) + (r0 + i) * a.o_stride + static_cast<int64_t>(h) * D + 4 * kb;
-#pragma unroll
-            for (int d = 0; d < D / 16; ++d)
-                *reinterpret_cast<uint2 *>(dst + 16 * d) = pack4<T>(w.o[t][d][0] * inv, w.o[t][d][1] * inv,
-                                                                    w.o[t][d][2] * inv, w.o[t][d][3] * inv);
-            if (a.lse && kb == 0)
-                a.lse[out] = w.l[t] == 0.0f ? -INFINITY : (w.m[t] + __builtin_amdgcn_logf(w.l[t])) * kLn2;
-        }
+    w.run(a, a.s.table + static_cast<int64_t>(b) * a.s.max_pages, head, t0, t1, len, minpos, maxlow, lane);
+    if (a.splits == 1) {
+        w.finish(a, head, r0, n, col0, lane);
+    } else {
+        const int64_t at = (static_cast<int64_t>(split) * a.c.heads + head) * a.s.T * a.per + static_cast<int64_t>(r0) * a.per;
+        w.keep(a.wide_ml + 2 * at, a.wide_part + at * D, static_cast<int>(cols), col0, lane);
     }
 }
 
@@ -649,7 +642,8 @@ __global__ __launch_bounds__(256) void kv_wide_merge_kernel(KvAttend a) {
     if (row < r0 || row >= r0 + n || static_cast<int64_t>(n) * a.per <= a.split_cols) return;
     float top = -INFINITY, sum = 0.0f, y0 = 0.0f, y1 = 0.0f;
     for (int k = 0; k < a.splits; ++k) {
-        const int64_t at = static_cast<int64_t>(k) * a.s.T * a.q_heads + out;
+        const int64_t at = (static_cast<int64_t>(k) * a.c.heads + h / a.per) * a.s.T * a.per +
+                           static_cast<int64_t>(row) * a.per + h % a.per;
         const float2 ml = *reinterpret_cast<const float2 *>(a.wide_ml + at * 2);
         const float2 z = *reinterpret_cast<const float2 *>(a.wide_part + at * D + d);
         const float now = fmaxf(top, ml.x);
@@ -672,16 +666,15 @@ __global__ __launch_bounds__(256) void kv_wide_merge_kernel(KvAttend a) {
 template <typename T, int D, int NG>
 hipError_t kv_attend_typed(const KvAttend &a, bool run_split, bool run_wide, bool merge, hipStream_t st) {
     if (run_split) {
-        const dim3 grid(static_cast<unsigned>(a.workers)), threads(64 * kSplitWaves);
+        const dim3 grid(static_cast<unsigned>(a.workers)), threads(64);
         if (a.tiles_col == 1)
             hipLaunchKernelGGL((kv_split_kernel<T, D, NG, 1>), grid, threads, 0, st, a);
         else if (a.tiles_col == 2)
             hipLaunchKernelGGL((kv_split_kernel<T, D, NG, 2>), grid, threads, 0, st, a);
-        else
+        else if constexpr (D < 256)   // (awq_kv.hip takes at most 2 column tiles at 256 channels)
             hipLaunchKernelGGL((kv_split_kernel<T, D, NG, 4>), grid, threads, 0, st, a);
         if (merge)
-            hipLaunchKernelGGL((kv_merge_kernel<T, D>), dim3(a.s.B * a.c.heads, 16 * a.tiles_col), dim3(D / 2), 0, st,
-                               a);
+            hipLaunchKernelGGL((kv_merge_kernel<T, D>), dim3(a.s.B * a.c.heads, a.part_cols), dim3(256), 0, st, a);
     }
     if (run_wide) {
         hipLaunchKernelGGL((kv_wide_kernel<T, D, NG>), dim3(a.units * a.c.heads, a.splits), dim3(256), 0, st, a);

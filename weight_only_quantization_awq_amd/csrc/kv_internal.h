@@ -92,18 +92,20 @@ struct KvAttend {
     int tiles_col;                // column tiles of 16 per item: 1, 2 or 4
     int workers;
     int2 *items;                  // [B*heads]: first worker and number of pieces (0: written already)
-    float *part, *part_ml;        // [workers][2][16*tiles_col][dim] and [..][2]
+    int part_cols;                // most columns of an item
+    float *part, *part_ml;        // [workers][2][part_cols][dim] and [..][2]
     // wide path
     int splits, units;
-    float *wide_part, *wide_ml;   // [splits][T*q_heads][dim] and [..][2]
+    float *wide_part, *wide_ml;   // [splits][heads][T*per][dim] and [..][2]
 };
 
 // A sequence's columns are its query rows x the query heads of one key head.
 constexpr int kKvSplitCols = 64;   // most columns of the split path (4 column tiles)
 constexpr int kKvWideCols = 256;   // columns of one workgroup of the wide path
 constexpr int kKvTile = 32;        // tokens of one step
-constexpr int kKvMinShare = 16;    // tiles: least share of a worker
-constexpr int kKvSnap = 7;         // tiles: pieces this short are not cut off (2 * snap < least share)
+constexpr int kKvItemCost = 3;     // what an item costs besides its tiles, in tiles
+constexpr int kKvMinShare = 8;     // least share of a worker, in tiles
+constexpr int kKvSnap = 2;         // tiles: pieces this short are not cut off (2 * snap < least share)
 
 hipError_t launch_kv_append(const KvCache &c, const KvBatch &s, const void *K, const void *V, int type,
                             int64_t k_stride, int64_t v_stride, hipStream_t st);
