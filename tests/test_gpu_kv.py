@@ -8,9 +8,11 @@ Attention, per output, with A = sum_t p_t |v'_t| and 2^-11 the half step of fp16
   - a score's float32 error e changes p by e, the sum of p by e:   A * 2e
   - float32 sums of P*v' and P over n tokens:        A * 2n * 2^-24
   - the output type's rounding:                       half a step of |O|
-e: a group's sum starts at -base*sum(q) and adds base + code times q (base 16 in
-bf16, 64 in fp16), at most `group` + 1 additions of partial sums no larger than
-M = (2*base + 15) * sum |q|, so group*2^-24*M*step; the groups' float32
+e: a group's sum adds base + code times q (base 16 in bf16, 64 in fp16), `group`
+additions of partial sums no larger than (base + 15) * sum |q|; step times it and
+lo - base*step times sum q (4 roundings of at most (2*base + 15) * sum |q| * step
+beyond |S|) then take the base out.  Both are within group*2^-24*M*step with
+M = (2*base + 15) * sum |q| for groups of 32 and more; the groups' float32
 combinations add 4 roundings of |S|; scores are in units of log2 (2 more).
 lse: e + 2^-22*(|lse| + 1) (exp2, log2 and the sum).
 """

@@ -151,9 +151,9 @@ awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, i
     const int64_t line = s.B * static_cast<int64_t>(c.heads) * (tiles + awq::kKvItemCost);
     const int64_t useful = (line + awq::kKvMinShare - 1) / awq::kKvMinShare;
     p->workers = static_cast<int>(useful < kSplitWorkers ? useful : kSplitWorkers);
-    p->merge = p->split && tiles > 2 * awq::kKvSnap;   // shorter items are never cut
-    p->units = static_cast<int>(s.row_start ? s.T * per / awq::kKvWideCols + s.B
-                                            : s.B * ((s.even * per + awq::kKvWideCols - 1) / awq::kKvWideCols));
+    p->merge = p->split && tiles > 2 * awq::kKvSnap + 1;   // shorter items are never cut
+    const int64_t wide = awq::kv_wide_cols(c.dim);
+    p->units = static_cast<int>(s.row_start ? s.T * per / wide + s.B : s.B * ((s.even * per + wide - 1) / wide));
     const int64_t groups = static_cast<int64_t>(p->units) * c.heads;
     p->splits = 1;
     if (p->wide && groups < kWideGroups) {

@@ -8,9 +8,8 @@
 // Both products run on 16x16x32 MFMAs, transposed (keys and values are the A
 // operand, queries and scores the B operand), 32 tokens a step:
 //  - S^T = codes·Q^T.  A code enters as the 16-bit float base + code, made by one
-//    and-or on the packed word (16 + code in bf16, 64 + code in fp16, exact).
-//    The accumulator starts at -base * sum q, so it ends at sum code*q; steps and
-//    lowest values are applied in float32.
+//    and-or on the packed word (16 + code in bf16, 64 + code in fp16, exact);
+//    steps and lowest values are applied in float32, the base taken out with the latter.
 //  - A lane's result rows are tokens 4kb..4kb+3 of one query, which are the
 //    tokens that its B operand of the second product takes: scores stay in
 //    their lane.
@@ -43,12 +42,26 @@ __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t b
     return (x & mask) | bits;
 }
 
+__device__ __forceinline__ float half_lo(uint32_t x) {
+    return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(x)));
+}
+__device__ __forceinline__ float half_hi(uint32_t x) {
+    return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(x >> 16)));
+}
+
+// A key pair (step, lo) as the factors of (sum (base + code)*q, sum q) in a score.
+__device__ __forceinline__ float2 key_factors(uint32_t pair, float base, float scale) {
+    const float step = half_lo(pair);
+    return make_float2(step * scale, fmaf(-base, step, half_hi(pair)) * scale);
+}
+
 template <typename T>
 struct KvType;
 template <>
 struct KvType<__bf16> {
     typedef bf16x8 vec8;
     static constexpr float base = 16.0f;
+    static __device__ __forceinline__ float2 key_pair(uint32_t p, float scale) { return key_factors(p, base, scale); }
     // codes of channels (2i, 2i+1) of a key word, + base.  (Base 128 would save the
     // shift of i = 0; its sums cancel 8 times as much in float32, which shows in lse.)
     static __device__ __forceinline__ uint32_t pair(uint32_t w, int i) {
@@ -63,6 +76,7 @@ template <>
 struct KvType<_Float16> {
     typedef half8 vec8;
     static constexpr float base = 64.0f;
+    static __device__ __forceinline__ float2 key_pair(uint32_t p, float scale) { return key_factors(p, base, scale); }
     static __device__ __forceinline__ uint32_t pair(uint32_t w, int i) {
         const uint32_t x = i == 0 ? w << 4 : w >> (4 * (i - 1));
         return and_or(x, 0x00F000F0u, 0x54005400u);
@@ -72,13 +86,16 @@ struct KvType<_Float16> {
     }
 };
 
-__device__ __forceinline__ float half_lo(uint32_t x) {
-    return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(x)));
-}
-__device__ __forceinline__ float half_hi(uint32_t x) {
-    return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(x >> 16)));
-}
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+
+// The bytes 0 and 2 of w hold two tokens' codes of two channels (low and high
+// nibbles): those codes, exact, in fp16.
+__device__ __forceinline__ void value_codes(uint32_t w, half2v &low, half2v &high) {
+    low = __builtin_bit_cast(half2v, and_or(w, 0x000F000Fu, 0x64006400u)) -
+          half2v{static_cast<_Float16>(1024), static_cast<_Float16>(1024)};
+    high = __builtin_bit_cast(half2v, and_or(w, 0x00F000F0u, 0x54005400u)) -
+           half2v{static_cast<_Float16>(64), static_cast<_Float16>(64)};
+}
 
 template <typename T>
 __device__ __forceinline__ uint2 pack4(float a, float b, float c, float d) {
@@ -107,11 +124,21 @@ __device__ __forceinline__ void load_words(const unsigned char *p, uint32_t *w) 
     }
 }
 
-// One step's codes and pairs, as a lane holds them.
+// One step's codes, as a lane's operands, and pairs: lanes 0..31 hold the key
+// pairs of tokens 0..31, lanes 32..63 the value pairs.
 template <int D, int NG>
 struct KvStep {
-    uint32_t k[2][D / 32], v[2][D / 32], kp[2][4 * NG], vp[2][4 * NG];
+    uint32_t k[2][D / 32], v[2][D / 32], pair[NG];
     bool ok0, ok1;   // the two 16-token halves exist
+};
+
+// A wave's pairs in LDS, made for reading by result rows (4 tokens of a lane):
+// keys as factors (key_factors), values as fp16 (step0, step2,
+// step1, step3, lo0, lo2, lo1, lo3), the order of the value bytes.
+template <int NG>
+struct KvPairs {
+    floatx4 k[2][NG][4][2];
+    uint4 v[2][NG][4];
 };
 
 // Page of token `tok` (uniform in a wave), -1 where there is none.
@@ -127,6 +154,7 @@ __device__ __forceinline__ void kv_load(const KvAttend &a, int head, int tok, in
     const int n = lane & 15, kb = lane >> 4, P = 1 << a.c.page_shift;
     s.ok0 = page0 >= 0;
     s.ok1 = page1 >= 0;
+    const unsigned char *pairs[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int page = h ? page1 : page0;
@@ -136,9 +164,37 @@ __device__ __forceinline__ void kv_load(const KvAttend &a, int head, int tok, in
             a.c.pages + (page < 0 ? 0 : page) * a.c.page_stride + head * a.c.block;
         load_words<D / 32>(b + slot * (D / 2) + (n * (D / 2) + kb * (D / 8)), s.k[h]);
         load_words<D / 32>(b + P * (D / 2) + slot * (D / 2) + (kb * 16 + n) * (D / 8), s.v[h]);
-        load_words<4 * NG>(b + P * D + slot * (4 * NG) + kb * (16 * NG), s.kp[h]);
-        load_words<4 * NG>(b + P * D + P * (4 * NG) + slot * (4 * NG) + kb * (16 * NG), s.vp[h]);
+        pairs[h] = b + P * D + slot * (4 * NG);
     }
+    load_words<NG>((kb & 1 ? pairs[1] : pairs[0]) + (kb >> 1) * P * (4 * NG) + n * (4 * NG), s.pair);
+}
+
+// A step's pairs into LDS.  Value pairs of tokens that do not exist become zero
+// (0 * NaN would not vanish).  One wave writes and reads them, in order.
+template <typename T, int D, int NG>
+__device__ __forceinline__ void kv_pairs(const KvAttend &a, const KvStep<D, NG> &s, int tok, int len, int lane,
+                                         KvPairs<NG> *lds) {
+    const int n = lane & 15, h = (lane >> 4) & 1;
+    const bool there = (h ? s.ok1 : s.ok0) && tok + 16 * h + n < len;
+    if (lane < 32) {
+        float *k = reinterpret_cast<float *>(&lds->k[h][0][0][0]) + 2 * n;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const float2 y = KvType<T>::key_pair(s.pair[g], a.scale_log2);
+            k[32 * g] = y.x;
+            k[32 * g + 1] = y.y;
+        }
+    } else {
+        const int r = n & 3, at = 8 * (n >> 2) + (r >> 1) + 2 * (r & 1);   // tokens 0, 2, 1, 3
+        uint16_t *v = reinterpret_cast<uint16_t *>(&lds->v[h][0][0]) + at;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const uint32_t p = there ? s.pair[g] : 0u;
+            v[32 * g] = static_cast<uint16_t>(p);
+            v[32 * g + 4] = static_cast<uint16_t>(p >> 16);
+        }
+    }
+    __builtin_amdgcn_wave_barrier();   // (the compiler's order; LDS runs a wave's accesses in turn)
 }
 
 // One wave's 16*NT columns: queries, running sums, output.
@@ -186,26 +242,20 @@ struct KvWave {
     }
 
     // Tokens tok .. tok+31.  edge: some of them may be hidden from some column.
-    __device__ __forceinline__ void step(const KvAttend &a, KvStep<D, NG> &s, int tok, int len, bool edge, int lane) {
+    __device__ __forceinline__ void step(const KvAttend &a, const KvStep<D, NG> &s, int tok, int len, bool edge,
+                                         int lane, KvPairs<NG> *lds) {
         const int kb = lane >> 4;
-        const float scale = a.scale_log2;
+        kv_pairs<T>(a, s, tok, len, lane, lds);
         floatx4 x[2][NT];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                float step[4], lo[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    step[r] = half_lo(s.kp[h][r * NG + g]) * scale;
-                    lo[r] = half_hi(s.kp[h][r * NG + g]) * scale;
-                }
+                const floatx4 k0 = lds->k[h][g][kb][0], k1 = lds->k[h][g][kb][1];
+                const float step[4] = {k0[0], k0[2], k1[0], k1[2]}, lo[4] = {k0[1], k0[3], k1[1], k1[3]};
                 floatx4 acc[NT];
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const float c0 = -KvType<T>::base * qs[t][g];
-                    acc[t] = floatx4{c0, c0, c0, c0};
-                }
+                for (int t = 0; t < NT; ++t) acc[t] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int j = g * (J / NG); j < (g + 1) * (J / NG); ++j) {
                     const uint32_t w = s.k[h][j];
@@ -217,10 +267,9 @@ struct KvWave {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float y = lo[r] * qs[t][g];
-                        x[h][t][r] = fmaf(step[r], acc[t][r], g == 0 ? y : x[h][t][r] + y);
-                    }
+                    for (int r = 0; r < 4; ++r)
+                        x[h][t][r] = fmaf(step[r], acc[t][r],
+                                          g == 0 ? lo[r] * qs[t][g] : fmaf(lo[r], qs[t][g], x[h][t][r]));
             }
         }
         if (edge) {
@@ -233,10 +282,6 @@ struct KvWave {
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
                         if (!there || p > pos[t] || p < low[t]) x[h][t][r] = -INFINITY;
-                    if (!there || p >= len) {
-#pragma unroll
-                        for (int g = 0; g < NG; ++g) s.vp[h][r * NG + g] = 0;
-                    }
                 }
         }
         half8 p[NT];
@@ -272,13 +317,11 @@ struct KvWave {
         for (int g = 0; g < NG; ++g) {
             half2v vs[2][2], vl[2][2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t p0 = s.vp[h][e * NG + g], p1 = s.vp[h][(e + 2) * NG + g];
-                    vs[h][e] = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(p1, p0, 0x05040100u));
-                    vl[h][e] = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(p1, p0, 0x07060302u));
-                }
+            for (int h = 0; h < 2; ++h) {
+                const uint4 v = lds->v[h][g][kb];
+                vs[h][0] = __builtin_bit_cast(half2v, v.x), vs[h][1] = __builtin_bit_cast(half2v, v.y);
+                vl[h][0] = __builtin_bit_cast(half2v, v.z), vl[h][1] = __builtin_bit_cast(half2v, v.w);
+            }
 #pragma unroll
             for (int b = g * (J / NG); b < (g + 1) * (J / NG); ++b) {
                 half2v lo[4], hi[4];
@@ -286,11 +329,8 @@ struct KvWave {
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const uint32_t w = s.v[h][b] >> (8 * e);
-                        const half2v cl = __builtin_bit_cast(half2v, and_or(w, 0x000F000Fu, 0x64006400u)) -
-                                          half2v{static_cast<_Float16>(1024), static_cast<_Float16>(1024)};
-                        const half2v ch = __builtin_bit_cast(half2v, and_or(w, 0x00F000F0u, 0x54005400u)) -
-                                          half2v{static_cast<_Float16>(64), static_cast<_Float16>(64)};
+                        half2v cl, ch;
+                        value_codes(s.v[h][b] >> (8 * e), cl, ch);
                         lo[2 * h + e] = __builtin_elementwise_fma(cl, vs[h][e], vl[h][e]);
                         hi[2 * h + e] = __builtin_elementwise_fma(ch, vs[h][e], vl[h][e]);
                     }
@@ -309,33 +349,40 @@ struct KvWave {
         }
     }
 
-    // Tokens of tiles t0 .. t1-1 of one sequence and head, the next tile's loads
-    // in flight while one is computed.  minpos / maxlow: the first last-visible
-    // and the last first-visible position of the columns.
+    // Tokens of tiles t0 .. t1-1 of one sequence and head.  The loads of the
+    // next kAhead tiles, and the page numbers of the one after, are in flight
+    // while a tile is computed.  minpos / maxlow: the first last-visible and the
+    // last first-visible position of the columns.
+    static constexpr int kAhead = NT * D <= 128 ? 2 : 1;
     __device__ __forceinline__ void run(const KvAttend &a, const int32_t *table, int head, int t0, int t1, int len,
-                                        int minpos, int maxlow, int lane) {
+                                        int minpos, int maxlow, int lane, KvPairs<NG> *lds) {
         if (t0 >= t1) return;
-        KvStep<D, NG> s0, s1;
-        int tok = t0 * kKvTile;
+        KvStep<D, NG> s[kAhead + 1];
+        int tok = t0 * kKvTile, p0 = -1, p1 = -1;
         const int end = t1 * kKvTile;
-        kv_load(a, head, tok, kv_page(a, table, tok, len), kv_page(a, table, tok + 16, len), lane, s0);
-        int p0 = -1, p1 = -1;   // pages of the tile after
-        if (tok + kKvTile < end) p0 = kv_page(a, table, tok + kKvTile, len), p1 = kv_page(a, table, tok + kKvTile + 16, len);
+        auto pages = [&](int t) {
+            if (t < end) p0 = kv_page(a, table, t, len), p1 = kv_page(a, table, t + 16, len);
+        };
+        pages(tok);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (tok + i * kKvTile < end) {
+                kv_load(a, head, tok + i * kKvTile, p0, p1, lane, s[i]);
+                pages(tok + (i + 1) * kKvTile);
+            }
+        }
         while (true) {
-            bool more = tok + kKvTile < end;
-            if (more) kv_load(a, head, tok + kKvTile, p0, p1, lane, s1);
-            if (tok + 2 * kKvTile < end)
-                p0 = kv_page(a, table, tok + 2 * kKvTile, len), p1 = kv_page(a, table, tok + 2 * kKvTile + 16, len);
-            step(a, s0, tok, len, hides(s0, tok, minpos, maxlow), lane);
-            tok += kKvTile;
-            if (!more) return;
-            more = tok + kKvTile < end;
-            if (more) kv_load(a, head, tok + kKvTile, p0, p1, lane, s0);
-            if (tok + 2 * kKvTile < end)
-                p0 = kv_page(a, table, tok + 2 * kKvTile, len), p1 = kv_page(a, table, tok + 2 * kKvTile + 16, len);
-            step(a, s1, tok, len, hides(s1, tok, minpos, maxlow), lane);
-            tok += kKvTile;
-            if (!more) return;
+#pragma unroll
+            for (int i = 0; i < kAhead + 1; ++i) {
+                const int next = tok + kAhead * kKvTile;
+                if (next < end) {
+                    kv_load(a, head, next, p0, p1, lane, s[(i + kAhead) % (kAhead + 1)]);
+                    pages(next + kKvTile);
+                }
+                step(a, s[i], tok, len, hides(s[i], tok, minpos, maxlow), lane, lds);
+                tok += kKvTile;
+                if (tok >= end) return;
+            }
         }
     }
     static __device__ __forceinline__ bool hides(const KvStep<D, NG> &s, int tok, int minpos, int maxlow) {
@@ -464,6 +511,7 @@ template <typename T, int D, int NG, int NT>
 __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(NT * D <= 256 ? 2 : 1))) void kv_split_kernel(
     KvAttend a) {
     const int lane = threadIdx.x;
+    __shared__ KvPairs<NG> pairs;
     KvLine line;
     line.base = 0;
     int total = 0;
@@ -472,11 +520,12 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(NT * D <= 25
         total += line.total;
     }
     total *= a.c.heads;
-    int share = (total + a.workers - 1) / a.workers;
-    if (share < kKvMinShare) share = kKvMinShare;
-    const int worker = blockIdx.x;
-    if (static_cast<int64_t>(worker) * share >= total) return;
-    const int x0 = worker * share, x1 = share < total - x0 ? x0 + share : total;
+    // worker w takes the line from w*total/workers on
+    const int worker = blockIdx.x, most = total / kKvMinShare > 1 ? total / kKvMinShare : 1;
+    const int workers = a.workers < most ? a.workers : most;
+    if (worker >= workers || total == 0) return;
+    const int x0 = static_cast<int>(static_cast<int64_t>(worker) * total / workers);
+    const int x1 = static_cast<int>((static_cast<int64_t>(worker) + 1) * total / workers);
 
     KvWave<T, D, NG, NT> w;
     KvItem it = kv_locate(a, line, x0, lane);
@@ -489,7 +538,7 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(NT * D <= 25
             const int minpos = a.causal ? it.len - it.n : it.len - 1;
             const int maxlow = a.window ? it.len - a.window : 0;
             w.run(a, a.s.table + static_cast<int64_t>(it.b) * a.s.max_pages, it.head, first + t0, first + t1, it.len,
-                  minpos, maxlow, lane);
+                  minpos, maxlow, lane, &pairs);
             const bool direct = t0 == 0 && t1 == it.tiles;
             if (direct) {
                 w.finish(a, it.head, it.r0, it.n, 0, lane);
@@ -499,8 +548,9 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(NT * D <= 25
                 w.keep(a.part_ml + 2 * at, a.part + at * D, it.n * a.per, 0, lane);
             }
             if (t0 == 0 && a.items && lane == 0) {
-                // pieces: this worker's and those of the workers whose start cuts the item
-                const int last = (it.end - kKvSnap - 1) / share;
+                // pieces: this worker's and those of the workers whose start cuts the item, the
+                // last of them the last that starts before it.end - kKvSnap
+                const int last = static_cast<int>((static_cast<int64_t>(it.end - kKvSnap) * workers + total - 1) / total) - 1;
                 a.items[it.b * a.c.heads + it.head] = direct ? make_int2(0, 0) : make_int2(worker, last - worker + 1);
             }
         }
@@ -535,10 +585,23 @@ __global__ __launch_bounds__(256) void kv_merge_kernel(KvAttend a) {
         for (int r = 0; r < 4; ++r) y[r] = y[r] * f0 + z[r] * f1;
         top = now;
     };
-    for (int k = group; k < it.y; k += kGroups) {
-        const int64_t at = (static_cast<int64_t>(it.x + k) * 2 + (k == 0 ? 1 : 0)) * a.part_cols + col;
-        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + at * 2);
-        join(ml.x, ml.y, *reinterpret_cast<const floatx4 *>(a.part + at * D + d));
+    constexpr int kAhead = 8;   // pieces in flight
+    for (int k0 = group; k0 < it.y; k0 += kAhead * kGroups) {
+        float2 ml[kAhead];
+        floatx4 z[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int k = k0 + i * kGroups;
+            if (k >= it.y) break;
+            const int64_t at = (static_cast<int64_t>(it.x + k) * 2 + (k == 0 ? 1 : 0)) * a.part_cols + col;
+            ml[i] = *reinterpret_cast<const float2 *>(a.part_ml + at * 2);
+            z[i] = *reinterpret_cast<const floatx4 *>(a.part + at * D + d);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (k0 + i * kGroups >= it.y) break;
+            join(ml[i].x, ml[i].y, z[i]);
+        }
     }
     __shared__ floatx4 ys[kGroups][kLanes];
     __shared__ float2 mls[kGroups];
@@ -557,22 +620,150 @@ __global__ __launch_bounds__(256) void kv_merge_kernel(KvAttend a) {
 }
 
 // ---------------------------------------------------------------------------
-// Wide path: sequences with more than 64 columns per key head (prompts,
-// chunks).  A workgroup takes 256 columns (rows x query heads of one key head),
-// 64 or 32 a wave, over one of `splits` equal parts of the tokens they see.
+// Wide path: sequences with more columns (prompts, chunks).
+//
+// A workgroup takes kv_wide_cols(D) columns (rows x query heads of one key
+// head), 32 a wave, over one of `splits` equal parts of the tokens they see, in
+// tiles of 8192/D tokens.  Here the matrix cores and the softmax bound it, so a
+// tile is unpacked once for all waves, into LDS, as 16-byte operands of
+// 32x32x16 MFMAs in reading order (every LDS access is contiguous); the
+// other half of the double buffer is filled between a tile's products and the
+// next barrier, from loads issued a tile earlier.  The same two layouts serve
+// this MFMA: result rows 8a + 4h + r of a lane are 4-token blocks, too.
+
+template <typename T>
+struct KvWideType;
+template <>
+struct KvWideType<__bf16> {
+    static __device__ __forceinline__ floatx16 mfma(uint4 a, bf16x8 b, floatx16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), b, c, 0, 0, 0);
+    }
+};
+template <>
+struct KvWideType<_Float16> {
+    static __device__ __forceinline__ floatx16 mfma(uint4 a, half8 b, floatx16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a), b, c, 0, 0, 0);
+    }
+};
+
+// What a thread unpacks of one tile: 1024/kThreads key words of one token (and
+// one of its pairs), 512/kThreads pieces of 8 tokens x 2 channels of the values.
+template <int D, int NG, int THREADS>
+struct KvWideLoad {
+    static constexpr int J = D / 32, TT = 8192 / D, KW = 1024 / THREADS, VI = 512 / THREADS;
+    uint32_t k[KW], kp, v[VI][2], vp[VI][8];
+    bool k_ok, v_ok[VI];
+    int k_page, v_page[VI];   // of the next tile
+
+    static __device__ __forceinline__ void piece(int i, int &m, int &b, int &h, int &u) {
+        const int x = threadIdx.x + THREADS * i;
+        m = x & 15, b = (x >> 4) % J, h = (x / (16 * J)) & 1, u = x / (32 * J);
+    }
+
+    __device__ __forceinline__ void pages(const KvAttend &a, const int32_t *table, int tok, int len) {
+        k_page = kv_page(a, table, tok + static_cast<int>(threadIdx.x) % TT, len);
+#pragma unroll
+        for (int i = 0; i < VI; ++i) {
+            int m, b, h, u;
+            piece(i, m, b, h, u);
+            v_page[i] = kv_page(a, table, tok + 16 * u, len);
+        }
+    }
+
+    __device__ __forceinline__ void load(const KvAttend &a, int head, int tok) {
+        const int P = 1 << a.c.page_shift;
+        auto block = [&](int page) {   // (page 0 in the place of one that does not exist)
+            return a.c.pages + (page < 0 ? 0 : page) * a.c.page_stride + head * a.c.block;
+        };
+        {
+            const int token = threadIdx.x % TT, c = threadIdx.x / TT, slot = (tok + token) & (P - 1);
+            k_ok = k_page >= 0;
+            const unsigned char *p = block(k_page);
+            load_words<KW>(p + slot * (D / 2) + c * (4 * KW), k);
+            if (c < NG) kp = *reinterpret_cast<const uint32_t *>(p + P * D + (slot * NG + c) * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < VI; ++i) {
+            int m, b, h, u;
+            piece(i, m, b, h, u);
+            const int slot = ((tok + 16 * u) & (P - 1)) + 4 * h;
+            v_ok[i] = v_page[i] >= 0;
+            const unsigned char *p = block(v_page[i]);
+            const unsigned char *q = p + P * (D / 2) + ((slot >> 2) * 16 + m) * (D / 8) + 4 * b;
+            v[i][0] = *reinterpret_cast<const uint32_t *>(q);
+            v[i][1] = *reinterpret_cast<const uint32_t *>(q + 4 * D);
+            const unsigned char *r = p + P * D + P * (4 * NG) + slot * (4 * NG) + 4 * (b * NG / J);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if constexpr (NG == 1) {
+                    load_words<4>(r + 32 * e, vp[i] + 4 * e);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        vp[i][4 * e + t] = *reinterpret_cast<const uint32_t *>(r + (8 * e + t) * (4 * NG));
+                }
+            }
+        }
+    }
+
+    // keys [octet][token], values [u][h][b][channel of 32], key pairs [g][token]
+    template <typename T>
+    __device__ __forceinline__ void unpack(const KvAttend &a, int tok, int len, uint4 *ks, uint4 *vs, float2 *pairs,
+                                           int *lost) const {
+        {
+            const int token = threadIdx.x % TT, c = threadIdx.x / TT;
+#pragma unroll
+            for (int i = 0; i < KW; ++i) {
+                const int w = c * KW + i, octet = 4 * (w % J) + w / J;
+                ks[octet * TT + token] = make_uint4(KvType<T>::pair(k[i], 0), KvType<T>::pair(k[i], 1),
+                                                    KvType<T>::pair(k[i], 2), KvType<T>::pair(k[i], 3));
+            }
+            if (c < NG) pairs[c * TT + token] = KvType<T>::key_pair(kp, a.scale_log2);
+            if (c == 0 && (token & 15) == 0) lost[token >> 4] = !k_ok;
+        }
+#pragma unroll
+        for (int i = 0; i < VI; ++i) {
+            int m, b, h, u;
+            piece(i, m, b, h, u);
+            uint32_t lo[4], hi[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                uint32_t q[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t)   // a token that does not exist is worth zero
+                    q[t] = v_ok[i] && tok + 16 * u + 8 * e + 4 * h + t < len ? vp[i][4 * e + t] : 0u;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const half2v s = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(q[t + 2], q[t], 0x05040100u));
+                    const half2v l = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(q[t + 2], q[t], 0x07060302u));
+                    half2v cl, ch;
+                    value_codes(v[i][e] >> (8 * t), cl, ch);
+                    lo[2 * e + t] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(cl, s, l));
+                    hi[2 * e + t] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(ch, s, l));
+                }
+            }
+            uint4 *dst = vs + ((u * 2 + h) * J + b) * 32 + m;
+            dst[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            dst[16] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        }
+    }
+};
 
 template <typename T, int D, int NG>
-__global__ __launch_bounds__(256) void kv_wide_kernel(KvAttend a) {
-    constexpr int NT = 4;
-    const int tid = threadIdx.x, lane = tid & 63;
+__global__ __launch_bounds__(2 * kv_wide_cols(D)) void kv_wide_kernel(KvAttend a) {
+    constexpr int kCols = kv_wide_cols(D), kThreads = 2 * kCols, J = D / 32, TT = 8192 / D, S = D / 16;
+    __shared__ uint4 ks[2][1024], vs[2][1024];
+    __shared__ float2 pairs[2][NG * TT];
+    __shared__ int lost[2][TT / 16];
+    const int tid = threadIdx.x, lane = tid & 63, n32 = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int head = blockIdx.x % a.c.heads;
     const int u = a.units - 1 - blockIdx.x / a.c.heads;   // the longest first
     const int split = blockIdx.y;
     int b, k, r0, n;
     if (a.s.row_start) {
-        b = kv_unit_sequence(a.s, u, a.per, kKvWideCols, 1);
-        k = u - kv_unit_first(a.s, b, a.per, kKvWideCols, 1);
+        b = kv_unit_sequence(a.s, u, a.per, kCols, 1);
+        k = u - kv_unit_first(a.s, b, a.per, kCols, 1);
     } else {
         const int each = a.units / a.s.B;
         b = u / each;
@@ -580,40 +771,166 @@ __global__ __launch_bounds__(256) void kv_wide_kernel(KvAttend a) {
     }
     kv_rows(a.s, b, r0, n);
     const int64_t cols = static_cast<int64_t>(n) * a.per;
-    if (cols <= a.split_cols || k < 0 || static_cast<int64_t>(k) * kKvWideCols >= cols) return;
-    const int len = kv_length(a.s, b, a.c.page_shift);
-    const int col0 = k * kKvWideCols + wave * (16 * NT);
-    const int p0 = len - n;
-    // rows of this workgroup and of this wave
-    const int last_col = static_cast<int>(cols) - 1;
+    if (cols <= a.split_cols || k < 0 || static_cast<int64_t>(k) * kCols >= cols) return;
+    const int len = kv_length(a.s, b, a.c.page_shift), p0 = len - n;
+    const int last_col = static_cast<int>(cols) - 1, col0 = k * kCols + wave * 32;
+    const int32_t *table = a.s.table + static_cast<int64_t>(b) * a.s.max_pages;
     auto row_of = [&](int c) { return (c < last_col ? c : last_col) / a.per; };
-    const int i0 = row_of(k * kKvWideCols), i1 = row_of(k * kKvWideCols + kKvWideCols - 1);
-    const int wi0 = row_of(col0), wi1 = row_of(col0 + 16 * NT - 1);
+    // tokens that some column of the workgroup sees, and that some of the wave sees
+    const int i0 = row_of(k * kCols), i1 = row_of(k * kCols + kCols - 1), wi0 = row_of(col0), wi1 = row_of(col0 + 31);
     int lo = a.window ? p0 + i0 - a.window + 1 : 0, hi = a.causal ? p0 + i1 + 1 : len;
-    lo = lo > 0 ? lo / kKvTile : 0;
-    hi = hi > 0 ? (hi + kKvTile - 1) / kKvTile : 0;
+    lo = lo > 0 ? lo / TT : 0;
+    hi = hi > 0 ? (hi + TT - 1) / TT : 0;
     int t0 = lo, t1 = hi;
     if (a.splits > 1) {
         const int part = (hi - lo + a.splits - 1) / a.splits;
-        t0 = lo + split * part;
+        t0 = lo + split * part < hi ? lo + split * part : hi;
         t1 = t0 + part < hi ? t0 + part : hi;
     }
-    const int wave_hi = a.causal ? (p0 + wi1 + kKvTile) / kKvTile : hi;   // (p0 + wi1 >= 0 or nothing visible)
-    if (p0 + wi1 < 0 && a.causal)
-        t1 = t0;
-    else if (wave_hi < t1)
-        t1 = wave_hi;
-    KvWave<T, D, NG, NT> w;
-    w.start(a, head, r0, n, len, col0, lane);
-    const int minpos = a.causal ? p0 + wi0 : len - 1;
-    const int maxlow = a.window ? p0 + wi1 - a.window + 1 : 0;
-    w.run(a, a.s.table + static_cast<int64_t>(b) * a.s.max_pages, head, t0, t1, len, minpos, maxlow, lane);
-    if (a.splits == 1) {
-        w.finish(a, head, r0, n, col0, lane);
-    } else {
-        const int64_t at = (static_cast<int64_t>(split) * a.c.heads + head) * a.s.T * a.per + static_cast<int64_t>(r0) * a.per;
-        w.keep(a.wide_ml + 2 * at, a.wide_part + at * D, static_cast<int>(cols), col0, lane);
+    const int wave_lo = a.window ? p0 + wi0 - a.window + 1 : 0, wave_hi = a.causal ? p0 + wi1 + 1 : len;
+    // where nothing is hidden from the wave's columns
+    const int minpos = a.causal ? p0 + wi0 : len - 1, maxlow = a.window ? p0 + wi1 - a.window + 1 : 0;
+
+    // this lane's column: its queries, their sums, its visible positions
+    typedef typename KvType<T>::vec8 vec8;
+    const int col = col0 + n32, row = col / a.per;
+    const bool real = row < n;
+    const int pos = real ? (a.causal ? p0 + row : len - 1) : -1, low = a.window ? p0 + row - a.window + 1 : 0;
+    vec8 q[S];
+    float qs[NG], m = -INFINITY, l = 0.0f;
+    floatx16 o[J];
+    {
+        const T *src = static_cast<const T *>(a.Q) + (r0 + (real ? row : 0)) * a.q_stride +
+                       static_cast<int64_t>(head * a.per + (col - row * a.per)) * D + 8 * h;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) qs[g] = 0.0f;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            vec8 x = {};
+            if (real) x = *reinterpret_cast<const vec8 *>(src + 16 * s);
+            q[s] = x;
+            float sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += static_cast<float>(x[e]);
+            qs[s * NG / S] += sum;
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) qs[g] += __shfl_xor(qs[g], 32);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[j][r] = 0.0f;
     }
+
+    KvWideLoad<D, NG, kThreads> in;
+    if (t0 < t1) {
+        in.pages(a, table, t0 * TT, len);
+        in.load(a, head, t0 * TT);
+        in.template unpack<T>(a, t0 * TT, len, ks[0], vs[0], pairs[0], lost[0]);
+        if (t0 + 1 < t1) {
+            in.pages(a, table, (t0 + 1) * TT, len);
+            in.load(a, head, (t0 + 1) * TT);
+        }
+        if (t0 + 2 < t1) in.pages(a, table, (t0 + 2) * TT, len);
+    }
+    for (int t = t0; t < t1; ++t) {
+        const int buf = (t - t0) & 1;
+        __syncthreads();   // this tile is in LDS, and the other buffer has been read
+#pragma unroll
+        for (int st = 0; st < TT / 32; ++st) {
+            const int tok = t * TT + 32 * st;
+            if (tok >= wave_hi || tok + 31 < wave_lo) continue;   // (uniform in the wave)
+            const bool gone0 = __builtin_amdgcn_readfirstlane(lost[buf][2 * st]) != 0;
+            const bool gone1 = __builtin_amdgcn_readfirstlane(lost[buf][2 * st + 1]) != 0;
+            float ref = m == -INFINITY ? 0.0f : m;
+            floatx16 x;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                floatx16 acc = {};
+#pragma unroll
+                for (int s = g * (S / NG); s < (g + 1) * (S / NG); ++s)
+                    acc = KvWideType<T>::mfma(ks[buf][(2 * s + h) * TT + 32 * st + n32], q[s], acc);
+                const floatx4 *kp = reinterpret_cast<const floatx4 *>(&pairs[buf][g * TT + 32 * st + 4 * h]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int r = 0; r < 4; r += 2) {
+                        const floatx4 y = kp[4 * e + r / 2];   // (step, lo) of two tokens
+                        x[4 * e + r] = fmaf(y[0], acc[4 * e + r], fmaf(y[1], qs[g], g == 0 ? -ref : x[4 * e + r]));
+                        x[4 * e + r + 1] =
+                            fmaf(y[2], acc[4 * e + r + 1], fmaf(y[3], qs[g], g == 0 ? -ref : x[4 * e + r + 1]));
+                    }
+            }
+            if (tok + 31 > minpos || tok < maxlow || gone0 || gone1) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int p = tok + 8 * (r >> 2) + 4 * h + (r & 3);
+                    if (p > pos || p < low || (r < 8 ? gone0 : gone1)) x[r] = -INFINITY;
+                }
+            }
+            float top = x[0];
+#pragma unroll
+            for (int r = 1; r < 16; ++r) top = fmaxf(top, x[r]);
+            if (__any(top > (m == -INFINITY ? -INFINITY : kLagLog2))) {
+                float now = fmaxf(m, top + ref);
+                now = fmaxf(now, __shfl_xor(now, 32));
+                const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - now);
+                m = now;
+                const float back = (m == -INFINITY ? 0.0f : m) - ref;
+                l *= f;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) x[r] -= back;
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) o[j][r] *= f;
+            }
+            half8 p[2];
+            constexpr int kOrder[4] = {0, 2, 1, 3};   // of the value bytes
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const float e = __builtin_amdgcn_exp2f(x[(r & ~3) + kOrder[r & 3]]);
+                l += e;
+                p[r >> 3][r & 7] = static_cast<_Float16>(e);
+            }
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+                    o[j] = KvWideType<_Float16>::mfma(vs[buf][(((2 * st + v) * 2 + h) * J + j) * 32 + n32], p[v], o[j]);
+        }
+        if (t + 1 < t1) {
+            in.template unpack<T>(a, (t + 1) * TT, len, ks[buf ^ 1], vs[buf ^ 1], pairs[buf ^ 1], lost[buf ^ 1]);
+            if (t + 2 < t1) in.load(a, head, (t + 2) * TT);
+            if (t + 3 < t1) in.pages(a, table, (t + 3) * TT, len);
+        }
+    }
+    l += __shfl_xor(l, 32);
+    if (!real) return;
+    const int qh = head * a.per + col - row * a.per;
+    if (a.splits > 1) {
+        const int64_t at = (static_cast<int64_t>(split) * a.c.heads + head) * a.s.T * a.per +
+                           static_cast<int64_t>(r0) * a.per + col;
+        if (h == 0) *reinterpret_cast<float2 *>(a.wide_ml + 2 * at) = make_float2(m, l);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<floatx4 *>(a.wide_part + at * D + 32 * j + 8 * e + 4 * h) =
+                    floatx4{o[j][4 * e], o[j][4 * e + 1], o[j][4 * e + 2], o[j][4 * e + 3]};
+        return;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    T *dst = static_cast<T *>(a.O) + (r0 + row) * a.o_stride + static_cast<int64_t>(qh) * D + 4 * h;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint2 *>(dst + 32 * j + 8 * e) = pack4<T>(
+                o[j][4 * e] * inv, o[j][4 * e + 1] * inv, o[j][4 * e + 2] * inv, o[j][4 * e + 3] * inv);
+    if (a.lse && h == 0)
+        a.lse[static_cast<int64_t>(r0 + row) * a.q_heads + qh] =
+            l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // Joins the splits of one row and query head (D/2 threads of a block each).
@@ -677,7 +994,8 @@ hipError_t kv_attend_typed(const KvAttend &a, bool run_split, bool run_wide, boo
             hipLaunchKernelGGL((kv_merge_kernel<T, D>), dim3(a.s.B * a.c.heads, a.part_cols), dim3(256), 0, st, a);
     }
     if (run_wide) {
-        hipLaunchKernelGGL((kv_wide_kernel<T, D, NG>), dim3(a.units * a.c.heads, a.splits), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((kv_wide_kernel<T, D, NG>), dim3(a.units * a.c.heads, a.splits), dim3(2 * kv_wide_cols(D)), 0,
+                           st, a);
         if (a.splits > 1) {
             const int64_t per = 256 / (D / 2), n = (static_cast<int64_t>(a.s.T) * a.q_heads + per - 1) / per;
             hipLaunchKernelGGL((kv_wide_merge_kernel<T, D>), dim3(static_cast<unsigned>(n)), dim3(256), 0, st, a);

@@ -101,7 +101,9 @@ struct KvAttend {
 
 // A sequence's columns are its query rows x the query heads of one key head.
 constexpr int kKvSplitCols = 64;   // most columns of the split path (4 column tiles)
-constexpr int kKvWideCols = 256;   // columns of one workgroup of the wide path
+// Columns of one workgroup of the wide path, 32 to a wave: 8 waves, or 4 where
+// the output alone takes 128 registers.
+constexpr int kv_wide_cols(int dim) { return dim > 128 ? 128 : 256; }
 constexpr int kKvTile = 32;        // tokens of one step
 constexpr int kKvItemCost = 3;     // what an item costs besides its tiles, in tiles
 constexpr int kKvMinShare = 8;     // least share of a worker, in tiles
