@@ -646,115 +646,154 @@ struct KvWideType<_Float16> {
     }
 };
 
-// What a thread unpacks of one tile: 1024/kThreads key words of one token (and
-// one of its pairs), 512/kThreads pieces of 8 tokens x 2 channels of the values.
+// What a thread unpacks of one tile: 1024/THREADS key words of one token (and
+// one of its pairs), 512/THREADS pieces of 8 tokens x 2 channels of the values.
+// Everything is loaded whether the token exists or not (from page 0 where it has
+// none), so the loop that calls this has no branches for it.
 template <int D, int NG, int THREADS>
 struct KvWideLoad {
     static constexpr int J = D / 32, TT = 8192 / D, KW = 1024 / THREADS, VI = 512 / THREADS;
     uint32_t k[KW], kp, v[VI][2], vp[VI][8];
+    int k_id, v_id[VI];      // page numbers of the next tile, as the table holds them
     bool k_ok, v_ok[VI];
-    int k_page, v_page[VI];   // of the next tile
+    uint32_t lo[4], hi[4];   // a piece being unpacked
+    int pair_from, pair_to, lost_to;
 
+    // Where this lane's key pair comes from and goes, and the wave's mark of missing
+    // keys; lanes and waves that have none write behind the others'.  (Opaque, or they
+    // become branches in the loop.)
+    __device__ __forceinline__ void init() {
+        pair_from = ((threadIdx.x & 15) * NG + (chunk() < NG ? chunk() : 0)) * 4;
+        pair_to = chunk() < NG ? chunk() * TT + token() : NG * TT;
+        lost_to = chunk() == 0 ? key_block() : TT / 16;
+        asm("" : "+v"(pair_from), "+v"(pair_to), "+v"(lost_to));
+    }
+    // The keys' 16-token block and the values' (u) are one for a wave, so pages,
+    // their checks and addresses cost scalar instructions only.
+    static __device__ __forceinline__ int wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+    static __device__ __forceinline__ int key_block() { return wave() % (TT / 16); }
+    static __device__ __forceinline__ int token() { return 16 * key_block() + (threadIdx.x & 15); }
+    static __device__ __forceinline__ int chunk() { return ((threadIdx.x >> 4) & 3) + 4 * (wave() / (TT / 16)); }
     static __device__ __forceinline__ void piece(int i, int &m, int &b, int &h, int &u) {
         const int x = threadIdx.x + THREADS * i;
-        m = x & 15, b = (x >> 4) % J, h = (x / (16 * J)) & 1, u = x / (32 * J);
+        m = x & 15, b = (x >> 4) % J, h = (x / (16 * J)) & 1, u = __builtin_amdgcn_readfirstlane(x / (32 * J));
+    }
+    // (len >= 1 here.  A vector load: a scalar one in flight would make every
+    // wait for an LDS operand a wait for all of them.)
+    static __device__ __forceinline__ int id_of(const KvAttend &a, const int32_t *table, int tok, int len) {
+        int at = (tok < len ? tok : len - 1) >> a.c.page_shift;
+        asm("" : "+v"(at));
+        return table[at];
+    }
+    static __device__ __forceinline__ const unsigned char *block(const KvAttend &a, int head, int id, int tok, int len,
+                                                                 bool &ok) {
+        id = __builtin_amdgcn_readfirstlane(id);
+        ok = (tok < len) & (id >= 0) & (id < a.c.n_pages);   // (no short circuit: no branches)
+        return a.c.pages + (id & -static_cast<int>(ok)) * a.c.page_stride + head * a.c.block;
     }
 
-    __device__ __forceinline__ void pages(const KvAttend &a, const int32_t *table, int tok, int len) {
-        k_page = kv_page(a, table, tok + static_cast<int>(threadIdx.x) % TT, len);
+    __device__ __forceinline__ void key_page(const KvAttend &a, const int32_t *table, int tok, int len) {
+        k_id = id_of(a, table, tok + 16 * key_block(), len);
+    }
+    __device__ __forceinline__ void value_pages(const KvAttend &a, const int32_t *table, int tok, int len) {
 #pragma unroll
         for (int i = 0; i < VI; ++i) {
             int m, b, h, u;
             piece(i, m, b, h, u);
-            v_page[i] = kv_page(a, table, tok + 16 * u, len);
+            v_id[i] = id_of(a, table, tok + 16 * u, len);
         }
     }
 
-    __device__ __forceinline__ void load(const KvAttend &a, int head, int tok) {
+    __device__ __forceinline__ void load_keys(const KvAttend &a, int head, int tok, int len) {
+        const int P = 1 << a.c.page_shift, at = tok + 16 * key_block(), slot = at & (P - 1), n = threadIdx.x & 15;
+        const unsigned char *p = block(a, head, k_id, at, len, k_ok);
+        load_words<KW>(p + slot * (D / 2) + static_cast<uint32_t>(n * (D / 2) + chunk() * (4 * KW)), k);
+        kp = *reinterpret_cast<const uint32_t *>(p + P * D + slot * (4 * NG) + static_cast<uint32_t>(pair_from));
+    }
+    __device__ __forceinline__ void load_values(const KvAttend &a, int head, int tok, int len) {
         const int P = 1 << a.c.page_shift;
-        auto block = [&](int page) {   // (page 0 in the place of one that does not exist)
-            return a.c.pages + (page < 0 ? 0 : page) * a.c.page_stride + head * a.c.block;
-        };
-        {
-            const int token = threadIdx.x % TT, c = threadIdx.x / TT, slot = (tok + token) & (P - 1);
-            k_ok = k_page >= 0;
-            const unsigned char *p = block(k_page);
-            load_words<KW>(p + slot * (D / 2) + c * (4 * KW), k);
-            if (c < NG) kp = *reinterpret_cast<const uint32_t *>(p + P * D + (slot * NG + c) * 4);
-        }
 #pragma unroll
         for (int i = 0; i < VI; ++i) {
             int m, b, h, u;
             piece(i, m, b, h, u);
-            const int slot = ((tok + 16 * u) & (P - 1)) + 4 * h;
-            v_ok[i] = v_page[i] >= 0;
-            const unsigned char *p = block(v_page[i]);
-            const unsigned char *q = p + P * (D / 2) + ((slot >> 2) * 16 + m) * (D / 8) + 4 * b;
-            v[i][0] = *reinterpret_cast<const uint32_t *>(q);
-            v[i][1] = *reinterpret_cast<const uint32_t *>(q + 4 * D);
-            const unsigned char *r = p + P * D + P * (4 * NG) + slot * (4 * NG) + 4 * (b * NG / J);
+            const int slot = (tok + 16 * u) & (P - 1);
+            const unsigned char *p = block(a, head, v_id[i], tok + 16 * u, len, v_ok[i]);
+            const unsigned char *q = p + P * (D / 2) + slot * (D / 2);
+            const uint32_t at = (h * 16 + m) * (D / 8) + 4 * b;
+            v[i][0] = *reinterpret_cast<const uint32_t *>(q + at);
+            v[i][1] = *reinterpret_cast<const uint32_t *>(q + 4 * D + at);
+            const unsigned char *r = p + P * D + P * (4 * NG) + slot * (4 * NG);
+            const uint32_t pair = h * (16 * NG) + 4 * (b * NG / J);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 if constexpr (NG == 1) {
-                    load_words<4>(r + 32 * e, vp[i] + 4 * e);
+                    load_words<4>(r + 32 * e + pair, vp[i] + 4 * e);
                 } else {
 #pragma unroll
                     for (int t = 0; t < 4; ++t)
-                        vp[i][4 * e + t] = *reinterpret_cast<const uint32_t *>(r + (8 * e + t) * (4 * NG));
+                        vp[i][4 * e + t] = *reinterpret_cast<const uint32_t *>(r + (8 * e + t) * (4 * NG) + pair);
                 }
             }
         }
     }
 
-    // keys [octet][token], values [u][h][b][channel of 32], key pairs [g][token]
+    // Key word i into ks[octet of channels][token].
     template <typename T>
-    __device__ __forceinline__ void unpack(const KvAttend &a, int tok, int len, uint4 *ks, uint4 *vs, float2 *pairs,
-                                           int *lost) const {
-        {
-            const int token = threadIdx.x % TT, c = threadIdx.x / TT;
-#pragma unroll
-            for (int i = 0; i < KW; ++i) {
-                const int w = c * KW + i, octet = 4 * (w % J) + w / J;
-                ks[octet * TT + token] = make_uint4(KvType<T>::pair(k[i], 0), KvType<T>::pair(k[i], 1),
-                                                    KvType<T>::pair(k[i], 2), KvType<T>::pair(k[i], 3));
-            }
-            if (c < NG) pairs[c * TT + token] = KvType<T>::key_pair(kp, a.scale_log2);
-            if (c == 0 && (token & 15) == 0) lost[token >> 4] = !k_ok;
-        }
+    __device__ __forceinline__ void unpack_key(int i, uint4 *ks) const {
+        const int w = chunk() * KW + i, octet = 4 * (w % J) + w / J;
+        ks[octet * TT + token()] = make_uint4(KvType<T>::pair(k[i], 0), KvType<T>::pair(k[i], 1),
+                                              KvType<T>::pair(k[i], 2), KvType<T>::pair(k[i], 3));
+    }
+    // Into pairs[group][token] and lost[16 tokens].
+    template <typename T>
+    __device__ __forceinline__ void unpack_pair(const KvAttend &a, float2 *pairs, int *lost) const {
+        pairs[pair_to] = KvType<T>::key_pair(kp, a.scale_log2);
+        lost[lost_to] = !k_ok;
+    }
+    // A value that does not exist is worth zero (0 * NaN would not vanish).
+    __device__ __forceinline__ void clear_values(int tok, int len) {
 #pragma unroll
         for (int i = 0; i < VI; ++i) {
             int m, b, h, u;
             piece(i, m, b, h, u);
-            uint32_t lo[4], hi[4];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                uint32_t q[4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t)   // a token that does not exist is worth zero
-                    q[t] = v_ok[i] && tok + 16 * u + 8 * e + 4 * h + t < len ? vp[i][4 * e + t] : 0u;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const half2v s = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(q[t + 2], q[t], 0x05040100u));
-                    const half2v l = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(q[t + 2], q[t], 0x07060302u));
-                    half2v cl, ch;
-                    value_codes(v[i][e] >> (8 * t), cl, ch);
-                    lo[2 * e + t] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(cl, s, l));
-                    hi[2 * e + t] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(ch, s, l));
-                }
-            }
-            uint4 *dst = vs + ((u * 2 + h) * J + b) * 32 + m;
-            dst[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            dst[16] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            for (int e = 0; e < 8; ++e)
+                if (!v_ok[i] || tok + 16 * u + 8 * (e >> 2) + 4 * h + (e & 3) >= len) vp[i][e] = 0u;
         }
+    }
+    __device__ __forceinline__ bool values_missing(int tok, int len) const {
+        bool bad = tok + TT > len;
+#pragma unroll
+        for (int i = 0; i < VI; ++i) bad |= !v_ok[i];
+        return bad;   // (uniform in the wave)
+    }
+    // Part 0..3 of value piece i: tokens (0, 2) or (1, 3) of one 4-token block; after
+    // the last, into vs[16 tokens][h][b][channel of 32].
+    __device__ __forceinline__ void unpack_value(int i, int part, uint4 *vs) {
+        const int e = part >> 1, t = part & 1;
+        const uint32_t *q = vp[i] + 4 * e;
+        const half2v s = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(q[t + 2], q[t], 0x05040100u));
+        const half2v l = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(q[t + 2], q[t], 0x07060302u));
+        half2v cl, ch;
+        value_codes(v[i][e] >> (8 * t), cl, ch);
+        lo[part] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(cl, s, l));
+        hi[part] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(ch, s, l));
+        if (part < 3) return;
+        int m, b, h, u;
+        piece(i, m, b, h, u);
+        uint4 *dst = vs + ((u * 2 + h) * J + b) * 32 + m;
+        dst[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        dst[16] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     }
 };
 
 template <typename T, int D, int NG>
 __global__ __launch_bounds__(2 * kv_wide_cols(D)) void kv_wide_kernel(KvAttend a) {
     constexpr int kCols = kv_wide_cols(D), kThreads = 2 * kCols, J = D / 32, TT = 8192 / D, S = D / 16;
+    constexpr int SUB = TT / 32;   // 32-token result tiles
     __shared__ uint4 ks[2][1024], vs[2][1024];
-    __shared__ float2 pairs[2][NG * TT];
-    __shared__ int lost[2][TT / 16];
+    __shared__ float2 pairs[3][NG * TT + 1];
+    __shared__ int lost[3][TT / 16 + 1];
     const int tid = threadIdx.x, lane = tid & 63, n32 = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int head = blockIdx.x % a.c.heads;
@@ -787,7 +826,6 @@ __global__ __launch_bounds__(2 * kv_wide_cols(D)) void kv_wide_kernel(KvAttend a
         t0 = lo + split * part < hi ? lo + split * part : hi;
         t1 = t0 + part < hi ? t0 + part : hi;
     }
-    const int wave_lo = a.window ? p0 + wi0 - a.window + 1 : 0, wave_hi = a.causal ? p0 + wi1 + 1 : len;
     // where nothing is hidden from the wave's columns
     const int minpos = a.causal ? p0 + wi0 : len - 1, maxlow = a.window ? p0 + wi1 - a.window + 1 : 0;
 
@@ -822,88 +860,204 @@ __global__ __launch_bounds__(2 * kv_wide_cols(D)) void kv_wide_kernel(KvAttend a
             for (int r = 0; r < 16; ++r) o[j][r] = 0.0f;
     }
 
-    KvWideLoad<D, NG, kThreads> in;
-    if (t0 < t1) {
-        in.pages(a, table, t0 * TT, len);
-        in.load(a, head, t0 * TT);
-        in.template unpack<T>(a, t0 * TT, len, ks[0], vs[0], pairs[0], lost[0]);
-        if (t0 + 1 < t1) {
-            in.pages(a, table, (t0 + 1) * TT, len);
-            in.load(a, head, (t0 + 1) * TT);
+    // Both products are 16 MFMAs a tile, each in a slot of its own: the operand of
+    // the MFMA four slots on is read from LDS, one MFMA issued, and a share of
+    // the tile's vector work done under it.  (The slots are fenced: left to
+    // itself the scheduler puts each read right before its MFMA and the vector work behind all.)
+    constexpr int kSlots = 16, kAhead = 4;
+    static_assert(SUB * S == kSlots && 2 * SUB * J == kSlots, "");
+    // The next tile's scores: one group's sums of (base + code) * q (NG = 1), or the
+    // scores themselves, into which the groups' sums are folded as they come.
+    floatx16 next[SUB], part[2];
+    uint4 f[kAhead];
+    // operand of slot i of the first product: with one group the result tiles alternate,
+    // else the groups of one result tile follow each other
+    auto key_slot = [&](int i, int &e, int &k) {
+        if (NG == 1)
+            e = i % SUB, k = i / SUB;
+        else
+            e = i / S, k = i % S;
+    };
+    auto read_key = [&](int t, int i) {
+        int e, k;
+        key_slot(i, e, k);
+        return ks[t & 1][(2 * k + h) * TT + 32 * e + n32];
+    };
+    auto fold = [&](int t3, int e, int g) {   // group g's sums into the scores
+        const float2 *kp = &pairs[t3][g * TT + 32 * e + 4 * h];
+        const floatx16 &y = part[(e * NG + g) & 1];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const float2 z = kp[8 * (r >> 2) + (r & 3)];
+            next[e][r] = fmaf(z.x, y[r], g == 0 ? z.y * qs[g] : fmaf(z.y, qs[g], next[e][r]));
         }
-        if (t0 + 2 < t1) in.pages(a, table, (t0 + 2) * TT, len);
+    };
+    auto score_slot = [&](int t, int t3, int i) {
+        int e, k;
+        key_slot(i, e, k);
+        const uint4 w = f[i % kAhead];
+        if (i + kAhead < kSlots) f[i % kAhead] = read_key(t, i + kAhead);
+        if constexpr (NG == 1) {
+            next[e] = KvWideType<T>::mfma(w, q[k], k == 0 ? floatx16{} : next[e]);
+        } else {
+            constexpr int M = S / NG;   // MFMAs of a group
+            floatx16 &y = part[(i / M) & 1];
+            y = KvWideType<T>::mfma(w, q[k], k % M == 0 ? floatx16{} : y);
+            if (i >= M && i % M == M - 1) fold(t3, (i / M - 1) / NG, (i / M - 1) % NG);   // the group before
+            if (i == kSlots - 1) fold(t3, e, NG - 1);
+        }
+    };
+    // The scores less the reference, two result rows (tokens) at a time, and their maximum.
+    floatx16 x[SUB];
+    float top = -INFINITY, ref = 0.0f;   // ref: m, or 0 before there is one
+    auto factors = [&](int t3, int i) {   // of two tokens
+        const float2 *kp = &pairs[t3][32 * (i / 8) + 4 * h + 8 * (i % 8 >> 1) + 2 * (i & 1)];
+        return floatx4{kp[0].x, kp[0].y, kp[1].x, kp[1].y};
+    };
+    auto relative = [&](floatx4 y, int i) {
+        const int e = i / 8, r = i % 8 * 2;
+        if constexpr (NG == 1) {
+            x[e][r] = fmaf(y[0], next[e][r], fmaf(y[1], qs[0], -ref));
+            x[e][r + 1] = fmaf(y[2], next[e][r + 1], fmaf(y[3], qs[0], -ref));
+        } else {
+            x[e][r] = next[e][r] - ref;
+            x[e][r + 1] = next[e][r + 1] - ref;
+        }
+        top = i == 0 ? fmaxf(x[e][r], x[e][r + 1]) : fmaxf(top, fmaxf(x[e][r], x[e][r + 1]));
+    };
+    auto start_scores = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) f[i] = read_key(t, i);
+    };
+
+    KvWideLoad<D, NG, kThreads> in;
+    in.init();
+    int t3 = t0 % 3;   // t % 3
+    if (t0 < t1) {
+        // keys run one tile ahead of values: K(t0), K(t0 + 1), V(t0) into LDS, K(t0 + 2), V(t0 + 1) on their way
+        auto keys = [&](int t) {
+#pragma unroll
+            for (int i = 0; i < in.KW; ++i) in.template unpack_key<T>(i, ks[t & 1]);
+            in.template unpack_pair<T>(a, pairs[t % 3], lost[t % 3]);
+        };
+        in.key_page(a, table, t0 * TT, len);
+        in.value_pages(a, table, t0 * TT, len);
+        in.load_keys(a, head, t0 * TT, len);
+        in.load_values(a, head, t0 * TT, len);
+        in.key_page(a, table, (t0 + 1) * TT, len);
+        in.value_pages(a, table, (t0 + 1) * TT, len);
+        keys(t0);
+        in.load_keys(a, head, (t0 + 1) * TT, len);
+        if (in.values_missing(t0 * TT, len)) in.clear_values(t0 * TT, len);
+#pragma unroll
+        for (int i = 0; i < 4 * in.VI; ++i) in.unpack_value(i / 4, i % 4, vs[t0 & 1]);
+        in.load_values(a, head, (t0 + 1) * TT, len);
+        in.key_page(a, table, (t0 + 2) * TT, len);
+        keys(t0 + 1);
+        in.load_keys(a, head, (t0 + 2) * TT, len);
+        in.key_page(a, table, (t0 + 3) * TT, len);
+        in.value_pages(a, table, (t0 + 2) * TT, len);
+        __syncthreads();
+        start_scores(t0);
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) score_slot(t0, t3, i);
+#pragma unroll
+        for (int i = 0; i < 8 * SUB; ++i) relative(NG == 1 ? factors(t3, i) : floatx4{}, i);
     }
     for (int t = t0; t < t1; ++t) {
-        const int buf = (t - t0) & 1;
-        __syncthreads();   // this tile is in LDS, and the other buffer has been read
+        const int tok = t * TT, buf = t & 1;
+        const int n3 = t3 == 2 ? 0 : t3 + 1, w3 = t3 == 0 ? 2 : t3 - 1;   // (t + 1) % 3, (t + 2) % 3
+        // K(t + 1) and V(t) are in LDS; K(t) and V(t - 1) have been read
+        __syncthreads();
+        if (in.values_missing(tok + TT, len)) in.clear_values(tok + TT, len);
+        bool gone[2 * SUB], some_gone = false;
 #pragma unroll
-        for (int st = 0; st < TT / 32; ++st) {
-            const int tok = t * TT + 32 * st;
-            if (tok >= wave_hi || tok + 31 < wave_lo) continue;   // (uniform in the wave)
-            const bool gone0 = __builtin_amdgcn_readfirstlane(lost[buf][2 * st]) != 0;
-            const bool gone1 = __builtin_amdgcn_readfirstlane(lost[buf][2 * st + 1]) != 0;
-            float ref = m == -INFINITY ? 0.0f : m;
-            floatx16 x;
+        for (int e = 0; e < 2 * SUB; ++e) {
+            gone[e] = __builtin_amdgcn_readfirstlane(lost[t3][e]) != 0;
+            some_gone |= gone[e];
+        }
+        if (tok + TT - 1 > minpos || tok < maxlow || some_gone) {
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                floatx16 acc = {};
-#pragma unroll
-                for (int s = g * (S / NG); s < (g + 1) * (S / NG); ++s)
-                    acc = KvWideType<T>::mfma(ks[buf][(2 * s + h) * TT + 32 * st + n32], q[s], acc);
-                const floatx4 *kp = reinterpret_cast<const floatx4 *>(&pairs[buf][g * TT + 32 * st + 4 * h]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int r = 0; r < 4; r += 2) {
-                        const floatx4 y = kp[4 * e + r / 2];   // (step, lo) of two tokens
-                        x[4 * e + r] = fmaf(y[0], acc[4 * e + r], fmaf(y[1], qs[g], g == 0 ? -ref : x[4 * e + r]));
-                        x[4 * e + r + 1] =
-                            fmaf(y[2], acc[4 * e + r + 1], fmaf(y[3], qs[g], g == 0 ? -ref : x[4 * e + r + 1]));
-                    }
-            }
-            if (tok + 31 > minpos || tok < maxlow || gone0 || gone1) {
+            for (int e = 0; e < SUB; ++e)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const int p = tok + 8 * (r >> 2) + 4 * h + (r & 3);
-                    if (p > pos || p < low || (r < 8 ? gone0 : gone1)) x[r] = -INFINITY;
+                    const int p = tok + 32 * e + 8 * (r >> 2) + 4 * h + (r & 3);
+                    if (p > pos || p < low || gone[2 * e + (r >> 3)]) x[e][r] = -INFINITY;
                 }
-            }
-            float top = x[0];
+            top = x[0][0];
 #pragma unroll
-            for (int r = 1; r < 16; ++r) top = fmaxf(top, x[r]);
-            if (__any(top > (m == -INFINITY ? -INFINITY : kLagLog2))) {
-                float now = fmaxf(m, top + ref);
-                now = fmaxf(now, __shfl_xor(now, 32));
-                const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - now);
-                m = now;
-                const float back = (m == -INFINITY ? 0.0f : m) - ref;
-                l *= f;
+            for (int e = 0; e < SUB; ++e)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) x[r] -= back;
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) o[j][r] *= f;
-            }
-            half8 p[2];
-            constexpr int kOrder[4] = {0, 2, 1, 3};   // of the value bytes
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const float e = __builtin_amdgcn_exp2f(x[(r & ~3) + kOrder[r & 3]]);
-                l += e;
-                p[r >> 3][r & 7] = static_cast<_Float16>(e);
-            }
-#pragma unroll
-            for (int v = 0; v < 2; ++v)
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-                    o[j] = KvWideType<_Float16>::mfma(vs[buf][(((2 * st + v) * 2 + h) * J + j) * 32 + n32], p[v], o[j]);
+                for (int r = 0; r < 16; ++r) top = fmaxf(top, x[e][r]);
         }
-        if (t + 1 < t1) {
-            in.template unpack<T>(a, (t + 1) * TT, len, ks[buf ^ 1], vs[buf ^ 1], pairs[buf ^ 1], lost[buf ^ 1]);
-            if (t + 2 < t1) in.load(a, head, (t + 2) * TT);
-            if (t + 3 < t1) in.pages(a, table, (t + 3) * TT, len);
+        if (__any(top > (m == -INFINITY ? -INFINITY : kLagLog2))) {
+            float now = fmaxf(m, top + ref);
+            now = fmaxf(now, __shfl_xor(now, 32));
+            const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - now);
+            m = now;
+            const float back = (m == -INFINITY ? 0.0f : m) - ref;
+            ref += back;
+            l *= f;
+#pragma unroll
+            for (int e = 0; e < SUB; ++e)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) x[e][r] -= back;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[j][r] *= f;
         }
+        // the first product of the next tile (of stale keys after the last one), under it P of this one
+        half8 p[2 * SUB];
+        constexpr int kOrder[4] = {0, 2, 1, 3};   // of the value bytes
+        start_scores(t + 1);
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+            __builtin_amdgcn_sched_barrier(0);
+            score_slot(t + 1, n3, i);
+#pragma unroll
+            for (int z = i * SUB; z < (i + 1) * SUB; ++z) {
+                const int e = z / 16, r = z % 16;
+                const float y = __builtin_amdgcn_exp2f(x[e][(r & ~3) + kOrder[r & 3]]);
+                l += y;
+                p[z / 8][z % 8] = static_cast<_Float16>(y);
+            }
+        }
+        // the second product, under it the unpacking of K(t + 2) and V(t + 1), the loads
+        // behind them, and what is left to do for the next tile's scores
+        floatx4 y0 = {}, y1 = {};
+        if (NG == 1) y0 = factors(n3, 0), y1 = factors(n3, 1);
+        auto read_value = [&](int i) { return vs[buf][((i / J * 2 + h) * J + i % J) * 32 + n32]; };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) f[i] = read_value(i);
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+            __builtin_amdgcn_sched_barrier(0);
+            const uint4 w = f[i % kAhead];
+            if (i + kAhead < kSlots) f[i % kAhead] = read_value(i + kAhead);
+            o[i % J] = KvWideType<_Float16>::mfma(w, p[i / J], o[i % J]);
+#pragma unroll
+            for (int z = i * SUB / 2; z < (i + 1) * SUB / 2; ++z) {   // (factors read two ahead)
+                const floatx4 y = z & 1 ? y1 : y0;
+                if (NG == 1 && z + 2 < 8 * SUB) (z & 1 ? y1 : y0) = factors(n3, z + 2);
+                relative(y, z);
+            }
+            if (i < in.KW) in.template unpack_key<T>(i, ks[buf]);
+            if (i == in.KW) {
+                in.template unpack_pair<T>(a, pairs[w3], lost[w3]);
+                in.load_keys(a, head, tok + 3 * TT, len);
+            }
+            constexpr int kFirst = in.KW + 1, kEach = in.VI == 1 ? 2 : 1;   // value parts from slot kFirst, every kEach
+            if (i >= kFirst && (i - kFirst) % kEach == 0 && (i - kFirst) / kEach < 4 * in.VI)
+                in.unpack_value((i - kFirst) / kEach / 4, (i - kFirst) / kEach % 4, vs[buf ^ 1]);
+            if (i == kFirst + kEach * (4 * in.VI - 1) + 1) in.load_values(a, head, tok + 2 * TT, len);
+            if (i == kSlots - 1) {
+                in.key_page(a, table, tok + 4 * TT, len);
+                in.value_pages(a, table, tok + 3 * TT, len);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        t3 = n3;
     }
     l += __shfl_xor(l, 32);
     if (!real) return;
