@@ -127,8 +127,8 @@ struct Plan {
     size_t items, part_ml, part, wide_ml, wide_part, total;
 };
 
-// 256 CUs: workers of the split path (waves, 2 a SIMD), workgroups of the wide path.
-constexpr int kSplitWorkers = 2048, kWideGroups = 512;
+// 256 CUs of 4 SIMDs; workgroups that fill them on the wide path.
+constexpr int kSimds = 1024, kWideGroups = 512;
 
 awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, int64_t max_rows, Plan *p) {
     if (q_heads < 1 || q_heads > 65535 || q_heads % c.heads != 0)
@@ -150,7 +150,8 @@ awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, i
     p->part_cols = static_cast<int>(need < p->split_cols && !p->wide ? need : p->split_cols);
     const int64_t line = s.B * static_cast<int64_t>(c.heads) * (tiles + awq::kKvItemCost);
     const int64_t useful = (line + awq::kKvMinShare - 1) / awq::kKvMinShare;
-    p->workers = static_cast<int>(useful < kSplitWorkers ? useful : kSplitWorkers);
+    const int64_t fill = kSimds * awq::kv_split_waves(c.dim, p->tiles_col);
+    p->workers = static_cast<int>(useful < fill ? useful : fill);
     p->merge = p->split && tiles > 2 * awq::kKvSnap + 1;   // shorter items are never cut
     const int64_t wide = awq::kv_wide_cols(c.dim);
     p->units = static_cast<int>(s.row_start ? s.T * per / wide + s.B : s.B * ((s.even * per + wide - 1) / wide));

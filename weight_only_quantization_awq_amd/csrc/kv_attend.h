@@ -353,7 +353,7 @@ struct KvWave {
     // next kAhead tiles, and the page numbers of the one after, are in flight
     // while a tile is computed.  minpos / maxlow: the first last-visible and the
     // last first-visible position of the columns.
-    static constexpr int kAhead = NT * D <= 128 ? 2 : 1;
+    static constexpr int kAhead = 1;
     __device__ __forceinline__ void run(const KvAttend &a, const int32_t *table, int head, int t0, int t1, int len,
                                         int minpos, int maxlow, int lane, KvPairs<NG> *lds) {
         if (t0 >= t1) return;
@@ -431,7 +431,7 @@ struct KvWave {
 // Split path: sequences with at most 16*NT columns per key head (decoding).
 //
 // The items (sequence, head) form one line, each kKvItemCost + its tiles long,
-// which the workers (one wave each, 2 to a SIMD) share equally: ragged
+// which the workers (one wave each, as many as the GPU holds) share equally: ragged
 // lengths and few long sequences load the GPU evenly, and nothing but the
 // lengths on the device decides it.  A worker that holds a whole item writes
 // its output; the pieces of an item that a boundary cuts go to the workspace
@@ -508,7 +508,7 @@ __device__ __forceinline__ int kv_cut(const KvItem &it, int x) {
 }
 
 template <typename T, int D, int NG, int NT>
-__global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(NT * D <= 256 ? 2 : 1))) void kv_split_kernel(
+__global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(kv_split_waves(D, NT)))) void kv_split_kernel(
     KvAttend a) {
     const int lane = threadIdx.x;
     __shared__ KvPairs<NG> pairs;

@@ -105,9 +105,14 @@ constexpr int kKvSplitCols = 64;   // most columns of the split path (4 column t
 // the output alone takes 128 registers.
 constexpr int kv_wide_cols(int dim) { return dim > 128 ? 128 : 256; }
 constexpr int kKvTile = 32;        // tokens of one step
-constexpr int kKvItemCost = 3;     // what an item costs besides its tiles, in tiles
-constexpr int kKvMinShare = 8;     // least share of a worker, in tiles
-constexpr int kKvSnap = 2;         // tiles: pieces this short are not cut off (2 * snap < least share)
+constexpr int kKvItemCost = 2;     // what an item costs besides its tiles, in tiles
+constexpr int kKvMinShare = 4;     // least share of a worker, in tiles
+constexpr int kKvSnap = 1;         // tiles: pieces this short are not cut off (2 * snap < least share)
+// Waves of the split path that a SIMD holds at once, by the registers of a wave's
+// output (dim x 16*NT columns) and what comes with it.
+constexpr int kv_split_waves(int dim, int nt) {
+    return nt * dim <= 64 ? 4 : nt * dim <= 128 ? 3 : nt * dim <= 256 && dim < 256 ? 2 : 1;
+}
 
 hipError_t launch_kv_append(const KvCache &c, const KvBatch &s, const void *K, const void *V, int type,
                             int64_t k_stride, int64_t v_stride, hipStream_t st);
