@@ -646,21 +646,28 @@ struct KvWideType<_Float16> {
     }
 };
 
-// What a thread unpacks of one tile: 1024/THREADS key words of one token (and
-// one of its pairs), 512/THREADS pieces of 8 tokens x 2 channels of the values.
+// Result tiles of 32 columns a wave holds, and the workgroup's threads and tile of tokens.
+constexpr int kv_wide_ct(int dim) { return 1; }
+constexpr int kv_wide_threads(int dim) { return kv_wide_cols(dim) / kv_wide_ct(dim) * 2; }
+constexpr int kv_wide_tile(int dim) { return 8192 / dim / kv_wide_ct(dim); }
+
+// What a thread unpacks of one tile: KW key words of one token (and one of its
+// pairs), VI pieces of 8 tokens x 2 channels of the values.
 // Everything is loaded whether the token exists or not (from page 0 where it has
 // none), so the loop that calls this has no branches for it.
 template <int D, int NG, int THREADS>
 struct KvWideLoad {
-    static constexpr int J = D / 32, TT = 8192 / D, KW = 1024 / THREADS, VI = 512 / THREADS;
-    uint32_t k[KW], kp, v[VI][2], vp[VI][8];
-    int k_id, v_id[VI];      // page numbers of the next tile, as the table holds them
-    bool k_ok, v_ok[VI];
-    uint32_t lo[4], hi[4];   // a piece being unpacked
+    static constexpr int J = D / 32, TT = kv_wide_tile(D), KW = TT * D / 8 / THREADS, VI = TT * D / 16 / THREADS;
+    uint32_t k[KW], kp, vp, v[VI][2];
+    int k_id, v_id[VI];   // page numbers of the next tile, as the table holds them
+    bool k_ok;
+    uint32_t v_there;        // all ones where this lane's token exists
+    uint4 pair[2];           // of the 8 tokens of a value piece being unpacked
+    uint32_t lo[4], hi[4];
     int pair_from, pair_to, lost_to;
 
-    // Where this lane's key pair comes from and goes, and the wave's mark of missing
-    // keys; lanes and waves that have none write behind the others'.  (Opaque, or they
+    // Where this lane's pairs come from and go, and the wave's mark of missing keys;
+    // lanes and waves that have none write behind the others'.  (Opaque, or they
     // become branches in the loop.)
     __device__ __forceinline__ void init() {
         pair_from = ((threadIdx.x & 15) * NG + (chunk() < NG ? chunk() : 0)) * 4;
@@ -704,11 +711,16 @@ struct KvWideLoad {
         }
     }
 
+    // Keys, and both pairs of this lane's token.
     __device__ __forceinline__ void load_keys(const KvAttend &a, int head, int tok, int len) {
         const int P = 1 << a.c.page_shift, at = tok + 16 * key_block(), slot = at & (P - 1), n = threadIdx.x & 15;
         const unsigned char *p = block(a, head, k_id, at, len, k_ok);
         load_words<KW>(p + slot * (D / 2) + static_cast<uint32_t>(n * (D / 2) + chunk() * (4 * KW)), k);
-        kp = *reinterpret_cast<const uint32_t *>(p + P * D + slot * (4 * NG) + static_cast<uint32_t>(pair_from));
+        const unsigned char *r = p + P * D + slot * (4 * NG);
+        kp = *reinterpret_cast<const uint32_t *>(r + static_cast<uint32_t>(pair_from));
+        vp = *reinterpret_cast<const uint32_t *>(r + P * (4 * NG) + static_cast<uint32_t>(pair_from));
+        // a value that does not exist is worth zero (0 * NaN would not vanish)
+        v_there = at + n < len && k_ok ? ~0u : 0u;
     }
     __device__ __forceinline__ void load_values(const KvAttend &a, int head, int tok, int len) {
         const int P = 1 << a.c.page_shift;
@@ -716,24 +728,12 @@ struct KvWideLoad {
         for (int i = 0; i < VI; ++i) {
             int m, b, h, u;
             piece(i, m, b, h, u);
+            bool ok;
             const int slot = (tok + 16 * u) & (P - 1);
-            const unsigned char *p = block(a, head, v_id[i], tok + 16 * u, len, v_ok[i]);
-            const unsigned char *q = p + P * (D / 2) + slot * (D / 2);
+            const unsigned char *q = block(a, head, v_id[i], tok + 16 * u, len, ok) + P * (D / 2) + slot * (D / 2);
             const uint32_t at = (h * 16 + m) * (D / 8) + 4 * b;
             v[i][0] = *reinterpret_cast<const uint32_t *>(q + at);
             v[i][1] = *reinterpret_cast<const uint32_t *>(q + 4 * D + at);
-            const unsigned char *r = p + P * D + P * (4 * NG) + slot * (4 * NG);
-            const uint32_t pair = h * (16 * NG) + 4 * (b * NG / J);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if constexpr (NG == 1) {
-                    load_words<4>(r + 32 * e + pair, vp[i] + 4 * e);
-                } else {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        vp[i][4 * e + t] = *reinterpret_cast<const uint32_t *>(r + (8 * e + t) * (4 * NG) + pair);
-                }
-            }
         }
     }
 
@@ -744,36 +744,28 @@ struct KvWideLoad {
         ks[octet * TT + token()] = make_uint4(KvType<T>::pair(k[i], 0), KvType<T>::pair(k[i], 1),
                                               KvType<T>::pair(k[i], 2), KvType<T>::pair(k[i], 3));
     }
-    // Into pairs[group][token] and lost[16 tokens].
+    // Into pairs[group][token] (key factors), vpairs[group][token] and lost[16 tokens].
     template <typename T>
-    __device__ __forceinline__ void unpack_pair(const KvAttend &a, float2 *pairs, int *lost) const {
+    __device__ __forceinline__ void unpack_pair(const KvAttend &a, float2 *pairs, uint32_t *vpairs, int *lost) const {
         pairs[pair_to] = KvType<T>::key_pair(kp, a.scale_log2);
+        vpairs[pair_to] = vp & v_there;
         lost[lost_to] = !k_ok;
     }
-    // A value that does not exist is worth zero (0 * NaN would not vanish).
-    __device__ __forceinline__ void clear_values(int tok, int len) {
-#pragma unroll
-        for (int i = 0; i < VI; ++i) {
-            int m, b, h, u;
-            piece(i, m, b, h, u);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (!v_ok[i] || tok + 16 * u + 8 * (e >> 2) + 4 * h + (e & 3) >= len) vp[i][e] = 0u;
-        }
-    }
-    __device__ __forceinline__ bool values_missing(int tok, int len) const {
-        bool bad = tok + TT > len;
-#pragma unroll
-        for (int i = 0; i < VI; ++i) bad |= !v_ok[i];
-        return bad;   // (uniform in the wave)
+    // The pairs of value piece i, out of vpairs.
+    __device__ __forceinline__ void read_pairs(int i, const uint32_t *vpairs) {
+        int m, b, h, u;
+        piece(i, m, b, h, u);
+        const uint4 *p = reinterpret_cast<const uint4 *>(vpairs + b * NG / J * TT + 16 * u + 4 * h);
+        pair[0] = p[0];
+        pair[1] = p[2];
     }
     // Part 0..3 of value piece i: tokens (0, 2) or (1, 3) of one 4-token block; after
     // the last, into vs[16 tokens][h][b][channel of 32].
     __device__ __forceinline__ void unpack_value(int i, int part, uint4 *vs) {
         const int e = part >> 1, t = part & 1;
-        const uint32_t *q = vp[i] + 4 * e;
-        const half2v s = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(q[t + 2], q[t], 0x05040100u));
-        const half2v l = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(q[t + 2], q[t], 0x07060302u));
+        const uint32_t q0 = t ? pair[e].y : pair[e].x, q2 = t ? pair[e].w : pair[e].z;
+        const half2v s = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(q2, q0, 0x05040100u));
+        const half2v l = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(q2, q0, 0x07060302u));
         half2v cl, ch;
         value_codes(v[i][e] >> (8 * t), cl, ch);
         lo[part] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(cl, s, l));
@@ -788,11 +780,12 @@ struct KvWideLoad {
 };
 
 template <typename T, int D, int NG>
-__global__ __launch_bounds__(2 * kv_wide_cols(D)) void kv_wide_kernel(KvAttend a) {
-    constexpr int kCols = kv_wide_cols(D), kThreads = 2 * kCols, J = D / 32, TT = 8192 / D, S = D / 16;
-    constexpr int SUB = TT / 32;   // 32-token result tiles
-    __shared__ uint4 ks[2][1024], vs[2][1024];
+__global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(KvAttend a) {
+    constexpr int kCols = kv_wide_cols(D), kThreads = kv_wide_threads(D), J = D / 32, TT = kv_wide_tile(D), S = D / 16;
+    constexpr int SUB = TT / 32, CT = kv_wide_ct(D);   // result tiles of 32 tokens x 32 columns: SUB x CT a wave
+    __shared__ uint4 ks[2][TT * D / 8], vs[2][TT * D / 8];
     __shared__ float2 pairs[3][NG * TT + 1];
+    __shared__ __align__(16) uint32_t vpairs[2][NG * TT + 4];
     __shared__ int lost[3][TT / 16 + 1];
     const int tid = threadIdx.x, lane = tid & 63, n32 = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -812,11 +805,11 @@ __global__ __launch_bounds__(2 * kv_wide_cols(D)) void kv_wide_kernel(KvAttend a
     const int64_t cols = static_cast<int64_t>(n) * a.per;
     if (cols <= a.split_cols || k < 0 || static_cast<int64_t>(k) * kCols >= cols) return;
     const int len = kv_length(a.s, b, a.c.page_shift), p0 = len - n;
-    const int last_col = static_cast<int>(cols) - 1, col0 = k * kCols + wave * 32;
+    const int last_col = static_cast<int>(cols) - 1, col0 = k * kCols + wave * (32 * CT);
     const int32_t *table = a.s.table + static_cast<int64_t>(b) * a.s.max_pages;
     auto row_of = [&](int c) { return (c < last_col ? c : last_col) / a.per; };
-    // tokens that some column of the workgroup sees, and that some of the wave sees
-    const int i0 = row_of(k * kCols), i1 = row_of(k * kCols + kCols - 1), wi0 = row_of(col0), wi1 = row_of(col0 + 31);
+    // tiles that some column of the workgroup sees
+    const int i0 = row_of(k * kCols), i1 = row_of(k * kCols + kCols - 1);
     int lo = a.window ? p0 + i0 - a.window + 1 : 0, hi = a.causal ? p0 + i1 + 1 : len;
     lo = lo > 0 ? lo / TT : 0;
     hi = hi > 0 ? (hi + TT - 1) / TT : 0;
@@ -827,52 +820,59 @@ __global__ __launch_bounds__(2 * kv_wide_cols(D)) void kv_wide_kernel(KvAttend a
         t1 = t0 + part < hi ? t0 + part : hi;
     }
     // where nothing is hidden from the wave's columns
-    const int minpos = a.causal ? p0 + wi0 : len - 1, maxlow = a.window ? p0 + wi1 - a.window + 1 : 0;
+    const int minpos = a.causal ? p0 + row_of(col0) : len - 1;
+    const int maxlow = a.window ? p0 + row_of(col0 + 32 * CT - 1) - a.window + 1 : 0;
 
-    // this lane's column: its queries, their sums, its visible positions
+    // this lane's columns: their queries, the sums of these, their visible positions
     typedef typename KvType<T>::vec8 vec8;
-    const int col = col0 + n32, row = col / a.per;
-    const bool real = row < n;
-    const int pos = real ? (a.causal ? p0 + row : len - 1) : -1, low = a.window ? p0 + row - a.window + 1 : 0;
-    vec8 q[S];
-    float qs[NG], m = -INFINITY, l = 0.0f;
-    floatx16 o[J];
-    {
+    int pos[CT], low[CT];
+    vec8 q[CT][S];
+    float qs[CT][NG], m[CT], l[CT], top[CT], ref[CT];   // ref: m, or 0 before there is one
+    floatx16 o[CT][J];
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+        const int col = col0 + 32 * c + n32, row = col / a.per;
+        const bool real = row < n;
+        pos[c] = real ? (a.causal ? p0 + row : len - 1) : -1;
+        low[c] = a.window ? p0 + row - a.window + 1 : 0;
         const T *src = static_cast<const T *>(a.Q) + (r0 + (real ? row : 0)) * a.q_stride +
                        static_cast<int64_t>(head * a.per + (col - row * a.per)) * D + 8 * h;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) qs[g] = 0.0f;
+        for (int g = 0; g < NG; ++g) qs[c][g] = 0.0f;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             vec8 x = {};
             if (real) x = *reinterpret_cast<const vec8 *>(src + 16 * s);
-            q[s] = x;
+            if (CT > 1 || D > 128) asm("" : "+a"(x));   // (in the registers that only MFMAs can read: the others fill up)
+            q[c][s] = x;
             float sum = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum += static_cast<float>(x[e]);
-            qs[s * NG / S] += sum;
+            qs[c][s * NG / S] += sum;
         }
 #pragma unroll
-        for (int g = 0; g < NG; ++g) qs[g] += __shfl_xor(qs[g], 32);
+        for (int g = 0; g < NG; ++g) qs[c][g] += __shfl_xor(qs[c][g], 32);
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) o[j][r] = 0.0f;
+            for (int r = 0; r < 16; ++r) o[c][j][r] = 0.0f;
+        m[c] = -INFINITY;
+        l[c] = ref[c] = 0.0f;
     }
 
-    // Both products are 16 MFMAs a tile, each in a slot of its own: the operand of
-    // the MFMA four slots on is read from LDS, one MFMA issued, and a share of
-    // the tile's vector work done under it.  (The slots are fenced: left to
-    // itself the scheduler puts each read right before its MFMA and the vector work behind all.)
-    constexpr int kSlots = 16, kAhead = 4;
-    static_assert(SUB * S == kSlots && 2 * SUB * J == kSlots, "");
+    // Both products are kSlots MFMAs a tile, each in a slot of its own: the operand
+    // of some slots on is read from LDS, one MFMA issued, and a share of the tile's
+    // vector work done under it.  (The slots are fenced: left to itself the
+    // scheduler puts each read right before its MFMA and the vector work behind all.)
+    constexpr int kSlots = SUB * CT * S, kReads = kSlots / CT, kAhead = 4;
+    static_assert(2 * SUB * CT * J == kSlots && kReads >= 2 * kAhead, "");
     // The next tile's scores: one group's sums of (base + code) * q (NG = 1), or the
     // scores themselves, into which the groups' sums are folded as they come.
-    floatx16 next[SUB], part[2];
+    floatx16 next[CT][SUB], part[2][CT];
     uint4 f[kAhead];
-    // operand of slot i of the first product: with one group the result tiles alternate,
-    // else the groups of one result tile follow each other
-    auto key_slot = [&](int i, int &e, int &k) {
+    // operand i of the first product: with one group the result tiles alternate, else
+    // the groups of one result tile follow each other
+    auto key_operand = [&](int i, int &e, int &k) {
         if (NG == 1)
             e = i % SUB, k = i / SUB;
         else
@@ -880,50 +880,74 @@ __global__ __launch_bounds__(2 * kv_wide_cols(D)) void kv_wide_kernel(KvAttend a
     };
     auto read_key = [&](int t, int i) {
         int e, k;
-        key_slot(i, e, k);
+        key_operand(i, e, k);
         return ks[t & 1][(2 * k + h) * TT + 32 * e + n32];
     };
-    auto fold = [&](int t3, int e, int g) {   // group g's sums into the scores
-        const float2 *kp = &pairs[t3][g * TT + 32 * e + 4 * h];
-        const floatx16 &y = part[(e * NG + g) & 1];
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const float2 z = kp[8 * (r >> 2) + (r & 3)];
-            next[e][r] = fmaf(z.x, y[r], g == 0 ? z.y * qs[g] : fmaf(z.y, qs[g], next[e][r]));
-        }
-    };
-    auto score_slot = [&](int t, int t3, int i) {
-        int e, k;
-        key_slot(i, e, k);
-        const uint4 w = f[i % kAhead];
-        if (i + kAhead < kSlots) f[i % kAhead] = read_key(t, i + kAhead);
-        if constexpr (NG == 1) {
-            next[e] = KvWideType<T>::mfma(w, q[k], k == 0 ? floatx16{} : next[e]);
-        } else {
-            constexpr int M = S / NG;   // MFMAs of a group
-            floatx16 &y = part[(i / M) & 1];
-            y = KvWideType<T>::mfma(w, q[k], k % M == 0 ? floatx16{} : y);
-            if (i >= M && i % M == M - 1) fold(t3, (i / M - 1) / NG, (i / M - 1) % NG);   // the group before
-            if (i == kSlots - 1) fold(t3, e, NG - 1);
-        }
-    };
-    // The scores less the reference, two result rows (tokens) at a time, and their maximum.
-    floatx16 x[SUB];
-    float top = -INFINITY, ref = 0.0f;   // ref: m, or 0 before there is one
-    auto factors = [&](int t3, int i) {   // of two tokens
-        const float2 *kp = &pairs[t3][32 * (i / 8) + 4 * h + 8 * (i % 8 >> 1) + 2 * (i & 1)];
+    auto factors = [&](int t3, int g, int i) {   // of tokens 2i, 2i + 1 of a lane's 8 * SUB
+        const float2 *kp = &pairs[t3][g * TT + 32 * (i / 8) + 4 * h + 8 * (i % 8 >> 1) + 2 * (i & 1)];
         return floatx4{kp[0].x, kp[0].y, kp[1].x, kp[1].y};
     };
-    auto relative = [&](floatx4 y, int i) {
+    // One group's sums into the scores, in M parts under the next group's MFMAs; a
+    // part's factors are read two slots earlier.
+    constexpr int M = S / NG, kFold = NG == 1 ? 1 : 8 / M;   // operands of a group; factors of a part
+    floatx4 z[2][kFold];
+    auto read_fold = [&](int t3, int i) {   // for operand i's slot: the group before
+#pragma unroll
+        for (int y = 0; y < kFold; ++y) z[i & 1][y] = factors(t3, (i / M - 1) % NG, 8 * ((i / M - 1) / NG) + i % M * kFold + y);
+    };
+    auto fold = [&](int i) {
+        const int e = (i / M - 1) / NG, g = (i / M - 1) % NG;
+#pragma unroll
+        for (int y = 0; y < kFold; ++y)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                const floatx4 f = z[i & 1][y];
+                const floatx16 &sum = part[(i / M - 1) & 1][c];
+                floatx16 &x = next[c][e];
+                const int r = 2 * (i % M * kFold + y);
+                x[r] = fmaf(f[0], sum[r], g == 0 ? f[1] * qs[c][g] : fmaf(f[1], qs[c][g], x[r]));
+                x[r + 1] = fmaf(f[2], sum[r + 1], g == 0 ? f[3] * qs[c][g] : fmaf(f[3], qs[c][g], x[r + 1]));
+            }
+    };
+    auto score_slot = [&](int t, int t3, int slot) {
+        const int i = slot / CT, c = slot % CT;
+        int e, k;
+        key_operand(i, e, k);
+        const uint4 w = f[i % kAhead];
+        if (c == CT - 1 && i + kAhead < kReads) f[i % kAhead] = read_key(t, i + kAhead);
+        if constexpr (NG == 1) {
+            next[c][e] = KvWideType<T>::mfma(w, q[c][k], k == 0 ? floatx16{} : next[c][e]);
+        } else {
+            floatx16 &y = part[(i / M) & 1][c];
+            y = KvWideType<T>::mfma(w, q[c][k], k % M == 0 ? floatx16{} : y);
+            if (c == CT - 1) {
+                if (i >= M) fold(i);
+                if (i + 2 >= M) read_fold(t3, i + 2);
+            }
+        }
+    };
+    auto end_scores = [&](int t3) {   // the last group
+        if constexpr (NG > 1) {
+#pragma unroll
+            for (int i = kReads; i < kReads + M; ++i) {
+                fold(i);
+                if (i + 2 < kReads + M) read_fold(t3, i + 2);
+            }
+        }
+    };
+    // The scores less the reference, two tokens at a time, and their maximum.
+    floatx16 x[CT][SUB];
+    auto relative = [&](floatx4 y, int i, int c) {
         const int e = i / 8, r = i % 8 * 2;
         if constexpr (NG == 1) {
-            x[e][r] = fmaf(y[0], next[e][r], fmaf(y[1], qs[0], -ref));
-            x[e][r + 1] = fmaf(y[2], next[e][r + 1], fmaf(y[3], qs[0], -ref));
+            x[c][e][r] = fmaf(y[0], next[c][e][r], fmaf(y[1], qs[c][0], -ref[c]));
+            x[c][e][r + 1] = fmaf(y[2], next[c][e][r + 1], fmaf(y[3], qs[c][0], -ref[c]));
         } else {
-            x[e][r] = next[e][r] - ref;
-            x[e][r + 1] = next[e][r + 1] - ref;
+            x[c][e][r] = next[c][e][r] - ref[c];
+            x[c][e][r + 1] = next[c][e][r + 1] - ref[c];
         }
-        top = i == 0 ? fmaxf(x[e][r], x[e][r + 1]) : fmaxf(top, fmaxf(x[e][r], x[e][r + 1]));
+        const float two = fmaxf(x[c][e][r], x[c][e][r + 1]);
+        top[c] = i == 0 ? two : fmaxf(top[c], two);
     };
     auto start_scores = [&](int t) {
 #pragma unroll
@@ -934,11 +958,12 @@ __global__ __launch_bounds__(2 * kv_wide_cols(D)) void kv_wide_kernel(KvAttend a
     in.init();
     int t3 = t0 % 3;   // t % 3
     if (t0 < t1) {
-        // keys run one tile ahead of values: K(t0), K(t0 + 1), V(t0) into LDS, K(t0 + 2), V(t0 + 1) on their way
+        // keys and pairs run one tile ahead of values: K(t0), K(t0 + 1), V(t0) into LDS,
+        // K(t0 + 2), V(t0 + 1) on their way
         auto keys = [&](int t) {
 #pragma unroll
             for (int i = 0; i < in.KW; ++i) in.template unpack_key<T>(i, ks[t & 1]);
-            in.template unpack_pair<T>(a, pairs[t % 3], lost[t % 3]);
+            in.template unpack_pair<T>(a, pairs[t % 3], vpairs[t & 1], lost[t % 3]);
         };
         in.key_page(a, table, t0 * TT, len);
         in.value_pages(a, table, t0 * TT, len);
@@ -948,28 +973,33 @@ __global__ __launch_bounds__(2 * kv_wide_cols(D)) void kv_wide_kernel(KvAttend a
         in.value_pages(a, table, (t0 + 1) * TT, len);
         keys(t0);
         in.load_keys(a, head, (t0 + 1) * TT, len);
-        if (in.values_missing(t0 * TT, len)) in.clear_values(t0 * TT, len);
-#pragma unroll
-        for (int i = 0; i < 4 * in.VI; ++i) in.unpack_value(i / 4, i % 4, vs[t0 & 1]);
-        in.load_values(a, head, (t0 + 1) * TT, len);
         in.key_page(a, table, (t0 + 2) * TT, len);
+        __syncthreads();   // the pairs of V(t0)
+#pragma unroll
+        for (int i = 0; i < 4 * in.VI; ++i) {
+            if (i % 4 == 0) in.read_pairs(i / 4, vpairs[t0 & 1]);
+            in.unpack_value(i / 4, i % 4, vs[t0 & 1]);
+        }
+        in.load_values(a, head, (t0 + 1) * TT, len);
+        in.value_pages(a, table, (t0 + 2) * TT, len);
         keys(t0 + 1);
         in.load_keys(a, head, (t0 + 2) * TT, len);
         in.key_page(a, table, (t0 + 3) * TT, len);
-        in.value_pages(a, table, (t0 + 2) * TT, len);
         __syncthreads();
         start_scores(t0);
 #pragma unroll
         for (int i = 0; i < kSlots; ++i) score_slot(t0, t3, i);
+        end_scores(t3);
 #pragma unroll
-        for (int i = 0; i < 8 * SUB; ++i) relative(NG == 1 ? factors(t3, i) : floatx4{}, i);
+        for (int i = 0; i < 8 * SUB; ++i)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) relative(NG == 1 ? factors(t3, 0, i) : floatx4{}, i, c);
     }
     for (int t = t0; t < t1; ++t) {
         const int tok = t * TT, buf = t & 1;
         const int n3 = t3 == 2 ? 0 : t3 + 1, w3 = t3 == 0 ? 2 : t3 - 1;   // (t + 1) % 3, (t + 2) % 3
         // K(t + 1) and V(t) are in LDS; K(t) and V(t - 1) have been read
         __syncthreads();
-        if (in.values_missing(tok + TT, len)) in.clear_values(tok + TT, len);
         bool gone[2 * SUB], some_gone = false;
 #pragma unroll
         for (int e = 0; e < 2 * SUB; ++e) {
@@ -978,80 +1008,92 @@ __global__ __launch_bounds__(2 * kv_wide_cols(D)) void kv_wide_kernel(KvAttend a
         }
         if (tok + TT - 1 > minpos || tok < maxlow || some_gone) {
 #pragma unroll
-            for (int e = 0; e < SUB; ++e)
+            for (int c = 0; c < CT; ++c) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int p = tok + 32 * e + 8 * (r >> 2) + 4 * h + (r & 3);
-                    if (p > pos || p < low || gone[2 * e + (r >> 3)]) x[e][r] = -INFINITY;
-                }
-            top = x[0][0];
+                for (int e = 0; e < SUB; ++e)
 #pragma unroll
-            for (int e = 0; e < SUB; ++e)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) top = fmaxf(top, x[e][r]);
+                    for (int r = 0; r < 16; ++r) {
+                        const int p = tok + 32 * e + 8 * (r >> 2) + 4 * h + (r & 3);
+                        if (p > pos[c] || p < low[c] || gone[2 * e + (r >> 3)]) x[c][e][r] = -INFINITY;
+                        top[c] = e + r == 0 ? x[c][0][0] : fmaxf(top[c], x[c][e][r]);
+                    }
+            }
         }
-        if (__any(top > (m == -INFINITY ? -INFINITY : kLagLog2))) {
-            float now = fmaxf(m, top + ref);
-            now = fmaxf(now, __shfl_xor(now, 32));
-            const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - now);
-            m = now;
-            const float back = (m == -INFINITY ? 0.0f : m) - ref;
-            ref += back;
-            l *= f;
+        bool above = false;
 #pragma unroll
-            for (int e = 0; e < SUB; ++e)
+        for (int c = 0; c < CT; ++c) above |= top[c] > (m[c] == -INFINITY ? -INFINITY : kLagLog2);
+        if (__any(above)) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) x[e][r] -= back;
+            for (int c = 0; c < CT; ++c) {
+                float now = fmaxf(m[c], top[c] + ref[c]);
+                now = fmaxf(now, __shfl_xor(now, 32));
+                const float g = m[c] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[c] - now);
+                m[c] = now;
+                const float back = (now == -INFINITY ? 0.0f : now) - ref[c];
+                ref[c] += back;
+                l[c] *= g;
 #pragma unroll
-            for (int j = 0; j < J; ++j)
+                for (int e = 0; e < SUB; ++e)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) o[j][r] *= f;
+                    for (int r = 0; r < 16; ++r) x[c][e][r] -= back;
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) o[c][j][r] *= g;
+            }
         }
         // the first product of the next tile (of stale keys after the last one), under it P of this one
-        half8 p[2 * SUB];
+        half8 p[CT][2 * SUB];
         constexpr int kOrder[4] = {0, 2, 1, 3};   // of the value bytes
         start_scores(t + 1);
 #pragma unroll
         for (int i = 0; i < kSlots; ++i) {
             __builtin_amdgcn_sched_barrier(0);
             score_slot(t + 1, n3, i);
+            constexpr int kEach = CT * SUB * 16 / kSlots;
 #pragma unroll
-            for (int z = i * SUB; z < (i + 1) * SUB; ++z) {
-                const int e = z / 16, r = z % 16;
-                const float y = __builtin_amdgcn_exp2f(x[e][(r & ~3) + kOrder[r & 3]]);
-                l += y;
-                p[z / 8][z % 8] = static_cast<_Float16>(y);
+            for (int z = i * kEach; z < (i + 1) * kEach; ++z) {
+                const int c = z / (16 * SUB), e = z / 16 % SUB, r = z % 16;
+                const float y = __builtin_amdgcn_exp2f(x[c][e][(r & ~3) + kOrder[r & 3]]);
+                l[c] += y;
+                p[c][2 * e + (r >> 3)][r & 7] = static_cast<_Float16>(y);
             }
         }
+        end_scores(n3);
         // the second product, under it the unpacking of K(t + 2) and V(t + 1), the loads
         // behind them, and what is left to do for the next tile's scores
-        floatx4 y0 = {}, y1 = {};
-        if (NG == 1) y0 = factors(n3, 0), y1 = factors(n3, 1);
+        floatx4 y[2] = {};
+        if (NG == 1) y[0] = factors(n3, 0, 0), y[1] = factors(n3, 0, 1);
         auto read_value = [&](int i) { return vs[buf][((i / J * 2 + h) * J + i % J) * 32 + n32]; };
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) f[i] = read_value(i);
 #pragma unroll
-        for (int i = 0; i < kSlots; ++i) {
+        for (int slot = 0; slot < kSlots; ++slot) {
             __builtin_amdgcn_sched_barrier(0);
+            const int i = slot / CT, c = slot % CT;
             const uint4 w = f[i % kAhead];
-            if (i + kAhead < kSlots) f[i % kAhead] = read_value(i + kAhead);
-            o[i % J] = KvWideType<_Float16>::mfma(w, p[i / J], o[i % J]);
+            if (c == CT - 1 && i + kAhead < kReads) f[i % kAhead] = read_value(i + kAhead);
+            o[c][i % J] = KvWideType<_Float16>::mfma(w, p[c][i / J], o[c][i % J]);
+            constexpr int kPairs = 8 * SUB * CT;
 #pragma unroll
-            for (int z = i * SUB / 2; z < (i + 1) * SUB / 2; ++z) {   // (factors read two ahead)
-                const floatx4 y = z & 1 ? y1 : y0;
-                if (NG == 1 && z + 2 < 8 * SUB) (z & 1 ? y1 : y0) = factors(n3, z + 2);
-                relative(y, z);
+            for (int z = slot * kPairs / kSlots; z < (slot + 1) * kPairs / kSlots; ++z) {   // (factors read two ahead)
+                const int two = z / CT;
+                relative(y[two & 1], two, z % CT);
+                if (NG == 1 && z % CT == CT - 1 && two + 2 < 8 * SUB) y[two & 1] = factors(n3, 0, two + 2);
             }
-            if (i < in.KW) in.template unpack_key<T>(i, ks[buf]);
-            if (i == in.KW) {
-                in.template unpack_pair<T>(a, pairs[w3], lost[w3]);
+            if (slot < in.KW) in.template unpack_key<T>(slot, ks[buf]);
+            if (slot == in.KW) {
+                in.template unpack_pair<T>(a, pairs[w3], vpairs[buf], lost[w3]);
                 in.load_keys(a, head, tok + 3 * TT, len);
             }
-            constexpr int kFirst = in.KW + 1, kEach = in.VI == 1 ? 2 : 1;   // value parts from slot kFirst, every kEach
-            if (i >= kFirst && (i - kFirst) % kEach == 0 && (i - kFirst) / kEach < 4 * in.VI)
-                in.unpack_value((i - kFirst) / kEach / 4, (i - kFirst) / kEach % 4, vs[buf ^ 1]);
-            if (i == kFirst + kEach * (4 * in.VI - 1) + 1) in.load_values(a, head, tok + 2 * TT, len);
-            if (i == kSlots - 1) {
+            // value parts from slot kFirst, every kEach
+            constexpr int kFirst = in.KW + 1, kEach = (kSlots - kFirst - 3) / (4 * in.VI);
+            if (slot >= kFirst && (slot - kFirst) % kEach == 0 && (slot - kFirst) / kEach < 4 * in.VI)
+                in.unpack_value((slot - kFirst) / kEach / 4, (slot - kFirst) / kEach % 4, vs[buf ^ 1]);
+            if ((slot + 1 - kFirst) % (4 * kEach) == 0 && (slot + 1 - kFirst) / (4 * kEach) < in.VI)
+                in.read_pairs((slot + 1 - kFirst) / (4 * kEach), vpairs[buf ^ 1]);
+            if (slot == kFirst + kEach * (4 * in.VI - 1) + 1) in.load_values(a, head, tok + 2 * TT, len);
+            if (slot == kSlots - 1) {
                 in.key_page(a, table, tok + 4 * TT, len);
                 in.value_pages(a, table, tok + 3 * TT, len);
             }
@@ -1059,32 +1101,37 @@ __global__ __launch_bounds__(2 * kv_wide_cols(D)) void kv_wide_kernel(KvAttend a
         __builtin_amdgcn_sched_barrier(0);
         t3 = n3;
     }
-    l += __shfl_xor(l, 32);
-    if (!real) return;
-    const int qh = head * a.per + col - row * a.per;
-    if (a.splits > 1) {
-        const int64_t at = (static_cast<int64_t>(split) * a.c.heads + head) * a.s.T * a.per +
-                           static_cast<int64_t>(r0) * a.per + col;
-        if (h == 0) *reinterpret_cast<float2 *>(a.wide_ml + 2 * at) = make_float2(m, l);
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+        l[c] += __shfl_xor(l[c], 32);
+        const int col = col0 + 32 * c + n32, row = col / a.per;
+        if (row >= n) continue;
+        const int qh = head * a.per + col - row * a.per;
+        if (a.splits > 1) {
+            const int64_t at = (static_cast<int64_t>(split) * a.c.heads + head) * a.s.T * a.per +
+                               static_cast<int64_t>(r0) * a.per + col;
+            if (h == 0) *reinterpret_cast<float2 *>(a.wide_ml + 2 * at) = make_float2(m[c], l[c]);
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<floatx4 *>(a.wide_part + at * D + 32 * j + 8 * e + 4 * h) =
+                        floatx4{o[c][j][4 * e], o[c][j][4 * e + 1], o[c][j][4 * e + 2], o[c][j][4 * e + 3]};
+            continue;
+        }
+        const float inv = l[c] == 0.0f ? 0.0f : 1.0f / l[c];
+        T *dst = static_cast<T *>(a.O) + (r0 + row) * a.o_stride + static_cast<int64_t>(qh) * D + 4 * h;
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                *reinterpret_cast<floatx4 *>(a.wide_part + at * D + 32 * j + 8 * e + 4 * h) =
-                    floatx4{o[j][4 * e], o[j][4 * e + 1], o[j][4 * e + 2], o[j][4 * e + 3]};
-        return;
+                *reinterpret_cast<uint2 *>(dst + 32 * j + 8 * e) =
+                    pack4<T>(o[c][j][4 * e] * inv, o[c][j][4 * e + 1] * inv, o[c][j][4 * e + 2] * inv,
+                             o[c][j][4 * e + 3] * inv);
+        if (a.lse && h == 0)
+            a.lse[static_cast<int64_t>(r0 + row) * a.q_heads + qh] =
+                l[c] == 0.0f ? -INFINITY : (m[c] + __builtin_amdgcn_logf(l[c])) * kLn2;
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    T *dst = static_cast<T *>(a.O) + (r0 + row) * a.o_stride + static_cast<int64_t>(qh) * D + 4 * h;
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint2 *>(dst + 32 * j + 8 * e) = pack4<T>(
-                o[j][4 * e] * inv, o[j][4 * e + 1] * inv, o[j][4 * e + 2] * inv, o[j][4 * e + 3] * inv);
-    if (a.lse && h == 0)
-        a.lse[static_cast<int64_t>(r0 + row) * a.q_heads + qh] =
-            l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // Joins the splits of one row and query head (D/2 threads of a block each).
@@ -1148,7 +1195,7 @@ hipError_t kv_attend_typed(const KvAttend &a, bool run_split, bool run_wide, boo
             hipLaunchKernelGGL((kv_merge_kernel<T, D>), dim3(a.s.B * a.c.heads, a.part_cols), dim3(256), 0, st, a);
     }
     if (run_wide) {
-        hipLaunchKernelGGL((kv_wide_kernel<T, D, NG>), dim3(a.units * a.c.heads, a.splits), dim3(2 * kv_wide_cols(D)), 0,
+        hipLaunchKernelGGL((kv_wide_kernel<T, D, NG>), dim3(a.units * a.c.heads, a.splits), dim3(kv_wide_threads(D)), 0,
                            st, a);
         if (a.splits > 1) {
             const int64_t per = 256 / (D / 2), n = (static_cast<int64_t>(a.s.T) * a.q_heads + per - 1) / per;
