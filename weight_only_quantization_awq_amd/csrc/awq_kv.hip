@@ -122,13 +122,14 @@ awq_status copy_checks(const awq_kv_cache *cache, const awq_kv_batch *batch, con
 
 // The launches of one attention call and its workspace (byte offsets).
 struct Plan {
-    bool split, wide, merge;
-    int tiles_col, split_cols, part_cols, workers, splits, units;
-    size_t items, part_ml, part, wide_ml, wide_part, total;
+    bool split, wide, merge, line, wide_merge;
+    int tiles_col, split_cols, part_cols, workers, units, wide_workers;
+    size_t items, part_ml, part, wide_items, wide_ml, wide_part, total;
 };
 
-// 256 CUs of 4 SIMDs; workgroups that fill them on the wide path.
-constexpr int kSimds = 1024, kWideGroups = 512;
+// 256 CUs of 4 SIMDs.  A workgroup of the wide path fills a CU; from 2 of them to a CU
+// on, the longest first load the GPU evenly without a line.
+constexpr int kSimds = 1024, kCus = 256;
 
 awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, int64_t max_rows, Plan *p) {
     if (q_heads < 1 || q_heads > 65535 || q_heads % c.heads != 0)
@@ -156,13 +157,12 @@ awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, i
     const int64_t wide = awq::kv_wide_cols(c.dim);
     p->units = static_cast<int>(s.row_start ? s.T * per / wide + s.B : s.B * ((s.even * per + wide - 1) / wide));
     const int64_t groups = static_cast<int64_t>(p->units) * c.heads;
-    p->splits = 1;
-    if (p->wide && groups < kWideGroups) {
-        int64_t n = (kWideGroups + groups - 1) / groups;
-        if (n > 16) n = 16;
-        if (n > tiles / 8) n = tiles / 8;
-        p->splits = static_cast<int>(n < 1 ? 1 : n);
-    }
+    const int64_t wide_tiles = (static_cast<int64_t>(s.max_pages) * (1 << c.page_shift) - 1) / awq::kv_wide_tile(c.dim) + 1;
+    p->line = p->wide && groups < 2 * kCus && p->units <= awq::kKvLineUnits;
+    const int64_t wide_line = groups * (wide_tiles + awq::kKvWideCost);
+    const int64_t wide_useful = (wide_line + awq::kKvWideMinShare - 1) / awq::kKvWideMinShare;
+    p->wide_workers = static_cast<int>(wide_useful < kCus ? wide_useful : kCus);
+    p->wide_merge = p->line && wide_tiles > 2 * awq::kKvWideSnap + 1;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -175,8 +175,9 @@ awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, i
         p->part_ml = take(n * 8);
         p->part = take(n * c.dim * 4);
     }
-    if (p->splits > 1) {
-        const size_t n = static_cast<size_t>(p->splits) * s.T * q_heads;
+    if (p->wide_merge) {
+        const size_t n = static_cast<size_t>(p->wide_workers) * 2 * wide;
+        p->wide_items = take(static_cast<size_t>(groups) * 8);
         p->wide_ml = take(n * 8);
         p->wide_part = take(n * c.dim * 4);
     }
@@ -261,15 +262,17 @@ awq_status awq_kv_attention(const awq_kv_cache *cache, const awq_kv_batch *batch
     a.tiles_col = p.tiles_col;
     a.part_cols = p.part_cols;
     a.workers = p.workers;
-    a.splits = p.splits;
     a.units = p.units;
+    a.line = p.line;
+    a.wide_workers = p.wide_workers;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     if (p.merge) {
         a.items = reinterpret_cast<int2 *>(ws + p.items);
         a.part_ml = reinterpret_cast<float *>(ws + p.part_ml);
         a.part = reinterpret_cast<float *>(ws + p.part);
     }
-    if (p.splits > 1) {
+    if (p.wide_merge) {
+        a.wide_items = reinterpret_cast<int2 *>(ws + p.wide_items);
         a.wide_ml = reinterpret_cast<float *>(ws + p.wide_ml);
         a.wide_part = reinterpret_cast<float *>(ws + p.wide_part);
     }

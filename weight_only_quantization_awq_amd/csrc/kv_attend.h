@@ -622,9 +622,11 @@ __global__ __launch_bounds__(256) void kv_merge_kernel(KvAttend a) {
 // ---------------------------------------------------------------------------
 // Wide path: sequences with more columns (prompts, chunks).
 //
-// A workgroup takes kv_wide_cols(D) columns (rows x query heads of one key
-// head), 32 a wave, over one of `splits` equal parts of the tokens they see, in
-// tiles of 8192/D tokens.  Here the matrix cores and the softmax bound it, so a
+// A workgroup takes a unit, kv_wide_cols(D) columns of a sequence (rows x query
+// heads of one key head, 32 a wave), over the tokens they see, in tiles of
+// kv_wide_tile(D).  Where units are few, they form a line that one workgroup a CU
+// shares equally, as on the split path (a unit costs kKvWideCost besides its
+// tiles); else each has a workgroup of its own, the longest first.  Here the matrix cores and the softmax bound it, so a
 // tile is unpacked once for all waves, into LDS, as 16-byte operands of
 // 32x32x16 MFMAs in reading order (every LDS access is contiguous); the
 // other half of the double buffer is filled between a tile's products and the
@@ -646,10 +648,44 @@ struct KvWideType<_Float16> {
     }
 };
 
-// Result tiles of 32 columns a wave holds, and the workgroup's threads and tile of tokens.
-constexpr int kv_wide_ct(int dim) { return 1; }
-constexpr int kv_wide_threads(int dim) { return kv_wide_cols(dim) / kv_wide_ct(dim) * 2; }
-constexpr int kv_wide_tile(int dim) { return 8192 / dim / kv_wide_ct(dim); }
+constexpr int kv_wide_threads(int dim) { return 2 * kv_wide_cols(dim); }
+
+// Unit u: a sequence's columns col0 .. (kv_wide_cols(D) of them at most), and the
+// tiles t0 .. t1-1 that some of them see (one at least, so that every unit is visited).
+struct KvUnit {
+    int b, r0, n, len, col0, t0, t1;
+};
+template <int D>
+__device__ __forceinline__ bool kv_unit(const KvAttend &a, int u, KvUnit &x) {
+    constexpr int kCols = kv_wide_cols(D), TT = kv_wide_tile(D);
+    int k;
+    if (a.s.row_start) {
+        x.b = kv_unit_sequence(a.s, u, a.per, kCols, 1);
+        k = u - kv_unit_first(a.s, x.b, a.per, kCols, 1);
+    } else {
+        const int each = a.units / a.s.B;
+        x.b = u / each;
+        k = u - x.b * each;
+    }
+    kv_rows(a.s, x.b, x.r0, x.n);
+    const int64_t cols = static_cast<int64_t>(x.n) * a.per;
+    if (cols <= a.split_cols || k < 0 || static_cast<int64_t>(k) * kCols >= cols) return false;
+    x.col0 = k * kCols;
+    x.len = kv_length(a.s, x.b, a.c.page_shift);
+    const int p0 = x.len - x.n, last = static_cast<int>(cols) - 1;
+    const int end = x.col0 + kCols - 1 < last ? x.col0 + kCols - 1 : last;
+    const int lo = a.window ? p0 + x.col0 / a.per - a.window + 1 : 0, hi = a.causal ? p0 + end / a.per + 1 : x.len;
+    x.t0 = lo > 0 ? lo / TT : 0;
+    x.t1 = hi > 0 ? (hi + TT - 1) / TT : 0;
+    if (x.t1 <= x.t0) x.t1 = x.t0 + 1;
+    return true;
+}
+// The tile at which a boundary `at` behind an item's begin cuts it (0 or tiles: not inside).
+__device__ __forceinline__ int kv_wide_cut(int at, int tiles) {
+    const int t = at - kKvWideCost;
+    if (t <= kKvWideSnap) return 0;
+    return tiles - t <= kKvWideSnap ? tiles : t;
+}
 
 // What a thread unpacks of one tile: KW key words of one token (and one of its
 // pairs), VI pieces of 8 tokens x 2 channels of the values.
@@ -685,10 +721,10 @@ struct KvWideLoad {
         const int x = threadIdx.x + THREADS * i;
         m = x & 15, b = (x >> 4) % J, h = (x / (16 * J)) & 1, u = __builtin_amdgcn_readfirstlane(x / (32 * J));
     }
-    // (len >= 1 here.  A vector load: a scalar one in flight would make every
+    // (A vector load: a scalar one in flight would make every
     // wait for an LDS operand a wait for all of them.)
     static __device__ __forceinline__ int id_of(const KvAttend &a, const int32_t *table, int tok, int len) {
-        int at = (tok < len ? tok : len - 1) >> a.c.page_shift;
+        int at = (tok < len ? tok : len > 0 ? len - 1 : 0) >> a.c.page_shift;
         asm("" : "+v"(at));
         return table[at];
     }
@@ -780,95 +816,64 @@ struct KvWideLoad {
 };
 
 template <typename T, int D, int NG>
-__global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(KvAttend a) {
+__device__ __forceinline__ void kv_wide_piece(const KvAttend &a, const KvUnit &unit, int head, int t0, int t1, int piece,
+                                              uint4 (&ks)[2][1024], uint4 (&vs)[2][1024],
+                                              float2 (&pairs)[3][NG * kv_wide_tile(D) + 1],
+                                              uint32_t (&vpairs)[2][NG * kv_wide_tile(D) + 4],
+                                              int (&lost)[3][kv_wide_tile(D) / 16 + 1]) {
     constexpr int kCols = kv_wide_cols(D), kThreads = kv_wide_threads(D), J = D / 32, TT = kv_wide_tile(D), S = D / 16;
-    constexpr int SUB = TT / 32, CT = kv_wide_ct(D);   // result tiles of 32 tokens x 32 columns: SUB x CT a wave
-    __shared__ uint4 ks[2][TT * D / 8], vs[2][TT * D / 8];
-    __shared__ float2 pairs[3][NG * TT + 1];
-    __shared__ __align__(16) uint32_t vpairs[2][NG * TT + 4];
-    __shared__ int lost[3][TT / 16 + 1];
-    const int tid = threadIdx.x, lane = tid & 63, n32 = lane & 31, h = lane >> 5;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int head = blockIdx.x % a.c.heads;
-    const int u = a.units - 1 - blockIdx.x / a.c.heads;   // the longest first
-    const int split = blockIdx.y;
-    int b, k, r0, n;
-    if (a.s.row_start) {
-        b = kv_unit_sequence(a.s, u, a.per, kCols, 1);
-        k = u - kv_unit_first(a.s, b, a.per, kCols, 1);
-    } else {
-        const int each = a.units / a.s.B;
-        b = u / each;
-        k = u - b * each;
-    }
-    kv_rows(a.s, b, r0, n);
-    const int64_t cols = static_cast<int64_t>(n) * a.per;
-    if (cols <= a.split_cols || k < 0 || static_cast<int64_t>(k) * kCols >= cols) return;
-    const int len = kv_length(a.s, b, a.c.page_shift), p0 = len - n;
-    const int last_col = static_cast<int>(cols) - 1, col0 = k * kCols + wave * (32 * CT);
-    const int32_t *table = a.s.table + static_cast<int64_t>(b) * a.s.max_pages;
+    constexpr int SUB = TT / 32;   // result tiles of 32 tokens x 32 columns a wave
+    const int lane = threadIdx.x & 63, n32 = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r0 = unit.r0, n = unit.n, len = unit.len, p0 = len - n;
+    const int last_col = n * a.per - 1, col0 = unit.col0 + wave * 32;
+    const int32_t *table = a.s.table + static_cast<int64_t>(unit.b) * a.s.max_pages;
     auto row_of = [&](int c) { return (c < last_col ? c : last_col) / a.per; };
-    // tiles that some column of the workgroup sees
-    const int i0 = row_of(k * kCols), i1 = row_of(k * kCols + kCols - 1);
-    int lo = a.window ? p0 + i0 - a.window + 1 : 0, hi = a.causal ? p0 + i1 + 1 : len;
-    lo = lo > 0 ? lo / TT : 0;
-    hi = hi > 0 ? (hi + TT - 1) / TT : 0;
-    int t0 = lo, t1 = hi;
-    if (a.splits > 1) {
-        const int part = (hi - lo + a.splits - 1) / a.splits;
-        t0 = lo + split * part < hi ? lo + split * part : hi;
-        t1 = t0 + part < hi ? t0 + part : hi;
-    }
     // where nothing is hidden from the wave's columns
     const int minpos = a.causal ? p0 + row_of(col0) : len - 1;
-    const int maxlow = a.window ? p0 + row_of(col0 + 32 * CT - 1) - a.window + 1 : 0;
+    const int maxlow = a.window ? p0 + row_of(col0 + 31) - a.window + 1 : 0;
 
-    // this lane's columns: their queries, the sums of these, their visible positions
+    // this lane's column: its queries, their sums, its visible positions
     typedef typename KvType<T>::vec8 vec8;
-    int pos[CT], low[CT];
-    vec8 q[CT][S];
-    float qs[CT][NG], m[CT], l[CT], top[CT], ref[CT];   // ref: m, or 0 before there is one
-    floatx16 o[CT][J];
-#pragma unroll
-    for (int c = 0; c < CT; ++c) {
-        const int col = col0 + 32 * c + n32, row = col / a.per;
-        const bool real = row < n;
-        pos[c] = real ? (a.causal ? p0 + row : len - 1) : -1;
-        low[c] = a.window ? p0 + row - a.window + 1 : 0;
+    const int col = col0 + n32, row = col / a.per;
+    const bool real = row < n;
+    const int pos = real ? (a.causal ? p0 + row : len - 1) : -1, low = a.window ? p0 + row - a.window + 1 : 0;
+    vec8 q[S];
+    float qs[NG], m = -INFINITY, l = 0.0f, top = -INFINITY, ref = 0.0f;   // ref: m, or 0 before there is one
+    floatx16 o[J];
+    {
         const T *src = static_cast<const T *>(a.Q) + (r0 + (real ? row : 0)) * a.q_stride +
                        static_cast<int64_t>(head * a.per + (col - row * a.per)) * D + 8 * h;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) qs[c][g] = 0.0f;
+        for (int g = 0; g < NG; ++g) qs[g] = 0.0f;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             vec8 x = {};
             if (real) x = *reinterpret_cast<const vec8 *>(src + 16 * s);
-            if (CT > 1 || D > 128) asm("" : "+a"(x));   // (in the registers that only MFMAs can read: the others fill up)
-            q[c][s] = x;
             float sum = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum += static_cast<float>(x[e]);
-            qs[c][s * NG / S] += sum;
+            qs[s * NG / S] += sum;
+            if (D > 128) asm("" : "+a"(x));   // (where the output fills the other registers)
+            q[s] = x;
         }
 #pragma unroll
-        for (int g = 0; g < NG; ++g) qs[c][g] += __shfl_xor(qs[c][g], 32);
+        for (int g = 0; g < NG; ++g) qs[g] += __shfl_xor(qs[g], 32);
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) o[c][j][r] = 0.0f;
-        m[c] = -INFINITY;
-        l[c] = ref[c] = 0.0f;
+            for (int r = 0; r < 16; ++r) o[j][r] = 0.0f;
     }
 
     // Both products are kSlots MFMAs a tile, each in a slot of its own: the operand
     // of some slots on is read from LDS, one MFMA issued, and a share of the tile's
     // vector work done under it.  (The slots are fenced: left to itself the
     // scheduler puts each read right before its MFMA and the vector work behind all.)
-    constexpr int kSlots = SUB * CT * S, kReads = kSlots / CT, kAhead = 4;
-    static_assert(2 * SUB * CT * J == kSlots && kReads >= 2 * kAhead, "");
+    constexpr int kSlots = SUB * S, kAhead = 4;
+    static_assert(2 * SUB * J == kSlots && kSlots >= 2 * kAhead, "");
     // The next tile's scores: one group's sums of (base + code) * q (NG = 1), or the
     // scores themselves, into which the groups' sums are folded as they come.
-    floatx16 next[CT][SUB], part[2][CT];
+    floatx16 next[SUB], part[2];
     uint4 f[kAhead];
     // operand i of the first product: with one group the result tiles alternate, else
     // the groups of one result tile follow each other
@@ -898,56 +903,51 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(KvAttend a)
     auto fold = [&](int i) {
         const int e = (i / M - 1) / NG, g = (i / M - 1) % NG;
 #pragma unroll
-        for (int y = 0; y < kFold; ++y)
-#pragma unroll
-            for (int c = 0; c < CT; ++c) {
-                const floatx4 f = z[i & 1][y];
-                const floatx16 &sum = part[(i / M - 1) & 1][c];
-                floatx16 &x = next[c][e];
-                const int r = 2 * (i % M * kFold + y);
-                x[r] = fmaf(f[0], sum[r], g == 0 ? f[1] * qs[c][g] : fmaf(f[1], qs[c][g], x[r]));
-                x[r + 1] = fmaf(f[2], sum[r + 1], g == 0 ? f[3] * qs[c][g] : fmaf(f[3], qs[c][g], x[r + 1]));
-            }
+        for (int y = 0; y < kFold; ++y) {
+            const floatx4 w = z[i & 1][y];
+            const floatx16 &sum = part[(i / M - 1) & 1];
+            floatx16 &x = next[e];
+            const int r = 2 * (i % M * kFold + y);
+            x[r] = fmaf(w[0], sum[r], g == 0 ? w[1] * qs[g] : fmaf(w[1], qs[g], x[r]));
+            x[r + 1] = fmaf(w[2], sum[r + 1], g == 0 ? w[3] * qs[g] : fmaf(w[3], qs[g], x[r + 1]));
+        }
     };
-    auto score_slot = [&](int t, int t3, int slot) {
-        const int i = slot / CT, c = slot % CT;
+    auto score_slot = [&](int t, int t3, int i) {
         int e, k;
         key_operand(i, e, k);
         const uint4 w = f[i % kAhead];
-        if (c == CT - 1 && i + kAhead < kReads) f[i % kAhead] = read_key(t, i + kAhead);
+        if (i + kAhead < kSlots) f[i % kAhead] = read_key(t, i + kAhead);
         if constexpr (NG == 1) {
-            next[c][e] = KvWideType<T>::mfma(w, q[c][k], k == 0 ? floatx16{} : next[c][e]);
+            next[e] = KvWideType<T>::mfma(w, q[k], k == 0 ? floatx16{} : next[e]);
         } else {
-            floatx16 &y = part[(i / M) & 1][c];
-            y = KvWideType<T>::mfma(w, q[c][k], k % M == 0 ? floatx16{} : y);
-            if (c == CT - 1) {
-                if (i >= M) fold(i);
-                if (i + 2 >= M) read_fold(t3, i + 2);
-            }
+            floatx16 &y = part[(i / M) & 1];
+            y = KvWideType<T>::mfma(w, q[k], k % M == 0 ? floatx16{} : y);
+            if (i >= M) fold(i);
+            if (i + 2 >= M) read_fold(t3, i + 2);
         }
     };
     auto end_scores = [&](int t3) {   // the last group
         if constexpr (NG > 1) {
 #pragma unroll
-            for (int i = kReads; i < kReads + M; ++i) {
+            for (int i = kSlots; i < kSlots + M; ++i) {
                 fold(i);
-                if (i + 2 < kReads + M) read_fold(t3, i + 2);
+                if (i + 2 < kSlots + M) read_fold(t3, i + 2);
             }
         }
     };
     // The scores less the reference, two tokens at a time, and their maximum.
-    floatx16 x[CT][SUB];
-    auto relative = [&](floatx4 y, int i, int c) {
+    floatx16 x[SUB];
+    auto relative = [&](floatx4 y, int i) {
         const int e = i / 8, r = i % 8 * 2;
         if constexpr (NG == 1) {
-            x[c][e][r] = fmaf(y[0], next[c][e][r], fmaf(y[1], qs[c][0], -ref[c]));
-            x[c][e][r + 1] = fmaf(y[2], next[c][e][r + 1], fmaf(y[3], qs[c][0], -ref[c]));
+            x[e][r] = fmaf(y[0], next[e][r], fmaf(y[1], qs[0], -ref));
+            x[e][r + 1] = fmaf(y[2], next[e][r + 1], fmaf(y[3], qs[0], -ref));
         } else {
-            x[c][e][r] = next[c][e][r] - ref[c];
-            x[c][e][r + 1] = next[c][e][r + 1] - ref[c];
+            x[e][r] = next[e][r] - ref;
+            x[e][r + 1] = next[e][r + 1] - ref;
         }
-        const float two = fmaxf(x[c][e][r], x[c][e][r + 1]);
-        top[c] = i == 0 ? two : fmaxf(top[c], two);
+        const float two = fmaxf(x[e][r], x[e][r + 1]);
+        top = i == 0 ? two : fmaxf(top, two);
     };
     auto start_scores = [&](int t) {
 #pragma unroll
@@ -991,9 +991,7 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(KvAttend a)
         for (int i = 0; i < kSlots; ++i) score_slot(t0, t3, i);
         end_scores(t3);
 #pragma unroll
-        for (int i = 0; i < 8 * SUB; ++i)
-#pragma unroll
-            for (int c = 0; c < CT; ++c) relative(NG == 1 ? factors(t3, 0, i) : floatx4{}, i, c);
+        for (int i = 0; i < 8 * SUB; ++i) relative(NG == 1 ? factors(t3, 0, i) : floatx4{}, i);
     }
     for (int t = t0; t < t1; ++t) {
         const int tok = t * TT, buf = t & 1;
@@ -1008,55 +1006,46 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(KvAttend a)
         }
         if (tok + TT - 1 > minpos || tok < maxlow || some_gone) {
 #pragma unroll
-            for (int c = 0; c < CT; ++c) {
+            for (int e = 0; e < SUB; ++e)
 #pragma unroll
-                for (int e = 0; e < SUB; ++e)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int p = tok + 32 * e + 8 * (r >> 2) + 4 * h + (r & 3);
-                        if (p > pos[c] || p < low[c] || gone[2 * e + (r >> 3)]) x[c][e][r] = -INFINITY;
-                        top[c] = e + r == 0 ? x[c][0][0] : fmaxf(top[c], x[c][e][r]);
-                    }
-            }
+                for (int r = 0; r < 16; ++r) {
+                    const int p = tok + 32 * e + 8 * (r >> 2) + 4 * h + (r & 3);
+                    if (p > pos || p < low || gone[2 * e + (r >> 3)]) x[e][r] = -INFINITY;
+                    top = e + r == 0 ? x[0][0] : fmaxf(top, x[e][r]);
+                }
         }
-        bool above = false;
+        if (__any(top > (m == -INFINITY ? -INFINITY : kLagLog2))) {
+            float now = fmaxf(m, top + ref);
+            now = fmaxf(now, __shfl_xor(now, 32));
+            const float g = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - now);
+            m = now;
+            const float back = (now == -INFINITY ? 0.0f : now) - ref;
+            ref += back;
+            l *= g;
 #pragma unroll
-        for (int c = 0; c < CT; ++c) above |= top[c] > (m[c] == -INFINITY ? -INFINITY : kLagLog2);
-        if (__any(above)) {
+            for (int e = 0; e < SUB; ++e)
 #pragma unroll
-            for (int c = 0; c < CT; ++c) {
-                float now = fmaxf(m[c], top[c] + ref[c]);
-                now = fmaxf(now, __shfl_xor(now, 32));
-                const float g = m[c] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[c] - now);
-                m[c] = now;
-                const float back = (now == -INFINITY ? 0.0f : now) - ref[c];
-                ref[c] += back;
-                l[c] *= g;
+                for (int r = 0; r < 16; ++r) x[e][r] -= back;
 #pragma unroll
-                for (int e = 0; e < SUB; ++e)
+            for (int j = 0; j < J; ++j)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) x[c][e][r] -= back;
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) o[c][j][r] *= g;
-            }
+                for (int r = 0; r < 16; ++r) o[j][r] *= g;
         }
         // the first product of the next tile (of stale keys after the last one), under it P of this one
-        half8 p[CT][2 * SUB];
+        half8 p[2 * SUB];
         constexpr int kOrder[4] = {0, 2, 1, 3};   // of the value bytes
         start_scores(t + 1);
 #pragma unroll
         for (int i = 0; i < kSlots; ++i) {
             __builtin_amdgcn_sched_barrier(0);
             score_slot(t + 1, n3, i);
-            constexpr int kEach = CT * SUB * 16 / kSlots;
+            constexpr int kEach = SUB * 16 / kSlots;
 #pragma unroll
             for (int z = i * kEach; z < (i + 1) * kEach; ++z) {
-                const int c = z / (16 * SUB), e = z / 16 % SUB, r = z % 16;
-                const float y = __builtin_amdgcn_exp2f(x[c][e][(r & ~3) + kOrder[r & 3]]);
-                l[c] += y;
-                p[c][2 * e + (r >> 3)][r & 7] = static_cast<_Float16>(y);
+                const int e = z / 16, r = z % 16;
+                const float y = __builtin_amdgcn_exp2f(x[e][(r & ~3) + kOrder[r & 3]]);
+                l += y;
+                p[2 * e + (r >> 3)][r & 7] = static_cast<_Float16>(y);
             }
         }
         end_scores(n3);
@@ -1070,16 +1059,14 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(KvAttend a)
 #pragma unroll
         for (int slot = 0; slot < kSlots; ++slot) {
             __builtin_amdgcn_sched_barrier(0);
-            const int i = slot / CT, c = slot % CT;
-            const uint4 w = f[i % kAhead];
-            if (c == CT - 1 && i + kAhead < kReads) f[i % kAhead] = read_value(i + kAhead);
-            o[c][i % J] = KvWideType<_Float16>::mfma(w, p[c][i / J], o[c][i % J]);
-            constexpr int kPairs = 8 * SUB * CT;
+            const uint4 w = f[slot % kAhead];
+            if (slot + kAhead < kSlots) f[slot % kAhead] = read_value(slot + kAhead);
+            o[slot % J] = KvWideType<_Float16>::mfma(w, p[slot / J], o[slot % J]);
+            constexpr int kPairs = 8 * SUB;
 #pragma unroll
             for (int z = slot * kPairs / kSlots; z < (slot + 1) * kPairs / kSlots; ++z) {   // (factors read two ahead)
-                const int two = z / CT;
-                relative(y[two & 1], two, z % CT);
-                if (NG == 1 && z % CT == CT - 1 && two + 2 < 8 * SUB) y[two & 1] = factors(n3, 0, two + 2);
+                relative(y[z & 1], z);
+                if (NG == 1 && z + 2 < kPairs) y[z & 1] = factors(n3, 0, z + 2);
             }
             if (slot < in.KW) in.template unpack_key<T>(slot, ks[buf]);
             if (slot == in.KW) {
@@ -1101,82 +1088,169 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(KvAttend a)
         __builtin_amdgcn_sched_barrier(0);
         t3 = n3;
     }
+    l += __shfl_xor(l, 32);
+    const int qh = head * a.per + col - row * a.per;
+    if (piece >= 0) {   // kept for a join
+        const int64_t at = static_cast<int64_t>(piece) * kCols + wave * 32 + n32;
+        if (h == 0) *reinterpret_cast<float2 *>(a.wide_ml + 2 * at) = make_float2(m, l);
 #pragma unroll
-    for (int c = 0; c < CT; ++c) {
-        l[c] += __shfl_xor(l[c], 32);
-        const int col = col0 + 32 * c + n32, row = col / a.per;
-        if (row >= n) continue;
-        const int qh = head * a.per + col - row * a.per;
-        if (a.splits > 1) {
-            const int64_t at = (static_cast<int64_t>(split) * a.c.heads + head) * a.s.T * a.per +
-                               static_cast<int64_t>(r0) * a.per + col;
-            if (h == 0) *reinterpret_cast<float2 *>(a.wide_ml + 2 * at) = make_float2(m[c], l[c]);
+        for (int j = 0; j < J; ++j)
 #pragma unroll
-            for (int j = 0; j < J; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    *reinterpret_cast<floatx4 *>(a.wide_part + at * D + 32 * j + 8 * e + 4 * h) =
-                        floatx4{o[c][j][4 * e], o[c][j][4 * e + 1], o[c][j][4 * e + 2], o[c][j][4 * e + 3]};
-            continue;
-        }
-        const float inv = l[c] == 0.0f ? 0.0f : 1.0f / l[c];
+            for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<floatx4 *>(a.wide_part + at * D + 32 * j + 8 * e + 4 * h) =
+                    floatx4{o[j][4 * e], o[j][4 * e + 1], o[j][4 * e + 2], o[j][4 * e + 3]};
+    } else if (real) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         T *dst = static_cast<T *>(a.O) + (r0 + row) * a.o_stride + static_cast<int64_t>(qh) * D + 4 * h;
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                *reinterpret_cast<uint2 *>(dst + 32 * j + 8 * e) =
-                    pack4<T>(o[c][j][4 * e] * inv, o[c][j][4 * e + 1] * inv, o[c][j][4 * e + 2] * inv,
-                             o[c][j][4 * e + 3] * inv);
+                *reinterpret_cast<uint2 *>(dst + 32 * j + 8 * e) = pack4<T>(
+                    o[j][4 * e] * inv, o[j][4 * e + 1] * inv, o[j][4 * e + 2] * inv, o[j][4 * e + 3] * inv);
         if (a.lse && h == 0)
             a.lse[static_cast<int64_t>(r0 + row) * a.q_heads + qh] =
-                l[c] == 0.0f ? -INFINITY : (m[c] + __builtin_amdgcn_logf(l[c])) * kLn2;
+                l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
     }
 }
 
-// Joins the splits of one row and query head (D/2 threads of a block each).
+template <typename T, int D, int NG>
+__global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(KvAttend a) {
+    constexpr int kThreads = kv_wide_threads(D), TT = kv_wide_tile(D);
+    __shared__ uint4 ks[2][1024], vs[2][1024];
+    __shared__ float2 pairs[3][NG * TT + 1];
+    __shared__ __align__(16) uint32_t vpairs[2][NG * TT + 4];
+    __shared__ int lost[3][TT / 16 + 1];
+    __shared__ int before[kKvLineUnits + 1];   // line mode: tiles (and costs) of one head of the units before
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int H = a.c.heads;
+    if (a.line) {
+        for (int i = tid; i < a.units; i += kThreads) {
+            KvUnit unit;
+            before[i + 1] = kv_unit<D>(a, i, unit) ? unit.t1 - unit.t0 + kKvWideCost : 0;
+        }
+        if (tid == 0) before[0] = 0;
+        __syncthreads();
+        if (wave == 0) {   // prefix sums, 64 units at a time
+            int sum = 0;
+            for (int i = 0; i < a.units; i += 64) {
+                int v = i + lane < a.units ? before[i + lane + 1] : 0;
+#pragma unroll
+                for (int d = 1; d < 64; d <<= 1) {
+                    const int up = __shfl_up(v, d);
+                    if (lane >= d) v += up;
+                }
+                if (i + lane < a.units) before[i + lane + 1] = sum + v;
+                sum += __builtin_amdgcn_readlane(v, 63);
+            }
+        }
+        __syncthreads();
+    }
+
+    // A piece at a time: unit u's tiles t0 .. t1-1 for one head.  (What the line needs is
+    // worked out anew for each, so that no register holds it meanwhile.)
+    for (int next_at = -1;;) {
+        KvUnit unit;
+        int head, t0, t1, piece = 0;
+        bool whole = true, more = false;
+        if (a.line) {
+            const int total = H * __builtin_amdgcn_readfirstlane(before[a.units]);
+            const int most = total / kKvWideMinShare > 1 ? total / kKvWideMinShare : 1;
+            const int workers = a.wide_workers < most ? a.wide_workers : most;
+            if (static_cast<int>(blockIdx.x) >= workers || total == 0) return;
+            // Workgroups go round the 8 XCDs; neighbours on the line, which read the same
+            // keys, get one XCD (and its L2).
+            const int xcd = blockIdx.x & 7, rest = workers & 7;
+            const int worker = xcd * (workers >> 3) + (xcd < rest ? xcd : rest) + (blockIdx.x >> 3);
+            const int x0 = static_cast<int>(static_cast<int64_t>(worker) * total / workers);
+            const int x1 = static_cast<int>((static_cast<int64_t>(worker) + 1) * total / workers);
+            const int at = next_at < 0 ? x0 : next_at, all = __builtin_amdgcn_readfirstlane(before[a.units]);
+            head = kv_clamp(at / all, 0, H - 1);
+            int lo = 0, hi = a.units;   // the last unit of the head that begins at or before it
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (head * all + __builtin_amdgcn_readfirstlane(before[mid]) <= at)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            const int item = head * all + __builtin_amdgcn_readfirstlane(before[lo]);
+            const int length = __builtin_amdgcn_readfirstlane(before[lo + 1] - before[lo]), tiles = length - kKvWideCost;
+            if (length <= 0 || !kv_unit<D>(a, lo, unit)) return;   // (not unless the tables change under the call)
+            const int end = item + length;
+            const int c0 = next_at < 0 ? kv_wide_cut(at - item, tiles) : 0;
+            const int c1 = x1 >= end ? tiles : kv_wide_cut(x1 - item, tiles);
+            whole = c0 == 0 && c1 == tiles;
+            more = end < x1;
+            next_at = end;
+            if (c0 == 0 && c1 > 0 && a.wide_items && tid == 0) {   // (as in kv_split_kernel)
+                const int last = static_cast<int>((static_cast<int64_t>(end - kKvWideSnap) * workers + total - 1) / total) - 1;
+                a.wide_items[lo * H + head] = whole ? make_int2(0, 0) : make_int2(worker, last - worker + 1);
+            }
+            if (c0 >= c1) {   // all of it belongs to another workgroup
+                if (!more) return;
+                continue;
+            }
+            t0 = unit.t0 + c0;
+            t1 = unit.t0 + c1;
+            piece = 2 * worker + (c0 == 0 ? 1 : 0);
+            __syncthreads();   // the piece before is done with LDS
+        } else {
+            head = blockIdx.x % H;
+            if (!kv_unit<D>(a, a.units - 1 - blockIdx.x / H, unit)) return;   // (the longest first)
+            t0 = unit.t0;
+            t1 = unit.t1;
+        }
+        kv_wide_piece<T, D, NG>(a, unit, head, t0, t1, whole ? -1 : piece, ks, vs, pairs, vpairs, lost);
+        if (!more) return;
+    }
+}
+
+// Joins the pieces of one (unit, head), blockIdx.x: D/4 threads a column.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void kv_wide_merge_kernel(KvAttend a) {
-    constexpr int kPer = 256 / (D / 2);
-    const int64_t out = static_cast<int64_t>(blockIdx.x) * kPer + threadIdx.x / (D / 2);
-    const int d = 2 * (threadIdx.x % (D / 2));
-    if (out >= static_cast<int64_t>(a.s.T) * a.q_heads) return;
-    const int row = static_cast<int>(out / a.q_heads), h = static_cast<int>(out - static_cast<int64_t>(row) * a.q_heads);
-    int b, r0, n;
-    if (a.s.row_start) {
-        int lo = 0, hi = a.s.B;   // the last sequence that starts at or before the row
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.s.row_start[mid] <= row)
-                lo = mid;
-            else
-                hi = mid;
+    constexpr int kLanes = D / 4, kPer = 256 / kLanes, kCols = kv_wide_cols(D);
+    const int item = blockIdx.x, u = item / a.c.heads, head = item - u * a.c.heads;
+    KvUnit unit;
+    if (!kv_unit<D>(a, u, unit)) return;
+    const int2 it = a.wide_items[item];
+    if (it.y == 0) return;
+    const int d = 4 * (threadIdx.x % kLanes);
+    const int c = blockIdx.y * kPer + threadIdx.x / kLanes, col = unit.col0 + c, row = col / a.per;
+    if (row >= unit.n) return;
+    float top = -INFINITY, sum = 0.0f;
+    floatx4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int kAhead = 4;   // pieces in flight
+    for (int k0 = 0; k0 < it.y; k0 += kAhead) {
+        float2 ml[kAhead];
+        floatx4 z[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (k0 + i >= it.y) break;
+            const int64_t at = (static_cast<int64_t>(it.x + k0 + i) * 2 + (k0 + i == 0 ? 1 : 0)) * kCols + c;
+            ml[i] = *reinterpret_cast<const float2 *>(a.wide_ml + at * 2);
+            z[i] = *reinterpret_cast<const floatx4 *>(a.wide_part + at * D + d);
         }
-        b = lo;
-    } else {
-        b = row / a.s.even;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (k0 + i >= it.y) break;
+            const float now = fmaxf(top, ml[i].x);
+            const float f0 = top == now ? 1.0f : __builtin_amdgcn_exp2f(top - now);
+            const float f1 = ml[i].x == now ? 1.0f : __builtin_amdgcn_exp2f(ml[i].x - now);
+            sum = sum * f0 + ml[i].y * f1;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) y[r] = y[r] * f0 + z[i][r] * f1;
+            top = now;
+        }
     }
-    kv_rows(a.s, b, r0, n);
-    if (row < r0 || row >= r0 + n || static_cast<int64_t>(n) * a.per <= a.split_cols) return;
-    float top = -INFINITY, sum = 0.0f, y0 = 0.0f, y1 = 0.0f;
-    for (int k = 0; k < a.splits; ++k) {
-        const int64_t at = (static_cast<int64_t>(k) * a.c.heads + h / a.per) * a.s.T * a.per +
-                           static_cast<int64_t>(row) * a.per + h % a.per;
-        const float2 ml = *reinterpret_cast<const float2 *>(a.wide_ml + at * 2);
-        const float2 z = *reinterpret_cast<const float2 *>(a.wide_part + at * D + d);
-        const float now = fmaxf(top, ml.x);
-        const float f0 = top == now ? 1.0f : __builtin_amdgcn_exp2f(top - now);
-        const float f1 = ml.x == now ? 1.0f : __builtin_amdgcn_exp2f(ml.x - now);
-        sum = sum * f0 + ml.y * f1;
-        y0 = y0 * f0 + z.x * f1;
-        y1 = y1 * f0 + z.y * f1;
-        top = now;
-    }
+    const int h = head * a.per + col - row * a.per;
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    T *dst = static_cast<T *>(a.O) + row * a.o_stride + static_cast<int64_t>(h) * D + d;
-    *reinterpret_cast<uint32_t *>(dst) = pack2<T>(y0 * inv, y1 * inv);
+    T *dst = static_cast<T *>(a.O) + (unit.r0 + row) * a.o_stride + static_cast<int64_t>(h) * D + d;
+    *reinterpret_cast<uint2 *>(dst) = pack4<T>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
     if (a.lse && d == 0)
-        a.lse[out] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+        a.lse[static_cast<int64_t>(unit.r0 + row) * a.q_heads + h] =
+            sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
 // ---------------------------------------------------------------------------
@@ -1195,12 +1269,11 @@ hipError_t kv_attend_typed(const KvAttend &a, bool run_split, bool run_wide, boo
             hipLaunchKernelGGL((kv_merge_kernel<T, D>), dim3(a.s.B * a.c.heads, a.part_cols), dim3(256), 0, st, a);
     }
     if (run_wide) {
-        hipLaunchKernelGGL((kv_wide_kernel<T, D, NG>), dim3(a.units * a.c.heads, a.splits), dim3(kv_wide_threads(D)), 0,
-                           st, a);
-        if (a.splits > 1) {
-            const int64_t per = 256 / (D / 2), n = (static_cast<int64_t>(a.s.T) * a.q_heads + per - 1) / per;
-            hipLaunchKernelGGL((kv_wide_merge_kernel<T, D>), dim3(static_cast<unsigned>(n)), dim3(256), 0, st, a);
-        }
+        hipLaunchKernelGGL((kv_wide_kernel<T, D, NG>), dim3(a.line ? a.wide_workers : a.units * a.c.heads),
+                           dim3(kv_wide_threads(D)), 0, st, a);
+        if (a.wide_items)
+            hipLaunchKernelGGL((kv_wide_merge_kernel<T, D>), dim3(a.units * a.c.heads, kv_wide_cols(D) / (1024 / D)),
+                               dim3(256), 0, st, a);
     }
     return hipGetLastError();
 }

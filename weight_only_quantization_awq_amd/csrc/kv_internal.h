@@ -95,8 +95,9 @@ struct KvAttend {
     int part_cols;                // most columns of an item
     float *part, *part_ml;        // [workers][2][part_cols][dim] and [..][2]
     // wide path
-    int splits, units;
-    float *wide_part, *wide_ml;   // [splits][heads][T*per][dim] and [..][2]
+    int units, line, wide_workers;
+    int2 *wide_items;             // [units*heads], as items; NULL where no unit is cut
+    float *wide_part, *wide_ml;   // [wide_workers][2][kv_wide_cols][dim] and [..][2]
 };
 
 // A sequence's columns are its query rows x the query heads of one key head.
@@ -104,6 +105,11 @@ constexpr int kKvSplitCols = 64;   // most columns of the split path (4 column t
 // Columns of one workgroup of the wide path, 32 to a wave: 8 waves, or 4 where
 // the output alone takes 128 registers.
 constexpr int kv_wide_cols(int dim) { return dim > 128 ? 128 : 256; }
+constexpr int kv_wide_tile(int dim) { return 8192 / dim; }   // tokens
+constexpr int kKvLineUnits = 1024;   // most units of the line mode
+constexpr int kKvWideCost = 3;       // what a unit costs besides its tiles, in tiles
+constexpr int kKvWideMinShare = 6;   // least share of a workgroup, in tiles
+constexpr int kKvWideSnap = 1;       // tiles: pieces this short are not cut off
 constexpr int kKvTile = 32;        // tokens of one step
 constexpr int kKvItemCost = 2;     // what an item costs besides its tiles, in tiles
 constexpr int kKvMinShare = 4;     // least share of a worker, in tiles
