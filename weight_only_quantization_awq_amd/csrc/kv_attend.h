@@ -893,18 +893,19 @@ __device__ __forceinline__ void kv_wide_piece(const KvAttend &a, const KvUnit &u
         return floatx4{kp[0].x, kp[0].y, kp[1].x, kp[1].y};
     };
     // One group's sums into the scores, in M parts under the next group's MFMAs; a
-    // part's factors are read two slots earlier.
+    // part's factors are read kFoldAhead slots earlier.
     constexpr int M = S / NG, kFold = NG == 1 ? 1 : 8 / M;   // operands of a group; factors of a part
-    floatx4 z[2][kFold];
+    constexpr int kFoldAhead = M > 2 ? 2 : 1;   // slots (a part of M = 2 has 4 factors)
+    floatx4 z[kFoldAhead][kFold];
     auto read_fold = [&](int t3, int i) {   // for operand i's slot: the group before
 #pragma unroll
-        for (int y = 0; y < kFold; ++y) z[i & 1][y] = factors(t3, (i / M - 1) % NG, 8 * ((i / M - 1) / NG) + i % M * kFold + y);
+        for (int y = 0; y < kFold; ++y) z[i % kFoldAhead][y] = factors(t3, (i / M - 1) % NG, 8 * ((i / M - 1) / NG) + i % M * kFold + y);
     };
     auto fold = [&](int i) {
         const int e = (i / M - 1) / NG, g = (i / M - 1) % NG;
 #pragma unroll
         for (int y = 0; y < kFold; ++y) {
-            const floatx4 w = z[i & 1][y];
+            const floatx4 w = z[i % kFoldAhead][y];
             const floatx16 &sum = part[(i / M - 1) & 1];
             floatx16 &x = next[e];
             const int r = 2 * (i % M * kFold + y);
@@ -923,7 +924,7 @@ __device__ __forceinline__ void kv_wide_piece(const KvAttend &a, const KvUnit &u
             floatx16 &y = part[(i / M) & 1];
             y = KvWideType<T>::mfma(w, q[k], k % M == 0 ? floatx16{} : y);
             if (i >= M) fold(i);
-            if (i + 2 >= M) read_fold(t3, i + 2);
+            if (i + kFoldAhead >= M) read_fold(t3, i + kFoldAhead);
         }
     };
     auto end_scores = [&](int t3) {   // the last group
@@ -931,7 +932,7 @@ __device__ __forceinline__ void kv_wide_piece(const KvAttend &a, const KvUnit &u
 #pragma unroll
             for (int i = kSlots; i < kSlots + M; ++i) {
                 fold(i);
-                if (i + 2 < kSlots + M) read_fold(t3, i + 2);
+                if (i + kFoldAhead < kSlots + M) read_fold(t3, i + kFoldAhead);
             }
         }
     };
