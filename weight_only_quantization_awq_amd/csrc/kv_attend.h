@@ -7,9 +7,9 @@
 //
 // Both products run on 16x16x32 MFMAs, transposed (keys and values are the A
 // operand, queries and scores the B operand), 32 tokens a step:
-//  - S^T = codes·Q^T.  A code enters as the 16-bit float base + code, made by one
-//    and-or on the packed word (16 + code in bf16, 64 + code in fp16, exact);
-//    steps and lowest values are applied in float32, the base taken out with the latter.
+//  - S^T = codes·Q^T.  A code enters as the 16-bit float 16 + code, exact, made by a
+//    shift and an and-or of the packed word; steps and lowest values are applied in
+//    float32, the base taken out with the latter.
 //  - A lane's result rows are tokens 4kb..4kb+3 of one query, which are the
 //    tokens that its B operand of the second product takes: scores stay in
 //    their lane.
@@ -49,10 +49,14 @@ __device__ __forceinline__ float half_hi(uint32_t x) {
     return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(x >> 16)));
 }
 
+// Key codes enter as 16 + code, the lowest base whose steps of one are all exact: its
+// part of a sum cancels against the lowest values' in float32, so it is kept small.
+constexpr float kKeyBase = 16.0f;
+
 // A key pair (step, lo) as the factors of (sum (base + code)*q, sum q) in a score.
-__device__ __forceinline__ float2 key_factors(uint32_t pair, float base, float scale) {
+__device__ __forceinline__ float2 key_factors(uint32_t pair, float scale) {
     const float step = half_lo(pair);
-    return make_float2(step * scale, fmaf(-base, step, half_hi(pair)) * scale);
+    return make_float2(step * scale, fmaf(-kKeyBase, step, half_hi(pair)) * scale);
 }
 
 template <typename T>
@@ -60,10 +64,8 @@ struct KvType;
 template <>
 struct KvType<__bf16> {
     typedef bf16x8 vec8;
-    static constexpr float base = 16.0f;
-    static __device__ __forceinline__ float2 key_pair(uint32_t p, float scale) { return key_factors(p, base, scale); }
-    // codes of channels (2i, 2i+1) of a key word, + base.  (Base 128 would save the
-    // shift of i = 0; its sums cancel 8 times as much in float32, which shows in lse.)
+    // The codes of channels (2i, 2i+1) of a key word, + base.  (Base 128 would save the
+    // shift of i = 0; its sums cancel 8 times as much.)
     static __device__ __forceinline__ uint32_t pair(uint32_t w, int i) {
         const uint32_t x = i == 0 ? w << 3 : w >> (4 * i - 3);
         return and_or(x, 0x00780078u, 0x41804180u);
@@ -75,11 +77,12 @@ struct KvType<__bf16> {
 template <>
 struct KvType<_Float16> {
     typedef half8 vec8;
-    static constexpr float base = 64.0f;
-    static __device__ __forceinline__ float2 key_pair(uint32_t p, float scale) { return key_factors(p, base, scale); }
+    // Of the forms that take as long: 64 + code cancels 3 to 4 times as much (lse was
+    // off by 1.8e-6 of itself instead of 5.7e-7); a code's own bits as a subnormal
+    // need no base, but these MFMAs align them as if they were 2^-14 (4e-6).
     static __device__ __forceinline__ uint32_t pair(uint32_t w, int i) {
-        const uint32_t x = i == 0 ? w << 4 : w >> (4 * (i - 1));
-        return and_or(x, 0x00F000F0u, 0x54005400u);
+        const uint32_t x = i < 2 ? w << (6 - 4 * i) : w >> (4 * i - 6);
+        return and_or(x, 0x03C003C0u, 0x4C004C00u);
     }
     static __device__ __forceinline__ floatx4 mfma(uint4 a, vec8 b, floatx4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(vec8, a), b, c, 0, 0, 0);
@@ -180,7 +183,7 @@ __device__ __forceinline__ void kv_pairs(const KvAttend &a, const KvStep<D, NG> 
         float *k = reinterpret_cast<float *>(&lds->k[h][0][0][0]) + 2 * n;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            const float2 y = KvType<T>::key_pair(s.pair[g], a.scale_log2);
+            const float2 y = key_factors(s.pair[g], a.scale_log2);
             k[32 * g] = y.x;
             k[32 * g + 1] = y.y;
         }
@@ -783,7 +786,7 @@ struct KvWideLoad {
     // Into pairs[group][token] (key factors), vpairs[group][token] and lost[16 tokens].
     template <typename T>
     __device__ __forceinline__ void unpack_pair(const KvAttend &a, float2 *pairs, uint32_t *vpairs, int *lost) const {
-        pairs[pair_to] = KvType<T>::key_pair(kp, a.scale_log2);
+        pairs[pair_to] = key_factors(kp, a.scale_log2);
         vpairs[pair_to] = vp & v_there;
         lost[lost_to] = !k_ok;
     }
