@@ -3,7 +3,7 @@
 // Quantiser, per group of one token and head, in float32:
 //   lo   = fp16(min x), step = fp16(max(max x - lo, 0) / 15)
 //   code = clamp(rint((x - lo) / step), 0, 15)   (0 where step is 0)
-// taken against the stored lo and step, with IEEE divisions, so the codes do
+// taken against the stored lo and step, with IEEE quotients, so the codes do
 // not depend on the machine's approximations.  Reading: code*step is exact in
 // float32 (4 + 11 significant bits), so code*step + lo rounds once there and
 // once in the output type.
@@ -103,9 +103,20 @@ __device__ __forceinline__ Place place(const KvCache &c, const KvBatch &s, int u
     return p;
 }
 
-// Codes, as 8 nibbles of one word in channel order, and the group's pair (step,
-// lowest) as fp16 bits.  The lanes of a group are GL neighbours.
-template <int GL>
+// Nibble of channel i in a word of 8 codes: values' are in channel order, keys' are
+// stored in the order 0,2,4,6,1,3,5,7.
+__device__ __forceinline__ constexpr int key_nibble(int i) { return (i >> 1) + 4 * (i & 1); }
+
+// Codes, as 8 nibbles of one word, and the group's pair (step, lowest) as fp16 bits.
+// The lanes of a group are GL neighbours.
+//
+// The quotients are IEEE's, from one reciprocal r = RN(1/step): q0 = RN(d*r) is off by
+// less than 1.5 ulp, e = d - q0*step is exact, and q0 + e*r differs from d/step by
+// less than 2^-23 ulp.  step has 11 bits, so d/step is no tie of 24-bit floats and is
+// 2^-12 ulp or more from every one: both round alike.  (Where e underflows, the code
+// is 0 either way.)  (Dividing 16 times a lane took
+// the arithmetic of an append above its memory time.)
+template <int GL, bool KEY>
 __device__ __forceinline__ uint32_t quantise(const float *x, uint32_t &pair) {
     float lo = x[0], hi = x[0];
 #pragma unroll
@@ -120,33 +131,15 @@ __device__ __forceinline__ uint32_t quantise(const float *x, uint32_t &pair) {
            (static_cast<uint32_t>(__builtin_bit_cast(uint16_t, lo16)) << 16);
     uint32_t w = 0;
     if (step > 0.0f) {
+        const float r = 1.0f / step;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float q = fminf(fmaxf(rintf((x[i] - lo) / step), 0.0f), 15.0f);
-            w |= static_cast<uint32_t>(q) << (4 * i);
+            const float d = x[i] - lo, q0 = d * r, q1 = fmaf(fmaf(-q0, step, d), r, q0);
+            const float q = fminf(fmaxf(rintf(q1), 0.0f), 15.0f);
+            w |= static_cast<uint32_t>(q) << (4 * (KEY ? key_nibble(i) : i));
         }
     }
     return w;
-}
-
-// Nibbles 0..7 in channel order -> the stored order 0,2,4,6,1,3,5,7.
-__device__ __forceinline__ uint32_t interleave(uint32_t w) {
-    uint32_t o = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        o |= ((w >> (8 * i)) & 15u) << (4 * i);
-        o |= ((w >> (8 * i + 4)) & 15u) << (16 + 4 * i);
-    }
-    return o;
-}
-__device__ __forceinline__ uint32_t deinterleave(uint32_t w) {
-    uint32_t o = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        o |= ((w >> (4 * i)) & 15u) << (8 * i);
-        o |= ((w >> (16 + 4 * i)) & 15u) << (8 * i + 4);
-    }
-    return o;
 }
 
 template <typename T, int D, int GROUP>
@@ -173,7 +166,7 @@ __global__ __launch_bounds__(kKvThreads) void kv_append_kernel(KvCache c, KvBatc
     const unsigned long long any = __ballot(bad);
     const int at = (threadIdx.x & 63) & ~(LT - 1);
     bad = ((any >> at) & ((1ull << LT) - 1)) != 0;
-    uint32_t kp, vp, kw = quantise<GL>(k, kp), vw = quantise<GL>(v, vp);
+    uint32_t kp, vp, kw = quantise<GL, true>(k, kp), vw = quantise<GL, false>(v, vp);
     if (bad) kp = 0x7E007E00u, vp = 0, kw = 0, vw = 0;
     // lane w holds channels 8w..8w+7; the byte of channel 32b + m takes its high
     // nibble from 16 channels on, two lanes further
@@ -192,7 +185,7 @@ __global__ __launch_bounds__(kKvThreads) void kv_append_kernel(KvCache c, KvBatc
     if (there) {
         const int P = 1 << c.page_shift;
         const int j = w >> 2, kb = w & 3;
-        *reinterpret_cast<uint32_t *>(p.block + p.slot * (D / 2) + 4 * (kb * J + j)) = interleave(kw);
+        *reinterpret_cast<uint32_t *>(p.block + p.slot * (D / 2) + 4 * (kb * J + j)) = kw;
         if (w % GL == 0) {
             uint32_t *pairs = reinterpret_cast<uint32_t *>(p.block + P * D);
             pairs[p.slot * NG + w / GL] = kp;
@@ -226,7 +219,7 @@ __global__ __launch_bounds__(kKvThreads) void kv_read_kernel(KvCache c, KvBatch 
     uint32_t kw = 0, kp = 0, vp = 0;
     const unsigned char *mine = reinterpret_cast<const unsigned char *>(bytes[sub]);
     if (there) {
-        kw = deinterleave(*reinterpret_cast<const uint32_t *>(p.block + p.slot * (D / 2) + 4 * (kb * J + j)));
+        kw = *reinterpret_cast<const uint32_t *>(p.block + p.slot * (D / 2) + 4 * (kb * J + j));
         const uint32_t *pairs = reinterpret_cast<const uint32_t *>(p.block + P * D);
         kp = pairs[p.slot * NG + w / GL];
         vp = pairs[P * NG + p.slot * NG + w / GL];
@@ -245,7 +238,7 @@ __global__ __launch_bounds__(kKvThreads) void kv_read_kernel(KvCache c, KvBatch 
         const bool lost = ks != ks;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            k[i] = fmaf(static_cast<float>((kw >> (4 * i)) & 15u), ks, kl);
+            k[i] = fmaf(static_cast<float>((kw >> (4 * key_nibble(i))) & 15u), ks, kl);
             const uint32_t q = (static_cast<uint32_t>(mine[(m0 + i) * (4 * J) + 4 * b + token]) >> shift) & 15u;
             v[i] = lost ? ks : fmaf(static_cast<float>(q), vs, vl);
         }
