@@ -1031,9 +1031,14 @@ __device__ __forceinline__ void kv_wide_piece(const KvAttend &a, const KvUnit &u
 #pragma unroll
                 for (int r = 0; r < 16; ++r) x[e][r] -= back;
 #pragma unroll
-            for (int j = 0; j < J; ++j)
+            for (int j = 0; j < J; ++j) {
+                // (at D = 256 sums stay in accumulation registers; without this the
+                // compiler copies all of them out before the branch, tile after tile)
+                if constexpr (D == 256) asm("" : "+a"(o[j]));
 #pragma unroll
                 for (int r = 0; r < 16; ++r) o[j][r] *= g;
+                if constexpr (D == 256) asm("" : "+a"(o[j]));
+            }
         }
         // the first product of the next tile (of stale keys after the last one), under it P of this one
         half8 p[2 * SUB];
