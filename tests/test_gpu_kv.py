@@ -8,7 +8,7 @@ Attention, per output, with A = sum_t p_t |v'_t| and 2^-11 the half step of fp16
   - a score's float32 error e changes p by e, the sum of p by e:   A * 2e
   - float32 sums of P*v' and P over n tokens:        A * 2n * 2^-24
   - the output type's rounding:                       half a step of |O|
-e: a group's sum adds base + code times q (base 16 in bf16, 64 in fp16), `group`
+e: a group's sum adds base + code times q (base 16), `group`
 additions of partial sums no larger than (base + 15) * sum |q|; step times it and
 lo - base*step times sum q (4 roundings of at most (2*base + 15) * sum |q| * step
 beyond |S|) then take the base out.  Both are within group*2^-24*M*step with
@@ -35,6 +35,7 @@ def awq():
     if not torch.cuda.is_available():
         pytest.skip("no GPU")
     from weight_only_quantization_awq_amd import awq
+    awq._lib = None   # (load anew: a test that reloads the module puts back a library that knows the classes of before)
     return awq
 
 
@@ -220,7 +221,7 @@ def test_append_of_four_tokens_and_of_single_ones_agree(awq):
 # ---- attention --------------------------------------------------------------
 
 def check(q, dtype, cache, got, lse, start, lengths, table, fill=0.0, **kw):
-    base = 16 if dtype == "bf16" else 64
+    base = 16
 
     def spread(step, key, x):   # bound on the float32 error of q.k' of each token
         mass = np.abs(x).sum() * (2 * base + 15)
@@ -474,6 +475,133 @@ def test_decoding_step_captured_in_a_graph(awq):
         torch.cuda.synchronize()
         assert torch.equal(c.pages, eager.pages)
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("dim,group,dtype", [(64, 32, "bf16"), (64, 64, "fp16"), (128, 32, "fp16"), (128, 64, "bf16"),
+                                             (128, 128, "bf16"), (256, 32, "bf16"), (256, 64, "fp16"), (256, 128, "bf16")])
+@pytest.mark.parametrize("window", [0, 200])
+def test_attention_of_few_long_chunks(awq, dim, group, dtype, window):
+    """Chunks whose columns and tokens are shared out among workgroups: pieces joined, next to
+    sequences without rows, of one row, with more rows than positions, and without tokens."""
+    rng = np.random.default_rng(dim + group + window)
+    heads, per, page = 2, 3, 16
+    lengths = [1300, 1, 0, 90, 700, 0, 515]
+    counts = [97, 1, 0, 93, 1, 40, 129]
+    table, n_pages = table_for(lengths, page, rng, extra=3)
+    cache = filled(rng, n_pages, heads, dim, group, page)
+    spoil(cache, table, lengths)
+    start = np.concatenate(([0], np.cumsum(counts)))
+    q = queries(rng, (int(start[-1]) + 3, heads * per, dim), dtype)
+    say("long chunks", dim, group, dtype, window)
+    got, lse = attend(awq, q, dtype, cache, start, lengths, table, fill=5.0, window=window, max_rows=129)
+    last = int(start[-1])
+    assert (got[last:] == 5.0).all()
+    check(q[:last], dtype, cache, got[:last], lse[:last], start, lengths, table, window=window)
+
+
+@pytest.mark.parametrize("dim,group", [(64, 32), (128, 128), (256, 64)])
+def test_attention_of_many_chunks(awq, dim, group):
+    """So many chunks that each (chunk, head) has a workgroup of its own."""
+    rng = np.random.default_rng(dim)
+    heads, per, page, batch, rows = 4, 5, 16, 131, 14
+    lengths = [int(x) for x in rng.integers(0, 60, batch)]
+    table, n_pages = table_for(lengths, page, rng)
+    cache = filled(rng, n_pages, heads, dim, group, page)
+    spoil(cache, table, lengths)
+    q = queries(rng, (batch * rows, heads * per, dim), "bf16")
+    say("many chunks", dim)
+    got, lse = attend(awq, q, "bf16", cache, None, lengths, table)
+    check(q, "bf16", cache, got, lse, None, lengths, table)
+
+
+@pytest.mark.parametrize("batch", [64, 65, 300])
+def test_attention_of_many_sequences(awq, batch):
+    """More sequences than one wave looks at at a time, most of them short."""
+    rng = np.random.default_rng(batch)
+    heads, per, dim, group, page = 3, 4, 128, 64, 16
+    lengths = [int(x) for x in np.exp(rng.uniform(-1, 6, batch))]
+    lengths[-1] = 900
+    table, n_pages = table_for(lengths, page, rng)
+    cache = filled(rng, n_pages, heads, dim, group, page)
+    spoil(cache, table, lengths)
+    q = queries(rng, (batch, heads * per, dim), "fp16")
+    say("many sequences", batch)
+    got, lse = attend(awq, q, "fp16", cache, None, lengths, table)
+    check(q, "fp16", cache, got, lse, None, lengths, table)
+
+
+def test_pages_far_apart(awq):
+    """Pages so far apart that offsets into the pool pass 2^32, written, read and attended to."""
+    rng = np.random.default_rng(23)
+    heads, per, dim, group, page, n = 2, 4, 128, 64, 16, 7
+    block = page * dim + 8 * page * (dim // group)
+    apart = (5 << 30) // (n - 1) // 16 * 16
+    far = torch.empty(apart * (n - 1) + heads * block, dtype=torch.uint8, device="cuda")
+    pages = far.as_strided((n, heads, block), (apart, block, 1))
+    pages.zero_()
+    dev, near = awq.KvCache(pages, dim, group, page), awq.kv_cache(n, heads, dim, group, page)
+    table, lengths = np.array([[6, 0, 5], [4, 1, 3]]), [45, 48]
+    rows = 45
+    k, v = (torch.randn(2 * rows, heads, dim, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    q = torch.randn(2 * rows, heads * per, dim, device="cuda", dtype=torch.bfloat16)
+    results = []
+    for x in (dev, near):
+        awq.kv_append(x, k, v, ints(table), ints(lengths))
+        one = torch.randn(2, heads * per, dim, device="cuda", dtype=torch.bfloat16, generator=torch.Generator("cuda").manual_seed(1))
+        results.append((x.pages.contiguous(), *awq.kv_read(x, ints(table), ints(lengths), 2 * rows),
+                        *awq.kv_attention(q, x, ints(table), ints(lengths), want_lse=True),
+                        *awq.kv_attention(one, x, ints(table), ints(lengths), want_lse=True)))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    assert (results[0][0] != 0).any(-1).any(-1).tolist() == [True, True, False, True, True, True, True]
+
+
+def test_chunk_captured_in_a_graph(awq):
+    """A ragged chunk and its attention, with joined pieces, captured twice with workspaces of their
+    own: replays in turn follow the tables that the program changes, and equal the eager calls."""
+    torch.manual_seed(29)
+    rng = np.random.default_rng(29)
+    heads, per, dim, group, page, batch, most, rows = 2, 4, 128, 64, 16, 3, 90, 250
+    c, eager = (awq.kv_cache(batch * most, heads, dim, group, page) for _ in range(2))
+    table = torch.randperm(batch * most, device="cuda").int().view(batch, most)
+    length, start = ints([300, 60, 9]), ints([0, 200, 201, 210])
+    old = torch.randn(2, 1200, heads, dim, device="cuda", dtype=torch.bfloat16)
+    for x in (c, eager):
+        awq.kv_append(x, old[0].repeat(batch, 1, 1), old[1].repeat(batch, 1, 1), table, ints([1200] * batch))
+    q = torch.zeros(rows, heads * per, dim, device="cuda", dtype=torch.bfloat16)
+    k, v = (torch.zeros(rows, heads, dim, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    size = awq.kv_attention_workspace_size(c, heads * per, rows, batch, most, True, 240)
+    assert size > 0
+
+    def step(x, o, w):
+        awq.kv_append(x, k, v, table, length, row_start=start)
+        return awq.kv_attention(q, x, table, length, row_start=start, max_rows=240, out=o, workspace=w, want_lse=True)
+
+    graphs = []
+    for _ in range(2):
+        out, ws = torch.zeros_like(q), torch.empty(size, dtype=torch.uint8, device="cuda")
+        step(c, out, ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            _, lse = step(c, out, ws)
+        graphs.append((graph, out, lse))
+    awq.kv_append(eager, k, v, table, length, row_start=start)   # the warm-ups' write
+    for i in range(6):
+        for x in (q, k, v):
+            x.copy_(torch.randn(x.shape, device="cuda"))
+        counts = rng.integers(0, 80, 3)
+        counts[i % 3] = 1 + 80 * (i % 4) // 3
+        start.copy_(ints(np.concatenate(([0], np.cumsum(counts)))))
+        length.copy_(ints(np.maximum(counts, rng.integers(0, 1200, 3))))
+        graph, out, lse = graphs[i % 2]
+        graph.replay()
+        torch.cuda.synchronize()
+        want, want_lse = step(eager, torch.empty_like(out), None)
+        torch.cuda.synchronize()
+        n = int(counts.sum())
+        assert torch.equal(c.pages, eager.pages)
+        assert torch.equal(out[:n], want[:n]) and torch.equal(lse[:n], want_lse[:n])
 
 
 def test_generation_through_the_cache(awq):

@@ -111,6 +111,7 @@ def test_attention_by_hand():
 @pytest.fixture(scope="module")
 def awq():
     from weight_only_quantization_awq_amd import awq
+    awq._lib = None   # (load anew: a test that reloads the module puts back a library that knows the classes of before)
     return awq
 
 
@@ -165,7 +166,8 @@ BAD_CACHE = [(dict(pages=None), ARG), (dict(pages=FAKE + 8), ARG), (dict(n_pages
              (dict(heads=0), SHAPE), (dict(dim=96), SHAPE), (dict(group=48), ARG), (dict(page=20), ARG)]
 BAD_BATCH = [(dict(batch=0), SHAPE), (dict(rows=-1), SHAPE), (dict(rows=7), SHAPE), (dict(max_pages=0), SHAPE),
              (dict(max_pages=1 << 40), SHAPE), (dict(max_pages=(1 << 62)), SHAPE), (dict(batch=1 << 62, rows=0), SHAPE),
-             (dict(rows=(1 << 62), row_start=FAKE), SHAPE), (dict(batch=1 << 20, rows=0, max_pages=1 << 16), SHAPE),
+             (dict(rows=(1 << 62), row_start=FAKE), SHAPE), (dict(rows=1 << 26, row_start=FAKE), SHAPE),
+             (dict(batch=1 << 20, rows=0), SHAPE), (dict(batch=1 << 20, rows=0, max_pages=1 << 16), SHAPE),
              (dict(kv_len=None), ARG), (dict(block_table=None), ARG), (dict(kv_len=FAKE + 2), ARG),
              (dict(block_table=FAKE + 1), ARG), (dict(row_start=FAKE + 2), ARG)]
 EVERY = [("cache", o, s) for o, s in BAD_CACHE] + [("batch", o, s) for o, s in BAD_BATCH]

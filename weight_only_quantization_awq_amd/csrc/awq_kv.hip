@@ -27,6 +27,10 @@ awq_status hip_status(hipError_t e, const char *what) {
 bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
 constexpr int64_t kMaxCount = int64_t(1) << 30;   // rows, columns, units and tiles stay int32
+// A launch has fewer than 2^32 threads: dim/2 to a unit of the copy kernels, and on the
+// wide path of the attention at most 512 to an item and to 256 of its columns.
+constexpr int64_t kMaxUnits = int64_t(1) << 25;   // (at dim 128)
+constexpr int64_t kMaxItems = int64_t(1) << 21;   // batch * heads
 
 // The sizes of a cache: 0 or the bytes of one (page, head).
 int64_t block_bytes(int page, int64_t heads, int dim, int group) {
@@ -64,8 +68,9 @@ awq_status check(const awq_kv_cache *cache, const awq_kv_batch *batch, awq::KvCa
         return fail(AWQ_ERR_SHAPE, "without row_start, rows (%lld) must be a multiple of batch (%lld)",
                     static_cast<long long>(batch->rows), static_cast<long long>(batch->batch));
     const int64_t tiles = (batch->max_pages * cache->page + awq::kKvTile - 1) / awq::kKvTile;
-    // units of the copy kernels and tiles of the attention's line
-    if ((batch->rows / 4 + 2 * batch->batch) * cache->heads > kMaxCount || batch->batch * cache->heads > kMaxCount ||
+    // units of the copy kernels, and tiles of the attention's line
+    if ((batch->rows / 4 + 2 * batch->batch) * cache->heads > kMaxUnits * 128 / cache->dim ||
+        batch->batch * cache->heads > kMaxItems ||
         batch->batch * cache->heads * (tiles + awq::kKvItemCost) > kMaxCount)
         return fail(AWQ_ERR_SHAPE, "batch * heads * max_pages or rows * heads too large for one call");
     int shift = 0;
@@ -127,8 +132,7 @@ struct Plan {
     size_t items, part_ml, part, wide_items, wide_ml, wide_part, total;
 };
 
-// 256 CUs of 4 SIMDs.  A workgroup of the wide path fills a CU; from 2 of them to a CU
-// on, the longest first load the GPU evenly without a line.
+// 256 CUs of 4 SIMDs.  A workgroup of the wide path fills a CU.
 constexpr int kSimds = 1024, kCus = 256;
 
 awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, int64_t max_rows, Plan *p) {
@@ -158,8 +162,8 @@ awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, i
     p->units = static_cast<int>(s.row_start ? s.T * per / wide + s.B : s.B * ((s.even * per + wide - 1) / wide));
     const int64_t groups = static_cast<int64_t>(p->units) * c.heads;
     const int64_t wide_tiles = (static_cast<int64_t>(s.max_pages) * (1 << c.page_shift) - 1) / awq::kv_wide_tile(c.dim) + 1;
-    p->line = p->wide && groups < 2 * kCus && p->units <= awq::kKvLineUnits;
     const int64_t wide_line = groups * (wide_tiles + awq::kKvWideCost);
+    p->line = p->wide && groups < awq::kKvLineUnits && wide_line <= kMaxCount;
     const int64_t wide_useful = (wide_line + awq::kKvWideMinShare - 1) / awq::kKvWideMinShare;
     p->wide_workers = static_cast<int>(wide_useful < kCus ? wide_useful : kCus);
     p->wide_merge = p->line && wide_tiles > 2 * awq::kKvWideSnap + 1;

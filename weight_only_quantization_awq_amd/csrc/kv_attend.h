@@ -570,8 +570,9 @@ template <typename T, int D>
 __global__ __launch_bounds__(256) void kv_merge_kernel(KvAttend a) {
     constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
     const int item = blockIdx.x, col = blockIdx.y;
-    const int2 it = a.items[item];
-    if (it.y == 0) return;
+    int2 it = a.items[item];
+    if (it.y <= 0 || it.x < 0 || it.x >= a.workers) return;
+    it.y = it.y < a.workers - it.x ? it.y : a.workers - it.x;   // (inside, should tables change under the call)
     const int b = item / a.c.heads, head = item - b * a.c.heads;
     int r0, n;
     kv_rows(a.s, b, r0, n);
@@ -629,12 +630,13 @@ __global__ __launch_bounds__(256) void kv_merge_kernel(KvAttend a) {
 // heads of one key head, 32 a wave), over the tokens they see, in tiles of
 // kv_wide_tile(D).  Where units are few, they form a line that one workgroup a CU
 // shares equally, as on the split path (a unit costs kKvWideCost besides its
-// tiles); else each has a workgroup of its own, the longest first.  Here the matrix cores and the softmax bound it, so a
-// tile is unpacked once for all waves, into LDS, as 16-byte operands of
-// 32x32x16 MFMAs in reading order (every LDS access is contiguous); the
-// other half of the double buffer is filled between a tile's products and the
-// next barrier, from loads issued a tile earlier.  The same two layouts serve
-// this MFMA: result rows 8a + 4h + r of a lane are 4-token blocks, too.
+// tiles); else each has a workgroup of its own, the longest first.  Here the matrix
+// cores and the vector work under them bound it, so a tile is unpacked once for all
+// waves, into LDS, as 16-byte operands of 32x32x16 MFMAs in reading order (every LDS
+// access is contiguous); the other half of the double buffer is filled between a
+// tile's MFMAs, from loads issued a tile earlier, keys one tile ahead of values.
+// The same two layouts serve this MFMA: result rows 8a + 4h + r of a lane are
+// 4-token blocks, too.
 
 template <typename T>
 struct KvWideType;
@@ -1223,8 +1225,9 @@ __global__ __launch_bounds__(256) void kv_wide_merge_kernel(KvAttend a) {
     const int item = blockIdx.x, u = item / a.c.heads, head = item - u * a.c.heads;
     KvUnit unit;
     if (!kv_unit<D>(a, u, unit)) return;
-    const int2 it = a.wide_items[item];
-    if (it.y == 0) return;
+    int2 it = a.wide_items[item];
+    if (it.y <= 0 || it.x < 0 || it.x >= a.wide_workers) return;
+    it.y = it.y < a.wide_workers - it.x ? it.y : a.wide_workers - it.x;   // (as in kv_merge_kernel)
     const int d = 4 * (threadIdx.x % kLanes);
     const int c = blockIdx.y * kPer + threadIdx.x / kLanes, col = unit.col0 + c, row = col / a.per;
     if (row >= unit.n) return;

@@ -106,7 +106,9 @@ constexpr int kKvSplitCols = 64;   // most columns of the split path (4 column t
 // the output alone takes 128 registers.
 constexpr int kv_wide_cols(int dim) { return dim > 128 ? 128 : 256; }
 constexpr int kv_wide_tile(int dim) { return 8192 / dim; }   // tokens
-constexpr int kKvLineUnits = 1024;   // most units of the line mode
+// With fewer (unit, head)s than this they form a line; from 2 to a CU on, the longest
+// first load the GPU evenly without its pieces.
+constexpr int kKvLineUnits = 512;
 constexpr int kKvWideCost = 3;       // what a unit costs besides its tiles, in tiles
 constexpr int kKvWideMinShare = 6;   // least share of a workgroup, in tiles
 constexpr int kKvWideSnap = 1;       // tiles: pieces this short are not cut off
@@ -124,7 +126,7 @@ hipError_t launch_kv_append(const KvCache &c, const KvBatch &s, const void *K, c
                             int64_t k_stride, int64_t v_stride, hipStream_t st);
 hipError_t launch_kv_read(const KvCache &c, const KvBatch &s, void *K, void *V, int type, int64_t k_stride,
                           int64_t v_stride, hipStream_t st);
-// run_split / run_wide / merge_*: which launches the call needs (awq_kv.hip)
+// run_split, run_wide, merge: the launches that the call needs (awq_kv.hip)
 hipError_t launch_kv_attend_64(const KvAttend &a, int type, bool run_split, bool run_wide, bool merge, hipStream_t st);
 hipError_t launch_kv_attend_128(const KvAttend &a, int type, bool run_split, bool run_wide, bool merge, hipStream_t st);
 hipError_t launch_kv_attend_256(const KvAttend &a, int type, bool run_split, bool run_wide, bool merge, hipStream_t st);
