@@ -514,6 +514,22 @@ def test_attention_of_many_chunks(awq, dim, group):
     check(q, "bf16", cache, got, lse, None, lengths, table)
 
 
+@pytest.mark.parametrize("batch", [60, 120])
+def test_attention_of_even_chunks(awq, batch):
+    """As many chunks of like lengths as a CU takes whole, one or two each; some have no tokens."""
+    rng = np.random.default_rng(batch)
+    heads, per, dim, group, page, rows = 4, 4, 128, 64, 32, 17
+    lengths = [int(x) for x in rng.integers(90, 129, batch)]
+    lengths[3] = lengths[batch // 2] = 0
+    table, n_pages = table_for(lengths, page, rng)
+    cache = filled(rng, n_pages, heads, dim, group, page)
+    spoil(cache, table, lengths)
+    q = queries(rng, (batch * rows, heads * per, dim), "fp16")
+    say("even chunks", batch)
+    got, lse = attend(awq, q, "fp16", cache, None, lengths, table)
+    check(q, "fp16", cache, got, lse, None, lengths, table)
+
+
 @pytest.mark.parametrize("batch", [64, 65, 300])
 def test_attention_of_many_sequences(awq, batch):
     """More sequences than one wave looks at at a time, most of them short."""

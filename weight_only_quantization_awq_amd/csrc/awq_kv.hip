@@ -132,8 +132,7 @@ struct Plan {
     size_t items, part_ml, part, wide_items, wide_ml, wide_part, total;
 };
 
-// 256 CUs of 4 SIMDs.  A workgroup of the wide path fills a CU.
-constexpr int kSimds = 1024, kCus = 256;
+constexpr int kSimds = 4 * awq::kKvCus;
 
 awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, int64_t max_rows, Plan *p) {
     if (q_heads < 1 || q_heads > 65535 || q_heads % c.heads != 0)
@@ -143,7 +142,7 @@ awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, i
     if (static_cast<int64_t>(s.T) * q_heads > kMaxCount) return fail(AWQ_ERR_SHAPE, "rows * q_heads too large for one call");
     const int64_t per = q_heads / c.heads;
     const int64_t most = s.row_start ? (max_rows == 0 || max_rows > s.T ? s.T : max_rows) : s.even;
-    const int64_t cols = most * per, limit = c.dim == 256 ? 32 : awq::kKvSplitCols;
+    const int64_t cols = most * per, limit = awq::kv_split_cols(c.dim);
     const int64_t tiles = (static_cast<int64_t>(s.max_pages) * (1 << c.page_shift) + awq::kKvTile - 1) / awq::kKvTile;
     *p = Plan{};
     p->wide = cols > limit;
@@ -165,7 +164,7 @@ awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, i
     const int64_t wide_line = groups * (wide_tiles + awq::kKvWideCost);
     p->line = p->wide && groups < awq::kKvLineUnits && wide_line <= kMaxCount;
     const int64_t wide_useful = (wide_line + awq::kKvWideMinShare - 1) / awq::kKvWideMinShare;
-    p->wide_workers = static_cast<int>(wide_useful < kCus ? wide_useful : kCus);
+    p->wide_workers = static_cast<int>(wide_useful < awq::kKvCus ? wide_useful : awq::kKvCus);
     p->wide_merge = p->line && wide_tiles > 2 * awq::kKvWideSnap + 1;
     size_t at = 0;
     auto take = [&](size_t bytes) {

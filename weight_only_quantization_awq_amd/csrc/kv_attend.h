@@ -1133,6 +1133,8 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(KvAttend a)
     __shared__ __align__(16) uint32_t vpairs[2][NG * TT + 4];
     __shared__ int lost[3][TT / 16 + 1];
     __shared__ int before[kKvLineUnits + 1];   // line mode: tiles (and costs) of one head of the units before
+    __shared__ uint16_t order[kKvLineUnits];   // the units, longest first
+    __shared__ int jobs, span;                 // whole units to hand out instead of the line (0: none), and their time
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int H = a.c.heads;
@@ -1141,7 +1143,7 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(KvAttend a)
             KvUnit unit;
             before[i + 1] = kv_unit<D>(a, i, unit) ? unit.t1 - unit.t0 + kKvWideCost : 0;
         }
-        if (tid == 0) before[0] = 0;
+        if (tid == 0) before[0] = jobs = span = 0;
         __syncthreads();
         if (wave == 0) {   // prefix sums, 64 units at a time
             int sum = 0;
@@ -1157,6 +1159,29 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(KvAttend a)
             }
         }
         __syncthreads();
+        // Pieces cost time: their sums go through memory and a join.  Where whole units,
+        // the longest first, take at most 6/5 of the line's share, they are handed out
+        // instead: the first kKvCus to a CU each, the (kKvCus + i)th behind the
+        // (kKvCus - 1 - i)th.  (6 ragged prompts of up to 6000 tokens, 94 tiles to a CU on
+        // the line and 97 without: 278 us on the line, 263 us without; one of 2400 rows
+        // over 4096, 59 tiles and 73: 176 us both ways.)
+        auto length = [&](int i) { return before[i + 1] - before[i]; };
+        for (int i = tid; i < a.units; i += kThreads) {
+            const int mine = length(i);
+            int rank = 0;
+            for (int j = 0; j < a.units; ++j) rank += length(j) > mine || (length(j) == mine && j < i) ? 1 : 0;
+            order[rank] = static_cast<uint16_t>(i);
+            if (mine > 0) atomicAdd(&jobs, H);
+        }
+        __syncthreads();
+        for (int i = tid; i < kKvCus; i += kThreads) {
+            const int first = kKvCus - 1 - i, second = kKvCus + i;
+            const int time = (first < jobs ? length(order[first / H]) : 0) + (second < jobs ? length(order[second / H]) : 0);
+            atomicMax(&span, time);
+        }
+        __syncthreads();
+        if (tid == 0 && 5 * static_cast<int64_t>(span) * a.wide_workers > 6 * static_cast<int64_t>(H) * before[a.units]) jobs = 0;
+        __syncthreads();
     }
 
     // A piece at a time: unit u's tiles t0 .. t1-1 for one head.  (What the line needs is
@@ -1166,17 +1191,23 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(KvAttend a)
         int head, t0, t1, piece = 0;
         bool whole = true, more = false;
         if (a.line) {
-            const int total = H * __builtin_amdgcn_readfirstlane(before[a.units]);
+            const int all = __builtin_amdgcn_readfirstlane(before[a.units]), total = H * all;
             const int most = total / kKvWideMinShare > 1 ? total / kKvWideMinShare : 1;
             const int workers = a.wide_workers < most ? a.wide_workers : most;
-            if (static_cast<int>(blockIdx.x) >= workers || total == 0) return;
+            const int whole_jobs = __builtin_amdgcn_readfirstlane(jobs);
+            if (static_cast<int>(blockIdx.x) >= (whole_jobs > 0 ? whole_jobs : workers) || total == 0) return;
             // Workgroups go round the 8 XCDs; neighbours on the line, which read the same
             // keys, get one XCD (and its L2).
             const int xcd = blockIdx.x & 7, rest = workers & 7;
             const int worker = xcd * (workers >> 3) + (xcd < rest ? xcd : rest) + (blockIdx.x >> 3);
-            const int x0 = static_cast<int>(static_cast<int64_t>(worker) * total / workers);
-            const int x1 = static_cast<int>((static_cast<int64_t>(worker) + 1) * total / workers);
-            const int at = next_at < 0 ? x0 : next_at, all = __builtin_amdgcn_readfirstlane(before[a.units]);
+            int x0 = static_cast<int>(static_cast<int64_t>(worker) * total / workers);
+            int x1 = static_cast<int>((static_cast<int64_t>(worker) + 1) * total / workers);
+            if (whole_jobs > 0) {   // this workgroup's unit, whole
+                const int u = __builtin_amdgcn_readfirstlane(order[blockIdx.x / H]);
+                x0 = (blockIdx.x % H) * all + __builtin_amdgcn_readfirstlane(before[u]);
+                x1 = x0 + __builtin_amdgcn_readfirstlane(before[u + 1] - before[u]);
+            }
+            const int at = next_at < 0 ? x0 : next_at;
             head = kv_clamp(at / all, 0, H - 1);
             int lo = 0, hi = a.units;   // the last unit of the head that begins at or before it
             while (hi - lo > 1) {
@@ -1281,7 +1312,7 @@ hipError_t kv_attend_typed(const KvAttend &a, bool run_split, bool run_wide, boo
             hipLaunchKernelGGL((kv_merge_kernel<T, D>), dim3(a.s.B * a.c.heads, a.part_cols), dim3(256), 0, st, a);
     }
     if (run_wide) {
-        hipLaunchKernelGGL((kv_wide_kernel<T, D, NG>), dim3(a.line ? a.wide_workers : a.units * a.c.heads),
+        hipLaunchKernelGGL((kv_wide_kernel<T, D, NG>), dim3(a.line && a.wide_workers > a.units * a.c.heads ? a.wide_workers : a.units * a.c.heads),
                            dim3(kv_wide_threads(D)), 0, st, a);
         if (a.wide_items)
             hipLaunchKernelGGL((kv_wide_merge_kernel<T, D>), dim3(a.units * a.c.heads, kv_wide_cols(D) / (1024 / D)),

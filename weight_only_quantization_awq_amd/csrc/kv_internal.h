@@ -101,20 +101,30 @@ struct KvAttend {
 };
 
 // A sequence's columns are its query rows x the query heads of one key head.
-constexpr int kKvSplitCols = 64;   // most columns of the split path (4 column tiles)
+// Most columns of the split path (4 column tiles of 16, or 2 at dim 256, where the
+// output of 4 does not fit the registers).  16 sequences of 4096 tokens, 8 key heads:
+// at dim 128 64 columns take 76 us on it and 97 on the wide path, 32 columns 46 and
+// 100; at dim 64 64 columns 49 and 76; at dim 256 (4 heads) 32 columns 59 and 90.
+constexpr int kv_split_cols(int dim) { return dim > 128 ? 32 : 64; }
 // Columns of one workgroup of the wide path, 32 to a wave: 8 waves, or 4 where
 // the output alone takes 128 registers.
 constexpr int kv_wide_cols(int dim) { return dim > 128 ? 128 : 256; }
 constexpr int kv_wide_tile(int dim) { return 8192 / dim; }   // tokens
-// With fewer (unit, head)s than this they form a line; from 2 to a CU on, the longest
-// first load the GPU evenly without its pieces.
-constexpr int kKvLineUnits = 512;
+constexpr int kKvCus = 256;          // a workgroup of the wide path fills a CU
+// With fewer (unit, head)s than this they may form a line; from 2 to a CU on, the
+// longest first load the GPU evenly without its pieces.  (128 rows over 32768 tokens:
+// 103 us on the line, 1044 us without; 5 ragged chunks at dim 256: 295 and 383 us; a
+// prompt of 4096, 512 units: 243 and 199 us.)
+constexpr int kKvLineUnits = 2 * kKvCus;
 constexpr int kKvWideCost = 3;       // what a unit costs besides its tiles, in tiles
-constexpr int kKvWideMinShare = 6;   // least share of a workgroup, in tiles
+constexpr int kKvWideMinShare = 6;   // least share of a workgroup, in tiles (12: within 1%)
 constexpr int kKvWideSnap = 1;       // tiles: pieces this short are not cut off
 constexpr int kKvTile = 32;        // tokens of one step
 constexpr int kKvItemCost = 2;     // what an item costs besides its tiles, in tiles
-constexpr int kKvMinShare = 4;     // least share of a worker, in tiles
+// Least share of a worker, in tiles: a worker's part costs as much as about 2 tiles,
+// but latency is what the small calls pay (one sequence of 65 tokens, 8 tiles instead
+// of 4: 11.8 us instead of 7.4; 64 of up to 8192: 31.9 instead of 30.0).
+constexpr int kKvMinShare = 4;
 constexpr int kKvSnap = 1;         // tiles: pieces this short are not cut off (2 * snap < least share)
 // Waves of the split path that a SIMD holds at once, by the registers of a wave's
 // output (dim x 16*NT columns) and what comes with it.
