@@ -502,7 +502,7 @@ awq_status awq_w4a16_gemm_ex(const void *X, int64_t M, int64_t D_in, int64_t D_o
  * value in the place of a zero point.  For one token's key (or value) row x of
  * one head, per group of `group` channels, in float32:
  *   lo   = fp16(min x)
- *   step = fp16( max(max x - lo, 0) / 15 )
+ *   step = fp16( max(max x - lo, 0) * (1/15) )              (1/15 as a float32)
  *   q    = clamp(round_half_even((x - lo) / step), 0, 15)   (0 where step is 0)
  * and the cache stands for q*step + lo.  Values below about 2^-24 vanish in the
  * fp16 step.  A head's token whose key or value row holds a NaN, an infinity or

@@ -19,7 +19,7 @@ def quantise(x, group):
     with np.errstate(all="ignore"):
         lo = xs.min(-1).astype(np.float16)
         lof = lo.astype(np.float32)
-        step = (np.maximum(xs.max(-1) - lof, np.float32(0)) / np.float32(15)).astype(np.float16)
+        step = (np.maximum(xs.max(-1) - lof, np.float32(0)) * (np.float32(1) / np.float32(15))).astype(np.float16)
         sf = step.astype(np.float32)
         q = np.rint((xs - lof[..., None]) / sf[..., None])
         q = np.where(sf[..., None] > 0, np.clip(np.nan_to_num(q, nan=0.0), 0, 15), 0)

@@ -165,6 +165,8 @@ def test_append_values_at_the_edges(awq):
     k[2], v[2] = 1e-7 * k[2], 3e-5 * v[2]                          # steps at the bottom of fp16
     k[3, 0, 5], v[4, 1, 9], k[5, 1, 63], v[6, 0, 0] = np.nan, np.inf, -np.inf, 32769.0
     k[7], v[7] = -0.0, 1e-30
+    k[8], k[8, :, 3], k[8, :, 35] = 0.11847, -181.5, -181.5
+    k[8, :, 9], k[8, :, 41] = 5.82421875, 5.82421875                # a step on a tie of fp16
     table, length = np.array([[1]]), [n]
     c = kv.Cache(2, heads, dim, group, page)
     dev = awq.kv_cache(2, heads, dim, group, page)

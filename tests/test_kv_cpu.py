@@ -67,6 +67,13 @@ def test_quantiser_error_is_half_a_step():
     assert (err <= s / 2 * (1 + 1e-5) + 2.0 ** -11 * low + 15 * (2.0 ** -11 * s + 2.0 ** -25)).all()
 
 
+def test_step_on_a_tie_of_fp16():
+    """The range times float32's 1/15, which lies above 1/15: 12.48828125, a tie, goes up to the odd neighbour."""
+    x = np.linspace(-181.5, 15 * 12.48828125 - 181.5, 32, dtype=np.float32)
+    _, step, _ = kv.quantise(x, 32)
+    assert step[0] == 12.4921875
+
+
 @pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf, 40000.0])
 def test_rows_that_do_not_fit_read_back_as_nan(bad):
     c = kv.Cache(1, 2, 64, 32, 16)

@@ -1,7 +1,7 @@
 // Writing the 4-bit key/value cache and reading it back (layout: kv_internal.h).
 //
 // Quantiser, per group of one token and head, in float32:
-//   lo   = fp16(min x), step = fp16(max(max x - lo, 0) / 15)
+//   lo   = fp16(min x), step = fp16(max(max x - lo, 0) * (1/15)), 1/15 in float32
 //   code = clamp(rint((x - lo) / step), 0, 15)   (0 where step is 0)
 // taken against the stored lo and step, with IEEE quotients, so the codes do
 // not depend on the machine's approximations.  Reading: code*step is exact in
@@ -125,7 +125,7 @@ __device__ __forceinline__ uint32_t quantise(const float *x, uint32_t &pair) {
     for (int m = 1; m < GL; m <<= 1) lo = fminf(lo, __shfl_xor(lo, m)), hi = fmaxf(hi, __shfl_xor(hi, m));
     const _Float16 lo16 = static_cast<_Float16>(lo);
     lo = static_cast<float>(lo16);
-    const _Float16 step16 = static_cast<_Float16>(fmaxf(hi - lo, 0.0f) / 15.0f);
+    const _Float16 step16 = static_cast<_Float16>(fmaxf(hi - lo, 0.0f) * (1.0f / 15.0f));
     const float step = static_cast<float>(step16);
     pair = static_cast<uint32_t>(__builtin_bit_cast(uint16_t, step16)) |
            (static_cast<uint32_t>(__builtin_bit_cast(uint16_t, lo16)) << 16);
