@@ -563,12 +563,12 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(kv_split_wav
     }
 }
 
-// Joins the pieces of one item's column: blockIdx.x = item, blockIdx.y = column.
-// D/4 threads hold its channels, and 1024/D groups of them take every
-// (1024/D)th piece; the groups join in LDS.
-template <typename T, int D>
+// Joins the pieces of CH channels of one item's column: blockIdx = (item, column, channels).
+// CH/4 threads hold the channels, and 1024/CH groups of them take every (1024/CH)th
+// piece; the groups join in LDS.
+template <typename T, int D, int CH>
 __global__ __launch_bounds__(256) void kv_merge_kernel(KvAttend a) {
-    constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
+    constexpr int kLanes = CH / 4, kGroups = 256 / kLanes;
     const int item = blockIdx.x, col = blockIdx.y;
     int2 it = a.items[item];
     if (it.y <= 0 || it.x < 0 || it.x >= a.workers) return;
@@ -577,7 +577,7 @@ __global__ __launch_bounds__(256) void kv_merge_kernel(KvAttend a) {
     int r0, n;
     kv_rows(a.s, b, r0, n);
     if (n == 0 || static_cast<int64_t>(n) * a.per > a.split_cols || col >= n * a.per) return;
-    const int d = 4 * (threadIdx.x % kLanes), group = threadIdx.x / kLanes;
+    const int x = threadIdx.x % kLanes, d = blockIdx.z * CH + 4 * x, group = threadIdx.x / kLanes;
     float top = -INFINITY, sum = 0.0f;
     floatx4 y = {0.0f, 0.0f, 0.0f, 0.0f};
     auto join = [&](float m, float l, floatx4 z) {
@@ -609,11 +609,15 @@ __global__ __launch_bounds__(256) void kv_merge_kernel(KvAttend a) {
     }
     __shared__ floatx4 ys[kGroups][kLanes];
     __shared__ float2 mls[kGroups];
-    ys[group][threadIdx.x % kLanes] = y;
-    if (d == 0) mls[group] = make_float2(top, sum);
-    __syncthreads();
+    for (int half = kGroups / 2; half > 0; half >>= 1) {
+        if (group >= half && group < 2 * half) {
+            ys[group][x] = y;
+            if (x == 0) mls[group] = make_float2(top, sum);
+        }
+        __syncthreads();
+        if (group < half) join(mls[group + half].x, mls[group + half].y, ys[group + half][x]);
+    }
     if (group != 0) return;
-    for (int g = 1; g < kGroups; ++g) join(mls[g].x, mls[g].y, ys[g][threadIdx.x]);
     const int i = col / a.per, h = head * a.per + col - i * a.per;
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     T *dst = static_cast<T *>(a.O) + (r0 + i) * a.o_stride + static_cast<int64_t>(h) * D + d;
@@ -1308,8 +1312,11 @@ hipError_t kv_attend_typed(const KvAttend &a, bool run_split, bool run_wide, boo
             hipLaunchKernelGGL((kv_split_kernel<T, D, NG, 2>), grid, threads, 0, st, a);
         else if constexpr (D < 256)   // (awq_kv.hip takes at most 2 column tiles at 256 channels)
             hipLaunchKernelGGL((kv_split_kernel<T, D, NG, 4>), grid, threads, 0, st, a);
-        if (merge)
-            hipLaunchKernelGGL((kv_merge_kernel<T, D>), dim3(a.s.B * a.c.heads, a.part_cols), dim3(256), 0, st, a);
+        const int64_t columns = static_cast<int64_t>(a.s.B) * a.c.heads * a.part_cols;
+        if (merge && columns <= kKvMergeFew)
+            hipLaunchKernelGGL((kv_merge_kernel<T, D, 32>), dim3(a.s.B * a.c.heads, a.part_cols, D / 32), dim3(256), 0, st, a);
+        else if (merge)
+            hipLaunchKernelGGL((kv_merge_kernel<T, D, D>), dim3(a.s.B * a.c.heads, a.part_cols), dim3(256), 0, st, a);
     }
     if (run_wide) {
         hipLaunchKernelGGL((kv_wide_kernel<T, D, NG>), dim3(a.line && a.wide_workers > a.units * a.c.heads ? a.wide_workers : a.units * a.c.heads),

@@ -126,6 +126,11 @@ constexpr int kKvItemCost = 2;     // what an item costs besides its tiles, in t
 // of 4: 11.8 us instead of 7.4; 64 of up to 8192: 31.9 instead of 30.0).
 constexpr int kKvMinShare = 4;
 constexpr int kKvSnap = 1;         // tiles: pieces this short are not cut off (2 * snap < least share)
+// Up to so many columns (of all items) have their pieces joined 32 channels to a
+// workgroup: few columns have many pieces each, which more workgroups read sooner (64
+// columns, dim 128, 131072 tokens: 52.5 -> 48.0 us in all; dim 256, 65536: 42.1 -> 34.0);
+// many are quicker with fewer workgroups (512 columns: 43.6 us and 44.9; 4096: 29.5 and 36.8).
+constexpr int kKvMergeFew = 256;
 // Waves of the split path that a SIMD holds at once, by the registers of a wave's
 // output (dim x 16*NT columns) and what comes with it.
 constexpr int kv_split_waves(int dim, int nt) {
