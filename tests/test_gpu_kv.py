@@ -516,6 +516,23 @@ def test_attention_of_many_chunks(awq, dim, group):
     check(q, "bf16", cache, got, lse, None, lengths, table)
 
 
+@pytest.mark.parametrize("most", [96, 97, 192, 193, 224])
+@pytest.mark.parametrize("dim,rows,batch", [(64, 1, 7), (128, 3, 1), (256, 2, 90)])
+def test_attention_of_short_sequences(awq, most, dim, rows, batch):
+    """Around the lengths up to which no sequence is cut."""
+    rng = np.random.default_rng(most + dim)
+    heads, per, group, page = 5, 4, 64, 32
+    lengths = [int(x) for x in rng.integers(0, most + 1, batch)]
+    lengths[0] = most
+    table, n_pages = table_for(lengths, page, rng)
+    cache = filled(rng, n_pages, heads, dim, group, page)
+    spoil(cache, table, lengths)
+    q = queries(rng, (batch * rows, heads * per, dim), "bf16")
+    say("short sequences", most, dim, batch)
+    got, lse = attend(awq, q, "bf16", cache, None, lengths, table)
+    check(q, "bf16", cache, got, lse, None, lengths, table)
+
+
 @pytest.mark.parametrize("batch", [60, 120])
 def test_attention_of_even_chunks(awq, batch):
     """As many chunks of like lengths as a CU takes whole, one or two each; some have no tokens."""

@@ -248,11 +248,11 @@ def test_no_rows_is_a_call_without_launches(awq):
 @built
 def test_short_tables_need_no_workspace(awq):
     lib = awq.load()
-    # 6 pages of 16 tokens: 3 tiles of 32, never cut; a longer one can be
-    assert lib.awq_kv_attention_workspace_size(_cache(awq), _batch(awq, max_pages=6), 8, 0) == 0
+    # 12 pages of 16 tokens: 6 tiles of 32, never cut; a longer one can be
+    assert lib.awq_kv_attention_workspace_size(_cache(awq), _batch(awq, max_pages=12), 8, 0) == 0
     assert lib.awq_last_error() == b""
-    assert lib.awq_kv_attention_workspace_size(_cache(awq), _batch(awq, max_pages=7), 8, 0) > 0
-    assert lib.awq_kv_attention_workspace_size(_cache(awq), _batch(awq, max_pages=7), 6, 0) == 0
+    assert lib.awq_kv_attention_workspace_size(_cache(awq), _batch(awq, max_pages=13), 8, 0) > 0
+    assert lib.awq_kv_attention_workspace_size(_cache(awq), _batch(awq, max_pages=13), 6, 0) == 0
     assert b"q_heads" in lib.awq_last_error()
 
 

@@ -700,8 +700,8 @@ def kv_attention(Q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, kv_
         raise TypeError(f"Q must be bfloat16 or float16 (got {dtype})")
     q, q_stride = _kv_rows(Q, "Q", dev, shape)
     b = _kv_batch(dev, block_table, kv_len, row_start, rows)
-    if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
+    if out is None:   # (empty_like costs 0.5 us less)
+        out = torch.empty_like(Q) if Q.is_contiguous() else torch.empty(shape, dtype=dtype, device=dev)
         o, o_stride = out.data_ptr(), q_heads * cache.dim
     elif out.dtype != dtype:
         raise TypeError("out must have the dtype of Q")

@@ -128,7 +128,7 @@ awq_status copy_checks(const awq_kv_cache *cache, const awq_kv_batch *batch, con
 // The launches of one attention call and its workspace (byte offsets).
 struct Plan {
     bool split, wide, merge, line, wide_merge;
-    int tiles_col, split_cols, part_cols, workers, units, wide_workers;
+    int snap, tiles_col, split_cols, part_cols, workers, units, wide_workers;
     size_t items, part_ml, part, wide_items, wide_ml, wide_part, total;
 };
 
@@ -156,7 +156,8 @@ awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, i
     const int64_t useful = (line + awq::kKvMinShare - 1) / awq::kKvMinShare;
     const int64_t fill = kSimds * awq::kv_split_waves(c.dim, p->tiles_col);
     p->workers = static_cast<int>(useful < fill ? useful : fill);
-    p->merge = p->split && tiles > 2 * awq::kKvSnap + 1;   // shorter items are never cut
+    p->snap = static_cast<int>(tiles <= awq::kKvWhole ? tiles : awq::kKvSnap);
+    p->merge = p->split && tiles > 2 * p->snap + 1;   // shorter items are never cut
     const int64_t wide = awq::kv_wide_cols(c.dim);
     p->units = static_cast<int>(s.row_start ? s.T * per / wide + s.B : s.B * ((s.even * per + wide - 1) / wide));
     const int64_t groups = static_cast<int64_t>(p->units) * c.heads;
@@ -265,6 +266,7 @@ awq_status awq_kv_attention(const awq_kv_cache *cache, const awq_kv_batch *batch
     a.tiles_col = p.tiles_col;
     a.part_cols = p.part_cols;
     a.workers = p.workers;
+    a.snap = p.snap;
     a.units = p.units;
     a.line = p.line;
     a.wide_workers = p.wide_workers;

@@ -352,40 +352,34 @@ struct KvWave {
         }
     }
 
-    // Tokens of tiles t0 .. t1-1 of one sequence and head.  The loads of the
-    // next kAhead tiles, and the page numbers of the one after, are in flight
-    // while a tile is computed.  minpos / maxlow: the first last-visible and the
-    // last first-visible position of the columns.
-    static constexpr int kAhead = 1;
+    // Tokens of tiles t0 .. t1-1 of one sequence and head.  The loads of the next tile,
+    // and the page numbers of the one after, are in flight while a tile is computed
+    // (loads two or three tiles ahead cost registers and with them waves: 64 sequences of
+    // up to 8192 tokens 31 -> 39 and 50 us).  minpos / maxlow: the first last-visible and
+    // the last first-visible position of the columns.
     __device__ __forceinline__ void run(const KvAttend &a, const int32_t *table, int head, int t0, int t1, int len,
                                         int minpos, int maxlow, int lane, KvPairs<NG> *lds) {
         if (t0 >= t1) return;
-        KvStep<D, NG> s[kAhead + 1];
+        KvStep<D, NG> now, then;
         int tok = t0 * kKvTile, p0 = -1, p1 = -1;
         const int end = t1 * kKvTile;
         auto pages = [&](int t) {
             if (t < end) p0 = kv_page(a, table, t, len), p1 = kv_page(a, table, t + 16, len);
         };
         pages(tok);
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (tok + i * kKvTile < end) {
-                kv_load(a, head, tok + i * kKvTile, p0, p1, lane, s[i]);
-                pages(tok + (i + 1) * kKvTile);
-            }
-        }
+        kv_load(a, head, tok, p0, p1, lane, now);
+        pages(tok + kKvTile);
+#pragma unroll 1
         while (true) {
-#pragma unroll
-            for (int i = 0; i < kAhead + 1; ++i) {
-                const int next = tok + kAhead * kKvTile;
-                if (next < end) {
-                    kv_load(a, head, next, p0, p1, lane, s[(i + kAhead) % (kAhead + 1)]);
-                    pages(next + kKvTile);
-                }
-                step(a, s[i], tok, len, hides(s[i], tok, minpos, maxlow), lane, lds);
-                tok += kKvTile;
-                if (tok >= end) return;
+            const int next = tok + kKvTile;
+            if (next < end) {
+                kv_load(a, head, next, p0, p1, lane, then);
+                pages(next + kKvTile);
             }
+            step(a, now, tok, len, hides(now, tok, minpos, maxlow), lane, lds);
+            tok = next;
+            if (tok >= end) return;
+            now = then;
         }
     }
     static __device__ __forceinline__ bool hides(const KvStep<D, NG> &s, int tok, int minpos, int maxlow) {
@@ -438,7 +432,7 @@ struct KvWave {
 // lengths and few long sequences load the GPU evenly, and nothing but the
 // lengths on the device decides it.  A worker that holds a whole item writes
 // its output; the pieces of an item that a boundary cuts go to the workspace
-// and kv_merge_kernel joins them in order.  Boundaries within kKvSnap tiles of an
+// and kv_merge_kernel joins them in order.  Boundaries within a.snap tiles of an
 // item's ends move there.
 
 __device__ __forceinline__ int kv_first_token(const KvAttend &a, int len, int n) {
@@ -504,10 +498,10 @@ __device__ __forceinline__ KvItem kv_locate(const KvAttend &a, KvLine &line, int
 }
 
 // The tile at which a boundary at x cuts an item (0 or tiles: not inside).
-__device__ __forceinline__ int kv_cut(const KvItem &it, int x) {
+__device__ __forceinline__ int kv_cut(const KvAttend &a, const KvItem &it, int x) {
     const int t = x - it.begin - kKvItemCost;
-    if (t <= kKvSnap) return 0;
-    return it.tiles - t <= kKvSnap ? it.tiles : t;
+    if (t <= a.snap) return 0;
+    return it.tiles - t <= a.snap ? it.tiles : t;
 }
 
 template <typename T, int D, int NG, int NT>
@@ -532,9 +526,9 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(kv_split_wav
 
     KvWave<T, D, NG, NT> w;
     KvItem it = kv_locate(a, line, x0, lane);
-    int t0 = x0 == it.begin ? 0 : kv_cut(it, x0);
+    int t0 = x0 == it.begin ? 0 : kv_cut(a, it, x0);
     while (true) {
-        const int t1 = x1 >= it.end ? it.tiles : kv_cut(it, x1);
+        const int t1 = x1 >= it.end ? it.tiles : kv_cut(a, it, x1);
         if (t0 < t1) {
             const int first = kv_first_token(a, it.len, it.n) / kKvTile;
             w.start(a, it.head, it.r0, it.n, it.len, 0, lane);
@@ -552,8 +546,8 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(kv_split_wav
             }
             if (t0 == 0 && a.items && lane == 0) {
                 // pieces: this worker's and those of the workers whose start cuts the item, the
-                // last of them the last that starts before it.end - kKvSnap
-                const int last = static_cast<int>((static_cast<int64_t>(it.end - kKvSnap) * workers + total - 1) / total) - 1;
+                // last of them the last that starts before it.end - a.snap
+                const int last = static_cast<int>((static_cast<int64_t>(it.end - a.snap) * workers + total - 1) / total) - 1;
                 a.items[it.b * a.c.heads + it.head] = direct ? make_int2(0, 0) : make_int2(worker, last - worker + 1);
             }
         }

@@ -91,6 +91,7 @@ struct KvAttend {
     // split path
     int tiles_col;                // column tiles of 16 per item: 1, 2 or 4
     int workers;
+    int snap;                     // tiles: pieces this short are not cut off
     int2 *items;                  // [B*heads]: first worker and number of pieces (0: written already)
     int part_cols;                // most columns of an item
     float *part, *part_ml;        // [workers][2][part_cols][dim] and [..][2]
@@ -126,6 +127,10 @@ constexpr int kKvItemCost = 2;     // what an item costs besides its tiles, in t
 // of 4: 11.8 us instead of 7.4; 64 of up to 8192: 31.9 instead of 30.0).
 constexpr int kKvMinShare = 4;
 constexpr int kKvSnap = 1;         // tiles: pieces this short are not cut off (2 * snap < least share)
+// Where no item can be longer (in tiles), none is cut: that saves the join, a launch of
+// 3 to 4 us (one sequence, 8 heads of 128: 4 tiles 12.4 us cut and 9.0 whole, 8 tiles 12.6
+// and 13.1, 12 tiles 12.5 and 17.5; heads of 256: 16.7 and 13.0, 16.5 and 20.6).
+constexpr int kKvWhole = 6;
 // Up to so many columns (of all items) have their pieces joined 32 channels to a
 // workgroup: few columns have many pieces each, which more workgroups read sooner (64
 // columns, dim 128, 131072 tokens: 52.5 -> 48.0 us in all; dim 256, 65536: 42.1 -> 34.0);
