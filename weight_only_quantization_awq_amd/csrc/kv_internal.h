@@ -137,9 +137,13 @@ constexpr int kKvWhole = 6;
 // many are quicker with fewer workgroups (512 columns: 43.6 us and 44.9; 4096: 29.5 and 36.8).
 constexpr int kKvMergeFew = 256;
 // Waves of the split path that a SIMD holds at once, by the registers of a wave's
-// output (dim x 16*NT columns) and what comes with it.
+// output (dim x 16*NT columns) and what comes with it: as many as do without spills, since
+// they hide each other's latency.  us with 1 / 2 / these / one or two more: dim 64, NT 1
+// (64 sequences of 4096) 114 / 72 / 53 / 81; dim 128, NT 1 (131072 tokens) 71 / 51 / 49 / 57;
+// dim 128, NT 2 (16 of 4096) 50 / 47 / 47 / 100; dim 256, NT 1 (48 of 4096) 85 / 64 / 64 / -;
+// dim 128, NT 4 (24 of 4096) 98 / 218 / 98 / -.
 constexpr int kv_split_waves(int dim, int nt) {
-    return nt * dim <= 64 ? 4 : nt * dim <= 128 ? 3 : nt * dim <= 256 && dim < 256 ? 2 : 1;
+    return nt * dim <= 64 ? 4 : nt * dim <= 128 ? 3 : nt * dim <= 256 ? 2 : 1;
 }
 
 hipError_t launch_kv_append(const KvCache &c, const KvBatch &s, const void *K, const void *V, int type,
