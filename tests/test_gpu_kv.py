@@ -132,6 +132,32 @@ def test_append_then_read_ragged(awq, dim, group, page, dtype):
         assert torch.equal(got.cpu(), torch.from_numpy(want).to(TYPES[dtype]))
 
 
+@pytest.mark.parametrize("dim,group", [(64, 32), (128, 128), (256, 64)])
+@pytest.mark.parametrize("batch", [63, 64, 65, 700, 4100])
+def test_append_and_read_of_many_sequences(awq, batch, dim, group):
+    """More sequences than a wave looks at at a time; the first rows belong to none."""
+    rng = np.random.default_rng(batch)
+    heads, page = 1, 16
+    counts = rng.choice([0, 0, 1, 1, 2, 7], batch)
+    lengths = [int(n + m) for n, m in zip(counts, rng.choice([0, 1, 5], batch))]
+    table, n_pages = table_for(lengths, page, rng)
+    start = 3 + np.concatenate(([0], np.cumsum(counts)))
+    rows = int(start[-1]) + 2
+    k, kd = values(rng, (rows, heads, dim), "fp16")
+    v, vd = values(rng, (rows, heads, dim), "fp16")
+    c = kv.Cache(n_pages, heads, dim, group, page, fill=0xA5)
+    dev = pool(awq, c)
+    say("many sequences", batch, dim)
+    awq.kv_append(dev, kd, vd, ints(table), ints(lengths), row_start=ints(start))
+    torch.cuda.synchronize()
+    kv.append(c, k, v, start, lengths, table)
+    assert np.array_equal(dev.pages.cpu().numpy(), c.bytes)
+    out = tuple(torch.full((rows, heads, dim), 7.0, dtype=torch.float32, device="cuda") for _ in range(2))
+    awq.kv_read(dev, ints(table), ints(lengths), rows, row_start=ints(start), out=out)
+    for got, want in zip(out, kv.read(c, rows, start, lengths, table, fill=7.0)):
+        assert np.array_equal(got.cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("each,lengths", [(1, [1, 2, 3, 4, 5, 64, 0, 17]), (5, [5, 6, 7, 8, 33, 3]), (4, [4, 8, 64]),
                                           (64, [64, 128])])
 def test_append_the_same_rows_for_each_sequence(awq, each, lengths):
@@ -620,7 +646,7 @@ def test_chunk_captured_in_a_graph(awq):
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             _, lse = step(c, out, ws)
-        graphs.append((graph, out, lse))
+        graphs.append((graph, out, lse, ws))   # (a graph's workspace has to live as long as the graph)
     awq.kv_append(eager, k, v, table, length, row_start=start)   # the warm-ups' write
     for i in range(6):
         for x in (q, k, v):
@@ -629,7 +655,7 @@ def test_chunk_captured_in_a_graph(awq):
         counts[i % 3] = 1 + 80 * (i % 4) // 3
         start.copy_(ints(np.concatenate(([0], np.cumsum(counts)))))
         length.copy_(ints(np.maximum(counts, rng.integers(0, 1200, 3))))
-        graph, out, lse = graphs[i % 2]
+        graph, out, lse, _ = graphs[i % 2]
         graph.replay()
         torch.cuda.synchronize()
         want, want_lse = step(eager, torch.empty_like(out), None)
