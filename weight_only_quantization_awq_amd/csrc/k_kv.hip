@@ -20,9 +20,9 @@
 // stores whole words where all 4 tokens are new, else single bytes (the other
 // tokens of the block may be written by another call at the same time).
 //
-// Measured: appending 5 ragged bf16 chunks of up to 4099 rows, 8 heads of 128 (36 MB
+// Measured: appending 5 ragged bf16 chunks of up to 4099 rows, 8 heads of 128 (25 MB
 // in and out), takes 13.1 us, the quantiser's vector work; reading 4 sequences of up to
-// 16384 back takes 21.6 us for 94 MB, 93% of a large copy's rate; calls on few rows are
+// 16384 back takes 20.2 us for 94 MB, a large copy's rate; calls on few rows are
 // a launch (4.0 and 3.0 us).
 #include "kv_internal.h"
 
@@ -81,32 +81,65 @@ struct Place {
     int slot;              // this lane's token within the page
 };
 
-__device__ __forceinline__ Place place(const KvCache &c, const KvBatch &s, int unit, int units_even, int head,
-                                       int token) {
-    Place p{-1, nullptr, 0};
-    int b, k;
-    if (s.row_start) {
-        b = kv_unit_sequence(s, unit, 1, 4, 2);
-        k = unit - kv_unit_first(s, b, 1, 4, 2);
-    } else {
-        b = unit / units_even;
-        k = unit - b * units_even;
+// kv_unit_sequence (1, 4, 2) of a unit that is one for the wave, all of whose lanes call:
+// 64 sequences to a load, so that up to 64 cost one load's latency and not the six of a
+// search by halves (reading 4 sequences of up to 16384: 22.8 -> 21.5 us).
+__device__ __forceinline__ int wave_sequence(const KvBatch &s, int unit, int lane) {
+    int lo = 0, n = s.B;
+    while (n > 1) {
+        const int step = (n + 63) >> 6, at = lane * step;
+        const int begun = __popcll(__ballot(at < n && kv_unit_first(s, lo + (at < n ? at : 0), 1, 4, 2) <= unit));
+        const int from = begun > 0 ? (begun - 1) * step : 0;
+        lo += from;
+        n = n - from < step ? n - from : step;
+        if (begun == 0) break;   // (the first rows belong to no sequence)
     }
-    int r0, n;
-    kv_rows(s, b, r0, n);
-    const int first = kv_length(s, b, c.page_shift) - n;   // position of the first new row (may be negative)
-    const int base = ((first >> 2) + k) * 4;               // (arithmetic shift: floor)
-    if (k < 0 || n == 0 || base >= first + n) return p;    // (base + 3 >= first for every k >= 0)
-    const int i = base + token - first;
-    if (i >= 0 && i < n) p.row = r0 + i;
-    if (base < 0) return p;
-    // base < first + n <= the table's span, and 4 aligned positions share a page
-    const int id = s.table[static_cast<int64_t>(b) * s.max_pages + (base >> c.page_shift)];
-    if (id < 0 || id >= c.n_pages) return p;
-    p.block = c.pages + id * c.page_stride + head * c.block;
-    p.slot = (base & ((1 << c.page_shift) - 1)) + token;
-    return p;
+    return lo;
 }
+
+// The place of a unit's token: row first, so that its loads can leave before the page's
+// number is there.  `unit` is one for LU lanes (32 at least); all lanes of the wave call.
+template <int LU>
+struct Finder {
+    int b, base;
+    Place p{-1, nullptr, 0};
+
+    __device__ __forceinline__ void row(const KvCache &c, const KvBatch &s, int unit, int units, int units_even, int token) {
+        int k;
+        b = 0;
+        base = -1;
+        if (s.row_start) {
+            const int lane = threadIdx.x & 63, u0 = __builtin_amdgcn_readlane(unit, 0);
+            b = wave_sequence(s, u0, lane);
+            if constexpr (LU < 64) {
+                const int u1 = __builtin_amdgcn_readlane(unit, 32);
+                const int b1 = u1 == u0 ? b : wave_sequence(s, u1, lane);
+                b = lane < 32 ? b : b1;
+            }
+            k = unit - kv_unit_first(s, b, 1, 4, 2);
+        } else {
+            if (unit >= units) return;
+            b = unit / units_even;
+            k = unit - b * units_even;
+        }
+        int r0, n;
+        kv_rows(s, b, r0, n);
+        const int first = kv_length(s, b, c.page_shift) - n;   // position of the first new row (may be negative)
+        const int at = ((first >> 2) + k) * 4;                 // (arithmetic shift: floor)
+        if (unit >= units || k < 0 || n == 0 || at >= first + n) return;   // (at + 3 >= first for every k >= 0)
+        const int i = at + token - first;
+        if (i >= 0 && i < n) p.row = r0 + i;
+        base = at;
+    }
+    __device__ __forceinline__ void page(const KvCache &c, const KvBatch &s, int head, int token) {
+        if (base < 0) return;
+        // base < first + n <= the table's span, and 4 aligned positions share a page
+        const int id = s.table[static_cast<int64_t>(b) * s.max_pages + (base >> c.page_shift)];
+        if (id < 0 || id >= c.n_pages) return;
+        p.block = c.pages + id * c.page_stride + head * c.block;
+        p.slot = (base & ((1 << c.page_shift) - 1)) + token;
+    }
+};
 
 // Nibble of channel i in a word of 8 codes: values' are in channel order, keys' are
 // stored in the order 0,2,4,6,1,3,5,7.
@@ -119,8 +152,7 @@ __device__ __forceinline__ constexpr int key_nibble(int i) { return (i >> 1) + 4
 // less than 1.5 ulp, e = d - q0*step is exact, and q0 + e*r differs from d/step by
 // less than 2^-23 ulp.  step has 11 bits, so d/step is no tie of 24-bit floats and is
 // 2^-12 ulp or more from every one: both round alike.  (Where e underflows, the code
-// is 0 either way.)  (Dividing 16 times a lane took
-// the arithmetic of an append above its memory time.)
+// is 0 either way.)  (With 16 divisions a lane the append of 25 MB took 16.5 us.)
 template <int GL, bool KEY>
 __device__ __forceinline__ uint32_t quantise(const float *x, uint32_t &pair) {
     float lo = x[0], hi = x[0];
@@ -157,14 +189,16 @@ __global__ __launch_bounds__(kKvThreads) void kv_append_kernel(KvCache c, KvBatc
     __shared__ uint32_t bytes[kKvThreads / LU][LU];   // value codes of each unit: 2*D bytes
     const int sub = threadIdx.x / LU, lane = threadIdx.x % LU, token = lane / LT, w = lane % LT;
     const int id = blockIdx.x * (kKvThreads / LU) + sub, unit = id / c.heads, head = id - unit * c.heads;
-    Place p{-1, nullptr, 0};
-    if (unit < units) p = place(c, s, unit, units_even, head, token);
-    const bool there = p.block != nullptr && p.row >= 0;
+    Finder<LU> f;
+    f.row(c, s, unit, units, units_even, token);
     float k[8] = {}, v[8] = {};
-    if (there) {
-        load8(K + p.row * k_stride + head * D + 8 * w, k);
-        load8(V + p.row * v_stride + head * D + 8 * w, v);
+    if (f.p.row >= 0) {
+        load8(K + f.p.row * k_stride + head * D + 8 * w, k);
+        load8(V + f.p.row * v_stride + head * D + 8 * w, v);
     }
+    f.page(c, s, head, token);
+    const Place p = f.p;
+    const bool there = p.block != nullptr && p.row >= 0;
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i) bad |= !(fabsf(k[i]) <= kKvMaxAbs) || !(fabsf(v[i]) <= kKvMaxAbs);
@@ -217,8 +251,10 @@ __global__ __launch_bounds__(kKvThreads) void kv_read_kernel(KvCache c, KvBatch 
     __shared__ uint32_t bytes[kKvThreads / LU][LU];
     const int sub = threadIdx.x / LU, lane = threadIdx.x % LU, token = lane / LT, w = lane % LT;
     const int id = blockIdx.x * (kKvThreads / LU) + sub, unit = id / c.heads, head = id - unit * c.heads;
-    Place p{-1, nullptr, 0};
-    if (unit < units) p = place(c, s, unit, units_even, head, token);
+    Finder<LU> f;
+    f.row(c, s, unit, units, units_even, token);
+    f.page(c, s, head, token);
+    const Place p = f.p;
     const bool there = p.block != nullptr;
     const int P = 1 << c.page_shift, j = w >> 2, kb = w & 3;
     uint32_t kw = 0, kp = 0, vp = 0;
