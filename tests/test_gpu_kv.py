@@ -36,6 +36,7 @@ def awq():
         pytest.skip("no GPU")
     from weight_only_quantization_awq_amd import awq
     awq._lib = None   # (load anew: a test that reloads the module puts back a library that knows the classes of before)
+    awq.load()
     return awq
 
 
@@ -589,6 +590,28 @@ def test_attention_of_many_sequences(awq, batch):
     say("many sequences", batch)
     got, lse = attend(awq, q, "fp16", cache, None, lengths, table)
     check(q, "fp16", cache, got, lse, None, lengths, table)
+
+
+@pytest.mark.parametrize("dim,group,rows", [(64, 64, 1), (128, 128, 6), (256, 32, 1), (64, 32, 90), (128, 32, 90), (256, 128, 90)])
+def test_queries_that_are_not_finite_keep_to_themselves(awq, dim, group, rows):
+    """A NaN in one query, infinities in another: those are not finite, every other one is as it was."""
+    rng = np.random.default_rng(dim + rows)
+    heads, per, page, batch = 2, 4, 16, 3
+    lengths = [700, 95, 240]
+    table, n_pages = table_for(lengths, page, rng)
+    dev = pool(awq, filled(rng, n_pages, heads, dim, group, page))
+    q = torch.from_numpy(queries(rng, (batch * rows, heads * per, dim), "bf16")).bfloat16().cuda()
+    bad = q.clone()
+    nan, inf = (0, 3), (batch * rows - 1, 6)
+    bad[nan][5] = float("nan")
+    bad[inf][7], bad[inf][40] = float("inf"), -float("inf")
+    say("queries", dim, rows)
+    (o, lse), (po, plse) = (awq.kv_attention(x, dev, ints(table), ints(lengths), want_lse=True) for x in (q, bad))
+    assert torch.isfinite(o).all()
+    assert torch.isnan(po[nan]).all() and torch.isnan(plse[nan]) and not torch.isfinite(plse[inf])
+    for at in (nan, inf):
+        po[at], plse[at] = o[at], lse[at]
+    assert torch.equal(po, o) and torch.equal(plse, lse)
 
 
 def test_pages_far_apart(awq):
