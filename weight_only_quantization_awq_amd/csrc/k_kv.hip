@@ -21,9 +21,9 @@
 // tokens of the block may be written by another call at the same time).
 //
 // Measured: appending 5 ragged bf16 chunks of up to 4099 rows, 8 heads of 128 (25 MB
-// in and out), takes 13.1 us, the quantiser's vector work; reading 4 sequences of up to
-// 16384 back takes 20.2 us for 94 MB, a large copy's rate; calls on few rows are
-// a launch (4.0 and 3.0 us).
+// in and out), takes 12.8 us, two thirds of it the issue of 500 vector instructions a
+// wave; reading 4 sequences of up to 16384 back takes 20.2 us for 94 MB, a large copy's
+// rate; calls on few rows are a launch (4.0 and 3.0 us).
 #include "kv_internal.h"
 
 namespace awq {
@@ -146,18 +146,21 @@ struct Finder {
 __device__ __forceinline__ constexpr int key_nibble(int i) { return (i >> 1) + 4 * (i & 1); }
 
 // Codes, as 8 nibbles of one word, and the group's pair (step, lowest) as fp16 bits.
-// The lanes of a group are GL neighbours.
+// The lanes of a group are GL neighbours.  fits: the lane's 8 values are within
+// +-kKvMaxAbs (their sum finds a NaN, which the minimum and maximum leave out).
 //
 // The quotients are IEEE's, from one reciprocal r = RN(1/step): q0 = RN(d*r) is off by
 // less than 1.5 ulp, e = d - q0*step is exact, and q0 + e*r differs from d/step by
 // less than 2^-23 ulp.  step has 11 bits, so d/step is no tie of 24-bit floats and is
 // 2^-12 ulp or more from every one: both round alike.  (Where e underflows, the code
 // is 0 either way.)  (With 16 divisions a lane the append of 25 MB took 16.5 us.)
+// Four codes join as the float c0 + 16*c1 + 256*c2 + 4096*c3, exact below 2^24.
 template <int GL, bool KEY>
-__device__ __forceinline__ uint32_t quantise(const float *x, uint32_t &pair) {
-    float lo = x[0], hi = x[0];
+__device__ __forceinline__ uint32_t quantise(const float *x, uint32_t &pair, bool &fits) {
+    float lo = x[0], hi = x[0], sum = x[0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) lo = fminf(lo, x[i]), hi = fmaxf(hi, x[i]);
+    for (int i = 1; i < 8; ++i) lo = fminf(lo, x[i]), hi = fmaxf(hi, x[i]), sum += x[i];
+    fits = (lo >= -kKvMaxAbs) & (hi <= kKvMaxAbs) & (sum == sum);
 #pragma unroll
     for (int m = 1; m < GL; m <<= 1) lo = fminf(lo, __shfl_xor(lo, m)), hi = fmaxf(hi, __shfl_xor(hi, m));
     const _Float16 lo16 = static_cast<_Float16>(lo);
@@ -166,17 +169,16 @@ __device__ __forceinline__ uint32_t quantise(const float *x, uint32_t &pair) {
     const float step = static_cast<float>(step16);
     pair = static_cast<uint32_t>(__builtin_bit_cast(uint16_t, step16)) |
            (static_cast<uint32_t>(__builtin_bit_cast(uint16_t, lo16)) << 16);
-    uint32_t w = 0;
-    if (step > 0.0f) {
-        const float r = 1.0f / step;
+    const float r = step > 0.0f ? 1.0f / step : 0.0f;   // (a step of 0 makes codes of 0)
+    float four[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float d = x[i] - lo, q0 = d * r, q1 = fmaf(fmaf(-q0, step, d), r, q0);
-            const float q = fminf(fmaxf(rintf(q1), 0.0f), 15.0f);
-            w |= static_cast<uint32_t>(q) << (4 * (KEY ? key_nibble(i) : i));
-        }
+    for (int i = 0; i < 8; ++i) {
+        const float d = x[i] - lo, q0 = d * r, q1 = fmaf(fmaf(-q0, step, d), r, q0);
+        const float q = rintf(__builtin_amdgcn_fmed3f(q1, 0.0f, 15.0f));   // (clamping to whole numbers first changes nothing)
+        const int at = KEY ? key_nibble(i) : i;
+        four[at >> 2] = fmaf(q, static_cast<float>(1 << (4 * (at & 3))), four[at >> 2]);
     }
-    return w;
+    return static_cast<uint32_t>(four[0]) | (static_cast<uint32_t>(four[1]) << 16);
 }
 
 template <typename T, int D, int GROUP>
@@ -199,13 +201,11 @@ __global__ __launch_bounds__(kKvThreads) void kv_append_kernel(KvCache c, KvBatc
     f.page(c, s, head, token);
     const Place p = f.p;
     const bool there = p.block != nullptr && p.row >= 0;
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) bad |= !(fabsf(k[i]) <= kKvMaxAbs) || !(fabsf(v[i]) <= kKvMaxAbs);
-    const unsigned long long any = __ballot(bad);
+    bool k_fits, v_fits;
+    uint32_t kp, vp, kw = quantise<GL, true>(k, kp, k_fits), vw = quantise<GL, false>(v, vp, v_fits);
+    const unsigned long long any = __ballot(!(k_fits & v_fits));
     const int at = (threadIdx.x & 63) & ~(LT - 1);
-    bad = ((any >> at) & ((1ull << LT) - 1)) != 0;
-    uint32_t kp, vp, kw = quantise<GL, true>(k, kp), vw = quantise<GL, false>(v, vp);
+    const bool bad = ((any >> at) & ((1ull << LT) - 1)) != 0;
     if (bad) kp = 0x7E007E00u, vp = 0, kw = 0, vw = 0;
     // lane w holds channels 8w..8w+7; the byte of channel 32b + m takes its high
     // nibble from 16 channels on, two lanes further
@@ -213,10 +213,11 @@ __global__ __launch_bounds__(kKvThreads) void kv_append_kernel(KvCache c, KvBatc
     unsigned char *mine = reinterpret_cast<unsigned char *>(bytes[sub]);
     if ((w & 2) == 0) {
         const int m0 = 8 * (w & 1), b = w >> 2;
+        const uint32_t even = (vw & 0x0F0F0F0Fu) | ((up & 0x0F0F0F0Fu) << 4);   // the bytes of channels m0, m0 + 2, ..
+        const uint32_t odd = ((vw >> 4) & 0x0F0F0F0Fu) | (up & 0xF0F0F0F0u);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            mine[(m0 + i) * (4 * J) + 4 * b + token] =
-                static_cast<unsigned char>(((vw >> (4 * i)) & 15u) | (((up >> (4 * i)) & 15u) << 4));
+            mine[(m0 + i) * (4 * J) + 4 * b + token] = static_cast<unsigned char>((i & 1 ? odd : even) >> (8 * (i >> 1)));
     }
     const unsigned int here = __syncthreads_count(there);   // (also the barrier before the bytes are read)
     // all 4 tokens of this unit?  (one block of bytes: 4 aligned positions share a page)
