@@ -592,7 +592,7 @@ awq_status awq_kv_read(const awq_kv_cache *cache, const awq_kv_batch *batch, voi
  *   max_rows  an upper bound on any sequence's rows, known on the host; 0 means
  *             `rows`.  It chooses the kernels: with row_start it should be
  *             given.  A sequence with more rows gets them unspecified
- *             (nothing outside O and lse is written).  Ignored without row_start.
+ *             (nothing outside O, lse and workspace is written).  Ignored without row_start.
  *   scale     > 0; S = scale * q.k'.
  *   causal    1: a row at position p sees positions <= p; 0: all of kv_len.
  *   window    > 0: and only positions > p - window (causal = 1); 0: no window.

@@ -128,7 +128,7 @@ awq_status copy_checks(const awq_kv_cache *cache, const awq_kv_batch *batch, con
 // The launches of one attention call and its workspace (byte offsets).
 struct Plan {
     bool split, wide, merge, line, wide_merge;
-    int snap, tiles_col, split_cols, part_cols, workers, units, wide_workers;
+    int snap, tiles_col, split_cols, workers, units, wide_workers;
     size_t items, part_ml, part, wide_items, wide_ml, wide_part, total;
 };
 
@@ -150,8 +150,9 @@ awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, i
     const int64_t need = p->wide ? per : cols;
     p->split = need <= limit && (!p->wide || s.row_start);
     p->tiles_col = need <= 16 ? 1 : need <= 32 ? 2 : 4;
-    p->split_cols = p->split ? 16 * p->tiles_col : 0;
-    p->part_cols = static_cast<int>(need < p->split_cols && !p->wide ? need : p->split_cols);
+    // What a sequence's columns are compared with on the device is what the workspace holds for
+    // each piece: one with more rows than max_rows is left out, not kept in too small a place.
+    p->split_cols = p->split ? static_cast<int>(p->wide ? 16 * p->tiles_col : need) : 0;
     const int64_t line = s.B * static_cast<int64_t>(c.heads) * (tiles + awq::kKvItemCost);
     const int64_t useful = (line + awq::kKvMinShare - 1) / awq::kKvMinShare;
     const int64_t fill = kSimds * awq::kv_split_waves(c.dim, p->tiles_col);
@@ -174,7 +175,7 @@ awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, i
         return here;
     };
     if (p->merge) {
-        const size_t n = static_cast<size_t>(p->workers) * 2 * p->part_cols;
+        const size_t n = static_cast<size_t>(p->workers) * 2 * p->split_cols;
         p->items = take(static_cast<size_t>(s.B) * c.heads * 8);
         p->part_ml = take(n * 8);
         p->part = take(n * c.dim * 4);
@@ -264,7 +265,6 @@ awq_status awq_kv_attention(const awq_kv_cache *cache, const awq_kv_batch *batch
     a.window = window > (int64_t(1) << 30) ? 0 : static_cast<int>(window);   // (no sequence is longer)
     a.split_cols = p.split_cols;
     a.tiles_col = p.tiles_col;
-    a.part_cols = p.part_cols;
     a.workers = p.workers;
     a.snap = p.snap;
     a.units = p.units;

@@ -440,20 +440,6 @@ struct KvWave {
 // key head (131072 tokens, 143 MB: 41 us and 6 for the join).  With fixed pieces of tokens
 // instead of the line, ragged batches wait for their longest sequence.
 
-__device__ __forceinline__ int kv_first_token(const KvAttend &a, int len, int n) {
-    if (!a.window) return 0;
-    const int low = len - n - a.window + 1;
-    return low > 0 ? low & ~(kKvTile - 1) : 0;
-}
-// Tiles of an item of sequence b; 0: not on the split path.
-__device__ __forceinline__ int kv_item_tiles(const KvAttend &a, int b, int &r0, int &n, int &len) {
-    kv_rows(a.s, b, r0, n);
-    len = kv_length(a.s, b, a.c.page_shift);
-    if (n == 0 || static_cast<int64_t>(n) * a.per > a.split_cols) return 0;
-    const int t = (len - kv_first_token(a, len, n) + kKvTile - 1) / kKvTile;
-    return t > 0 ? t : 1;   // an empty item is visited, too: its output is zero
-}
-
 // 64 sequences of the line, one to a lane.
 struct KvLine {
     int chunk, base;          // sequences 64*chunk ..; where the first one's items begin
@@ -502,13 +488,6 @@ __device__ __forceinline__ KvItem kv_locate(const KvAttend &a, KvLine &line, int
     return it;
 }
 
-// The tile at which a boundary at x cuts an item (0 or tiles: not inside).
-__device__ __forceinline__ int kv_cut(const KvAttend &a, const KvItem &it, int x) {
-    const int t = x - it.begin - kKvItemCost;
-    if (t <= a.snap) return 0;
-    return it.tiles - t <= a.snap ? it.tiles : t;
-}
-
 template <typename T, int D, int NG, int NT>
 __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(kv_split_waves(D, NT)))) void kv_split_kernel(
     KvAttend a) {
@@ -522,18 +501,15 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(kv_split_wav
         total += line.total;
     }
     total *= a.c.heads;
-    // worker w takes the line from w*total/workers on
-    const int worker = blockIdx.x, most = total / kKvMinShare > 1 ? total / kKvMinShare : 1;
-    const int workers = a.workers < most ? a.workers : most;
+    const int worker = blockIdx.x, workers = kv_workers(a, total);
     if (worker >= workers || total == 0) return;
-    const int x0 = static_cast<int>(static_cast<int64_t>(worker) * total / workers);
-    const int x1 = static_cast<int>((static_cast<int64_t>(worker) + 1) * total / workers);
+    const int x0 = kv_share(worker, total, workers), x1 = kv_share(worker + 1, total, workers);
 
     KvWave<T, D, NG, NT> w;
     KvItem it = kv_locate(a, line, x0, lane);
-    int t0 = x0 == it.begin ? 0 : kv_cut(a, it, x0);
+    int t0 = x0 == it.begin ? 0 : kv_cut(a, it.begin, it.tiles, x0);
     while (true) {
-        const int t1 = x1 >= it.end ? it.tiles : kv_cut(a, it, x1);
+        const int t1 = x1 >= it.end ? it.tiles : kv_cut(a, it.begin, it.tiles, x1);
         if (t0 < t1) {
             const int first = kv_first_token(a, it.len, it.n) / kKvTile;
             w.start(a, it.head, it.r0, it.n, it.len, 0, lane);
@@ -545,8 +521,7 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(kv_split_wav
             if (direct) {
                 w.finish(a, it.head, it.r0, it.n, 0, lane);
             } else {
-                // of a worker's two pieces, the one that begins its item goes second
-                const int64_t at = (static_cast<int64_t>(worker) * 2 + (t0 == 0 ? 1 : 0)) * a.part_cols;
+                const int64_t at = kv_piece(a, worker, t0 == 0);
                 w.keep(a.part_ml + 2 * at, a.part + at * D, it.n * a.per, 0, lane);
             }
             if (t0 == 0 && a.items && lane == 0) {
@@ -596,7 +571,7 @@ __global__ __launch_bounds__(256) void kv_merge_kernel(KvAttend a) {
         for (int i = 0; i < kAhead; ++i) {
             const int k = k0 + i * kGroups;
             if (k >= it.y) break;
-            const int64_t at = (static_cast<int64_t>(it.x + k) * 2 + (k == 0 ? 1 : 0)) * a.part_cols + col;
+            const int64_t at = kv_piece(a, it.x + k, k == 0) + col;
             ml[i] = *reinterpret_cast<const float2 *>(a.part_ml + at * 2);
             z[i] = *reinterpret_cast<const floatx4 *>(a.part + at * D + d);
         }
@@ -1319,11 +1294,11 @@ hipError_t kv_attend_typed(const KvAttend &a, bool run_split, bool run_wide, boo
             hipLaunchKernelGGL((kv_split_kernel<T, D, NG, 2>), grid, threads, 0, st, a);
         else if constexpr (D < 256)   // (awq_kv.hip takes at most 2 column tiles at 256 channels)
             hipLaunchKernelGGL((kv_split_kernel<T, D, NG, 4>), grid, threads, 0, st, a);
-        const int64_t columns = static_cast<int64_t>(a.s.B) * a.c.heads * a.part_cols;
+        const int64_t columns = static_cast<int64_t>(a.s.B) * a.c.heads * a.split_cols;
         if (merge && columns <= kKvMergeFew)
-            hipLaunchKernelGGL((kv_merge_kernel<T, D, 32>), dim3(a.s.B * a.c.heads, a.part_cols, D / 32), dim3(256), 0, st, a);
+            hipLaunchKernelGGL((kv_merge_kernel<T, D, 32>), dim3(a.s.B * a.c.heads, a.split_cols, D / 32), dim3(256), 0, st, a);
         else if (merge)
-            hipLaunchKernelGGL((kv_merge_kernel<T, D, D>), dim3(a.s.B * a.c.heads, a.part_cols), dim3(256), 0, st, a);
+            hipLaunchKernelGGL((kv_merge_kernel<T, D, D>), dim3(a.s.B * a.c.heads, a.split_cols), dim3(256), 0, st, a);
     }
     if (run_wide) {
         hipLaunchKernelGGL((kv_wide_kernel<T, D, NG>), dim3(a.line && a.wide_workers > a.units * a.c.heads ? a.wide_workers : a.units * a.c.heads),

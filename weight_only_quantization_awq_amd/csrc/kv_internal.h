@@ -40,10 +40,10 @@ struct KvBatch {
 
 constexpr float kKvMaxAbs = 32768.0f;   // larger values (and NaN) are stored as NaN
 
-__device__ __forceinline__ int kv_clamp(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
+__host__ __device__ __forceinline__ int kv_clamp(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
 
 // First row and number of rows of sequence b, inside [0, T) whatever the table holds.
-__device__ __forceinline__ void kv_rows(const KvBatch &s, int b, int &r0, int &n) {
+__host__ __device__ __forceinline__ void kv_rows(const KvBatch &s, int b, int &r0, int &n) {
     if (!s.row_start) {
         r0 = b * s.even;
         n = s.even;
@@ -54,7 +54,7 @@ __device__ __forceinline__ void kv_rows(const KvBatch &s, int b, int &r0, int &n
 }
 
 // Tokens of sequence b, inside what its row of the page table holds.
-__device__ __forceinline__ int kv_length(const KvBatch &s, int b, int page_shift) {
+__host__ __device__ __forceinline__ int kv_length(const KvBatch &s, int b, int page_shift) {
     return kv_clamp(s.kv_len[b], 0, s.max_pages << page_shift);
 }
 
@@ -87,14 +87,14 @@ struct KvAttend {
     int q_heads, per;             // query heads, and query heads per key head
     float scale_log2;             // scale * log2(e)
     int causal, window;
-    int split_cols;               // sequences with at most this many columns take the split path
+    int split_cols;               // sequences with at most this many columns take the split path; a
+                                  // piece's place in the workspace holds as many
     // split path
     int tiles_col;                // column tiles of 16 per item: 1, 2 or 4
     int workers;
     int snap;                     // tiles: pieces this short are not cut off
     int2 *items;                  // [B*heads]: first worker and number of pieces (0: written already)
-    int part_cols;                // most columns of an item
-    float *part, *part_ml;        // [workers][2][part_cols][dim] and [..][2]
+    float *part, *part_ml;        // [workers][2][split_cols][dim] and [..][2]
     // wide path
     int units, line, wide_workers;
     int2 *wide_items;             // [units*heads], as items; NULL where no unit is cut
@@ -144,6 +144,39 @@ constexpr int kKvMergeFew = 256;
 // dim 128, NT 4 (24 of 4096) 98 / 218 / 98 / -.
 constexpr int kv_split_waves(int dim, int nt) {
     return nt * dim <= 64 ? 4 : nt * dim <= 128 ? 3 : nt * dim <= 256 ? 2 : 1;
+}
+
+// The split path's line (kv_attend.h).
+__host__ __device__ __forceinline__ int kv_first_token(const KvAttend &a, int len, int n) {
+    if (!a.window) return 0;
+    const int low = len - n - a.window + 1;
+    return low > 0 ? low & ~(kKvTile - 1) : 0;
+}
+// Tiles of an item of sequence b; 0: not on the split path.
+__host__ __device__ __forceinline__ int kv_item_tiles(const KvAttend &a, int b, int &r0, int &n, int &len) {
+    kv_rows(a.s, b, r0, n);
+    len = kv_length(a.s, b, a.c.page_shift);
+    if (n == 0 || static_cast<int64_t>(n) * a.per > a.split_cols) return 0;
+    const int t = (len - kv_first_token(a, len, n) + kKvTile - 1) / kKvTile;
+    return t > 0 ? t : 1;   // an empty item is visited, too: its output is zero
+}
+// Workers that share a line of this length, and where worker w's share begins (w = workers: the line's end).
+__host__ __device__ __forceinline__ int kv_workers(const KvAttend &a, int total) {
+    const int most = total / kKvMinShare > 1 ? total / kKvMinShare : 1;
+    return a.workers < most ? a.workers : most;
+}
+__host__ __device__ __forceinline__ int kv_share(int w, int total, int workers) {
+    return static_cast<int>(static_cast<int64_t>(w) * total / workers);
+}
+// The tile at which a boundary at x cuts an item that begins at `begin` (0 or tiles: not inside).
+__host__ __device__ __forceinline__ int kv_cut(const KvAttend &a, int begin, int tiles, int x) {
+    const int t = x - begin - kKvItemCost;
+    if (t <= a.snap) return 0;
+    return tiles - t <= a.snap ? tiles : t;
+}
+// First column of a piece in the workspace: of a worker's two, the one that begins its item goes second.
+__host__ __device__ __forceinline__ int64_t kv_piece(const KvAttend &a, int worker, bool begins) {
+    return (static_cast<int64_t>(worker) * 2 + (begins ? 1 : 0)) * a.split_cols;
 }
 
 hipError_t launch_kv_append(const KvCache &c, const KvBatch &s, const void *K, const void *V, int type,
