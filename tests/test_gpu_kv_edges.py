@@ -56,3 +56,41 @@ def test_more_rows_than_max_rows(awq, dim, per, max_rows):
     rows = np.concatenate([np.arange(start[b], start[b + 1]) for b in keep])
     some = np.concatenate(([0], np.cumsum([counts[b] for b in keep])))
     base.check(q[rows], "fp16", cache, got[rows.tolist()], lse[rows.tolist()], some, [lengths[b] for b in keep], table[keep])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim,group,rows", [(64, 64, 1), (128, 32, 5), (256, 128, 1), (64, 32, 40), (128, 128, 40), (256, 64, 40)])
+def test_weights_far_below_the_largest(awq, dim, group, rows, dtype):
+    """One key holds nearly all of the softmax and its value is zero: what is left is the sum of
+    thousands of weights of about 2^-26 of it.
+
+    P is fp16 and at least 2^7 for the largest weight of a wave's tokens, which is no larger than
+    the largest of all; so P's rounding is 2^-11 of P or, below fp16's normal range, 2^-25, which is
+    2^-32 of the largest weight w: over the tokens w * 2^-32 * sum |v'_t| at most.  An output
+    below fp16's normal range is off by 2^-25 more."""
+    rng = np.random.default_rng(dim + rows)
+    heads, per, page, n = 1, 8, 16, 3000
+    k = rng.uniform(-1, 1, (n, heads, dim)).astype(np.float32)
+    k[:, 0, 0] = 0.3 * rng.standard_normal(n)
+    k[0, 0, :], k[0, 0, 0] = 0.0, 18.0
+    v = rng.standard_normal((n, heads, dim)).astype(np.float32) + 1
+    v[0] = 0.0
+    table = rng.permutation(-(-n // page))[None]
+    cache = kv.Cache(table.size, heads, dim, group, page)
+    kv.append(cache, k, v, None, [n], table)
+    q = np.zeros((rows, heads * per, dim), np.float32)
+    q[:, :, 0] = 1 + np.arange(per) / 128
+    say("weights", dim, group, rows, dtype)
+    got, lse = base.attend(awq, q, dtype, cache, None, [n], table, scale=1.0)
+    o, want_lse, a, _ = kv.attention(cache, q, None, [n], table, scale=1.0)
+    values = np.abs(np.stack([cache.read(int(table[0, t // page]), t % page)[1][0] for t in range(n)]).astype(np.float64))
+    # a score is off by less than group * 2^-24 * 47 * step * sum |q|, the largest step being the first token's
+    e = group * 2.0 ** -24 * 47 * 18 / 15 * 1.2
+    low = 2.0 ** -32 * np.cumsum(values, 0)[n - rows:, None, :]   # (w <= 1)
+    tol = a * (2.0 ** -10 + 2 * e + 2 * n * 2.0 ** -24) + low
+    half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -11
+    tol = tol + half * (np.abs(o) + tol) + (2.0 ** -25 if dtype == "fp16" else 0)
+    assert (tol < 0.2 * a).all()   # (so that what is lost would be seen)
+    off = np.abs(got.double().cpu().numpy() - o)
+    assert (off <= tol).all(), (off / tol).max()
+    assert (np.abs(lse.double().cpu().numpy() - want_lse) <= e + 2.0 ** -22 * (np.abs(want_lse) + 1)).all()

@@ -15,10 +15,14 @@
 //    their lane.
 //  - O^T = V'^T·P^T in fp16: codes become fp16 by and-or (1024 + code, 64 + code),
 //    an exact packed subtraction, and one packed fma with (step, lo): v' is
-//    rounded once, to 11 bits.  P = exp2(S - m) <= 2^8 is rounded to 11 bits, too.
-//  - The softmax reference m of a query (shared by its 4 lanes) moves only when
-//    a score exceeds it by 2^8, so most steps need no cross-lane maximum and no
-//    rescaling.  Sums l and m stay in float32.
+//    rounded once, to 11 bits.  P = exp2(S - m) <= 2^15 is rounded to 11 bits, too.
+//  - The softmax reference m of a query (shared by its 4 lanes) is put 2^7 below the
+//    largest score (log2: 7 less) and moves only when one exceeds it by 2^15, so most
+//    steps need no cross-lane maximum and no rescaling, and the largest P is 2^7 or more:
+//    weights keep their 11 bits down to 2^-21 of the largest, and are off by 2^-32 of it
+//    below.  (With m at the largest score itself those bounds were 2^-14 and 2^-25, and a key
+//    that outweighs a long sequence 2^25 times made all of the others vanish.)  Sums l
+//    and m stay in float32.
 //
 // Masked scores are set to -inf after the product, so whatever a masked key holds
 // is dropped; value pairs of tokens that do not exist (behind the length, on a
@@ -31,7 +35,8 @@ namespace awq {
 namespace {
 
 constexpr float kLn2 = 0.693147180559945309f;
-constexpr float kLagLog2 = 8.0f;   // scores may exceed the reference by this (log2): P <= 2^8 fits fp16
+constexpr float kHeadLog2 = 7.0f;    // the reference lies this far below the largest score (log2) when it is set,
+constexpr float kMostLog2 = 15.0f;   // and scores may exceed it by this: P <= 2^15 fits fp16
 
 // (x & mask) | bits in one instruction: VOP3 takes no literals, so the empty asm
 // statements keep both constants in registers.  (The instruction itself is the
@@ -292,8 +297,8 @@ struct KvWave {
         for (int t = 0; t < NT; ++t) {
             const float top = fmaxf(fmaxf(fmaxf(x[0][t][0], x[0][t][1]), fmaxf(x[0][t][2], x[0][t][3])),
                                     fmaxf(fmaxf(x[1][t][0], x[1][t][1]), fmaxf(x[1][t][2], x[1][t][3])));
-            if (__any(top > m[t] + kLagLog2)) {
-                float now = fmaxf(m[t], top);
+            if (__any(top > m[t] + kMostLog2)) {
+                float now = fmaxf(m[t], top - kHeadLog2);
                 now = fmaxf(now, __shfl_xor(now, 16));
                 now = fmaxf(now, __shfl_xor(now, 32));
                 const float f = m[t] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[t] - now);
@@ -1006,8 +1011,8 @@ __device__ __forceinline__ void kv_wide_piece(const KvAttend &a, const KvUnit &u
                     top = e + r == 0 ? x[0][0] : fmaxf(top, x[e][r]);
                 }
         }
-        if (__any(top > (m == -INFINITY ? -INFINITY : kLagLog2))) {
-            float now = fmaxf(m, top + ref);
+        if (__any(top > (m == -INFINITY ? -INFINITY : kMostLog2))) {
+            float now = fmaxf(m, top + ref - kHeadLog2);
             now = fmaxf(now, __shfl_xor(now, 32));
             const float g = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - now);
             m = now;
