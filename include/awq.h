@@ -596,6 +596,8 @@ awq_status awq_kv_read(const awq_kv_cache *cache, const awq_kv_batch *batch, voi
  *   scale     > 0; S = scale * q.k'.
  *   causal    1: a row at position p sees positions <= p; 0: all of kv_len.
  *   window    > 0: and only positions > p - window (causal = 1); 0: no window.
+ *             Positions that no row of the call sees may lie in slots that were never
+ *             written.
  *   lse       device, [rows, q_heads] float32, the natural logarithm of the sum
  *             of exp S over what the row sees; may be NULL.
  * A row that sees nothing (kv_len 0, no position, no page) gets O = 0 and

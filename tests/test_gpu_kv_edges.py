@@ -94,3 +94,28 @@ def test_weights_far_below_the_largest(awq, dim, group, rows, dtype):
     off = np.abs(got.double().cpu().numpy() - o)
     assert (off <= tol).all(), (off / tol).max()
     assert (np.abs(lse.double().cpu().numpy() - want_lse) <= e + 2.0 ** -22 * (np.abs(want_lse) + 1)).all()
+
+
+@pytest.mark.parametrize("dim,group,page,rows", [(64, 64, 16, 1), (128, 32, 64, 5), (256, 64, 16, 1), (64, 32, 32, 90),
+                                                 (128, 128, 256, 90), (256, 128, 16, 70)])
+@pytest.mark.parametrize("window", [1, 40, 250])
+def test_slots_before_every_window(awq, dim, group, page, rows, window):
+    """Slots that no row's window reaches hold NaN bytes, as memory that was never written may (a
+    cache that was given the window's tokens alone): nothing of them is seen."""
+    rng = np.random.default_rng(dim + rows + window)
+    heads, per = 2, 4
+    lengths = [700, rows + window + 3, 333, 90, 1]
+    table, n_pages = base.table_for(lengths, page, rng)
+    cache = base.filled(rng, n_pages, heads, dim, group, page)
+    base.spoil(cache, table, lengths)
+    n = 4 * (dim // group)
+    for b, length in enumerate(lengths):
+        for t in range(max(0, length - rows - window + 1)):
+            for value in (0, 1):
+                at = cache.pair_at(value, t % page)
+                cache.bytes[table[b, t // page]][:, at:at + n] = 0xFF
+    q = base.queries(rng, (rows * len(lengths), heads * per, dim), "bf16")
+    say("before the window", dim, group, page, rows, window)
+    got, lse = base.attend(awq, q, "bf16", cache, None, lengths, table, window=window)
+    assert torch.isfinite(got).all()
+    base.check(q, "bf16", cache, got, lse, None, lengths, table, window=window)

@@ -26,7 +26,8 @@
 //
 // Masked scores are set to -inf after the product, so whatever a masked key holds
 // is dropped; value pairs of tokens that do not exist (behind the length, on a
-// page outside the cache) are zeroed, since 0 * NaN would not vanish.
+// page outside the cache) or that no row's window reaches are zeroed, since 0 * NaN
+// would not vanish.
 #pragma once
 
 #include "kv_internal.h"
@@ -177,13 +178,18 @@ __device__ __forceinline__ void kv_load(const KvAttend &a, int head, int tok, in
     load_words<NG>((kb & 1 ? pairs[1] : pairs[0]) + (kb >> 1) * P * (4 * NG) + n * (4 * NG), s.pair);
 }
 
-// A step's pairs into LDS.  Value pairs of tokens that do not exist become zero
-// (0 * NaN would not vanish).  One wave writes and reads them, in order.
+// Whether a position is one of lowest .. len - 1 (0 <= lowest <= len).
+__device__ __forceinline__ bool kv_seen(int p, int lowest, int len) {
+    return static_cast<uint32_t>(p - lowest) < static_cast<uint32_t>(len - lowest);
+}
+
+// A step's pairs into LDS.  Value pairs of tokens that do not exist, or that no row
+// sees, become zero (0 * NaN would not vanish).  One wave writes and reads them, in order.
 template <typename T, int D, int NG>
-__device__ __forceinline__ void kv_pairs(const KvAttend &a, const KvStep<D, NG> &s, int tok, int len, int lane,
-                                         KvPairs<NG> *lds) {
+__device__ __forceinline__ void kv_pairs(const KvAttend &a, const KvStep<D, NG> &s, int tok, int lowest, int len,
+                                         int lane, KvPairs<NG> *lds) {
     const int n = lane & 15, h = (lane >> 4) & 1;
-    const bool there = (h ? s.ok1 : s.ok0) && tok + 16 * h + n < len;
+    const bool there = (h ? s.ok1 : s.ok0) && kv_seen(tok + 16 * h + n, lowest, len);
     if (lane < 32) {
         float *k = reinterpret_cast<float *>(&lds->k[h][0][0][0]) + 2 * n;
 #pragma unroll
@@ -250,10 +256,10 @@ struct KvWave {
     }
 
     // Tokens tok .. tok+31.  edge: some of them may be hidden from some column.
-    __device__ __forceinline__ void step(const KvAttend &a, const KvStep<D, NG> &s, int tok, int len, bool edge,
-                                         int lane, KvPairs<NG> *lds) {
+    __device__ __forceinline__ void step(const KvAttend &a, const KvStep<D, NG> &s, int tok, int lowest, int len,
+                                         bool edge, int lane, KvPairs<NG> *lds) {
         const int kb = lane >> 4;
-        kv_pairs<T>(a, s, tok, len, lane, lds);
+        kv_pairs<T>(a, s, tok, lowest, len, lane, lds);
         floatx4 x[2][NT];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -362,8 +368,8 @@ struct KvWave {
     // (loads two or three tiles ahead cost registers and with them waves: 64 sequences of
     // up to 8192 tokens 31 -> 39 and 50 us).  minpos / maxlow: the first last-visible and
     // the last first-visible position of the columns.
-    __device__ __forceinline__ void run(const KvAttend &a, const int32_t *table, int head, int t0, int t1, int len,
-                                        int minpos, int maxlow, int lane, KvPairs<NG> *lds) {
+    __device__ __forceinline__ void run(const KvAttend &a, const int32_t *table, int head, int t0, int t1, int lowest,
+                                        int len, int minpos, int maxlow, int lane, KvPairs<NG> *lds) {
         if (t0 >= t1) return;
         KvStep<D, NG> now, then;
         int tok = t0 * kKvTile, p0 = -1, p1 = -1;
@@ -381,7 +387,7 @@ struct KvWave {
                 kv_load(a, head, next, p0, p1, lane, then);
                 pages(next + kKvTile);
             }
-            step(a, now, tok, len, hides(now, tok, minpos, maxlow), lane, lds);
+            step(a, now, tok, lowest, len, hides(now, tok, minpos, maxlow), lane, lds);
             tok = next;
             if (tok >= end) return;
             now = then;
@@ -520,8 +526,8 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(kv_split_wav
             w.start(a, it.head, it.r0, it.n, it.len, 0, lane);
             const int minpos = a.causal ? it.len - it.n : it.len - 1;
             const int maxlow = a.window ? it.len - a.window : 0;
-            w.run(a, a.s.table + static_cast<int64_t>(it.b) * a.s.max_pages, it.head, first + t0, first + t1, it.len,
-                  minpos, maxlow, lane, &pairs);
+            w.run(a, a.s.table + static_cast<int64_t>(it.b) * a.s.max_pages, it.head, first + t0, first + t1,
+                  kv_lowest(a, it.len, it.n), it.len, minpos, maxlow, lane, &pairs);
             const bool direct = t0 == 0 && t1 == it.tiles;
             if (direct) {
                 w.finish(a, it.head, it.r0, it.n, 0, lane);
@@ -693,7 +699,7 @@ struct KvWideLoad {
     uint32_t k[KW], kp, vp, v[VI][2];
     int k_id, v_id[VI];   // page numbers of the next tile, as the table holds them
     bool k_ok;
-    uint32_t v_there;        // all ones where this lane's token exists
+    uint32_t v_there;        // all ones where this lane's token exists and some row sees it
     uint4 pair[2];           // of the 8 tokens of a value piece being unpacked
     uint32_t lo[4], hi[4];
     int pair_from, pair_to, lost_to;
@@ -744,15 +750,15 @@ struct KvWideLoad {
     }
 
     // Keys, and both pairs of this lane's token.
-    __device__ __forceinline__ void load_keys(const KvAttend &a, int head, int tok, int len) {
+    __device__ __forceinline__ void load_keys(const KvAttend &a, int head, int tok, int lowest, int len) {
         const int P = 1 << a.c.page_shift, at = tok + 16 * key_block(), slot = at & (P - 1), n = threadIdx.x & 15;
         const unsigned char *p = block(a, head, k_id, at, len, k_ok);
         load_words<KW>(p + slot * (D / 2) + static_cast<uint32_t>(n * (D / 2) + chunk() * (4 * KW)), k);
         const unsigned char *r = p + P * D + slot * (4 * NG);
         kp = *reinterpret_cast<const uint32_t *>(r + static_cast<uint32_t>(pair_from));
         vp = *reinterpret_cast<const uint32_t *>(r + P * (4 * NG) + static_cast<uint32_t>(pair_from));
-        // a value that does not exist is worth zero (0 * NaN would not vanish)
-        v_there = at + n < len && k_ok ? ~0u : 0u;
+        // a value that does not exist, or that no row sees, is worth zero (0 * NaN would not vanish)
+        v_there = kv_seen(at + n, lowest, len) && k_ok ? ~0u : 0u;
     }
     __device__ __forceinline__ void load_values(const KvAttend &a, int head, int tok, int len) {
         const int P = 1 << a.c.page_shift;
@@ -821,7 +827,7 @@ __device__ __forceinline__ void kv_wide_piece(const KvAttend &a, const KvUnit &u
     constexpr int SUB = TT / 32;   // result tiles of 32 tokens x 32 columns a wave
     const int lane = threadIdx.x & 63, n32 = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r0 = unit.r0, n = unit.n, len = unit.len, p0 = len - n;
+    const int r0 = unit.r0, n = unit.n, len = unit.len, p0 = len - n, lowest = kv_lowest(a, len, n);
     const int last_col = n * a.per - 1, col0 = unit.col0 + wave * 32;
     const int32_t *table = a.s.table + static_cast<int64_t>(unit.b) * a.s.max_pages;
     auto row_of = [&](int c) { return (c < last_col ? c : last_col) / a.per; };
@@ -964,12 +970,12 @@ __device__ __forceinline__ void kv_wide_piece(const KvAttend &a, const KvUnit &u
         };
         in.key_page(a, table, t0 * TT, len);
         in.value_pages(a, table, t0 * TT, len);
-        in.load_keys(a, head, t0 * TT, len);
+        in.load_keys(a, head, t0 * TT, lowest, len);
         in.load_values(a, head, t0 * TT, len);
         in.key_page(a, table, (t0 + 1) * TT, len);
         in.value_pages(a, table, (t0 + 1) * TT, len);
         keys(t0);
-        in.load_keys(a, head, (t0 + 1) * TT, len);
+        in.load_keys(a, head, (t0 + 1) * TT, lowest, len);
         in.key_page(a, table, (t0 + 2) * TT, len);
         __syncthreads();   // the pairs of V(t0)
 #pragma unroll
@@ -980,7 +986,7 @@ __device__ __forceinline__ void kv_wide_piece(const KvAttend &a, const KvUnit &u
         in.load_values(a, head, (t0 + 1) * TT, len);
         in.value_pages(a, table, (t0 + 2) * TT, len);
         keys(t0 + 1);
-        in.load_keys(a, head, (t0 + 2) * TT, len);
+        in.load_keys(a, head, (t0 + 2) * TT, lowest, len);
         in.key_page(a, table, (t0 + 3) * TT, len);
         __syncthreads();
         start_scores(t0);
@@ -1073,7 +1079,7 @@ __device__ __forceinline__ void kv_wide_piece(const KvAttend &a, const KvUnit &u
             if (slot < in.KW) in.template unpack_key<T>(slot, ks[buf]);
             if (slot == in.KW) {
                 in.template unpack_pair<T>(a, pairs[w3], vpairs[buf], lost[w3]);
-                in.load_keys(a, head, tok + 3 * TT, len);
+                in.load_keys(a, head, tok + 3 * TT, lowest, len);
             }
             // value parts from slot kFirst, every kEach
             constexpr int kFirst = in.KW + 1, kEach = (kSlots - kFirst - 3) / (4 * in.VI);

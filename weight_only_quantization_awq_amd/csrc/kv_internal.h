@@ -146,11 +146,17 @@ constexpr int kv_split_waves(int dim, int nt) {
     return nt * dim <= 64 ? 4 : nt * dim <= 128 ? 3 : nt * dim <= 256 ? 2 : 1;
 }
 
-// The split path's line (kv_attend.h).
-__host__ __device__ __forceinline__ int kv_first_token(const KvAttend &a, int len, int n) {
+// First position that any of a sequence's rows sees: what lies before it is treated as
+// what lies behind its length, whatever its slots hold.
+__host__ __device__ __forceinline__ int kv_lowest(const KvAttend &a, int len, int n) {
     if (!a.window) return 0;
     const int low = len - n - a.window + 1;
-    return low > 0 ? low & ~(kKvTile - 1) : 0;
+    return low > 0 ? low : 0;
+}
+
+// The split path's line (kv_attend.h).
+__host__ __device__ __forceinline__ int kv_first_token(const KvAttend &a, int len, int n) {
+    return kv_lowest(a, len, n) & ~(kKvTile - 1);
 }
 // Tiles of an item of sequence b; 0: not on the split path.
 __host__ __device__ __forceinline__ int kv_item_tiles(const KvAttend &a, int b, int &r0, int &n, int &len) {
