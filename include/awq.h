@@ -594,13 +594,15 @@ awq_status awq_kv_read(const awq_kv_cache *cache, const awq_kv_batch *batch, voi
  *             given.  A sequence with more rows gets them unspecified
  *             (nothing outside O, lse and workspace is written).  Ignored without row_start.
  *   scale     > 0; S = scale * q.k'.
- *   causal    1: a row at position p sees positions <= p; 0: all of kv_len.
+ *   causal    1: a row at position p sees positions <= p; 0: every row sees all of
+ *             kv_len, those without a position too (n > kv_len: queries of one
+ *             sequence over the keys of another).
  *   window    > 0: and only positions > p - window (causal = 1); 0: no window.
  *             Positions that no row of the call sees may lie in slots that were never
  *             written.
  *   lse       device, [rows, q_heads] float32, the natural logarithm of the sum
  *             of exp S over what the row sees; may be NULL.
- * A row that sees nothing (kv_len 0, no position, no page) gets O = 0 and
+ * A row that sees nothing (kv_len 0, no page, with causal = 1 no position) gets O = 0 and
  * lse = -inf.  Products and sums are float32; a softmax weight enters the second
  * product as fp16, off by 2^-11 of itself at most or, where it is below 2^-21 of the
  * row's largest, by 2^-32 of that; v' enters as fp16.  Results are deterministic.

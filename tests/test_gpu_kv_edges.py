@@ -119,3 +119,26 @@ def test_slots_before_every_window(awq, dim, group, page, rows, window):
     got, lse = base.attend(awq, q, "bf16", cache, None, lengths, table, window=window)
     assert torch.isfinite(got).all()
     base.check(q, "bf16", cache, got, lse, None, lengths, table, window=window)
+
+
+@pytest.mark.parametrize("rows", [9, 95])
+def test_rows_without_a_position(awq, rows):
+    """More rows than the sequence has positions: with causal = 1 the first ones see nothing, with
+    causal = 0 every row sees all positions, so equal queries get equal rows."""
+    rng = np.random.default_rng(rows)
+    heads, per, dim, group, page, length = 2, 4, 128, 64, 16, 7
+    table = np.array([[1, 0]])
+    cache = base.filled(rng, 2, heads, dim, group, page)
+    base.spoil(cache, table, [length])
+    q = np.repeat(base.queries(rng, (1, heads * per, dim), "fp16"), rows, 0)
+    say("no position", rows)
+    got, lse = base.attend(awq, q, "fp16", cache, None, [length], table, fill=3.0)
+    base.check(q, "fp16", cache, got, lse, None, [length], table)
+    assert (got[:rows - length] == 0).all() and torch.isneginf(lse[:rows - length]).all()
+    assert torch.isfinite(lse[rows - length:]).all()
+    free, free_lse = base.attend(awq, q, "fp16", cache, None, [length], table, fill=3.0, causal=False)
+    base.check(q, "fp16", cache, free, free_lse, None, [length], table, causal=False)
+    assert torch.isfinite(free_lse).all()
+    assert torch.equal(free, free[-1:].expand_as(free)) and torch.equal(free_lse, free_lse[-1:].expand_as(free_lse))
+    # the last row sees the same either way
+    assert torch.equal(free[-1], got[-1])

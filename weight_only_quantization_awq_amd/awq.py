@@ -687,6 +687,7 @@ def kv_attention(Q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, kv_
     a row sees its own position).  ``max_rows``: an upper bound on any
     sequence's rows, known on the host; give it with ``row_start``.  ``scale``
     defaults to dim ** -0.5.  ``window`` > 0: only the last ``window`` positions.
+    Without ``causal`` every row sees all ``kv_len[b]`` positions, whatever its own.
     ``workspace``: uint8 of :func:`kv_attention_workspace_size` bytes (None
     allocates it).  Returns the output like Q, and with ``want_lse`` also the
     float32 log-sum-exp [rows, q_heads] (-inf, and output 0, where a row sees
