@@ -142,3 +142,81 @@ def test_rows_without_a_position(awq, rows):
     assert torch.equal(free, free[-1:].expand_as(free)) and torch.equal(free_lse, free_lse[-1:].expand_as(free_lse))
     # the last row sees the same either way
     assert torch.equal(free[-1], got[-1])
+
+
+@pytest.mark.parametrize("dim,group", [(64, 32), (64, 64), (128, 32), (128, 128), (256, 64), (256, 128)])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_lse_after_far_lower_scores(awq, dim, group, rows):
+    """The first 128 scores lie at -20000, the others around 0 and alone count: lse is as exact as
+    they are.
+
+    A later score's key has |k'| < 2 and one channel that counts (q = 1), its step is below 0.25:
+    e < group * 2^-24 * 47 * 0.25 + 6 * 2^-24 * 2.  The wide path forms it relative to a reference
+    of -64 (log2) at the lowest, so |S - ref| < 128 and its rounding is 2^-18; one more such
+    rounding moves it to its own reference: ln 2 * 2^-17 in all."""
+    rng = np.random.default_rng(dim + group + rows)
+    heads, per, page, n = 1, 8, 16, 128 + rows
+    k = rng.uniform(-1, 1, (n, heads, dim)).astype(np.float32)
+    k[:128] = 0.0
+    k[:128, 0, 0] = -20000.0
+    v = rng.standard_normal((n, heads, dim)).astype(np.float32)
+    table = rng.permutation(-(-n // page))[None]
+    cache = kv.Cache(table.size, heads, dim, group, page)
+    kv.append(cache, k, v, None, [n], table)
+    q = np.zeros((rows, heads * per, dim), np.float32)
+    q[:, :, 0] = 1.0
+    say("after lower scores", dim, group, rows)
+    got, lse = base.attend(awq, q, "bf16", cache, None, [n], table, scale=1.0)
+    o, want, a, _ = kv.attention(cache, q, None, [n], table, scale=1.0)
+    e = group * 2.0 ** -24 * 47 * 0.25 + 6 * 2.0 ** -24 * 2 + np.log(2) * 2.0 ** -17
+    off = np.abs(lse.double().cpu().numpy() - want)
+    assert (off <= e + 2.0 ** -22 * (np.abs(want) + 1)).all(), off.max()
+    tol = a * (2.0 ** -10 + 2 * e + 2 * n * 2.0 ** -24)
+    assert (np.abs(got.double().cpu().numpy() - o) <= tol + 2.0 ** -8 * (np.abs(o) + tol)).all()
+
+
+@pytest.mark.parametrize("dim,group", [(64, 32), (128, 32), (128, 64), (256, 64)])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_scores_that_are_all_very_low(awq, dim, group, rows):
+    """Every score is about -20000: what counts are their differences, from another group of
+    channels.  A score is off by 8 roundings of 20000 * log2(e) at most, next to the second group's
+    own (|k'| and |q| of its one channel below 4, its step below 0.5)."""
+    rng = np.random.default_rng(dim + rows)
+    heads, per, page, n = 1, 8, 16, 700
+    k = rng.uniform(-1, 1, (n, heads, dim)).astype(np.float32)
+    k[:, 0, :group] = -20000.0
+    k[:, 0, group] *= 3
+    v = rng.standard_normal((n, heads, dim)).astype(np.float32)
+    table = rng.permutation(-(-n // page))[None]
+    cache = kv.Cache(table.size, heads, dim, group, page)
+    kv.append(cache, k, v, None, [n], table)
+    q = np.zeros((rows, heads * per, dim), np.float32)
+    q[:, :, 0] = 1.0
+    q[:, :, group] = np.linspace(0, 1, per)
+    say("low scores", dim, group, rows)
+    got, lse = base.attend(awq, q, "bf16", cache, None, [n], table, scale=1.0)
+    o, want, a, _ = kv.attention(cache, q, None, [n], table, scale=1.0)
+    e = 8 * 2.0 ** -24 * 20000 + group * 2.0 ** -24 * 47 * 0.5 + 6 * 2.0 ** -24 * 4
+    assert (np.abs(lse.double().cpu().numpy() - want) <= e + 2.0 ** -22 * np.abs(want)).all()
+    tol = a * (2.0 ** -10 + 2 * e + 2 * n * 2.0 ** -24)
+    assert (np.abs(got.double().cpu().numpy() - o) <= tol + 2.0 ** -8 * (np.abs(o) + tol)).all()
+
+
+@pytest.mark.parametrize("dim,group", [(64, 64), (128, 64), (256, 32)])
+def test_chunk_of_rising_scores(awq, dim, group):
+    """Many rows, so the wide path: scores that rise or fall along the sequence by far more than a
+    reference lets them, and equal ones."""
+    rng = np.random.default_rng(dim)
+    heads, per, page, length, rows = 1, 4, 64, 900, 70
+    table = np.arange(15)[None]
+    k = rng.standard_normal((length, 1, dim)).astype(np.float32)
+    k[:, 0, 0] = np.linspace(-60, 60, length)
+    v = rng.standard_normal((length, 1, dim)).astype(np.float32)
+    cache = kv.Cache(15, heads, dim, group, page)
+    kv.append(cache, k, v, None, [length], table)
+    q = np.zeros((rows, per, dim))
+    q[:, 0, 0], q[:, 1, 0], q[:, 2, :] = 8.0, -8.0, -0.5
+    for dtype in ("bf16", "fp16"):
+        say("rising", dim, group, dtype)
+        got, lse = base.attend(awq, q, dtype, cache, None, [length], table, scale=1.0)
+        base.check(q, dtype, cache, got, lse, None, [length], table, scale=1.0)

@@ -38,6 +38,7 @@ namespace {
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kHeadLog2 = 7.0f;    // the reference lies this far below the largest score (log2) when it is set,
 constexpr float kMostLog2 = 15.0f;   // and scores may exceed it by this: P <= 2^15 fits fp16
+constexpr float kFloorLog2 = 64.0f;  // the wide path's scores are formed relative to no less than -64
 
 // (x & mask) | bits in one instruction: VOP3 takes no literals, so the empty asm
 // statements keep both constants in registers.  (The instruction itself is the
@@ -841,7 +842,10 @@ __device__ __forceinline__ void kv_wide_piece(const KvAttend &a, const KvUnit &u
     const bool real = row < n;
     const int pos = real ? (a.causal ? p0 + row : len - 1) : -1, low = a.window ? p0 + row - a.window + 1 : 0;
     vec8 q[S];
-    float qs[NG], m = -INFINITY, l = 0.0f, top = -INFINITY, ref = 0.0f;   // ref: m, or 0 before there is one
+    // Scores x are formed relative to ref: m, but no less than -kFloorLog2, and 0 before there is one.  Where m is
+    // lower, limit sends every tile through the shift to m.  (x carries 2^-24 of its distance from ref: relative
+    // to an m of -1000, later scores around 0 put lse off by 1e-5; now it is 2^-24 * (|S| + kFloorLog2) at most.)
+    float qs[NG], m = -INFINITY, l = 0.0f, top = -INFINITY, ref = 0.0f, limit = -INFINITY;
     floatx16 o[J];
     {
         const T *src = static_cast<const T *>(a.Q) + (r0 + (real ? row : 0)) * a.q_stride +
@@ -1017,13 +1021,14 @@ __device__ __forceinline__ void kv_wide_piece(const KvAttend &a, const KvUnit &u
                     top = e + r == 0 ? x[0][0] : fmaxf(top, x[e][r]);
                 }
         }
-        if (__any(top > (m == -INFINITY ? -INFINITY : kMostLog2))) {
+        if (__any(top > limit)) {
             float now = fmaxf(m, top + ref - kHeadLog2);
             now = fmaxf(now, __shfl_xor(now, 32));
             const float g = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - now);
             m = now;
             const float back = (now == -INFINITY ? 0.0f : now) - ref;
-            ref += back;
+            ref = now == -INFINITY ? 0.0f : fmaxf(now, -kFloorLog2);
+            limit = now < -kFloorLog2 ? -INFINITY : kMostLog2;
             l *= g;
 #pragma unroll
             for (int e = 0; e < SUB; ++e)
