@@ -32,3 +32,15 @@ def test_every_piece_has_its_own_place(tmp_path):
     r = subprocess.run([exe], capture_output=True, text=True, env=env, timeout=300)
     assert r.returncode == 0, (r.stdout[-3000:], r.stderr[-3000:])
     assert "pieces in their places" in r.stdout
+
+
+@pytest.mark.timeout(600)
+def test_schedule_of_the_wide_path(tmp_path):
+    if not os.path.exists(HIPCC):
+        pytest.skip("ROCm toolchain not present")
+    exe = str(tmp_path / "kv_schedule_driver")
+    r = subprocess.run([HIPCC, *BASE, "-I", CSRC, os.path.join(ROOT, "tests", "sanitizer", "kv_schedule_driver.cpp"), "-o", exe],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and "schedules hold" in r.stdout, r.stdout

@@ -697,6 +697,16 @@ __device__ __forceinline__ int kv_wide_cut(int at, int tiles) {
 template <int D, int NG, int THREADS>
 struct KvWideLoad {
     static constexpr int J = D / 32, TT = kv_wide_tile(D), KW = TT * D / 8 / THREADS, VI = TT * D / 16 / THREADS;
+    // What is done under each MFMA of the second product: the key words and pairs in the first
+    // KW + 1 slots, then the 4 parts of each value piece, evenly spread; a piece's pairs are read
+    // at the end of the slot before its first part.  -1: none in this slot.
+    static constexpr int kSlots = TT / 32 * (D / 16), kFirst = KW + 1, kEach = (kSlots - kFirst - 3) / (4 * VI);
+    static constexpr int part_at(int slot) {
+        const int x = slot - kFirst;
+        return x >= 0 && x % kEach == 0 && x / kEach < 4 * VI ? x / kEach : -1;
+    }
+    static constexpr int pairs_at(int slot) { return part_at(slot + 1) >= 0 && part_at(slot + 1) % 4 == 0 ? part_at(slot + 1) / 4 : -1; }
+    static constexpr int kLoad = kFirst + kEach * (4 * VI - 1) + 1;   // the slot of the next loads, behind the last part
     uint32_t k[KW], kp, vp, v[VI][2];
     int k_id, v_id[VI];   // page numbers of the next tile, as the table holds them
     bool k_ok;
@@ -1086,13 +1096,9 @@ __device__ __forceinline__ void kv_wide_piece(const KvAttend &a, const KvUnit &u
                 in.template unpack_pair<T>(a, pairs[w3], vpairs[buf], lost[w3]);
                 in.load_keys(a, head, tok + 3 * TT, lowest, len);
             }
-            // value parts from slot kFirst, every kEach
-            constexpr int kFirst = in.KW + 1, kEach = (kSlots - kFirst - 3) / (4 * in.VI);
-            if (slot >= kFirst && (slot - kFirst) % kEach == 0 && (slot - kFirst) / kEach < 4 * in.VI)
-                in.unpack_value((slot - kFirst) / kEach / 4, (slot - kFirst) / kEach % 4, vs[buf ^ 1]);
-            if ((slot + 1 - kFirst) % (4 * kEach) == 0 && (slot + 1 - kFirst) / (4 * kEach) < in.VI)
-                in.read_pairs((slot + 1 - kFirst) / (4 * kEach), vpairs[buf ^ 1]);
-            if (slot == kFirst + kEach * (4 * in.VI - 1) + 1) in.load_values(a, head, tok + 2 * TT, len);
+            if (in.part_at(slot) >= 0) in.unpack_value(in.part_at(slot) / 4, in.part_at(slot) % 4, vs[buf ^ 1]);
+            if (in.pairs_at(slot) >= 0) in.read_pairs(in.pairs_at(slot), vpairs[buf ^ 1]);
+            if (slot == in.kLoad) in.load_values(a, head, tok + 2 * TT, len);
             if (slot == kSlots - 1) {
                 in.key_page(a, table, tok + 4 * TT, len);
                 in.value_pages(a, table, tok + 3 * TT, len);
