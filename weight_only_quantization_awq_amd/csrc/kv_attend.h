@@ -184,12 +184,22 @@ __device__ __forceinline__ bool kv_seen(int p, int lowest, int len) {
     return static_cast<uint32_t>(p - lowest) < static_cast<uint32_t>(len - lowest);
 }
 
+// Orders a wave's LDS accesses for its own lanes: what one lane wrote, another reads, as other
+// types (float and uint16_t, read as vectors), so nothing else keeps the compiler from moving
+// either.  LDS itself runs a wave's accesses in turn: no instruction comes of this.
+__device__ __forceinline__ void kv_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // A step's pairs into LDS.  Value pairs of tokens that do not exist, or that no row
 // sees, become zero (0 * NaN would not vanish).  One wave writes and reads them, in order.
 template <typename T, int D, int NG>
 __device__ __forceinline__ void kv_pairs(const KvAttend &a, const KvStep<D, NG> &s, int tok, int lowest, int len,
                                          int lane, KvPairs<NG> *lds) {
     const int n = lane & 15, h = (lane >> 4) & 1;
+    kv_lds_order();   // the tile before has been read
     const bool there = (h ? s.ok1 : s.ok0) && kv_seen(tok + 16 * h + n, lowest, len);
     if (lane < 32) {
         float *k = reinterpret_cast<float *>(&lds->k[h][0][0][0]) + 2 * n;
@@ -209,7 +219,7 @@ __device__ __forceinline__ void kv_pairs(const KvAttend &a, const KvStep<D, NG> 
             v[32 * g + 4] = static_cast<uint16_t>(p >> 16);
         }
     }
-    __builtin_amdgcn_wave_barrier();   // (the compiler's order; LDS runs a wave's accesses in turn)
+    kv_lds_order();
 }
 
 // One wave's 16*NT columns: queries, running sums, output.
