@@ -220,3 +220,36 @@ def test_chunk_of_rising_scores(awq, dim, group):
         say("rising", dim, group, dtype)
         got, lse = base.attend(awq, q, dtype, cache, None, [length], table, scale=1.0)
         base.check(q, dtype, cache, got, lse, None, [length], table, scale=1.0)
+
+
+def test_pages_that_are_given_other_memory(awq):
+    """A cache whose pages move to a larger pool goes on there, and the old memory stays as it was;
+    without memory the calls are refused."""
+    rng = np.random.default_rng(31)
+    heads, per, dim, group, page, n = 2, 4, 64, 32, 16, 40
+    table, lengths = np.array([[1, 0, 2]]), [n]
+    k, kd = base.values(rng, (n, heads, dim), "bf16")
+    v, vd = base.values(rng, (n, heads, dim), "bf16")
+    c = awq.kv_cache(3, heads, dim, group, page)
+    old = c.pages.detach()
+    larger = torch.zeros((5,) + tuple(old.shape[1:]), dtype=torch.uint8, device="cuda")
+    say("other memory")
+    awq.kv_append(c, kd[:20], vd[:20], base.ints(table), base.ints([20]))
+    was = old.clone()
+    larger[:3].copy_(old)
+    c.pages.set_(larger)
+    awq.kv_append(c, kd[20:], vd[20:], base.ints(table), base.ints(lengths))
+    cache = kv.Cache(5, heads, dim, group, page)
+    kv.append(cache, k, v, None, lengths, table)
+    assert torch.equal(old, was)
+    assert np.array_equal(larger.cpu().numpy(), cache.bytes)
+    q = base.queries(rng, (1, heads * per, dim), "bf16")
+    got, lse = awq.kv_attention(torch.from_numpy(q).bfloat16().cuda(), c, base.ints(table), base.ints(lengths), want_lse=True)
+    base.check(q, "bf16", cache, got, lse, None, lengths, table)
+    larger.untyped_storage().resize_(0)
+    for call in (lambda: awq.kv_append(c, kd, vd, base.ints(table), base.ints(lengths)),
+                 lambda: awq.kv_read(c, base.ints(table), base.ints(lengths), n),
+                 lambda: awq.kv_attention(torch.zeros(1, 8, dim, dtype=torch.bfloat16, device="cuda"), c, base.ints(table),
+                                          base.ints(lengths))):
+        with pytest.raises(ValueError):
+            call()

@@ -522,7 +522,8 @@ class KvCache:
     """A pool of pages of 4-bit keys and values (include/awq.h: awq_kv_cache).
 
     ``pages`` is uint8 [n_pages, heads, block]; the pages may lie apart (a slice
-    of a larger pool), each one contiguous.  :func:`kv_cache` makes one.
+    of a larger pool), each one contiguous.  :func:`kv_cache` makes one.  Calls use the
+    memory that ``pages`` has at the time: it may be given other storage (``set_``).
     """
     pages: torch.Tensor
     dim: int           # channels of a head: 64, 128 or 256
@@ -540,7 +541,12 @@ class KvCache:
         if p.stride(2) != 1 or p.stride(1) != block:
             raise ValueError("each page must be contiguous")
         stride = p.stride(0) if n > 1 else size    # torch gives a single page any stride
+        end = p.storage_offset() + (n - 1) * stride + size if n else 0
+        if p.untyped_storage().nbytes() < end:
+            raise ValueError("the memory of the pages has been given up, or is smaller than they are")
         object.__setattr__(self, "_c", _KvCacheC(p.data_ptr(), n, stride, heads, self.dim, self.group, self.page))
+        object.__setattr__(self, "_at", p.data_ptr())
+        object.__setattr__(self, "_ptr", p.data_ptr)
         object.__setattr__(self, "_device", p.device)
         object.__setattr__(self, "heads", heads)
 
@@ -558,6 +564,14 @@ def kv_cache(n_pages: int, heads: int, dim: int, group: int = 128, page: int = 1
     """A pool of ``n_pages`` pages (all zero, which reads back as zero)."""
     block = kv_page_size(page, heads, dim, group) // heads
     return KvCache(torch.zeros(n_pages, heads, block, dtype=torch.uint8, device=device), dim, group, page)
+
+
+def _kv_pool(cache: KvCache):
+    """The cache's C struct and its device, anew where the pages' memory is no longer where it was
+    (0.15 us; resizing storage, smaller or larger, moves it)."""
+    if cache._ptr() != cache._at:
+        cache.__post_init__()
+    return cache._c, cache._device
 
 
 def _kv_rows(x: torch.Tensor, name: str, device, shape) -> tuple[int, int]:
@@ -627,7 +641,7 @@ def kv_append(cache: KvCache, K: torch.Tensor, V: torch.Tensor, block_table: tor
     for each sequence without ``row_start``) and become the last of its ``kv_len[b]``
     positions; position p lies in page ``block_table[b, p // page]``.
     """
-    dev = cache._device
+    c, dev = _kv_pool(cache)
     rows = K.shape[0]
     shape = (rows, cache.heads, cache.dim)
     if V.dtype != K.dtype:
@@ -635,7 +649,7 @@ def kv_append(cache: KvCache, K: torch.Tensor, V: torch.Tensor, block_table: tor
     b = _kv_batch(dev, block_table, kv_len, row_start, rows)
     k, k_stride = _kv_rows(K, "K", dev, shape)
     v, v_stride = _kv_rows(V, "V", dev, shape)
-    _kv_call(dev, _lib.awq_kv_append, cache._c, b, k, v, _kv_type(K.dtype), k_stride, v_stride)
+    _kv_call(dev, _lib.awq_kv_append, c, b, k, v, _kv_type(K.dtype), k_stride, v_stride)
 
 
 def kv_read(cache: KvCache, block_table: torch.Tensor, kv_len: torch.Tensor, rows: int,
@@ -647,7 +661,7 @@ def kv_read(cache: KvCache, block_table: torch.Tensor, kv_len: torch.Tensor, row
     sequence, all of them where its rows are ``kv_len[b]``.  Rows that belong to
     no sequence are left as they were in ``out`` (unspecified in new tensors).
     """
-    dev = cache._device
+    c, dev = _kv_pool(cache)
     shape = (rows, cache.heads, cache.dim)
     b = _kv_batch(dev, block_table, kv_len, row_start, rows)
     if out is None:
@@ -657,7 +671,7 @@ def kv_read(cache: KvCache, block_table: torch.Tensor, kv_len: torch.Tensor, row
         raise TypeError("both outputs must have one dtype")
     k, k_stride = _kv_rows(K, "K", dev, shape)
     v, v_stride = _kv_rows(V, "V", dev, shape)
-    _kv_call(dev, _lib.awq_kv_read, cache._c, b, k, v, _kv_type(K.dtype), k_stride, v_stride)
+    _kv_call(dev, _lib.awq_kv_read, c, b, k, v, _kv_type(K.dtype), k_stride, v_stride)
     return K, V
 
 
@@ -693,7 +707,7 @@ def kv_attention(Q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, kv_
     float32 log-sum-exp [rows, q_heads] (-inf, and output 0, where a row sees
     nothing).
     """
-    dev = cache._device
+    c, dev = _kv_pool(cache)
     rows, q_heads = Q.shape[0], Q.shape[1]
     shape = (rows, q_heads, cache.dim)
     dtype = Q.dtype
@@ -712,10 +726,10 @@ def kv_attention(Q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, kv_
     if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != dev
                                   or not workspace.is_contiguous()):
         raise ValueError("workspace must be contiguous uint8 on the cache's GPU")
-    need = _kv_workspace(cache._c, b, q_heads, max_rows or 0)
+    need = _kv_workspace(c, b, q_heads, max_rows or 0)
     if need and (workspace is None or workspace.numel() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _kv_call(dev, _lib.awq_kv_attention, cache._c, b, q, _KV_TYPES[dtype], q_heads, q_stride, max_rows or 0,
+    _kv_call(dev, _lib.awq_kv_attention, c, b, q, _KV_TYPES[dtype], q_heads, q_stride, max_rows or 0,
              cache.dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, o, o_stride,
              lse.data_ptr() if want_lse else None, workspace.data_ptr() if need else None,
              workspace.numel() if need else 0)
