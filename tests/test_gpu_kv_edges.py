@@ -253,3 +253,77 @@ def test_pages_that_are_given_other_memory(awq):
                                           base.ints(lengths))):
         with pytest.raises(ValueError):
             call()
+
+
+def lse_errors(awq, dim, group, rows, dtype, off_centre, n=65, heads=8, per=4, page=16):
+    """Root mean squares, over all rows: the error of lse, that of the same formula in float32, and the one
+    that the base in the key codes accounts for.  All against float64 over the values that are read back.
+
+    The last: codes enter as 16 + c, so a group's sum over 32 channels at a time passes through
+    partial sums of (16 + c) q, each rounded to float32 (at most half an ulp, evenly spread: 2^-24 / sqrt 3
+    of it), times the step; the base's part of the lowest value, (lo - 16 step) * sum q, takes two
+    such roundings.  A row's lse is off by the weighted mean of its scores' errors."""
+    batch = 8 if rows == 1 else 2
+    t = base.TYPES[dtype]
+    g = torch.Generator("cuda").manual_seed(dim + group + rows)
+
+    def draw(*shape):
+        return torch.randn(*shape, generator=g, device="cuda")
+
+    def tokens():
+        x = draw(batch * n, heads, dim)
+        if off_centre:   # as projections give keys: some channels large and far from 0
+            size = torch.exp(1.5 * draw(heads, dim) - 0.5)
+            x = 1.5 * draw(heads, dim) * size + x * size
+        return x.to(t)
+
+    pages = -(-n // page)
+    cache = awq.kv_cache(batch * pages, heads, dim, group, page)
+    table = torch.randperm(batch * pages, generator=g, device="cuda").int().view(batch, pages)
+    length = base.ints([n] * batch)
+    awq.kv_append(cache, tokens(), tokens(), table, length)
+    q = draw(batch * rows, heads * per, dim).to(t)
+    say("lse", dim, group, rows, dtype, off_centre)
+    _, lse = awq.kv_attention(q, cache, table, length, want_lse=True)
+    key = awq.kv_read(cache, table, length, batch * n, dtype=torch.float32)[0].view(batch, n, heads, dim).transpose(1, 2)
+    hidden = torch.arange(n, device="cuda") > torch.arange(n - rows, n, device="cuda")[:, None]
+
+    def scores(kind):
+        x = q.to(kind).view(batch, rows, heads, per, dim).permute(0, 2, 1, 3, 4).reshape(batch, heads, rows * per, dim)
+        s = torch.matmul(x, key.to(kind).transpose(-1, -2).contiguous()) * dim ** -0.5
+        return s.view(batch, heads, rows, per, n).masked_fill(hidden[:, None], -float("inf"))
+
+    s = scores(torch.float64)
+    want, single = torch.logsumexp(s, -1), torch.logsumexp(scores(torch.float32), -1)
+    ng, blocks = dim // group, cache.pages[table.long()].cpu().numpy()   # [batch, pages, heads, bytes]
+    pair = np.ascontiguousarray(blocks[..., page * dim:page * dim + 4 * page * ng]).view(np.float16)
+    pair = torch.from_numpy(pair.reshape(batch, pages, heads, page, ng, 2).astype(np.float64)).cuda()
+    pair = pair.permute(0, 2, 1, 3, 4, 5).reshape(batch, heads, pages * page, ng, 2)[:, :, :n]
+    step, lo = pair[..., 0], pair[..., 1]
+    code = ((key.double().unflatten(-1, (ng, group)) - lo[..., None]) / step.clamp_min(1e-9)[..., None]).round()
+    x = q.double().view(batch, rows, heads, per, ng, group // 32, 32).permute(0, 2, 1, 3, 4, 5, 6)   # [b, h, rows, per, ng, k, 32]
+    y = (16 + code).unflatten(-1, (-1, 32))                                                       # [b, h, n, ng, k, 32]
+    variance = torch.zeros_like(s)
+    for i in range(ng):
+        total = 0.0
+        for k in range(group // 32):
+            total = total + torch.matmul(x[:, :, :, :, i, k].flatten(2, 3), y[:, :, :, i, k].transpose(-1, -2).contiguous())
+            variance += (total * step[:, :, None, :, i]).square().view(s.shape)
+        low = (lo - 16 * step)[:, :, None, None, :, i] * x[:, :, :, :, i].sum((-1, -2))[..., None]
+        variance += 2 * low.square()
+    weight = torch.softmax(s, -1)
+    model = (weight.square() * variance).sum(-1) * (2.0 ** -48 / 3 / dim)
+    got = lse.double().view(batch, rows, heads, per).transpose(1, 2)
+    return tuple(float(v.mean().sqrt()) for v in ((got - want).square(), (single.double() - want).square(), model))
+
+
+@pytest.mark.parametrize("off_centre", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim,group", [(64, 32), (128, 32), (128, 128), (256, 64), (256, 128)])
+@pytest.mark.parametrize("rows", [1, 64])
+def test_lse_is_as_exact_as_float32_and_its_base(awq, dim, group, rows, dtype, off_centre):
+    """Not above what float32 arithmetic and the base of 16 account for (a base of 64 costs 3 times as
+    much), both with 1.3 for a sample's spread."""
+    error, single, model = lse_errors(awq, dim, group, rows, dtype, off_centre)
+    say("error %.2e float32 %.2e base %.2e" % (error, single, model))
+    assert error <= 1.3 * np.hypot(single, model)
