@@ -603,9 +603,12 @@ awq_status awq_kv_read(const awq_kv_cache *cache, const awq_kv_batch *batch, voi
  *   lse       device, [rows, q_heads] float32, the natural logarithm of the sum
  *             of exp S over what the row sees; may be NULL.
  * A row that sees nothing (kv_len 0, no page, with causal = 1 no position) gets O = 0 and
- * lse = -inf.  Products and sums are float32; a softmax weight enters the second
- * product as fp16, off by 2^-11 of itself at most or, where it is below 2^-21 of the
- * row's largest, by 2^-32 of that; v' enters as fp16.  Results are deterministic.
+ * lse = -inf.  Products and sums are float32.  A key's codes enter them as 16 + code:
+ * where the channels of a group lie far apart, scores and lse are off by up to 7
+ * times what float32 products of the values would leave.  A softmax weight enters the
+ * second product as fp16, off by 2^-11 of itself at most or, where it is below 2^-21
+ * of the row's largest, by 2^-32 of that; v' enters as fp16.  Results are
+ * deterministic.
  *   workspace device, 16-byte aligned, at least awq_kv_attention_workspace_size(...)
  *             bytes (0: none needed, or invalid arguments, for which
  *             awq_last_error() is not empty).  Contents on entry do not matter; calls

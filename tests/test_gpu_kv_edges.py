@@ -255,14 +255,16 @@ def test_pages_that_are_given_other_memory(awq):
             call()
 
 
-def lse_errors(awq, dim, group, rows, dtype, off_centre, n=65, heads=8, per=4, page=16):
+def lse_errors(awq, dim, group, rows, dtype, off_centre, whole=False, n=65, heads=8, per=4, page=16):
     """Root mean squares, over all rows: the error of lse, that of the same formula in float32, and the one
     that the base in the key codes accounts for.  All against float64 over the values that are read back.
 
     The last: codes enter as 16 + c, so a group's sum over 32 channels at a time passes through
     partial sums of (16 + c) q, each rounded to float32 (at most half an ulp, evenly spread: 2^-24 / sqrt 3
-    of it), times the step; the base's part of the lowest value, (lo - 16 step) * sum q, takes two
-    such roundings.  A row's lse is off by the weighted mean of its scores' errors."""
+    of it), times the step.  On the wide path the base's part of the lowest value, (lo - 16 step) *
+    sum q, takes two such roundings; on the split path the middle's part, (lo + 7.5 step) * sum q, and
+    the score that it makes with the codes' part take one each.  A row's lse is off by the weighted
+    mean of its scores' errors.  whole: queries are whole numbers, whose partial sums are exact."""
     batch = 8 if rows == 1 else 2
     t = base.TYPES[dtype]
     g = torch.Generator("cuda").manual_seed(dim + group + rows)
@@ -282,7 +284,8 @@ def lse_errors(awq, dim, group, rows, dtype, off_centre, n=65, heads=8, per=4, p
     table = torch.randperm(batch * pages, generator=g, device="cuda").int().view(batch, pages)
     length = base.ints([n] * batch)
     awq.kv_append(cache, tokens(), tokens(), table, length)
-    q = draw(batch * rows, heads * per, dim).to(t)
+    q = draw(batch * rows, heads * per, dim)
+    q = (q.round() if whole else q).to(t)
     say("lse", dim, group, rows, dtype, off_centre)
     _, lse = awq.kv_attention(q, cache, table, length, want_lse=True)
     key = awq.kv_read(cache, table, length, batch * n, dtype=torch.float32)[0].view(batch, n, heads, dim).transpose(1, 2)
@@ -303,14 +306,20 @@ def lse_errors(awq, dim, group, rows, dtype, off_centre, n=65, heads=8, per=4, p
     code = ((key.double().unflatten(-1, (ng, group)) - lo[..., None]) / step.clamp_min(1e-9)[..., None]).round()
     x = q.double().view(batch, rows, heads, per, ng, group // 32, 32).permute(0, 2, 1, 3, 4, 5, 6)   # [b, h, rows, per, ng, k, 32]
     y = (16 + code).unflatten(-1, (-1, 32))                                                       # [b, h, n, ng, k, 32]
-    variance = torch.zeros_like(s)
+    variance, score = torch.zeros_like(s), torch.zeros_like(s)
     for i in range(ng):
-        total = 0.0
+        total, some = 0.0, x[:, :, :, :, i].sum((-1, -2))[..., None]
         for k in range(group // 32):
             total = total + torch.matmul(x[:, :, :, :, i, k].flatten(2, 3), y[:, :, :, i, k].transpose(-1, -2).contiguous())
-            variance += (total * step[:, :, None, :, i]).square().view(s.shape)
-        low = (lo - 16 * step)[:, :, None, None, :, i] * x[:, :, :, :, i].sum((-1, -2))[..., None]
-        variance += 2 * low.square()
+            if not whole:
+                variance += (total * step[:, :, None, :, i]).square().view(s.shape)
+        if rows > 1:
+            variance += 2 * ((lo - 16 * step)[:, :, None, None, :, i] * some).square()
+        else:
+            score += (lo + 7.5 * step)[:, :, None, None, :, i] * some
+            variance += score.square()
+            score += step[:, :, None, None, :, i] * (total.view(s.shape) - 23.5 * some)
+            variance += score.square()
     weight = torch.softmax(s, -1)
     model = (weight.square() * variance).sum(-1) * (2.0 ** -48 / 3 / dim)
     got = lse.double().view(batch, rows, heads, per).transpose(1, 2)
@@ -326,4 +335,15 @@ def test_lse_is_as_exact_as_float32_and_its_base(awq, dim, group, rows, dtype, o
     much), both with 1.3 for a sample's spread."""
     error, single, model = lse_errors(awq, dim, group, rows, dtype, off_centre)
     say("error %.2e float32 %.2e base %.2e" % (error, single, model))
+    assert error <= 1.3 * np.hypot(single, model)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim,group", [(64, 32), (128, 32), (128, 128), (256, 64), (256, 128)])
+def test_base_of_key_codes_leaves_single_tokens_exactly(awq, dim, group, dtype):
+    """With queries of whole numbers the sums over 16 + c are exact, so nothing but the roundings of
+    the middle's part and of the scores is left (taking the base out with the lowest value would cost
+    three roundings of 23.5 steps each)."""
+    error, single, model = lse_errors(awq, dim, group, 1, dtype, True, whole=True)
+    say("error %.2e float32 %.2e roundings %.2e" % (error, single, model))
     assert error <= 1.3 * np.hypot(single, model)

@@ -9,7 +9,7 @@
 // operand, queries and scores the B operand), 32 tokens a step:
 //  - S^T = codes·Q^T.  A code enters as the 16-bit float 16 + code, exact, made by a
 //    shift and an and-or of the packed word; steps and lowest values are applied in
-//    float32, the base taken out with the latter.
+//    float32, where the base is taken out.
 //  - A lane's result rows are tokens 4kb..4kb+3 of one query, which are the
 //    tokens that its B operand of the second product takes: scores stay in
 //    their lane.
@@ -65,14 +65,25 @@ __device__ __forceinline__ float half_hi(uint32_t x) {
     return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(x >> 16)));
 }
 
-// Key codes enter as 16 + code, the lowest base whose steps of one are all exact: its
-// part of a sum cancels against the lowest values' in float32, so it is kept small.
+// Key codes enter as 16 + code, the lowest base whose steps of one are all exact.  It leaves a
+// score by one of two ways, both with what float32 has left of sums that are (16 + code) / code
+// times as large:
+//  - in the lowest value's factor (a pair as the factors of (sum (base + code)*q, sum q) in a
+//    score, scaled): no instruction, on the wide path, where one more for each score and group
+//    takes 2.5 to 6%;
 constexpr float kKeyBase = 16.0f;
-
-// A key pair (step, lo) as the factors of (sum (base + code)*q, sum q) in a score.
 __device__ __forceinline__ float2 key_factors(uint32_t pair, float scale) {
     const float step = half_lo(pair);
     return make_float2(step * scale, fmaf(-kKeyBase, step, half_hi(pair)) * scale);
+}
+//  - from the sum itself, with the middle of the codes, on the split path (a pair as the factors of
+//    (sum (code - middle)*q, sum q), unscaled and exact; 0 to 1% of the time).  One token over 65
+//    keys whose channels lie far apart, bf16: lse off by 1.5e-7 in the median of 100 inputs and by
+//    1.5e-6 at most, by the first way 3.6e-7 and 1.8e-6, in float32 over the values 7e-8 and 3.2e-7.
+constexpr float kKeyMiddle = 7.5f;
+__device__ __forceinline__ float2 key_middle(uint32_t pair) {
+    const float step = half_lo(pair);
+    return make_float2(step, fmaf(kKeyMiddle, step, half_hi(pair)));
 }
 
 template <typename T>
@@ -152,7 +163,7 @@ struct KvStep {
 };
 
 // A wave's pairs in LDS, made for reading by result rows (4 tokens of a lane):
-// keys as factors (key_factors), values as fp16 (step0, step2,
+// keys as factors (key_middle), values as fp16 (step0, step2,
 // step1, step3, lo0, lo2, lo1, lo3), the order of the value bytes.
 template <int NG>
 struct KvPairs {
@@ -214,7 +225,7 @@ __device__ __forceinline__ void kv_pairs(const KvAttend &a, const KvStep<D, NG> 
         float *k = reinterpret_cast<float *>(&lds->k[h][0][0][0]) + 2 * n;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            const float2 y = key_factors(s.pair[g], a.scale_log2);
+            const float2 y = key_middle(s.pair[g]);
             k[32 * g] = y.x;
             k[32 * g + 1] = y.y;
         }
@@ -302,7 +313,7 @@ struct KvWave {
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        x[h][t][r] = fmaf(step[r], acc[t][r],
+                        x[h][t][r] = fmaf(step[r], fmaf(-(kKeyBase + kKeyMiddle), qs[t][g], acc[t][r]),
                                           g == 0 ? lo[r] * qs[t][g] : fmaf(lo[r], qs[t][g], x[h][t][r]));
             }
         }
@@ -321,8 +332,8 @@ struct KvWave {
         half8 p[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const float top = fmaxf(fmaxf(fmaxf(x[0][t][0], x[0][t][1]), fmaxf(x[0][t][2], x[0][t][3])),
-                                    fmaxf(fmaxf(x[1][t][0], x[1][t][1]), fmaxf(x[1][t][2], x[1][t][3])));
+            const float top = a.scale_log2 * fmaxf(fmaxf(fmaxf(x[0][t][0], x[0][t][1]), fmaxf(x[0][t][2], x[0][t][3])),
+                                                   fmaxf(fmaxf(x[1][t][0], x[1][t][1]), fmaxf(x[1][t][2], x[1][t][3])));
             if (__any(top > m[t] + kMostLog2)) {
                 float now = fmaxf(m[t], top - kHeadLog2);
                 now = fmaxf(now, __shfl_xor(now, 16));
@@ -342,7 +353,7 @@ struct KvWave {
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float e = __builtin_amdgcn_exp2f(x[h][t][kOrder[r]] - ref);
+                    const float e = __builtin_amdgcn_exp2f(fmaf(x[h][t][kOrder[r]], a.scale_log2, -ref));
                     l[t] += e;
                     p[t][4 * h + r] = static_cast<_Float16>(e);
                 }
