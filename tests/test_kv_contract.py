@@ -60,3 +60,13 @@ def test_a_cache_without_its_memory_is_refused(left):
         awq._kv_pool(c)
     with pytest.raises(ValueError):
         awq.KvCache(pages, 128)
+
+
+@built
+def test_caches_can_be_looked_up():
+    """The caches of a model's layers, in a list and as keys."""
+    import torch
+    from weight_only_quantization_awq_amd import awq
+    layers = [awq.KvCache(torch.zeros(4, 8, 2176, dtype=torch.uint8), 128) for _ in range(3)]
+    assert layers.index(layers[2]) == 2 and layers[0] != layers[1]
+    assert {c: i for i, c in enumerate(layers)}[layers[1]] == 1

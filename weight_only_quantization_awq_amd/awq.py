@@ -517,7 +517,7 @@ def w4a16_gemm_noalloc(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tens
 _KV_TYPES = {torch.float32: AWQ_F32, torch.bfloat16: AWQ_BF16, torch.float16: AWQ_F16}
 
 
-@dataclass(frozen=True)
+@dataclass(frozen=True, eq=False)   # a cache equals itself alone
 class KvCache:
     """A pool of pages of 4-bit keys and values (include/awq.h: awq_kv_cache).
 
