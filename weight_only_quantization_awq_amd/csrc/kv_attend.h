@@ -104,9 +104,10 @@ struct KvType<__bf16> {
 template <>
 struct KvType<_Float16> {
     typedef half8 vec8;
-    // Of the forms that take as long: 64 + code cancels 3 to 4 times as much (lse was
-    // off by 1.8e-6 of itself instead of 5.7e-7); a code's own bits as a subnormal
-    // need no base, but these MFMAs align them as if they were 2^-14 (4e-6).
+    // Of the forms that take as long: 64 + code puts lse 3 to 4 times as far off (keys with
+    // channels far apart, dim 128, 64 rows over 65 keys: 3.3e-5 in the root mean square and
+    // 9.5e-6 with 16); a code's own bits as a subnormal need no base, but these MFMAs align
+    // them as if they were 2^-14 (7.8e-5).
     static __device__ __forceinline__ uint32_t pair(uint32_t w, int i) {
         const uint32_t x = i < 2 ? w << (6 - 4 * i) : w >> (4 * i - 6);
         return and_or(x, 0x03C003C0u, 0x4C004C00u);
@@ -476,9 +477,10 @@ struct KvWave {
 // and kv_merge_kernel joins them in order.  Boundaries within a.snap tiles of an
 // item's ends move there.
 //
-// Memory bounds it where heads have few queries (24 x 2047 tokens, 32 heads, group 32,
-// 252 MB: 66 us, 82% of a large copy's rate) and the unpacking beside it where 8 share a
-// key head (131072 tokens, 143 MB: 41 us and 6 for the join).  With fixed pieces of tokens
+// What bounds it is the wait for loads, one tile ahead and 3 waves a SIMD: waves spend 55 to 59%
+// of their time in it, while vector units are active 44 to 59% of the cycles and the matrix
+// cores 7 to 9% (24 x 2047 tokens, 32 heads, group 32, 252 MB: 64 us, 3.9 TB/s; 131072
+// tokens, 8 heads, 143 MB: 42 us, 3.4 TB/s, and 6 for the join).  With fixed pieces of tokens
 // instead of the line, ragged batches wait for their longest sequence.
 
 // 64 sequences of the line, one to a lane.
@@ -657,12 +659,13 @@ __global__ __launch_bounds__(256) void kv_merge_kernel(KvAttend a) {
 // 4-token blocks, too.
 //
 // Measured: a causal prompt of 4096 rows, 32 query heads on 8 of 128, 172 to 190 us
-// (0.72 to 0.80 PFLOP/s): the matrix cores are busy 32% of the cycles and the vector units
-// 46%, on the same issue slots, and LDS 39%.  Two waves a SIMD beat one of 64 columns
-// (187 and 269 us).  At dim 256 the output of 32 columns fills half the registers, so one
-// wave has a SIMD and its own issue (~740 instructions a tile, 32 of them MFMAs) is the
-// bound (5 ragged chunks of up to 1031 rows over 6007 tokens: 300 us); two waves of 16
-// columns read every operand twice and took 337.
+// (0.72 to 0.80 PFLOP/s): the matrix cores are busy 35% of the cycles, the vector units 50%
+// and LDS 43%; a wave waits for operands, loads and barriers 33% of its time and for its
+// turn to issue 25%.  Two waves a SIMD beat one of 64 columns (187 and 269 us).  At dim 256 the
+// output of 32 columns fills half the registers, so a SIMD has one wave: it issues
+// (~740 instructions a tile, 32 of them MFMAs) 62% of its time and waits 29%, with no other
+// to fill in (5 ragged chunks of up to 1031 rows over 6007 tokens: 300 us; MFMA 17%, VALU
+// 36%, LDS 32%); two waves of 16 columns read every operand twice and took 337.
 
 template <typename T>
 struct KvWideType;

@@ -138,10 +138,11 @@ constexpr int kKvWhole = 6;
 constexpr int kKvMergeFew = 256;
 // Waves of the split path that a SIMD holds at once, by the registers of a wave's
 // output (dim x 16*NT columns) and what comes with it: as many as do without spills, since
-// they hide each other's latency.  us with 1 / 2 / these / one or two more: dim 64, NT 1
-// (64 sequences of 4096) 114 / 72 / 53 / 81; dim 128, NT 1 (131072 tokens) 71 / 51 / 49 / 57;
-// dim 128, NT 2 (16 of 4096) 50 / 47 / 47 / 100; dim 256, NT 1 (48 of 4096) 85 / 64 / 64 / -;
-// dim 128, NT 4 (24 of 4096) 98 / 218 / 98 / -.
+// they hide each other's latency.  us with 1 / 2 / 3 / 4, at group 32 (the largest group has the
+// same fastest): dim 64 (8 heads), NT 1 (64 sequences of 4096) 108 / 69 / 60 / 53, NT 2
+// (16 of 4096) 47 / 36 / 31 / 45, NT 4 (16 of 4096) 61 / 47 / 87 / 215; dim 128 (8 heads), NT 1 (131072
+// tokens) 72 / 52 / 47 / 56, NT 2 (16 of 4096) 57 / 46 / 90 / 196, NT 4 (24 of 4096) 118 / 289 / 602 / 744;
+// dim 256 (4 heads), NT 1 (48 of 4096) 98 / 70 / 203 / 294, NT 2 (16 of 4096) 59 / 144 / 236 / 289.
 constexpr int kv_split_waves(int dim, int nt) {
     return nt * dim <= 64 ? 4 : nt * dim <= 128 ? 3 : nt * dim <= 256 ? 2 : 1;
 }
