@@ -58,6 +58,47 @@ def test_more_rows_than_max_rows(awq, dim, per, max_rows):
     base.check(q[rows], "fp16", cache, got[rows.tolist()], lse[rows.tolist()], some, [lengths[b] for b in keep], table[keep])
 
 
+def test_rows_that_grow_past_max_rows_under_a_graph(awq):
+    """A captured call whose row_start later gives sequences more rows than max_rows: replays leave
+    those out, and equal the eager call, its guard and the other sequences' rows as they should be."""
+    rng = np.random.default_rng(37)
+    heads, per, dim, group, page, max_rows, rows = 2, 1, 128, 128, 16, 2, 40
+    lengths = [1800, 40, 1300, 900]
+    table, n_pages = base.table_for(lengths, page, rng)
+    cache = base.filled(rng, n_pages, heads, dim, group, page)
+    dev, table_d, length = base.pool(awq, cache), base.ints(table), base.ints(lengths)
+    q = torch.from_numpy(base.queries(rng, (rows, heads * per, dim), "bf16")).bfloat16().cuda()
+    start = base.ints([0, 1, 3, 5, 6])
+    size = awq.kv_attention_workspace_size(dev, heads * per, rows, 4, table.shape[1], True, max_rows)
+    room = torch.full((size + 65536,), 0xA5, dtype=torch.uint8, device="cuda")
+    out = torch.zeros_like(q)
+
+    def step(o, w):
+        return awq.kv_attention(q, dev, table_d, length, row_start=start, max_rows=max_rows, out=o, workspace=w, want_lse=True)
+
+    step(out, room[:size])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _, lse = step(out, room[:size])
+    for i, counts in enumerate([(1, 2, 2, 1), (1, 16, 2, 3), (9, 1, 20, 2), (3, 3, 3, 3), (2, 1, 0, 2)]):
+        at = np.concatenate(([0], np.cumsum(counts)))
+        start.copy_(base.ints(at))
+        out.fill_(7.0)
+        say("replay", i, counts)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert (room[size:] == 0xA5).all()
+        assert (out[int(at[-1]):] == 7.0).all()
+        want, want_lse = step(torch.full_like(out, 7.0), None)
+        for b in range(4):
+            if counts[b] <= max_rows:
+                r = slice(int(at[b]), int(at[b + 1]))
+                assert torch.equal(out[r], want[r]) and torch.equal(lse[r], want_lse[r])
+                if counts[b]:
+                    base.check(q[r].float().cpu().numpy(), "bf16", cache, out[r], lse[r], [0, counts[b]], [lengths[b]], table[b:b + 1])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("dim,group,rows", [(64, 64, 1), (128, 32, 5), (256, 128, 1), (64, 32, 40), (128, 128, 40), (256, 64, 40)])
 def test_weights_far_below_the_largest(awq, dim, group, rows, dtype):
