@@ -165,7 +165,10 @@ __device__ __forceinline__ uint32_t quantise(const float *x, uint32_t &pair, boo
     for (int m = 1; m < GL; m <<= 1) lo = fminf(lo, __shfl_xor(lo, m)), hi = fmaxf(hi, __shfl_xor(hi, m));
     const _Float16 lo16 = static_cast<_Float16>(lo);
     lo = static_cast<float>(lo16);
-    const _Float16 step16 = static_cast<_Float16>(fmaxf(hi - lo, 0.0f) * (1.0f / 15.0f));
+    // (the product is rounded to float32 before fp16, which one instruction for both would leave out)
+    float range = fmaxf(hi - lo, 0.0f) * (1.0f / 15.0f);
+    asm("" : "+v"(range));
+    const _Float16 step16 = static_cast<_Float16>(range);
     const float step = static_cast<float>(step16);
     pair = static_cast<uint32_t>(__builtin_bit_cast(uint16_t, step16)) |
            (static_cast<uint32_t>(__builtin_bit_cast(uint16_t, lo16)) << 16);
