@@ -563,6 +563,42 @@ typedef struct {
  * (0 if the arguments are invalid; awq_last_error() says why). */
 size_t awq_kv_page_size(int page, int64_t heads, int dim, int group);
 
+/* What awq_kv_tables writes, in device memory, apart from the table; no output may be an input.
+ *   kv_len     [batch] int32: the lengths with the step's rows.
+ *   row_start  [batch + 1] int32: where each sequence's rows begin.
+ *   taken      [1] int32: how many of the free pages are handed out then.
+ *   position   [rows] int32, slot [rows] int64: each row's position, and page*size + slot of
+ *              the place where its token goes; -1 for rows that belong to no sequence (and
+ *              slots on pages that do not exist).  Either may be NULL.
+ */
+typedef struct {
+    int32_t *kv_len, *row_start, *taken, *position;
+    int64_t *slot;
+} awq_kv_step;
+
+/*
+ * awq_kv_tables - the tables of a step, from the lengths of its sequences.
+ *   page         tokens of a page (a power of two, 16..256).
+ *   batch        number of sequences, 1..2^21.   max_pages  columns of block_table.
+ *   kv_len       device, [batch] int32: the lengths before the step (bounded to
+ *                0 .. max_pages*page).
+ *   count        device, [batch] int32: the rows that each sequence adds (bounded to
+ *                0 .. what its row of the table still holds).
+ *   free_pages   device, [n_free] int32: pages to hand out, in order.
+ *   taken        device, [1] int32: how many of them are handed out already; NULL: none.
+ *   block_table  device, [batch, max_pages] int32: sequence by sequence, the pages that its
+ *                new rows begin are the next free ones, and -1 where there are none left
+ *                (rows there are dropped by awq_kv_append; `taken` then exceeds n_free).
+ *                Other entries are left as they are.
+ *   rows         elements of step->position and step->slot.
+ * The outputs serve the same step's awq_kv_append and awq_kv_attention (awq_kv_batch) on the
+ * same stream; a captured graph follows the arrays.  Calling again with the same arguments
+ * writes the same.
+ */
+awq_status awq_kv_tables(int page, int64_t batch, int64_t max_pages, const int32_t *kv_len, const int32_t *count,
+                         const int32_t *free_pages, int64_t n_free, const int32_t *taken, int32_t *block_table, int64_t rows,
+                         const awq_kv_step *step, hipStream_t stream);
+
 /*
  * awq_kv_append - quantise the rows' keys and values into the cache.
  *   K, V      device, [rows, heads, dim] of type t (AWQ_F32, AWQ_BF16 or AWQ_F16),
@@ -574,6 +610,42 @@ size_t awq_kv_page_size(int page, int64_t heads, int dim, int group);
  */
 awq_status awq_kv_append(const awq_kv_cache *cache, const awq_kv_batch *batch, const void *K, const void *V,
                          awq_dtype t, int64_t k_stride, int64_t v_stride, hipStream_t stream);
+
+/* Norms and rotation of awq_kv_append_rotated.
+ *   cos_sin      device, [positions, 2, rot/2] float32, 16-byte aligned: the cosines of a
+ *                position's angles, then their sines.  May be NULL where rot is 0.
+ *   positions    1..2^30.
+ *   rot          channels that are rotated, the first ones: a multiple of 16 up to dim; 0: none.
+ *   interleaved  0: channel i < rot/2 pairs with i + rot/2; 1: channel 2i with 2i + 1; both have
+ *                angle i.
+ *   q_weight, k_weight  device, [dim] float32, 16-byte aligned; NULL: no norm.
+ *   eps          positive and finite where there is a weight.
+ */
+typedef struct {
+    const float *cos_sin;
+    int64_t positions;
+    int rot, interleaved;
+    const float *q_weight, *k_weight;
+    double eps;
+} awq_kv_rotation;
+
+/*
+ * awq_kv_append_rotated - normalise and rotate the rows' queries and keys, write the queries
+ * and quantise keys and values into the cache, in one pass.
+ *   Q, Q_out  device, [rows, q_heads, dim] of type t, rows q_stride / q_out_stride elements
+ *             apart (as in awq_kv_append); Q_out may be Q.
+ *   K, V, t   as for awq_kv_append.
+ * For each head's row x at position p, each operation rounded to float32:
+ *   u = 1 / sqrt(mean x^2 + eps)   (in 64 bits, rounded once);   y = (x * u) * weight
+ *   a pair (y1, y2) becomes (y1*cos - y2*sin, y2*cos + y1*sin) with p's angles.
+ * Queries are rounded once more, to type t; keys are quantised from float32 (so the cache
+ * holds the same as after awq_kv_append of the float32 keys).  A row at a position that
+ * cos_sin does not hold (rot > 0) gets queries of NaN and is stored as NaN.  Queries of rows
+ * without a position are zero; rows that belong to no sequence are left as they were.
+ */
+awq_status awq_kv_append_rotated(const awq_kv_cache *cache, const awq_kv_batch *batch, const awq_kv_rotation *rotation,
+                                 const void *Q, const void *K, const void *V, awq_dtype t, int64_t q_heads, int64_t q_stride,
+                                 int64_t k_stride, int64_t v_stride, void *Q_out, int64_t q_out_stride, hipStream_t stream);
 
 /*
  * awq_kv_read - the rows' keys and values as the cache stands for them:

@@ -1,0 +1,313 @@
+"""A step's tables and the rotated append on the GPU against the oracle.
+
+Everything is equal, bit for bit: the tables are whole numbers, and the rotation is defined
+by its roundings to float32 (the norm's inside is in 64 bits, where the order of the sum moves
+the rounded result about once in 2^28 rows: not at these seeds)."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv_oracle as kv
+from oracle import kv_step_oracle as step
+from tests.gpu_util import say
+from tests.test_gpu_kv import TYPES, ints, pool, table_for, values
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def awq():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from weight_only_quantization_awq_amd import awq
+    awq._lib = None   # (load anew: a test that reloads the module puts back a library that knows the classes of before)
+    awq.load()
+    return awq
+
+
+# ---- tables -----------------------------------------------------------------
+
+def check_tables(awq, page, kv_len, count, free, taken, table, rows, out=None):
+    want = step.tables(page, kv_len, count, free, taken or 0, table, rows)
+    dev = ints(table)
+    got = awq.kv_tables(dev, ints(kv_len), ints(count), ints(free), None if taken is None else ints([taken]), page=page,
+                        rows=rows, out=out)
+    torch.cuda.synchronize()
+    parts = [dev, got.kv_len, got.row_start, got.taken, got.position, got.slot]
+    for name, x, y in zip(("table", "kv_len", "row_start", "taken", "position", "slot"), parts, want):
+        if x is None:
+            assert rows == 0
+            continue
+        assert np.array_equal(x.cpu().numpy().reshape(-1), np.asarray(y).reshape(-1)), name
+    return got
+
+
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("batch", [1, 2, 63, 64, 65, 1023, 1024, 1025, 2500])
+def test_tables(awq, batch, page):
+    rng = np.random.default_rng(batch + page)
+    most = 9
+    kv_len = rng.integers(0, most * page + 1, batch)
+    kv_len[rng.random(batch) < 0.2] = 0
+    kv_len[rng.random(batch) < 0.2] = page * 3      # full pages
+    kv_len[rng.random(batch) < 0.02] = -5
+    kv_len[rng.random(batch) < 0.02] = 1 << 30
+    count = np.where(rng.random(batch) < 0.6, 1, rng.integers(0, 3 * page, batch))
+    count[rng.random(batch) < 0.1] = 0
+    count[rng.random(batch) < 0.05] = -(1 << 31)
+    count[rng.random(batch) < 0.02] = (1 << 31) - 1
+    table = rng.integers(-1, 50000, (batch, most))
+    free = rng.permutation(100000)[:4 * batch + 3]
+    rows = int(np.clip(count, 0, 3 * page).sum()) + 7
+    say("tables", batch, page)
+    check_tables(awq, page, kv_len, count, free, 3, table, rows)
+    check_tables(awq, page, kv_len, count, free, None, table, 0)
+    check_tables(awq, page, kv_len, count, free[:batch // 3], 0, table, rows // 2)   # pages run out, maps end early
+    check_tables(awq, page, kv_len, count, free[:0], -4, table, rows)
+
+
+def test_tables_of_long_prompts(awq):
+    """Thousands of pages of one sequence, between sequences that add none."""
+    rng = np.random.default_rng(5)
+    kv_len, count = [0, 31, 100, 0, 17], [0, 100001, 0, 33000, 1]
+    free = rng.permutation(20000)
+    say("tables of prompts")
+    check_tables(awq, 16, kv_len, count, free, 0, np.full((5, 7000), -1), 133010)
+
+
+def test_tables_write_to_given_tensors_and_again(awq):
+    table = np.full((3, 4), -1)
+    table[0, 0] = 11
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = awq.KvStep(torch.full((3,), 9, **i32), torch.full((4,), 9, **i32), torch.full((1,), 9, **i32),
+                     None, torch.full((6,), 9, dtype=torch.int64, device="cuda"))
+    args = (ints([5, 0, 0]), ints([1, 2, 0]), ints([7, 8, 9]), ints([1]))
+    dev = ints(table)
+    for _ in range(2):
+        assert awq.kv_tables(dev, *args, page=16, rows=6, out=out) is out
+        assert out.kv_len.tolist() == [6, 2, 0] and out.row_start.tolist() == [0, 1, 3, 3] and out.taken.tolist() == [2]
+        assert out.slot.tolist() == [11 * 16 + 5, 8 * 16, 8 * 16 + 1, -1, -1, -1]
+        assert dev.tolist() == [[11, -1, -1, -1], [8, -1, -1, -1], [-1] * 4]
+    with pytest.raises(awq.AwqError):
+        awq.kv_tables(dev, *args, page=16, rows=6, out=awq.KvStep(args[0], out.row_start, out.taken, None, out.slot))
+    with pytest.raises(ValueError):
+        awq.kv_tables(dev, *args, page=16, rows=5, out=out)
+
+
+def test_tables_in_a_graph_grow_the_sequences(awq):
+    """A captured step that feeds its own results to the next replay."""
+    page, batch = 16, 37
+    rng = np.random.default_rng(2)
+    kv_len, table = rng.integers(0, 40, batch), np.full((batch, 12), -1)
+    free = rng.permutation(1000)[:400]
+    dev, length, count, taken = ints(table), ints(kv_len), ints(np.ones(batch)), ints([0])
+    pages = ints(free)
+    table[:, :3] = -1
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        out = awq.kv_tables(dev.clone(), length, count, pages, taken, page=page, rows=batch)   # (its tensors)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        awq.kv_tables(dev, length, count, pages, taken, page=page, rows=batch, out=out)
+        length.copy_(out.kv_len)
+        taken.copy_(out.taken)
+    want = (table, kv_len, None, 0)
+    for i in range(40):
+        if i == 20:
+            count[3] = 30
+        graph.replay()
+        n = np.ones(batch, int)
+        if i >= 20:
+            n[3] = 30
+        want = step.tables(page, want[1], n, free, want[3], want[0], batch)
+        torch.cuda.synchronize()
+        torch.ones(1000, device="cuda").sum().item()   # (the program's own work between the replays)
+        assert np.array_equal(dev.cpu().numpy(), want[0]) and np.array_equal(length.cpu().numpy(), want[1])
+        assert np.array_equal(out.slot.cpu().numpy(), want[5]) and int(taken) == want[3]
+
+
+# ---- the rotated append -----------------------------------------------------
+
+def angles(n, rot, base=10000.0):
+    a = np.arange(n)[:, None] * base ** (-np.arange(0, rot, 2) / rot)
+    return np.stack((np.cos(a), np.sin(a)), 1).astype(np.float32)
+
+
+def weight(rng, dim):
+    return (1 + 0.3 * rng.standard_normal(dim)).astype(np.float32)
+
+
+def dev(x):
+    return None if x is None else torch.from_numpy(x).cuda()
+
+
+def same(got, want):
+    """Equal, NaN to NaN (whatever its bits)."""
+    want = torch.from_numpy(want).to(got.dtype)
+    got = got.cpu()
+    return torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(got.nan_to_num(0.0), want.nan_to_num(0.0)) \
+        and torch.equal(torch.isinf(got), torch.isinf(want))
+
+
+def check_bytes(pages, cache):
+    """The pool's bytes are the oracle's, slots that were not written included.  A lowest value of zero may
+    have either sign: the minimum of +0 and -0 is both, and q*step + lo is the same with either
+    (q*step is +0 or more; a group of zeros has step 0, and 0*0 + -0 = 0)."""
+    got, want = pages.pages.cpu().numpy().copy(), cache.bytes.copy()
+    for x in (got, want):
+        low = x[..., cache.page * cache.dim:].reshape(*x.shape[:2], -1, 2, 2)[..., 1, :]   # (step, lo) in fp16
+        low[..., 1][(low[..., 0] == 0) & (low[..., 1] == 0x80)] = 0
+        x[..., cache.page * cache.dim:].reshape(*x.shape[:2], -1, 2, 2)[..., 1, :] = low
+    off = np.argwhere(got != want)
+    assert len(off) == 0, (len(off), [(*map(int, i), int(got[tuple(i)]), int(want[tuple(i)])) for i in off[:12]])
+
+
+SIZES = [(64, 32, 16), (64, 64, 64), (128, 32, 32), (128, 64, 16), (128, 128, 128), (256, 32, 16), (256, 64, 256), (256, 128, 32)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("dim,group,page", SIZES)
+@pytest.mark.parametrize("rot,interleaved,norm", [("all", False, True), ("all", True, False), (48, False, False), (16, True, True),
+                                                  (0, False, True)])
+def test_append_rotated_ragged(awq, dim, group, page, dtype, rot, interleaved, norm):
+    """Sequences without rows, of one row, longer than their positions, on pages that do not exist, behind
+    the angles' end; rows behind the last sequence."""
+    rng = np.random.default_rng(dim + group + page + (0 if rot == "all" else rot))
+    heads, q_heads = 3, 9
+    rot = dim if rot == "all" else rot
+    lengths = [37, 0, 1, 70, 5, 4, 23, 8]
+    counts = [33, 0, 1, 1, 9, 4, 2, 6]          # 9 > 5: four rows have no position
+    table, n_pages = table_for(lengths, page, rng)
+    table[6, :] = n_pages                        # a page behind the pool
+    table[3, -(-70 // page) - 1] = -1            # the last token's page is gone
+    start = np.concatenate(([0], np.cumsum(counts)))
+    rows = int(start[-1]) + 5
+    (q, qd), (k, kd), (v, vd) = (values(rng, (rows, h, dim), dtype) for h in (q_heads, heads, heads))
+    cs = angles(35, rot) if rot else None        # (two rows and the row at 69 lie behind)
+    qw, kw = (weight(rng, dim) if norm else None for _ in range(2))
+    c = kv.Cache(n_pages, heads, dim, group, page, fill=0xA5)
+    pages = pool(awq, c)
+    out = torch.full((rows, q_heads, dim), 7.0, dtype=TYPES[dtype], device="cuda")
+    say("append_rotated", dim, group, page, dtype, rot, interleaved, norm)
+    got = awq.kv_append_rotated(pages, qd, kd, vd, ints(table), ints(lengths), dev(cs), row_start=ints(start), q_weight=dev(qw),
+                                k_weight=dev(kw), eps=1e-5, interleaved=interleaved, out=out)
+    torch.cuda.synchronize()
+    assert got is out
+    want = step.append_rotated(c, q, k, v, start, lengths, table, cs, qw, kw, 1e-5, interleaved, fill=7.0)
+    assert same(out, want)
+    check_bytes(pages, c)
+
+
+@pytest.mark.parametrize("dim,heads,q_heads", [(64, 1, 1), (64, 2, 66), (128, 8, 64), (128, 1, 17), (256, 5, 5), (256, 2, 18)])
+@pytest.mark.parametrize("batch", [1, 5, 64, 65, 700])
+def test_append_rotated_of_even_batches(awq, batch, dim, heads, q_heads):
+    """One or three rows each, heads of every remainder, tensors that are slices of a fused projection, in place."""
+    rng = np.random.default_rng(batch + dim)
+    per, page, group = 1 if batch % 2 else 3, 16, 64
+    lengths = rng.integers(0, 40, batch)
+    table, n_pages = table_for(lengths, page, rng)
+    rows = batch * per
+    all_heads = q_heads + 2 * heads
+    x, xd = values(rng, (rows, all_heads, dim), "bf16")
+    cut = [slice(0, q_heads), slice(q_heads, q_heads + heads), slice(q_heads + heads, all_heads)]
+    cs, qw, kw = angles(40, dim), weight(rng, dim), weight(rng, dim)
+    c = kv.Cache(n_pages, heads, dim, group, page)
+    pages = pool(awq, c)
+    say("append_rotated", dim, heads, q_heads, batch)
+    qd, kd, vd = (xd[:, s] for s in cut)
+    got = awq.kv_append_rotated(pages, qd, kd, vd, ints(table), ints(lengths), dev(cs), q_weight=dev(qw), k_weight=dev(kw), out=qd)
+    torch.cuda.synchronize()
+    want = step.append_rotated(c, x[:, cut[0]], x[:, cut[1]], x[:, cut[2]], None, lengths, table, cs, qw, kw)
+    assert got is qd and same(xd[:, cut[0]], want)
+    assert same(xd[:, q_heads:], x[:, q_heads:])                    # keys and values stay as they were
+    check_bytes(pages, c)
+
+
+def test_append_rotated_of_values_that_are_not_finite(awq):
+    """NaN and infinities keep to their head's row; norms bring large rows back into the cache's range."""
+    rng = np.random.default_rng(4)
+    dim, heads = 128, 4
+    for norm in (False, True):
+        (q, _), (k, _), (v, _) = (values(rng, (6, heads, dim), "fp32") for _ in range(3))
+        q[0, 1, 3], q[1, 2, 100], k[2, 0, 7], k[3, 1, 64], v[4, 2, 5] = np.nan, np.inf, np.nan, -np.inf, 1e9
+        k[5, 3] *= 1e18                                             # a square beyond float32, but for the norm's 64 bits
+        q[5, 0] *= 1e25
+        k[0, 2] = 0.0
+        for bf16 in (False, True):
+            if bf16:
+                q, k, v = (torch.from_numpy(x).bfloat16().float().numpy() for x in (q, k, v))
+            cs, w = angles(50, dim), weight(rng, dim) if norm else None
+            c = kv.Cache(2, heads, dim, 64, 16)
+            pages = pool(awq, c)
+            say("append_rotated not finite", norm, bf16)
+            t = torch.bfloat16 if bf16 else torch.float32
+            out = awq.kv_append_rotated(pages, *(torch.from_numpy(x).to(t).cuda() for x in (q, k, v)), ints([[1]]), ints([14]), dev(cs),
+                                        q_weight=dev(w), k_weight=dev(w))
+            torch.cuda.synchronize()
+            want = step.append_rotated(c, q, k, v, None, [14], np.array([[1]]), cs, w, w)
+            assert same(out, want)
+            check_bytes(pages, c)
+
+
+def test_append_rotated_equals_append_without_norm_and_angles(awq):
+    rng = np.random.default_rng(6)
+    q, k, v = (torch.from_numpy(rng.standard_normal((40, h, 128)).astype(np.float32)).half().cuda() for h in (8, 2, 2))
+    a, b = (awq.kv_cache(8, 2, 128) for _ in range(2))
+    table, length = ints([[3, 1, 5], [0, 2, 4]]), ints([21, 40])
+    say("append_rotated of nothing")
+    out = awq.kv_append_rotated(a, q, k, v, table, length, None)
+    awq.kv_append(b, k, v, table, length)
+    assert torch.equal(a.pages, b.pages) and torch.equal(out[:20], q[:20]) and torch.equal(out[20:], q[20:])
+
+
+def test_append_rotated_on_a_stream_and_in_a_graph(awq):
+    """Lengths move on between the replays; the eager result is the same."""
+    rng = np.random.default_rng(8)
+    dim, heads, q_heads, batch = 128, 2, 16, 9
+    (q, qd), (k, kd), (v, vd) = (values(rng, (batch, h, dim), "bf16") for h in (q_heads, heads, heads))
+    lengths = rng.integers(1, 30, batch)
+    table, n_pages = table_for(lengths + 20, 16, rng)
+    cs, w = angles(64, dim), weight(rng, dim)
+    c = kv.Cache(n_pages, heads, dim, 128, 16)
+    pages, length, tab, csd, wd = pool(awq, c), ints(lengths), ints(table), dev(cs), dev(w)
+    out = torch.empty_like(qd)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    say("append_rotated graph")
+    with torch.cuda.stream(side):
+        awq.kv_append_rotated(pages, qd, kd, vd, tab, length, csd, q_weight=wd, k_weight=wd, out=out)
+    side.synchronize()
+    assert same(out, step.append_rotated(c, q, k, v, None, lengths, table, cs, w, w))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        length.add_(1)
+        awq.kv_append_rotated(pages, qd, kd, vd, tab, length, csd, q_weight=wd, k_weight=wd, out=out)
+    for i in range(1, 18):
+        graph.replay()
+        torch.cuda.synchronize()
+        torch.ones(1000, device="cuda").sum().item()
+        assert same(out, step.append_rotated(c, q, k, v, None, lengths + i, table, cs, w, w)), i
+        check_bytes(pages, c)
+
+
+def test_bindings_refuse(awq):
+    c = awq.kv_cache(4, 2, 64, group=64)
+    q, k = torch.zeros(2, 4, 64, device="cuda", dtype=torch.bfloat16), torch.zeros(2, 2, 64, device="cuda", dtype=torch.bfloat16)
+    table, length, cs = ints([[0], [1]]), ints([1, 1]), dev(angles(4, 64))
+    ok = dict(cache=c, Q=q, K=k, V=k, block_table=table, kv_len=length, cos_sin=cs)
+    awq.kv_append_rotated(**ok)
+    for bad, error in ((dict(cos_sin=cs.double()), TypeError), (dict(cos_sin=cs[:, 0]), ValueError), (dict(cos_sin=cs.cpu()), ValueError),
+                       (dict(cos_sin=dev(angles(4, 40))), awq.AwqError), (dict(cos_sin=dev(angles(4, 96))), awq.AwqError),
+                       (dict(q_weight=cs[0, 0]), ValueError), (dict(k_weight=torch.zeros(64, device="cuda").half()), TypeError),
+                       (dict(k_weight=torch.zeros(64, device="cuda"), eps=0.0), awq.AwqError), (dict(V=k.half()), TypeError),
+                       (dict(Q=q[..., :32]), ValueError), (dict(K=k[:1]), ValueError), (dict(out=q.half()), TypeError),
+                       (dict(out=q[:1]), ValueError), (dict(kv_len=length.long()), TypeError), (dict(block_table=table[:1]), ValueError)):
+        with pytest.raises(error):
+            awq.kv_append_rotated(**{**ok, **bad})
+    for bad, error in ((dict(kv_len=length[:1]), ValueError), (dict(count=length.long()), TypeError), (dict(free_pages=table), ValueError),
+                       (dict(taken=length), ValueError), (dict(page=8), awq.AwqError), (dict(rows=-1), RuntimeError)):
+        with pytest.raises(error):
+            awq.kv_tables(**{**dict(block_table=table, kv_len=length, count=length, free_pages=length), **bad})

@@ -36,7 +36,11 @@ __all__ = [
     "KvCache",
     "kv_page_size",
     "kv_cache",
+    "KvStep",
+    "kv_tables",
     "kv_append",
+    "kv_rotation_table",
+    "kv_append_rotated",
     "kv_read",
     "kv_attention_workspace_size",
     "kv_attention",
@@ -103,6 +107,17 @@ class _KvBatchC(ctypes.Structure):
                 ("block_table", _vp)]
 
 
+class _KvRotationC(ctypes.Structure):
+    """awq_kv_rotation"""
+    _fields_ = [("cos_sin", _vp), ("positions", _i64), ("rot", _int), ("interleaved", _int), ("q_weight", _vp),
+                ("k_weight", _vp), ("eps", ctypes.c_double)]
+
+
+class _KvStepC(ctypes.Structure):
+    """awq_kv_step"""
+    _fields_ = [("kv_len", _vp), ("row_start", _vp), ("taken", _vp), ("position", _vp), ("slot", _vp)]
+
+
 _kvc = ctypes.POINTER(_KvCacheC)
 _kvb = ctypes.POINTER(_KvBatchC)
 
@@ -140,6 +155,9 @@ SIGNATURES = {
                                  _vp]),
     "awq_kv_page_size": (_sz, [_int, _i64, _int, _int]),
     "awq_kv_append": (_int, [_kvc, _kvb, _vp, _vp, _int, _i64, _i64, _vp]),
+    "awq_kv_append_rotated": (_int, [_kvc, _kvb, ctypes.POINTER(_KvRotationC), _vp, _vp, _vp, _int, _i64, _i64, _i64, _i64,
+                                     _vp, _i64, _vp]),
+    "awq_kv_tables": (_int, [_int, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _i64, ctypes.POINTER(_KvStepC), _vp]),
     "awq_kv_read": (_int, [_kvc, _kvb, _vp, _vp, _int, _i64, _i64, _vp]),
     "awq_kv_attention_workspace_size": (_sz, [_kvc, _kvb, _i64, _i64]),
     "awq_kv_attention": (_int, [_kvc, _kvb, _vp, _int, _i64, _i64, _i64, ctypes.c_float, _int, _i64, _vp, _i64, _vp,
@@ -650,6 +668,115 @@ def kv_append(cache: KvCache, K: torch.Tensor, V: torch.Tensor, block_table: tor
     k, k_stride = _kv_rows(K, "K", dev, shape)
     v, v_stride = _kv_rows(V, "V", dev, shape)
     _kv_call(dev, _lib.awq_kv_append, c, b, k, v, _kv_type(K.dtype), k_stride, v_stride)
+
+
+@dataclass(frozen=True)
+class KvStep:
+    """What :func:`kv_tables` gives: a step's ``kv_len`` and ``row_start`` for the other calls, the
+    free pages ``taken`` so far, and each row's ``position`` and ``slot`` (None without ``rows``)."""
+    kv_len: torch.Tensor              # int32 [batch]
+    row_start: torch.Tensor           # int32 [batch + 1]
+    taken: torch.Tensor               # int32 [1]
+    position: torch.Tensor | None     # int32 [rows]
+    slot: torch.Tensor | None         # int64 [rows]
+
+
+def kv_tables(block_table: torch.Tensor, kv_len: torch.Tensor, count: torch.Tensor, free_pages: torch.Tensor,
+              taken: torch.Tensor | None = None, page: int = 16, rows: int = 0, out: KvStep | None = None) -> KvStep:
+    """The tables of a step in which sequence b, ``kv_len[b]`` tokens long, adds ``count[b]`` rows.
+
+    The pages that new rows begin come from ``free_pages`` behind the first ``taken`` of them
+    and are written into ``block_table`` (-1 where none are left; ``taken`` of the result then
+    exceeds their number).  ``rows``: with positions and slots of so many rows, -1 for those
+    that belong to no sequence.  ``out``: a :class:`KvStep` to write to; none of its tensors may
+    be an input.  Everything stays on the GPU: a captured step can grow its sequences.
+    """
+    dev = block_table.device
+    if dev.type != "cuda":
+        raise ValueError("block_table must be a GPU tensor")
+    table = _kv_ints(block_table, "block_table", dev, None)
+    batch, max_pages = block_table.shape
+    if out is None:
+        ints = torch.empty(2 * batch + 2 + rows, dtype=torch.int32, device=dev).split((batch, batch + 1, 1, rows))
+        out = KvStep(ints[0], ints[1], ints[2], ints[3] if rows else None,
+                     torch.empty(rows, dtype=torch.int64, device=dev) if rows else None)
+        s = _KvStepC(*[x.data_ptr() for x in ints], out.slot.data_ptr() if rows else None)
+    else:
+        if out.slot is not None and (out.slot.dtype is not torch.int64 or out.slot.device != dev
+                                     or out.slot.shape != (rows,) or not out.slot.is_contiguous()):
+            raise ValueError(f"slot must be contiguous int64 [{rows}] on the table's GPU")
+        s = _KvStepC(_kv_ints(out.kv_len, "out.kv_len", dev, (batch,)), _kv_ints(out.row_start, "out.row_start", dev, (batch + 1,)),
+                     _kv_ints(out.taken, "out.taken", dev, (1,)),
+                     None if out.position is None else _kv_ints(out.position, "out.position", dev, (rows,)),
+                     None if out.slot is None else out.slot.data_ptr())
+    if free_pages.dim() != 1:
+        raise ValueError("free_pages must have one dimension")
+    _kv_call(dev, _lib.awq_kv_tables, page, batch, max_pages, _kv_ints(kv_len, "kv_len", dev, (batch,)),
+             _kv_ints(count, "count", dev, (batch,)), _kv_ints(free_pages, "free_pages", dev, None), free_pages.shape[0],
+             None if taken is None else _kv_ints(taken, "taken", dev, (1,)), table, rows, s)
+    return out
+
+
+def kv_rotation_table(positions: int, rot: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """Cosines and sines [positions, 2, rot/2] of the angles p * base^(-2i/rot), taken in 64 bits and
+    rounded once to float32 (for :func:`kv_append_rotated`; scaled frequencies are a table of one's own)."""
+    freq = base ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.stack((angle.cos(), angle.sin()), 1).float()
+
+
+def _kv_floats(x: torch.Tensor, name: str, device, shape) -> int:
+    """Pointer of a float32 tensor on the cache's GPU."""
+    if x.dtype is not torch.float32:
+        raise TypeError(f"{name} must be float32 (got {x.dtype})")
+    if x.device != device or not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and on the cache's GPU")
+    if x.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)} (got {list(x.shape)})")
+    return x.data_ptr()
+
+
+def kv_append_rotated(cache: KvCache, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, block_table: torch.Tensor,
+                      kv_len: torch.Tensor, cos_sin: torch.Tensor | None, row_start: torch.Tensor | None = None,
+                      q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                      interleaved: bool = False, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Normalise and rotate queries [rows, q_heads, dim] and keys, and append keys and values.
+
+    Rows and positions as in :func:`kv_append`.  ``q_weight`` / ``k_weight`` (float32 [dim]):
+    each head's row is divided by the root of its mean square plus ``eps`` and multiplied by
+    the weight; None leaves it.  ``cos_sin`` (float32 [positions, 2, rot/2], see
+    :func:`kv_rotation_table`): the first rot channels are rotated by the row's position, in
+    halves or (``interleaved``) in neighbouring pairs; None rotates nothing.  A position that
+    it does not hold gives NaN.  Returns the queries for :func:`kv_attention` (``out`` may be Q).
+    """
+    c, dev = _kv_pool(cache)
+    rows, q_heads = Q.shape[0], Q.shape[1]
+    shape, kv_shape, dtype = (rows, q_heads, cache.dim), (rows, cache.heads, cache.dim), Q.dtype
+    if K.dtype != dtype or V.dtype != dtype:
+        raise TypeError("Q, K and V must have one dtype")
+    b = _kv_batch(dev, block_table, kv_len, row_start, rows)
+    q, q_stride = _kv_rows(Q, "Q", dev, shape)
+    k, k_stride = _kv_rows(K, "K", dev, kv_shape)
+    v, v_stride = _kv_rows(V, "V", dev, kv_shape)
+    if out is None:
+        out = torch.empty_like(Q) if Q.is_contiguous() else torch.empty(shape, dtype=dtype, device=dev)
+        o, o_stride = out.data_ptr(), q_heads * cache.dim
+    elif out.dtype != dtype:
+        raise TypeError("out must have the dtype of Q")
+    else:
+        o, o_stride = _kv_rows(out, "out", dev, shape)
+    positions = rot = table = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 3:
+            raise ValueError("cos_sin must be [positions, 2, rot/2]")
+        positions, rot = cos_sin.shape[0], 2 * cos_sin.shape[2]
+        table = _kv_floats(cos_sin, "cos_sin", dev, (positions, 2, rot // 2))
+    weights = (cache.dim,)
+    r = _KvRotationC(table, positions, rot, 1 if interleaved else 0,
+                     None if q_weight is None else _kv_floats(q_weight, "q_weight", dev, weights),
+                     None if k_weight is None else _kv_floats(k_weight, "k_weight", dev, weights), eps)
+    _kv_call(dev, _lib.awq_kv_append_rotated, c, b, r, q, k, v, _kv_type(dtype), q_heads, q_stride, k_stride, v_stride, o, o_stride)
+    return out
 
 
 def kv_read(cache: KvCache, block_table: torch.Tensor, kv_len: torch.Tensor, rows: int,

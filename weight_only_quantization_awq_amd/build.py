@@ -19,7 +19,7 @@ CALIB_LIB = os.path.join(PKG, "libawq_calib.so")
 
 SOURCES = ["awq_api.hip", "awq_noalloc.hip", "k_stats.hip", "k_search.hip", "k_pack.hip", "k_decode.hip",
            "k_prefill.hip", "k_clip.hip", "awq_kv.hip", "k_kv.hip", "k_kv_attend_64.hip", "k_kv_attend_128.hip",
-           "k_kv_attend_256.hip"]
+           "k_kv_attend_256.hip", "awq_kv_step.hip", "k_kv_rotate.hip", "k_kv_tables.hip"]
 CALIB_SOURCES = ["calib.hip"]
 
 # Packed fp32 VALU forms are disabled (-packed-fp32-ops); no fast-math, no

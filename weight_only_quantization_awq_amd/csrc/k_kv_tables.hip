@@ -1,0 +1,143 @@
+// A step's page table, row starts, positions and slots, from the lengths of its sequences.
+//
+// With P tokens to a page and cap = max_pages * P, for sequence b of length L_b that adds
+// count_b rows:
+//   n_b = clamp(count_b, 0, cap - L_b),  L'_b = L_b + n_b,  start_b = sum_{c < b} n_c
+//   have_b = ceil(L_b / P),  need_b = ceil(L'_b / P) - have_b,  first_b = taken + sum_{c < b} need_c
+//   table[b, have_b + j] = free[first_b + j]  (-1 behind the list's end),  j < need_b
+//   row r of b: position L_b + r - start_b, slot table[b, position / P] * P + position % P
+//
+// One launch.  Every workgroup forms both sums over all sequences by itself (8 bytes a
+// sequence, which the caches hold), a run of sequences to a thread, so that workgroups need
+// not wait for each other; then each takes its share of the sequences, of the new pages and
+// of the rows, all spread evenly, whichever sequences they belong to.  A row's or page's
+// sequence is found by halves among the threads' runs, in LDS, and then within the run.
+#include "kv_internal.h"
+
+namespace awq {
+
+namespace {
+
+constexpr int kStepThreads = 1024;
+
+struct Tables {
+    const KvTables &a;
+    int cap;
+
+    __device__ __forceinline__ int length(int b) const { return kv_clamp(a.kv_len[b], 0, cap); }
+    __device__ __forceinline__ int rows(int b, int len) const { return kv_clamp(a.count[b], 0, cap - len); }
+    __device__ __forceinline__ int pages(int len) const { return (len + (1 << a.page_shift) - 1) >> a.page_shift; }
+};
+
+// Inclusive sums of two values over the workgroup's threads (which all call).
+__device__ __forceinline__ void sum_up(int64_t &x, int64_t &y, int64_t (&waves)[2][kStepThreads / 64]) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t ux = __shfl_up(x, d), uy = __shfl_up(y, d);
+        if (lane >= d) x += ux, y += uy;
+    }
+    if (lane == 63) waves[0][wave] = x, waves[1][wave] = y;
+    __syncthreads();
+    for (int i = 0; i < wave; ++i) x += waves[0][i], y += waves[1][i];
+}
+
+// The last run whose sum before it is at most z (before[0] = 0 <= z).
+__device__ __forceinline__ int run_of(const int64_t *before, int runs, int64_t z) {
+    int lo = 0, hi = runs;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (before[mid] <= z)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ int saturated(int64_t x) { return x > INT32_MAX ? INT32_MAX : static_cast<int>(x); }
+
+__global__ __launch_bounds__(kStepThreads) void kv_tables_kernel(KvTables a) {
+    __shared__ int64_t rows_before[kStepThreads], pages_before[kStepThreads], waves[2][kStepThreads / 64], all[2];
+    const int tid = threadIdx.x;
+    const Tables t{a, a.max_pages << a.page_shift};
+    const int each = (a.B + kStepThreads - 1) / kStepThreads, runs = (a.B + each - 1) / each;   // sequences of a run
+    const int b0 = tid * each, b1 = b0 + each < a.B ? b0 + each : a.B;
+    int64_t n_sum = 0, need_sum = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int len = t.length(b), n = t.rows(b, len);
+        n_sum += n;
+        need_sum += t.pages(len + n) - t.pages(len);
+    }
+    const int64_t mine_n = n_sum, mine_need = need_sum;
+    sum_up(n_sum, need_sum, waves);
+    rows_before[tid] = n_sum - mine_n;
+    pages_before[tid] = need_sum - mine_need;
+    if (tid == kStepThreads - 1) all[0] = n_sum, all[1] = need_sum;
+    __syncthreads();
+    const int64_t total = all[0], need_total = all[1], taken = a.taken && *a.taken > 0 ? *a.taken : 0;
+    auto page_of = [&](int64_t k) { return taken + k < a.n_free ? a.free_pages[taken + k] : -1; };   // the k-th new page
+
+    // lengths and row starts
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kStepThreads, here = static_cast<int64_t>(blockIdx.x) * kStepThreads + tid;
+    for (int64_t i = here; i < a.B; i += step) {
+        const int b = static_cast<int>(i), run = b / each;
+        int64_t start = rows_before[run];
+        for (int k = run * each; k < b; ++k) start += t.rows(k, t.length(k));
+        const int len = t.length(b);
+        a.new_len[b] = len + t.rows(b, len);
+        a.row_start[b] = saturated(start);
+    }
+    if (here == 0) {
+        a.row_start[a.B] = saturated(total);
+        *a.new_taken = saturated(taken + need_total);
+    }
+    // the table's new entries
+    for (int64_t k = here; k < need_total; k += step) {
+        int b = run_of(pages_before, runs, k) * each;
+        int64_t j = k - pages_before[b / each];
+        int len = 0;
+        for (; b < a.B; ++b) {   // (ends within the run)
+            len = t.length(b);
+            const int need = t.pages(len + t.rows(b, len)) - t.pages(len);
+            if (j < need) break;
+            j -= need;
+        }
+        if (b < a.B) a.table[static_cast<int64_t>(b) * a.max_pages + t.pages(len) + j] = page_of(k);
+    }
+    // positions and slots of the rows
+    for (int64_t r = here; r < a.T; r += step) {
+        int position = -1;
+        int64_t slot = -1;
+        if (r < total) {
+            const int run = run_of(rows_before, runs, r);
+            int b = run * each, len = 0, n = 0;
+            int64_t i = r - rows_before[run], pages = pages_before[run];
+            for (; b < a.B; ++b) {
+                len = t.length(b), n = t.rows(b, len);
+                if (i < n) break;
+                i -= n;
+                pages += t.pages(len + n) - t.pages(len);
+            }
+            if (b < a.B) {
+                position = len + static_cast<int>(i);
+                const int p = position >> a.page_shift, have = t.pages(len);
+                const int id = p < have ? a.table[static_cast<int64_t>(b) * a.max_pages + p] : page_of(pages + p - have);
+                if (id >= 0) slot = (static_cast<int64_t>(id) << a.page_shift) + (position & ((1 << a.page_shift) - 1));
+            }
+        }
+        if (a.position) a.position[r] = position;
+        if (a.slot) a.slot[r] = slot;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_kv_tables(const KvTables &a, hipStream_t st) {
+    const int64_t most = a.T > a.B ? a.T : a.B, groups = (most + kStepThreads - 1) / kStepThreads;
+    hipLaunchKernelGGL(kv_tables_kernel, dim3(static_cast<unsigned>(groups < 1 ? 1 : groups > kKvCus ? kKvCus : groups)),
+                       dim3(kStepThreads), 0, st, a);
+    return hipGetLastError();
+}
+
+}  // namespace awq

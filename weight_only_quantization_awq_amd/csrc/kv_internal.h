@@ -1,4 +1,4 @@
-// Internal declarations of the 4-bit key/value cache (k_kv.hip, kv_attend.h, awq_kv.hip).
+// Internal declarations of the 4-bit key/value cache (k_kv*.hip, kv_attend.h, awq_kv*.hip).
 //
 // One block of bytes per (page, head), blocks of a page in head order, page
 // size P tokens, D channels, groups of `group` channels, NG = D / group:
@@ -186,6 +186,27 @@ __host__ __device__ __forceinline__ int64_t kv_piece(const KvAttend &a, int work
     return (static_cast<int64_t>(worker) * 2 + (begins ? 1 : 0)) * a.split_cols;
 }
 
+// Norms and rotation of kv_append_rotated (k_kv_rotate.hip).
+struct KvTurn {
+    const float *cos_sin;              // [positions][2][rot/2]
+    int positions, rot, neighbours;
+    const float *q_weight, *k_weight;  // [dim], NULL: no norm
+    double eps;
+};
+
+// A step's tables (k_kv_tables.hip).
+struct KvTables {
+    const int32_t *kv_len, *count, *free_pages, *taken;
+    int64_t n_free, T;
+    int32_t *table, *new_len, *row_start, *new_taken, *position;
+    int64_t *slot;
+    int B, max_pages, page_shift;
+};
+
+hipError_t launch_kv_append_rotated(const KvCache &c, const KvBatch &s, const KvTurn &t, const void *Q, const void *K,
+                                    const void *V, void *Qo, int type, int q_heads, int64_t q_stride, int64_t k_stride,
+                                    int64_t v_stride, int64_t o_stride, hipStream_t st);
+hipError_t launch_kv_tables(const KvTables &a, hipStream_t st);
 hipError_t launch_kv_append(const KvCache &c, const KvBatch &s, const void *K, const void *V, int type,
                             int64_t k_stride, int64_t v_stride, hipStream_t st);
 hipError_t launch_kv_read(const KvCache &c, const KvBatch &s, void *K, void *V, int type, int64_t k_stride,
