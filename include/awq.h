@@ -693,6 +693,36 @@ awq_status awq_kv_attention(const awq_kv_cache *cache, const awq_kv_batch *batch
                             int64_t window, void *O, int64_t o_stride, float *lse, void *workspace,
                             size_t workspace_bytes, hipStream_t stream);
 
+/* What the rows of awq_kv_attention_ex see, besides what awq_kv_attention says.
+ *   window        > 0: positions > p - window (causal = 1); 0: no window.
+ *   sinks         > 0, with a window: and the first `sinks` positions, t <= p.
+ *   prefix_len    device, [1] int32, NULL: no prefix.  The first prefix_len positions of every
+ *                 sequence lie in the pages of prefix_table, device, [prefix_pages] int32
+ *                 (bounded as kv_len and block_table are), and are read from there, once for
+ *                 the whole batch; block_table holds the positions from prefix_len on, and what it
+ *                 holds for the others does not matter (their columns are there: position p
+ *                 is still in column p / page).  kv_len counts the prefix.  No window then.
+ */
+typedef struct {
+    int64_t window, sinks;
+    const int32_t *prefix_table, *prefix_len;
+    int64_t prefix_pages;
+} awq_kv_view;
+
+/*
+ * awq_kv_attention_ex - awq_kv_attention with sinks, or with a shared prefix.
+ * Other arguments, results and the workspace's use as for awq_kv_attention, which is this
+ * call with a view of its window.  The results with a prefix differ from those of
+ * the same positions in one table by float32 roundings of the join.  The workspace then also
+ * holds rows * q_heads * (dim + 2) float32.  Rows that see nothing of their sequence are
+ * computed against the prefix and left out of the results: padded slots cost time, not more.
+ */
+size_t awq_kv_attention_workspace_size_ex(const awq_kv_cache *cache, const awq_kv_batch *batch, const awq_kv_view *view,
+                                          int64_t q_heads, int64_t max_rows);
+awq_status awq_kv_attention_ex(const awq_kv_cache *cache, const awq_kv_batch *batch, const awq_kv_view *view, const void *Q,
+                               awq_dtype t, int64_t q_heads, int64_t q_stride, int64_t max_rows, float scale, int causal, void *O,
+                               int64_t o_stride, float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

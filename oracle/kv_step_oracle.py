@@ -74,3 +74,56 @@ def append_rotated(cache, q, k, v, row_start, kv_len, table, cos_sin, q_weight=N
     with np.errstate(all="ignore"):
         kv.append(cache, turned(k, k_weight, cos_sin, at, eps, interleaved), np.asarray(v, np.float32), row_start, kv_len, table)
     return out
+
+
+def sees(position, t, causal, window, sinks):
+    """Which of the positions t a row at `position` sees."""
+    see = np.ones(len(t), bool)
+    if causal:
+        see &= t <= position
+    if window:
+        see &= (t > position - window) | (t < sinks)
+    return see
+
+
+def attention(cache, q, row_start, kv_len, table, scale=None, causal=True, window=0, sinks=0, prefix=None, fill=0.0, spread=None):
+    """kv_oracle.attention with sinks and with a prefix = (table [pages], length) that holds the first positions
+    of every sequence: (O, lse, A, E) in float64."""
+    rows, q_heads, dim = q.shape
+    per, page = q_heads // cache.heads, cache.page
+    scale = dim ** -0.5 if scale is None else scale
+    o, a = np.full(q.shape, fill, np.float64), np.zeros(q.shape, np.float64)
+    lse, err = np.full(q.shape[:2], fill, np.float64), np.zeros(q.shape[:2], np.float64)
+    common = min(max(int(prefix[1]), 0), len(prefix[0]) * page) if prefix is not None else 0
+    for b, (r0, n, length) in enumerate(kv.sequences(rows, len(kv_len), row_start, kv_len, table, page)):
+        if n == 0:
+            continue
+        pg = [int(prefix[0][t // page] if t < common else table[b, t // page]) for t in range(length)]
+        wanted = np.zeros(length, bool)
+        for i in range(n):
+            wanted |= sees(length - n + i, np.arange(length), causal, window, sinks)
+        real = np.array([t for t in range(length) if wanted[t] and 0 <= pg[t] < len(cache.bytes)], int)
+        got = [cache.read(pg[t], t % page) for t in real]
+        kk, vv = (np.array([g[x] for g in got], np.float64).reshape(len(real), cache.heads, dim) for x in (0, 1))
+        steps = np.zeros((len(real), cache.heads, dim))
+        for x, t in enumerate(real):
+            p = cache.pair_at(0, t % page)
+            pair = np.ascontiguousarray(cache.bytes[pg[t]][:, p:p + 4 * (dim // cache.group)]).view(np.float16)
+            steps[x] = np.repeat(pair.reshape(cache.heads, -1, 2)[..., 0].astype(np.float64), cache.group, -1)
+        for i in range(n):
+            see = sees(length - n + i, real, causal, window, sinks)
+            for h in range(q_heads):
+                if not see.any():
+                    o[r0 + i, h], lse[r0 + i, h] = 0.0, -np.inf
+                    continue
+                with np.errstate(all="ignore"):
+                    x = q[r0 + i, h].astype(np.float64)
+                    s = kk[see, h // per] @ x * scale
+                    top = s.max()
+                    p = np.exp(s - top)
+                    o[r0 + i, h] = p @ vv[see, h // per] / p.sum()
+                    a[r0 + i, h] = p @ np.abs(vv[see, h // per]) / p.sum()
+                    lse[r0 + i, h] = top + np.log(p.sum())
+                    if spread is not None:
+                        err[r0 + i, h] = scale * spread(steps[see, h // per], kk[see, h // per], x).max()
+    return o, lse, a, err

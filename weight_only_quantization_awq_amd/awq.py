@@ -118,6 +118,11 @@ class _KvStepC(ctypes.Structure):
     _fields_ = [("kv_len", _vp), ("row_start", _vp), ("taken", _vp), ("position", _vp), ("slot", _vp)]
 
 
+class _KvViewC(ctypes.Structure):
+    """awq_kv_view"""
+    _fields_ = [("window", _i64), ("sinks", _i64), ("prefix_table", _vp), ("prefix_len", _vp), ("prefix_pages", _i64)]
+
+
 _kvc = ctypes.POINTER(_KvCacheC)
 _kvb = ctypes.POINTER(_KvBatchC)
 
@@ -162,6 +167,9 @@ SIGNATURES = {
     "awq_kv_attention_workspace_size": (_sz, [_kvc, _kvb, _i64, _i64]),
     "awq_kv_attention": (_int, [_kvc, _kvb, _vp, _int, _i64, _i64, _i64, ctypes.c_float, _int, _i64, _vp, _i64, _vp,
                                 _vp, _sz, _vp]),
+    "awq_kv_attention_workspace_size_ex": (_sz, [_kvc, _kvb, ctypes.POINTER(_KvViewC), _i64, _i64]),
+    "awq_kv_attention_ex": (_int, [_kvc, _kvb, ctypes.POINTER(_KvViewC), _vp, _int, _i64, _i64, _i64, ctypes.c_float, _int, _vp,
+                                   _i64, _vp, _vp, _sz, _vp]),
 }
 
 
@@ -802,8 +810,11 @@ def kv_read(cache: KvCache, block_table: torch.Tensor, kv_len: torch.Tensor, row
     return K, V
 
 
-def _kv_workspace(cache_c, batch_c, q_heads: int, max_rows: int) -> int:
-    n = _lib.awq_kv_attention_workspace_size(cache_c, batch_c, q_heads, max_rows)
+def _kv_workspace(cache_c, batch_c, view_c, q_heads: int, max_rows: int) -> int:
+    if view_c is None:
+        n = _lib.awq_kv_attention_workspace_size(cache_c, batch_c, q_heads, max_rows)
+    else:
+        n = _lib.awq_kv_attention_workspace_size_ex(cache_c, batch_c, view_c, q_heads, max_rows)
     if n == 0:
         msg = _lib.awq_last_error()
         if msg:
@@ -812,23 +823,28 @@ def _kv_workspace(cache_c, batch_c, q_heads: int, max_rows: int) -> int:
 
 
 def kv_attention_workspace_size(cache: KvCache, q_heads: int, rows: int, batch: int, max_pages: int,
-                                ragged: bool = False, max_rows: int | None = None) -> int:
-    """Bytes of workspace of a :func:`kv_attention` call (``ragged``: with row_start)."""
+                                ragged: bool = False, max_rows: int | None = None, prefix_pages: int = 0) -> int:
+    """Bytes of workspace of a :func:`kv_attention` call (``ragged``: with row_start; ``prefix_pages``: of its prefix)."""
     b = _KvBatchC(rows, batch, max_pages, 4 if ragged else None, None, None)   # only whether it is NULL counts
-    return _kv_workspace(cache._c, b, q_heads, max_rows or 0)
+    return _kv_workspace(cache._c, b, _KvViewC(0, 0, None, 4, prefix_pages) if prefix_pages else None, q_heads, max_rows or 0)
 
 
 def kv_attention(Q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, kv_len: torch.Tensor,
                  row_start: torch.Tensor | None = None, max_rows: int | None = None, scale: float | None = None,
                  causal: bool = True, window: int = 0, want_lse: bool = False, out: torch.Tensor | None = None,
-                 workspace: torch.Tensor | None = None):
+                 workspace: torch.Tensor | None = None, sinks: int = 0,
+                 prefix: tuple[torch.Tensor, torch.Tensor] | None = None):
     """Attention of the queries [rows, q_heads, dim] (bf16 or fp16) over the cache.
 
     Rows and positions as in :func:`kv_append` (append the rows' keys first:
     a row sees its own position).  ``max_rows``: an upper bound on any
     sequence's rows, known on the host; give it with ``row_start``.  ``scale``
-    defaults to dim ** -0.5.  ``window`` > 0: only the last ``window`` positions.
+    defaults to dim ** -0.5.  ``window`` > 0: only the last ``window`` positions,
+    and with ``sinks`` > 0 the first ``sinks`` ones too.
     Without ``causal`` every row sees all ``kv_len[b]`` positions, whatever its own.
+    ``prefix`` = (table int32 [pages], length int32 [1]): the first length positions of every
+    sequence (counted by ``kv_len``) lie in the table's pages instead of ``block_table``'s and are
+    read once for the whole batch; not with a window.
     ``workspace``: uint8 of :func:`kv_attention_workspace_size` bytes (None
     allocates it).  Returns the output like Q, and with ``want_lse`` also the
     float32 log-sum-exp [rows, q_heads] (-inf, and output 0, where a row sees
@@ -853,13 +869,26 @@ def kv_attention(Q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, kv_
     if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != dev
                                   or not workspace.is_contiguous()):
         raise ValueError("workspace must be contiguous uint8 on the cache's GPU")
-    need = _kv_workspace(c, b, q_heads, max_rows or 0)
+    view = None
+    if prefix is not None:
+        table, length = prefix
+        if table.dim() != 1:
+            raise ValueError("the prefix's table must have one dimension")
+        view = _KvViewC(window, sinks, _kv_ints(table, "the prefix's table", dev, None),
+                        _kv_ints(length, "the prefix's length", dev, (1,)), table.shape[0])
+    elif sinks != 0:
+        view = _KvViewC(window, sinks, None, None, 0)
+    need = _kv_workspace(c, b, view, q_heads, max_rows or 0)
     if need and (workspace is None or workspace.numel() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _kv_call(dev, _lib.awq_kv_attention, c, b, q, _KV_TYPES[dtype], q_heads, q_stride, max_rows or 0,
-             cache.dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, o, o_stride,
-             lse.data_ptr() if want_lse else None, workspace.data_ptr() if need else None,
-             workspace.numel() if need else 0)
+    lse_at, ws, ws_bytes = (lse.data_ptr() if want_lse else None), *((workspace.data_ptr(), workspace.numel()) if need else (None, 0))
+    scale, causal = cache.dim ** -0.5 if scale is None else scale, 1 if causal else 0
+    if view is None:
+        _kv_call(dev, _lib.awq_kv_attention, c, b, q, _KV_TYPES[dtype], q_heads, q_stride, max_rows or 0, scale, causal, window, o,
+                 o_stride, lse_at, ws, ws_bytes)
+    else:
+        _kv_call(dev, _lib.awq_kv_attention_ex, c, b, view, q, _KV_TYPES[dtype], q_heads, q_stride, max_rows or 0, scale, causal, o,
+                 o_stride, lse_at, ws, ws_bytes)
     return (out, lse) if want_lse else out
 
 

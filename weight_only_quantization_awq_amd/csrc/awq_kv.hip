@@ -202,6 +202,71 @@ awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, i
     return AWQ_OK;
 }
 
+// The launches of one run, with its part of the workspace.
+awq_status launch(awq::KvAttend a, const Plan &p, awq_dtype t, unsigned char *ws, hipStream_t stream) {
+    a.split_cols = p.split_cols;
+    a.tiles_col = p.tiles_col;
+    a.workers = p.workers;
+    a.snap = p.snap;
+    a.units = p.units;
+    a.line = p.line;
+    a.wide_workers = p.wide_workers;
+    if (p.merge) {
+        a.items = reinterpret_cast<int2 *>(ws + p.items);
+        a.part_ml = reinterpret_cast<float *>(ws + p.part_ml);
+        a.part = reinterpret_cast<float *>(ws + p.part);
+    }
+    if (p.wide_merge) {
+        a.wide_items = reinterpret_cast<int2 *>(ws + p.wide_items);
+        a.wide_ml = reinterpret_cast<float *>(ws + p.wide_ml);
+        a.wide_part = reinterpret_cast<float *>(ws + p.wide_part);
+    }
+    hipError_t h;
+    if (a.c.dim == 64)
+        h = awq::launch_kv_attend_64(a, t, p.split, p.wide, p.merge, stream);
+    else if (a.c.dim == 128)
+        h = awq::launch_kv_attend_128(a, t, p.split, p.wide, p.merge, stream);
+    else
+        h = awq::launch_kv_attend_256(a, t, p.split, p.wide, p.merge, stream);
+    return kv_hip_status(h, "awq_kv_attention launch");
+}
+
+// A call: one run, or with a shared prefix two, one behind the other, which use the
+// same part of the workspace; what the first leaves for the second lies behind it.
+struct Call {
+    awq::KvAttend a;
+    Plan plan, first;
+    awq::KvBatch prefix_s;   // all rows as one sequence over the prefix
+    bool prefix;
+    size_t join, join_ml, total;
+};
+
+awq_status plan_call(const awq_kv_cache *cache, const awq_kv_batch *batch, const awq_kv_view *view, int64_t q_heads,
+                     int64_t max_rows, Call *x) {
+    if (!view) return kv_fail(AWQ_ERR_ARG, "view must be non-NULL");
+    awq_status e = plan(x->a.c, x->a.s, q_heads, max_rows, &x->plan);
+    if (e != AWQ_OK) return e;
+    x->total = x->plan.total;
+    x->prefix = view->prefix_len != nullptr;
+    if (!x->prefix) return AWQ_OK;
+    awq_kv_batch all = *batch;
+    all.batch = 1;
+    all.max_pages = view->prefix_pages;
+    all.row_start = nullptr;
+    all.kv_len = view->prefix_len;
+    all.block_table = view->prefix_table;
+    awq::KvCache c;
+    if (view->prefix_pages < 1 || view->prefix_pages > kKvMaxCount)
+        return kv_fail(AWQ_ERR_SHAPE, "prefix_pages must be >= 1 (got %lld)", static_cast<long long>(view->prefix_pages));
+    if ((e = kv_check(cache, &all, &c, &x->prefix_s, true)) != AWQ_OK) return e;
+    if ((e = plan(c, x->prefix_s, q_heads, 0, &x->first)) != AWQ_OK) return e;
+    const size_t heads = static_cast<size_t>(batch->rows) * static_cast<size_t>(q_heads);
+    x->join_ml = x->plan.total > x->first.total ? x->plan.total : x->first.total;
+    x->join = x->join_ml + (heads * 8 + 255) / 256 * 256;
+    x->total = x->join + (heads * cache->dim * 4 + 255) / 256 * 256;
+    return AWQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -229,41 +294,52 @@ awq_status awq_kv_read(const awq_kv_cache *cache, const awq_kv_batch *batch, voi
     return kv_hip_status(awq::launch_kv_read(c, s, K, V, t, k_stride, v_stride, stream), "awq_kv_read launch");
 }
 
-size_t awq_kv_attention_workspace_size(const awq_kv_cache *cache, const awq_kv_batch *batch, int64_t q_heads,
-                                       int64_t max_rows) {
+size_t awq_kv_attention_workspace_size_ex(const awq_kv_cache *cache, const awq_kv_batch *batch, const awq_kv_view *view,
+                                          int64_t q_heads, int64_t max_rows) {
     awq::report_error(AWQ_OK, "");
-    awq::KvCache c{};
-    awq::KvBatch s{};
-    Plan p{};
-    if (kv_check(cache, batch, &c, &s, true) != AWQ_OK || plan(c, s, q_heads, max_rows, &p) != AWQ_OK) return 0;
-    return p.total;
+    Call x{};
+    if (kv_check(cache, batch, &x.a.c, &x.a.s, true) != AWQ_OK || plan_call(cache, batch, view, q_heads, max_rows, &x) != AWQ_OK) return 0;
+    return x.total;
 }
 
-awq_status awq_kv_attention(const awq_kv_cache *cache, const awq_kv_batch *batch, const void *Q, awq_dtype t,
-                            int64_t q_heads, int64_t q_stride, int64_t max_rows, float scale, int causal,
-                            int64_t window, void *O, int64_t o_stride, float *lse, void *workspace,
-                            size_t workspace_bytes, hipStream_t stream) {
+size_t awq_kv_attention_workspace_size(const awq_kv_cache *cache, const awq_kv_batch *batch, int64_t q_heads,
+                                       int64_t max_rows) {
+    const awq_kv_view view{};
+    return awq_kv_attention_workspace_size_ex(cache, batch, &view, q_heads, max_rows);
+}
+
+awq_status awq_kv_attention_ex(const awq_kv_cache *cache, const awq_kv_batch *batch, const awq_kv_view *view, const void *Q,
+                               awq_dtype t, int64_t q_heads, int64_t q_stride, int64_t max_rows, float scale, int causal, void *O,
+                               int64_t o_stride, float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream) {
     awq::report_error(AWQ_OK, "");
-    awq::KvAttend a{};
-    Plan p{};
+    Call x{};
+    awq::KvAttend &a = x.a;
     awq_status e = kv_check(cache, batch, &a.c, &a.s);
     if (e != AWQ_OK) return e;
     if (t != AWQ_BF16 && t != AWQ_F16) return kv_fail(AWQ_ERR_DTYPE, "Q must be AWQ_BF16 or AWQ_F16 (got %d)", static_cast<int>(t));
-    if ((e = plan(a.c, a.s, q_heads, max_rows, &p)) != AWQ_OK) return e;
+    if ((e = plan_call(cache, batch, view, q_heads, max_rows, &x)) != AWQ_OK) return e;
     const int64_t least = q_heads * cache->dim;
     if ((e = kv_check_rows(Q, "Q", t, batch->rows, q_stride, least)) != AWQ_OK) return e;
     if ((e = kv_check_rows(O, "O", t, batch->rows, o_stride, least)) != AWQ_OK) return e;
     if (!kv_aligned(lse, 4)) return kv_fail(AWQ_ERR_ARG, "lse must be 4-byte aligned");
     if (!(scale > 0.0f) || !isfinite(scale)) return kv_fail(AWQ_ERR_ARG, "scale must be positive and finite (got %g)", scale);
     if (causal != 0 && causal != 1) return kv_fail(AWQ_ERR_ARG, "causal must be 0 or 1 (got %d)", causal);
+    const int64_t window = view->window, sinks = view->sinks;
     if (window < 0) return kv_fail(AWQ_ERR_ARG, "window must be >= 0 (0: none)");
     if (window > 0 && !causal) return kv_fail(AWQ_ERR_ARG, "a window needs causal = 1");
+    if (sinks < 0) return kv_fail(AWQ_ERR_ARG, "sinks must be >= 0 (0: none)");
+    if (sinks > 0 && window == 0) return kv_fail(AWQ_ERR_ARG, "sinks need a window");
+    if (x.prefix) {
+        if (window > 0) return kv_fail(AWQ_ERR_ARG, "a shared prefix and a window exclude each other");
+        if (!view->prefix_table || !kv_aligned(view->prefix_table, 4) || !kv_aligned(view->prefix_len, 4))
+            return kv_fail(AWQ_ERR_ARG, "prefix_table and prefix_len must be non-NULL, 4-byte aligned");
+    }
     if (batch->rows == 0) return AWQ_OK;
-    if (p.total > 0) {
-        if (!workspace) return kv_fail(AWQ_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", p.total);
+    if (x.total > 0) {
+        if (!workspace) return kv_fail(AWQ_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", x.total);
         if (!kv_aligned(workspace, 16)) return kv_fail(AWQ_ERR_WORKSPACE, "workspace must be 16-byte aligned");
-        if (workspace_bytes < p.total)
-            return kv_fail(AWQ_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", workspace_bytes, p.total);
+        if (workspace_bytes < x.total)
+            return kv_fail(AWQ_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", workspace_bytes, x.total);
     }
     a.Q = Q;
     a.O = O;
@@ -275,32 +351,33 @@ awq_status awq_kv_attention(const awq_kv_cache *cache, const awq_kv_batch *batch
     a.scale_log2 = scale * 1.44269504088896341f;
     a.causal = causal;
     a.window = window > (int64_t(1) << 30) ? 0 : static_cast<int>(window);   // (no sequence is longer)
-    a.split_cols = p.split_cols;
-    a.tiles_col = p.tiles_col;
-    a.workers = p.workers;
-    a.snap = p.snap;
-    a.units = p.units;
-    a.line = p.line;
-    a.wide_workers = p.wide_workers;
+    awq::KvView v{};
+    v.sinks = a.window == 0 ? 0 : static_cast<int>(sinks > kKvMaxCount ? kKvMaxCount : sinks);
+    if (v.sinks > 0 || x.prefix) a.view = &v;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
-    if (p.merge) {
-        a.items = reinterpret_cast<int2 *>(ws + p.items);
-        a.part_ml = reinterpret_cast<float *>(ws + p.part_ml);
-        a.part = reinterpret_cast<float *>(ws + p.part);
+    if (x.prefix) {
+        v.join = reinterpret_cast<float *>(ws + x.join);
+        v.join_ml = reinterpret_cast<float *>(ws + x.join_ml);
+        v.shared = 1;
+        v.own = a.s;
+        awq::KvAttend first = a;
+        first.s = x.prefix_s;
+        if ((e = launch(first, x.first, t, ws, stream)) != AWQ_OK) return e;
+        v.shared = 0;
+        v.prefix_len = view->prefix_len;
+        v.prefix_most = x.prefix_s.max_pages << a.c.page_shift;
     }
-    if (p.wide_merge) {
-        a.wide_items = reinterpret_cast<int2 *>(ws + p.wide_items);
-        a.wide_ml = reinterpret_cast<float *>(ws + p.wide_ml);
-        a.wide_part = reinterpret_cast<float *>(ws + p.wide_part);
-    }
-    hipError_t h;
-    if (a.c.dim == 64)
-        h = awq::launch_kv_attend_64(a, t, p.split, p.wide, p.merge, stream);
-    else if (a.c.dim == 128)
-        h = awq::launch_kv_attend_128(a, t, p.split, p.wide, p.merge, stream);
-    else
-        h = awq::launch_kv_attend_256(a, t, p.split, p.wide, p.merge, stream);
-    return kv_hip_status(h, "awq_kv_attention launch");
+    return launch(a, x.plan, t, ws, stream);
+}
+
+awq_status awq_kv_attention(const awq_kv_cache *cache, const awq_kv_batch *batch, const void *Q, awq_dtype t,
+                            int64_t q_heads, int64_t q_stride, int64_t max_rows, float scale, int causal,
+                            int64_t window, void *O, int64_t o_stride, float *lse, void *workspace,
+                            size_t workspace_bytes, hipStream_t stream) {
+    awq_kv_view view{};
+    view.window = window;
+    return awq_kv_attention_ex(cache, batch, &view, Q, t, q_heads, q_stride, max_rows, scale, causal, O, o_stride, lse, workspace,
+                               workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -200,10 +200,86 @@ __device__ __forceinline__ void kv_load(const KvAttend &a, int head, int tok, in
     load_words<NG>((kb & 1 ? pairs[1] : pairs[0]) + (kb >> 1) * P * (4 * NG) + n * (4 * NG), s.pair);
 }
 
-// Whether a position is one of lowest .. len - 1 (0 <= lowest <= len).
-__device__ __forceinline__ bool kv_seen(int p, int lowest, int len) {
+// Whether a position is one of lowest .. len - 1 (0 <= lowest <= len) or of the sinks before it.
+__device__ __forceinline__ bool kv_seen(const KvAttend &, int p, int lowest, int len) {
     return static_cast<uint32_t>(p - lowest) < static_cast<uint32_t>(len - lowest);
 }
+__device__ __forceinline__ bool kv_seen(const KvAttendView &a, int p, int lowest, int len) {
+    return (static_cast<uint32_t>(p - lowest) < static_cast<uint32_t>(len - lowest)) |
+           (static_cast<uint32_t>(p) < static_cast<uint32_t>(a.v.sinks < len ? a.v.sinks : len));
+}
+// A position as it compares with the first that a column sees: sinks lie behind all of them.
+// (A number, and opaque: joined conditions of a step's positions and columns take more scalar
+// registers than there are.)
+__device__ __forceinline__ int kv_place(const KvAttend &, int p) { return p; }
+__device__ __forceinline__ int kv_place(const KvAttendView &a, int p) {
+    int q = p < a.v.sinks ? INT32_MAX : p;
+    asm("" : "+v"(q));
+    return q;
+}
+// Whether one of the positions tok .. tok + tile - 1 may lie before some column's.
+__device__ __forceinline__ bool kv_some_before(const KvAttend &, int tok, int, int maxlow) { return tok < maxlow; }
+__device__ __forceinline__ bool kv_some_before(const KvAttendView &a, int tok, int tile, int maxlow) {
+    return tok < maxlow && tok + tile > a.v.sinks;
+}
+
+// Of the rows of a run over a shared prefix: the last position that row `row` of the call sees in
+// its own sequence, -1 where it sees nothing or there is no such sequence.
+__device__ __forceinline__ int kv_own_limit(const KvAttend &, int) { return -1; }
+__device__ __forceinline__ int kv_own_limit(const KvAttendView &a, int row) {
+    const KvBatch &s = a.v.own;
+    const int b = s.row_start ? kv_unit_sequence(s, row, 1, 1, 0) : row / s.even;
+    int r0, n;
+    kv_rows(s, b, r0, n);
+    if (row < r0 || row >= r0 + n) return -1;
+    const int len = kv_length(s, b, a.c.page_shift);
+    return a.causal ? len - n + (row - r0) : len - 1;
+}
+__device__ __forceinline__ int kv_wave_min(int x) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int y = __shfl_xor(x, d);
+        x = y < x ? y : x;
+    }
+    return __builtin_amdgcn_readfirstlane(x);
+}
+
+// Sums for the second run: of a column, and of 4 of its channels.
+__device__ __forceinline__ void kv_leave(const KvAttend &, int, int, float, float) {}
+__device__ __forceinline__ void kv_leave(const KvAttendView &a, int row, int qh, float m, float l) {
+    *reinterpret_cast<float2 *>(a.v.join_ml + 2 * (static_cast<int64_t>(row) * a.q_heads + qh)) = make_float2(m, l);
+}
+__device__ __forceinline__ void kv_leave4(const KvAttend &, int, int, int, floatx4) {}
+__device__ __forceinline__ void kv_leave4(const KvAttendView &a, int row, int qh, int d, floatx4 y) {
+    *reinterpret_cast<floatx4 *>(a.v.join + (static_cast<int64_t>(row) * a.q_heads + qh) * a.c.dim + d) = y;
+}
+
+// A column's sums (m, l) joined with those that the run over the shared prefix left for its row
+// and head: own *= f0 and prefix *= f1 make them one.  sees: the row sees some position (else
+// the prefix's sums mean nothing).
+struct KvJoin {
+    float f0 = 1.0f, f1 = 0.0f;
+    const float *part = nullptr;   // NULL: nothing to join
+    __device__ __forceinline__ KvJoin(const KvAttend &, int, int, bool, float &, float &) {}
+    __device__ __forceinline__ KvJoin(const KvAttendView &a, int row, int qh, bool sees, float &m, float &l) {
+        if (!a.v.join || !sees) return;
+        const int64_t at = static_cast<int64_t>(row) * a.q_heads + qh;
+        const float2 ml = *reinterpret_cast<const float2 *>(a.v.join_ml + 2 * at);
+        const float now = fmaxf(m, ml.x);
+        f0 = m == now ? 1.0f : __builtin_amdgcn_exp2f(m - now);
+        f1 = ml.x == now ? 1.0f : __builtin_amdgcn_exp2f(ml.x - now);
+        l = l * f0 + ml.y * f1;
+        m = now;
+        part = a.v.join + at * a.c.dim;
+    }
+    __device__ __forceinline__ floatx4 operator()(floatx4 y, int d) const {
+        if (!part) return y;
+        const floatx4 z = *reinterpret_cast<const floatx4 *>(part + d);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y[r] = y[r] * f0 + z[r] * f1;
+        return y;
+    }
+};
 
 // Orders a wave's LDS accesses for its own lanes: what one lane wrote, another reads, as other
 // types (float and uint16_t, read as vectors), so nothing else keeps the compiler from moving
@@ -216,12 +292,12 @@ __device__ __forceinline__ void kv_lds_order() {
 
 // A step's pairs into LDS.  Value pairs of tokens that do not exist, or that no row
 // sees, become zero (0 * NaN would not vanish).  One wave writes and reads them, in order.
-template <typename T, int D, int NG>
-__device__ __forceinline__ void kv_pairs(const KvAttend &a, const KvStep<D, NG> &s, int tok, int lowest, int len,
+template <typename T, int D, int NG, typename A>
+__device__ __forceinline__ void kv_pairs(const A &a, const KvStep<D, NG> &s, int tok, int lowest, int len,
                                          int lane, KvPairs<NG> *lds) {
     const int n = lane & 15, h = (lane >> 4) & 1;
     kv_lds_order();   // the tile before has been read
-    const bool there = (h ? s.ok1 : s.ok0) && kv_seen(tok + 16 * h + n, lowest, len);
+    const bool there = (h ? s.ok1 : s.ok0) && kv_seen(a, tok + 16 * h + n, lowest, len);
     if (lane < 32) {
         float *k = reinterpret_cast<float *>(&lds->k[h][0][0][0]) + 2 * n;
 #pragma unroll
@@ -253,16 +329,25 @@ struct KvWave {
     float m[NT], l[NT];               // reference (log2) and this lane's share of the sum
     int pos[NT], low[NT];             // last and first visible position (pos -1: no such column)
 
-    __device__ __forceinline__ void start(const KvAttend &a, int head, int r0, int n, int len, int col0, int lane) {
-        const int kb = lane >> 4;
+    // Returns the least of the columns' last visible positions.
+    template <typename A>
+    __device__ __forceinline__ int start(const A &a, int head, int r0, int n, int len, int col0, int lane) {
+        const int kb = lane >> 4, prefix = kv_prefix(a, len);
+        int least = a.causal ? len - n : len - 1;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int c = col0 + 16 * t + (lane & 15), i = c / a.per;
             const bool real = i < n;
             const T *src = static_cast<const T *>(a.Q) + (r0 + (real ? i : 0)) * a.q_stride +
                            static_cast<int64_t>(head * a.per + (c - i * a.per)) * D + 8 * kb;
-            pos[t] = real ? (a.causal ? len - n + i : len - 1) : -1;
-            low[t] = a.window ? len - n + i - a.window + 1 : 0;
+            pos[t] = real ? (a.causal && !kv_shared(a) ? len - n + i : len - 1) : -1;
+            low[t] = a.window ? len - n + i - a.window + 1 : prefix;
+            if (kv_shared(a)) {   // (what a row that sees nothing gets here is not joined)
+                const int limit = real ? kv_own_limit(a, i) : -1;
+                if (limit >= 0 && limit < pos[t]) pos[t] = limit;
+                const int least_here = kv_wave_min(real ? pos[t] : len - 1);
+                least = t == 0 || least_here < least ? least_here : least;
+            }
 #pragma unroll
             for (int g = 0; g < NG; ++g) qs[t][g] = 0.0f;
 #pragma unroll
@@ -285,10 +370,12 @@ struct KvWave {
             m[t] = -INFINITY;
             l[t] = 0.0f;
         }
+        return least;
     }
 
     // Tokens tok .. tok+31.  edge: some of them may be hidden from some column.
-    __device__ __forceinline__ void step(const KvAttend &a, const KvStep<D, NG> &s, int tok, int lowest, int len,
+    template <typename A>
+    __device__ __forceinline__ void step(const A &a, const KvStep<D, NG> &s, int tok, int lowest, int len,
                                          bool edge, int lane, KvPairs<NG> *lds) {
         const int kb = lane >> 4;
         kv_pairs<T>(a, s, tok, lowest, len, lane, lds);
@@ -324,10 +411,11 @@ struct KvWave {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int p = tok + 16 * h + 4 * kb + r;
+                    const int place = kv_place(a, p);
                     const bool there = h ? s.ok1 : s.ok0;
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
-                        if (!there || p > pos[t] || p < low[t]) x[h][t][r] = -INFINITY;
+                        if (!there || p > pos[t] || place < low[t]) x[h][t][r] = -INFINITY;
                 }
         }
         half8 p[NT];
@@ -395,42 +483,51 @@ struct KvWave {
         }
     }
 
-    // Tokens of tiles t0 .. t1-1 of one sequence and head.  The loads of the next tile,
-    // and the page numbers of the one after, are in flight while a tile is computed
-    // (loads two or three tiles ahead cost registers and with them waves: 64 sequences of
-    // up to 8192 tokens 31 -> 39 and 50 us).  minpos / maxlow: the first last-visible and
-    // the last first-visible position of the columns.
-    __device__ __forceinline__ void run(const KvAttend &a, const int32_t *table, int head, int t0, int t1, int lowest,
-                                        int len, int minpos, int maxlow, int lane, KvPairs<NG> *lds) {
+    // Tokens of tiles t0 .. t1-1 of one sequence and head: sink_tiles from position 0 on, then those
+    // from `first` on.  The loads of the next tile, and the page numbers of the one after, are in
+    // flight while a tile is computed (loads two or three tiles ahead cost registers and with them
+    // waves: 64 sequences of up to 8192 tokens 31 -> 39 and 50 us).  minpos / maxlow: the first
+    // last-visible and the last first-visible position (behind the sinks) of the columns.
+    template <typename A>
+    __device__ __forceinline__ void run(const A &a, const int32_t *table, int head, int t0, int t1, int sink_tiles,
+                                        int first, int lowest, int len, int minpos, int maxlow, int lane, KvPairs<NG> *lds) {
         if (t0 >= t1) return;
         KvStep<D, NG> now, then;
-        int tok = t0 * kKvTile, p0 = -1, p1 = -1;
-        const int end = t1 * kKvTile;
+        const int gap = first - sink_tiles * kKvTile;   // (positions; sink_tiles is 0 without a view)
+        auto token = [&](int t) { return t * kKvTile + (t < sink_tiles ? 0 : gap); };
+        auto after = [&](int t) {
+            t += kKvTile;
+            return sink_tiles > 0 && t == sink_tiles * kKvTile ? first : t;
+        };
+        int tok = token(t0), p0 = -1, p1 = -1;
+        const int end = token(t1 - 1) + kKvTile;
         auto pages = [&](int t) {
             if (t < end) p0 = kv_page(a, table, t, len), p1 = kv_page(a, table, t + 16, len);
         };
         pages(tok);
         kv_load(a, head, tok, p0, p1, lane, now);
-        pages(tok + kKvTile);
+        pages(after(tok));
 #pragma unroll 1
         while (true) {
-            const int next = tok + kKvTile;
+            const int next = after(tok);
             if (next < end) {
                 kv_load(a, head, next, p0, p1, lane, then);
-                pages(next + kKvTile);
+                pages(after(next));
             }
-            step(a, now, tok, lowest, len, hides(now, tok, minpos, maxlow), lane, lds);
+            step(a, now, tok, lowest, len, hides(a, now, tok, minpos, maxlow), lane, lds);
             tok = next;
             if (tok >= end) return;
             now = then;
         }
     }
-    static __device__ __forceinline__ bool hides(const KvStep<D, NG> &s, int tok, int minpos, int maxlow) {
-        return tok + kKvTile - 1 > minpos || tok < maxlow || !s.ok0 || !s.ok1;   // (minpos < length)
+    template <typename A>
+    static __device__ __forceinline__ bool hides(const A &a, const KvStep<D, NG> &s, int tok, int minpos, int maxlow) {
+        return tok + kKvTile - 1 > minpos || kv_some_before(a, tok, kKvTile, maxlow) || !s.ok0 || !s.ok1;   // (minpos < length)
     }
 
     // Output and lse of the columns col0 .. of a sequence's rows.
-    __device__ __forceinline__ void finish(const KvAttend &a, int head, int r0, int n, int col0, int lane) {
+    template <typename A>
+    __device__ __forceinline__ void finish(const A &a, int head, int r0, int n, int len, int col0, int lane) {
         const int kb = lane >> 4;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -438,12 +535,20 @@ struct KvWave {
             l[t] += __shfl_xor(l[t], 16);
             l[t] += __shfl_xor(l[t], 32);
             if (i >= n) continue;
+            if (kv_shared(a)) {   // sums for the second run
+                if (kb == 0) kv_leave(a, r0 + i, h, m[t], l[t]);
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d) kv_leave4(a, r0 + i, h, 16 * d + 4 * kb, o[t][d]);
+                continue;
+            }
+            const KvJoin join(a, r0 + i, h, a.causal ? len - n + i >= 0 : len > 0, m[t], l[t]);
             const float inv = l[t] == 0.0f ? 0.0f : 1.0f / l[t];
             T *dst = static_cast<T *>(a.O) + (r0 + i) * a.o_stride + static_cast<int64_t>(h) * D + 4 * kb;
 #pragma unroll
-            for (int d = 0; d < D / 16; ++d)
-                *reinterpret_cast<uint2 *>(dst + 16 * d) =
-                    pack4<T>(o[t][d][0] * inv, o[t][d][1] * inv, o[t][d][2] * inv, o[t][d][3] * inv);
+            for (int d = 0; d < D / 16; ++d) {
+                const floatx4 y = join(o[t][d], 16 * d + 4 * kb);
+                *reinterpret_cast<uint2 *>(dst + 16 * d) = pack4<T>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+            }
             if (a.lse && kb == 0)
                 a.lse[static_cast<int64_t>(r0 + i) * a.q_heads + h] = kv_lse(m[t], l[t]);
         }
@@ -488,7 +593,8 @@ struct KvLine {
     int chunk, base;          // sequences 64*chunk ..; where the first one's items begin
     int length, upto, total;  // of one head: this lane's sequence, up to its end, all 64
 
-    __device__ __forceinline__ void load(const KvAttend &a, int c, int lane) {
+    template <typename A>
+    __device__ __forceinline__ void load(const A &a, int c, int lane) {
         chunk = c;
         int r0, n, len;
         const int b = 64 * c + lane, t = b < a.s.B ? kv_item_tiles(a, b, r0, n, len) : 0;
@@ -508,7 +614,8 @@ struct KvItem {
 };
 
 // The item at x (0 <= x < the line's length), at or behind the line's present chunk.
-__device__ __forceinline__ KvItem kv_locate(const KvAttend &a, KvLine &line, int x, int lane) {
+template <typename A>
+__device__ __forceinline__ KvItem kv_locate(const A &a, KvLine &line, int x, int lane) {
     const int H = a.c.heads;
     while (x >= line.base + H * line.total && 64 * (line.chunk + 1) < a.s.B) {
         line.base += H * line.total;
@@ -531,9 +638,8 @@ __device__ __forceinline__ KvItem kv_locate(const KvAttend &a, KvLine &line, int
     return it;
 }
 
-template <typename T, int D, int NG, int NT>
-__global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(kv_split_waves(D, NT)))) void kv_split_kernel(
-    KvAttend a) {
+template <typename T, int D, int NG, int NT, typename A>
+__global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(kv_split_waves(D, NT)))) void kv_split_kernel(A a) {
     const int lane = threadIdx.x;
     __shared__ KvPairs<NG> pairs;
     KvLine line;
@@ -554,15 +660,14 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(kv_split_wav
     while (true) {
         const int t1 = x1 >= it.end ? it.tiles : kv_cut(a, it.begin, it.tiles, x1);
         if (t0 < t1) {
-            const int first = kv_first_token(a, it.len, it.n) / kKvTile;
-            w.start(a, it.head, it.r0, it.n, it.len, 0, lane);
-            const int minpos = a.causal ? it.len - it.n : it.len - 1;
-            const int maxlow = a.window ? it.len - a.window : 0;
-            w.run(a, a.s.table + static_cast<int64_t>(it.b) * a.s.max_pages, it.head, first + t0, first + t1,
+            const int first = kv_first_token(a, it.len, it.n);
+            const int minpos = w.start(a, it.head, it.r0, it.n, it.len, 0, lane);
+            const int maxlow = a.window ? it.len - a.window : kv_prefix(a, it.len);
+            w.run(a, a.s.table + static_cast<int64_t>(it.b) * a.s.max_pages, it.head, t0, t1, kv_sink_tiles(a, first, kKvTile), first,
                   kv_lowest(a, it.len, it.n), it.len, minpos, maxlow, lane, &pairs);
             const bool direct = t0 == 0 && t1 == it.tiles;
             if (direct) {
-                w.finish(a, it.head, it.r0, it.n, 0, lane);
+                w.finish(a, it.head, it.r0, it.n, it.len, 0, lane);
             } else {
                 const int64_t at = kv_piece(a, worker, t0 == 0);
                 w.keep(a.part_ml + 2 * at, a.part + at * D, it.n * a.per, 0, lane);
@@ -580,11 +685,28 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(kv_split_wav
     }
 }
 
+// Channels d .. d+3 of a column whose pieces have been joined: its sums for the second run
+// (shared), or its output.
+template <typename T, int D, typename A>
+__device__ __forceinline__ void kv_put4(const A &a, int row, int qh, bool sees, int d, floatx4 y, float m, float l) {
+    if (kv_shared(a)) {
+        if (d == 0) kv_leave(a, row, qh, m, l);
+        kv_leave4(a, row, qh, d, y);
+        return;
+    }
+    const KvJoin join(a, row, qh, sees, m, l);
+    y = join(y, d);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    *reinterpret_cast<uint2 *>(static_cast<T *>(a.O) + row * a.o_stride + static_cast<int64_t>(qh) * D + d) =
+        pack4<T>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+    if (a.lse && d == 0) a.lse[static_cast<int64_t>(row) * a.q_heads + qh] = kv_lse(m, l);
+}
+
 // Joins the pieces of CH channels of one item's column: blockIdx = (item, column, channels).
 // CH/4 threads hold the channels, and 1024/CH groups of them take every (1024/CH)th
 // piece; the groups join in LDS.
-template <typename T, int D, int CH>
-__global__ __launch_bounds__(256) void kv_merge_kernel(KvAttend a) {
+template <typename T, int D, int CH, typename A>
+__global__ __launch_bounds__(256) void kv_merge_kernel(A a) {
     constexpr int kLanes = CH / 4, kGroups = 256 / kLanes;
     const int item = blockIdx.x, col = blockIdx.y;
     int2 it = a.items[item];
@@ -635,12 +757,8 @@ __global__ __launch_bounds__(256) void kv_merge_kernel(KvAttend a) {
         if (group < half) join(mls[group + half].x, mls[group + half].y, ys[group + half][x]);
     }
     if (group != 0) return;
-    const int i = col / a.per, h = head * a.per + col - i * a.per;
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    T *dst = static_cast<T *>(a.O) + (r0 + i) * a.o_stride + static_cast<int64_t>(h) * D + d;
-    *reinterpret_cast<uint2 *>(dst) = pack4<T>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
-    if (a.lse && d == 0)
-        a.lse[static_cast<int64_t>(r0 + i) * a.q_heads + h] = kv_lse(top, sum);
+    const int i = col / a.per, len = kv_length(a.s, b, a.c.page_shift);
+    kv_put4<T, D>(a, r0 + i, head * a.per + col - i * a.per, a.causal ? len - n + i >= 0 : len > 0, d, y, top, sum);
 }
 
 // ---------------------------------------------------------------------------
@@ -686,11 +804,12 @@ constexpr int kv_wide_threads(int dim) { return 2 * kv_wide_cols(dim); }
 
 // Unit u: a sequence's columns col0 .. (kv_wide_cols(D) of them at most), and the
 // tiles t0 .. t1-1 that some of them see (one at least, so that every unit is visited).
+// Tiles before sink_tiles (with sinks, t0 is 0) lie at t, the others `skip` tiles further on.
 struct KvUnit {
-    int b, r0, n, len, col0, t0, t1;
+    int b, r0, n, len, col0, t0, t1, sink_tiles, skip;
 };
-template <int D>
-__device__ __forceinline__ bool kv_unit(const KvAttend &a, int u, KvUnit &x) {
+template <int D, typename A>
+__device__ __forceinline__ bool kv_unit(const A &a, int u, KvUnit &x) {
     constexpr int kCols = kv_wide_cols(D), TT = kv_wide_tile(D);
     int k;
     if (a.s.row_start) {
@@ -708,10 +827,18 @@ __device__ __forceinline__ bool kv_unit(const KvAttend &a, int u, KvUnit &x) {
     x.len = kv_length(a.s, x.b, a.c.page_shift);
     const int p0 = x.len - x.n, last = static_cast<int>(cols) - 1;
     const int end = x.col0 + kCols - 1 < last ? x.col0 + kCols - 1 : last;
-    const int lo = a.window ? p0 + x.col0 / a.per - a.window + 1 : 0, hi = a.causal ? p0 + end / a.per + 1 : x.len;
+    const int lo = a.window ? p0 + x.col0 / a.per - a.window + 1 : kv_prefix(a, x.len);
+    const int hi = a.causal && !kv_shared(a) ? p0 + end / a.per + 1 : x.len;
     x.t0 = lo > 0 ? lo / TT : 0;
     x.t1 = hi > 0 ? (hi + TT - 1) / TT : 0;
     if (x.t1 <= x.t0) x.t1 = x.t0 + 1;
+    x.sink_tiles = kv_sink_tiles(a, x.t0 * TT, TT);
+    x.skip = 0;
+    if (x.sink_tiles > 0) {
+        x.skip = x.t0 - x.sink_tiles;
+        x.t1 -= x.skip;
+        x.t0 = 0;
+    }
     return true;
 }
 // The tile at which a boundary `at` behind an item's begin cuts it (0 or tiles: not inside).
@@ -792,7 +919,8 @@ struct KvWideLoad {
     }
 
     // Keys, and both pairs of this lane's token.
-    __device__ __forceinline__ void load_keys(const KvAttend &a, int head, int tok, int lowest, int len) {
+    template <typename A>
+    __device__ __forceinline__ void load_keys(const A &a, int head, int tok, int lowest, int len) {
         const int P = 1 << a.c.page_shift, at = tok + 16 * key_block(), slot = at & (P - 1), n = threadIdx.x & 15;
         const unsigned char *p = block(a, head, k_id, at, len, k_ok);
         load_words<KW>(p + slot * (D / 2) + static_cast<uint32_t>(n * (D / 2) + chunk() * (4 * KW)), k);
@@ -800,7 +928,7 @@ struct KvWideLoad {
         kp = *reinterpret_cast<const uint32_t *>(r + static_cast<uint32_t>(pair_from));
         vp = *reinterpret_cast<const uint32_t *>(r + P * (4 * NG) + static_cast<uint32_t>(pair_from));
         // a value that does not exist, or that no row sees, is worth zero (0 * NaN would not vanish)
-        v_there = kv_seen(at + n, lowest, len) && k_ok ? ~0u : 0u;
+        v_there = kv_seen(a, at + n, lowest, len) && k_ok ? ~0u : 0u;
     }
     __device__ __forceinline__ void load_values(const KvAttend &a, int head, int tok, int len) {
         const int P = 1 << a.c.page_shift;
@@ -859,8 +987,8 @@ struct KvWideLoad {
     }
 };
 
-template <typename T, int D, int NG>
-__device__ __forceinline__ void kv_wide_piece(const KvAttend &a, const KvUnit &unit, int head, int t0, int t1, int piece,
+template <typename T, int D, int NG, typename A>
+__device__ __forceinline__ void kv_wide_piece(const A &a, const KvUnit &unit, int head, int t0, int t1, int piece,
                                               uint4 (&ks)[2][1024], uint4 (&vs)[2][1024],
                                               float2 (&pairs)[3][NG * kv_wide_tile(D) + 1],
                                               uint32_t (&vpairs)[2][NG * kv_wide_tile(D) + 4],
@@ -874,14 +1002,21 @@ __device__ __forceinline__ void kv_wide_piece(const KvAttend &a, const KvUnit &u
     const int32_t *table = a.s.table + static_cast<int64_t>(unit.b) * a.s.max_pages;
     auto row_of = [&](int c) { return (c < last_col ? c : last_col) / a.per; };
     // where nothing is hidden from the wave's columns
-    const int minpos = a.causal ? p0 + row_of(col0) : len - 1;
-    const int maxlow = a.window ? p0 + row_of(col0 + 31) - a.window + 1 : 0;
+    int minpos = a.causal ? p0 + row_of(col0) : len - 1;
+    const int maxlow = a.window ? p0 + row_of(col0 + 31) - a.window + 1 : kv_prefix(a, len);
+    auto token = [&](int t) { return (t < unit.sink_tiles ? t : t + unit.skip) * TT; };
 
     // this lane's column: its queries, their sums, its visible positions
     typedef typename KvType<T>::vec8 vec8;
     const int col = col0 + n32, row = col / a.per;
     const bool real = row < n;
-    const int pos = real ? (a.causal ? p0 + row : len - 1) : -1, low = a.window ? p0 + row - a.window + 1 : 0;
+    int pos = real ? (a.causal && !kv_shared(a) ? p0 + row : len - 1) : -1;
+    const int low = a.window ? p0 + row - a.window + 1 : kv_prefix(a, len);
+    if (kv_shared(a)) {   // (what a row that sees nothing gets here is not joined)
+        const int limit = real ? kv_own_limit(a, row) : -1;
+        if (limit >= 0 && limit < pos) pos = limit;
+        minpos = kv_wave_min(real ? pos : len - 1);
+    }
     vec8 q[S];
     // Scores x are formed relative to ref: m, but no less than -kFloorLog2, and 0 before there is one.  Where m is
     // lower, limit sends every tile through the shift to m.  (x carries 2^-24 of its distance from ref: relative
@@ -1013,26 +1148,26 @@ __device__ __forceinline__ void kv_wide_piece(const KvAttend &a, const KvUnit &u
             for (int i = 0; i < in.KW; ++i) in.template unpack_key<T>(i, ks[t & 1]);
             in.template unpack_pair<T>(a, pairs[t % 3], vpairs[t & 1], lost[t % 3]);
         };
-        in.key_page(a, table, t0 * TT, len);
-        in.value_pages(a, table, t0 * TT, len);
-        in.load_keys(a, head, t0 * TT, lowest, len);
-        in.load_values(a, head, t0 * TT, len);
-        in.key_page(a, table, (t0 + 1) * TT, len);
-        in.value_pages(a, table, (t0 + 1) * TT, len);
+        in.key_page(a, table, token(t0), len);
+        in.value_pages(a, table, token(t0), len);
+        in.load_keys(a, head, token(t0), lowest, len);
+        in.load_values(a, head, token(t0), len);
+        in.key_page(a, table, token(t0 + 1), len);
+        in.value_pages(a, table, token(t0 + 1), len);
         keys(t0);
-        in.load_keys(a, head, (t0 + 1) * TT, lowest, len);
-        in.key_page(a, table, (t0 + 2) * TT, len);
+        in.load_keys(a, head, token(t0 + 1), lowest, len);
+        in.key_page(a, table, token(t0 + 2), len);
         __syncthreads();   // the pairs of V(t0)
 #pragma unroll
         for (int i = 0; i < 4 * in.VI; ++i) {
             if (i % 4 == 0) in.read_pairs(i / 4, vpairs[t0 & 1]);
             in.unpack_value(i / 4, i % 4, vs[t0 & 1]);
         }
-        in.load_values(a, head, (t0 + 1) * TT, len);
-        in.value_pages(a, table, (t0 + 2) * TT, len);
+        in.load_values(a, head, token(t0 + 1), len);
+        in.value_pages(a, table, token(t0 + 2), len);
         keys(t0 + 1);
-        in.load_keys(a, head, (t0 + 2) * TT, lowest, len);
-        in.key_page(a, table, (t0 + 3) * TT, len);
+        in.load_keys(a, head, token(t0 + 2), lowest, len);
+        in.key_page(a, table, token(t0 + 3), len);
         __syncthreads();
         start_scores(t0);
 #pragma unroll
@@ -1042,7 +1177,7 @@ __device__ __forceinline__ void kv_wide_piece(const KvAttend &a, const KvUnit &u
         for (int i = 0; i < 8 * SUB; ++i) relative(NG == 1 ? factors(t3, 0, i) : floatx4{}, i);
     }
     for (int t = t0; t < t1; ++t) {
-        const int tok = t * TT, buf = t & 1;
+        const int tok = token(t), buf = t & 1;
         const int n3 = t3 == 2 ? 0 : t3 + 1, w3 = t3 == 0 ? 2 : t3 - 1;   // (t + 1) % 3, (t + 2) % 3
         // K(t + 1) and V(t) are in LDS; K(t) and V(t - 1) have been read
         __syncthreads();
@@ -1052,13 +1187,13 @@ __device__ __forceinline__ void kv_wide_piece(const KvAttend &a, const KvUnit &u
             gone[e] = __builtin_amdgcn_readfirstlane(lost[t3][e]) != 0;
             some_gone |= gone[e];
         }
-        if (tok + TT - 1 > minpos || tok < maxlow || some_gone) {
+        if (tok + TT - 1 > minpos || kv_some_before(a, tok, TT, maxlow) || some_gone) {
 #pragma unroll
             for (int e = 0; e < SUB; ++e)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const int p = tok + 32 * e + 8 * (r >> 2) + 4 * h + (r & 3);
-                    if (p > pos || p < low || gone[2 * e + (r >> 3)]) x[e][r] = -INFINITY;
+                    if (p > pos || kv_place(a, p) < low || gone[2 * e + (r >> 3)]) x[e][r] = -INFINITY;
                     top = e + r == 0 ? x[0][0] : fmaxf(top, x[e][r]);
                 }
         }
@@ -1125,14 +1260,14 @@ __device__ __forceinline__ void kv_wide_piece(const KvAttend &a, const KvUnit &u
             if (slot < in.KW) in.template unpack_key<T>(slot, ks[buf]);
             if (slot == in.KW) {
                 in.template unpack_pair<T>(a, pairs[w3], vpairs[buf], lost[w3]);
-                in.load_keys(a, head, tok + 3 * TT, lowest, len);
+                in.load_keys(a, head, token(t + 3), lowest, len);
             }
             if (in.part_at(slot) >= 0) in.unpack_value(in.part_at(slot) / 4, in.part_at(slot) % 4, vs[buf ^ 1]);
             if (in.pairs_at(slot) >= 0) in.read_pairs(in.pairs_at(slot), vpairs[buf ^ 1]);
-            if (slot == in.kLoad) in.load_values(a, head, tok + 2 * TT, len);
+            if (slot == in.kLoad) in.load_values(a, head, token(t + 2), len);
             if (slot == kSlots - 1) {
-                in.key_page(a, table, tok + 4 * TT, len);
-                in.value_pages(a, table, tok + 3 * TT, len);
+                in.key_page(a, table, token(t + 4), len);
+                in.value_pages(a, table, token(t + 3), len);
             }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -1149,22 +1284,31 @@ __device__ __forceinline__ void kv_wide_piece(const KvAttend &a, const KvUnit &u
             for (int e = 0; e < 4; ++e)
                 *reinterpret_cast<floatx4 *>(a.wide_part + at * D + 32 * j + 8 * e + 4 * h) =
                     floatx4{o[j][4 * e], o[j][4 * e + 1], o[j][4 * e + 2], o[j][4 * e + 3]};
+    } else if (real && kv_shared(a)) {   // sums for the second run
+        if (h == 0) kv_leave(a, r0 + row, qh, m, l);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                kv_leave4(a, r0 + row, qh, 32 * j + 8 * e + 4 * h, floatx4{o[j][4 * e], o[j][4 * e + 1], o[j][4 * e + 2], o[j][4 * e + 3]});
     } else if (real) {
+        const KvJoin join(a, r0 + row, qh, a.causal ? p0 + row >= 0 : len > 0, m, l);
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         T *dst = static_cast<T *>(a.O) + (r0 + row) * a.o_stride + static_cast<int64_t>(qh) * D + 4 * h;
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                *reinterpret_cast<uint2 *>(dst + 32 * j + 8 * e) = pack4<T>(
-                    o[j][4 * e] * inv, o[j][4 * e + 1] * inv, o[j][4 * e + 2] * inv, o[j][4 * e + 3] * inv);
+            for (int e = 0; e < 4; ++e) {
+                const floatx4 y = join(floatx4{o[j][4 * e], o[j][4 * e + 1], o[j][4 * e + 2], o[j][4 * e + 3]}, 32 * j + 8 * e + 4 * h);
+                *reinterpret_cast<uint2 *>(dst + 32 * j + 8 * e) = pack4<T>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+            }
         if (a.lse && h == 0)
             a.lse[static_cast<int64_t>(r0 + row) * a.q_heads + qh] = kv_lse(m, l);
     }
 }
 
-template <typename T, int D, int NG>
-__global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(KvAttend a) {
+template <typename T, int D, int NG, typename A>
+__global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(A a) {
     constexpr int kThreads = kv_wide_threads(D), TT = kv_wide_tile(D);
     __shared__ uint4 ks[2][1024], vs[2][1024];
     __shared__ float2 pairs[3][NG * TT + 1];
@@ -1288,8 +1432,8 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(KvAttend a)
 }
 
 // Joins the pieces of one (unit, head), blockIdx.x: D/4 threads a column.
-template <typename T, int D>
-__global__ __launch_bounds__(256) void kv_wide_merge_kernel(KvAttend a) {
+template <typename T, int D, typename A>
+__global__ __launch_bounds__(256) void kv_wide_merge_kernel(A a) {
     constexpr int kLanes = D / 4, kPer = 256 / kLanes, kCols = kv_wide_cols(D);
     const int item = blockIdx.x, u = item / a.c.heads, head = item - u * a.c.heads;
     KvUnit unit;
@@ -1325,37 +1469,33 @@ __global__ __launch_bounds__(256) void kv_wide_merge_kernel(KvAttend a) {
             top = now;
         }
     }
-    const int h = head * a.per + col - row * a.per;
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    T *dst = static_cast<T *>(a.O) + (unit.r0 + row) * a.o_stride + static_cast<int64_t>(h) * D + d;
-    *reinterpret_cast<uint2 *>(dst) = pack4<T>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
-    if (a.lse && d == 0)
-        a.lse[static_cast<int64_t>(unit.r0 + row) * a.q_heads + h] = kv_lse(top, sum);
+    kv_put4<T, D>(a, unit.r0 + row, head * a.per + col - row * a.per, a.causal ? unit.len - unit.n + row >= 0 : unit.len > 0, d, y,
+                  top, sum);
 }
 
 // ---------------------------------------------------------------------------
 
-template <typename T, int D, int NG>
-hipError_t kv_attend_typed(const KvAttend &a, bool run_split, bool run_wide, bool merge, hipStream_t st) {
+template <typename T, int D, int NG, typename A>
+hipError_t kv_attend_typed(const A &a, bool run_split, bool run_wide, bool merge, hipStream_t st) {
     if (run_split) {
         const dim3 grid(static_cast<unsigned>(a.workers)), threads(64);
         if (a.tiles_col == 1)
-            hipLaunchKernelGGL((kv_split_kernel<T, D, NG, 1>), grid, threads, 0, st, a);
+            hipLaunchKernelGGL((kv_split_kernel<T, D, NG, 1, A>), grid, threads, 0, st, a);
         else if (a.tiles_col == 2)
-            hipLaunchKernelGGL((kv_split_kernel<T, D, NG, 2>), grid, threads, 0, st, a);
+            hipLaunchKernelGGL((kv_split_kernel<T, D, NG, 2, A>), grid, threads, 0, st, a);
         else if constexpr (D < 256)   // (awq_kv.hip takes at most 2 column tiles at 256 channels)
-            hipLaunchKernelGGL((kv_split_kernel<T, D, NG, 4>), grid, threads, 0, st, a);
+            hipLaunchKernelGGL((kv_split_kernel<T, D, NG, 4, A>), grid, threads, 0, st, a);
         const int64_t columns = static_cast<int64_t>(a.s.B) * a.c.heads * a.split_cols;
         if (merge && columns <= kKvMergeFew)
-            hipLaunchKernelGGL((kv_merge_kernel<T, D, 32>), dim3(a.s.B * a.c.heads, a.split_cols, D / 32), dim3(256), 0, st, a);
+            hipLaunchKernelGGL((kv_merge_kernel<T, D, 32, A>), dim3(a.s.B * a.c.heads, a.split_cols, D / 32), dim3(256), 0, st, a);
         else if (merge)
-            hipLaunchKernelGGL((kv_merge_kernel<T, D, D>), dim3(a.s.B * a.c.heads, a.split_cols), dim3(256), 0, st, a);
+            hipLaunchKernelGGL((kv_merge_kernel<T, D, D, A>), dim3(a.s.B * a.c.heads, a.split_cols), dim3(256), 0, st, a);
     }
     if (run_wide) {
-        hipLaunchKernelGGL((kv_wide_kernel<T, D, NG>), dim3(a.line && a.wide_workers > a.units * a.c.heads ? a.wide_workers : a.units * a.c.heads),
+        hipLaunchKernelGGL((kv_wide_kernel<T, D, NG, A>), dim3(a.line && a.wide_workers > a.units * a.c.heads ? a.wide_workers : a.units * a.c.heads),
                            dim3(kv_wide_threads(D)), 0, st, a);
         if (a.wide_items)
-            hipLaunchKernelGGL((kv_wide_merge_kernel<T, D>), dim3(a.units * a.c.heads, kv_wide_cols(D) / (1024 / D)),
+            hipLaunchKernelGGL((kv_wide_merge_kernel<T, D, A>), dim3(a.units * a.c.heads, kv_wide_cols(D) / (1024 / D)),
                                dim3(256), 0, st, a);
     }
     return hipGetLastError();
@@ -1363,6 +1503,13 @@ hipError_t kv_attend_typed(const KvAttend &a, bool run_split, bool run_wide, boo
 
 template <int D, int NG>
 hipError_t kv_attend_group(const KvAttend &a, int type, bool run_split, bool run_wide, bool merge, hipStream_t st) {
+    if (a.view) {
+        KvAttendView v;
+        static_cast<KvAttend &>(v) = a;
+        v.v = *a.view;
+        if (type == 1) return kv_attend_typed<__bf16, D, NG>(v, run_split, run_wide, merge, st);
+        return kv_attend_typed<_Float16, D, NG>(v, run_split, run_wide, merge, st);
+    }
     if (type == 1) return kv_attend_typed<__bf16, D, NG>(a, run_split, run_wide, merge, st);
     return kv_attend_typed<_Float16, D, NG>(a, run_split, run_wide, merge, st);
 }

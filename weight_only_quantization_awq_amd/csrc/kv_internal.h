@@ -77,6 +77,20 @@ __device__ __forceinline__ int kv_unit_sequence(const KvBatch &s, int u, int per
     return lo;
 }
 
+// What a call has besides, with sinks or a shared prefix.
+struct KvView {
+    int sinks;                    // first positions that stay visible under the window
+    // A prefix that all sequences share takes two runs: first of all rows over the prefix
+    // (shared = 1: `s` is one sequence of all rows, the prefix its length and table, `own` the
+    // sequences themselves), which leaves sums in `join`; then of each sequence over its own
+    // positions, from *prefix_len on, which joins them.
+    int shared;
+    KvBatch own;
+    const int32_t *prefix_len;    // NULL: no prefix, or the first run
+    int prefix_most;              // positions that the prefix's table holds
+    float *join, *join_ml;        // [T][q_heads][dim] and [..][2]; NULL: no prefix
+};
+
 struct KvAttend {
     KvCache c;
     KvBatch s;
@@ -99,7 +113,28 @@ struct KvAttend {
     int units, line, wide_workers;
     int2 *wide_items;             // [units*heads], as items; NULL where no unit is cut
     float *wide_part, *wide_ml;   // [wide_workers][2][kv_wide_cols][dim] and [..][2]
+    const KvView *view;           // (host memory) NULL: none
 };
+
+// The arguments of a kernel with a view.  Kernels and their functions take either type, A; what
+// only a view has is a constant for KvAttend, so that calls without one pay nothing for it.
+// (One kernel for both cost them 3% on long caches, 5% at dim 256 and 23%, 4 us, on items of
+// few tiles; fields set to constants in a copy of the arguments, which is then held in registers,
+// half of that.)
+struct KvAttendView : KvAttend {
+    KvView v;
+};
+__host__ __device__ __forceinline__ int kv_sinks(const KvAttend &) { return 0; }
+__host__ __device__ __forceinline__ int kv_sinks(const KvAttendView &a) { return a.v.sinks; }
+__host__ __device__ __forceinline__ bool kv_shared(const KvAttend &) { return false; }
+__host__ __device__ __forceinline__ bool kv_shared(const KvAttendView &a) { return a.v.shared != 0; }
+// Positions before this one lie in a shared prefix, which has been attended to already.
+__host__ __device__ __forceinline__ int kv_prefix(const KvAttend &, int) { return 0; }
+__host__ __device__ __forceinline__ int kv_prefix(const KvAttendView &a, int len) {
+    if (!a.v.prefix_len) return 0;
+    const int n = kv_clamp(*a.v.prefix_len, 0, a.v.prefix_most);
+    return n < len ? n : len;
+}
 
 // A sequence's columns are its query rows x the query heads of one key head.
 // Most columns of the split path (4 column tiles of 16, or 2 at dim 256, where the
@@ -147,25 +182,35 @@ constexpr int kv_split_waves(int dim, int nt) {
     return nt * dim <= 64 ? 4 : nt * dim <= 128 ? 3 : nt * dim <= 256 ? 2 : 1;
 }
 
-// First position that any of a sequence's rows sees: what lies before it is treated as
-// what lies behind its length, whatever its slots hold.
-__host__ __device__ __forceinline__ int kv_lowest(const KvAttend &a, int len, int n) {
-    if (!a.window) return 0;
+// First position behind the sinks that any of a sequence's rows sees: what lies before it is
+// treated as what lies behind its length, whatever its slots hold.
+template <typename A>
+__host__ __device__ __forceinline__ int kv_lowest(const A &a, int len, int n) {
+    if (!a.window) return kv_prefix(a, len);
     const int low = len - n - a.window + 1;
     return low > 0 ? low : 0;
 }
 
 // The split path's line (kv_attend.h).
-__host__ __device__ __forceinline__ int kv_first_token(const KvAttend &a, int len, int n) {
+template <typename A>
+__host__ __device__ __forceinline__ int kv_first_token(const A &a, int len, int n) {
     return kv_lowest(a, len, n) & ~(kKvTile - 1);
 }
-// Tiles of an item of sequence b; 0: not on the split path.
-__host__ __device__ __forceinline__ int kv_item_tiles(const KvAttend &a, int b, int &r0, int &n, int &len) {
+// Whole tiles of `tile` tokens before `first` (a multiple of it) that hold sinks.
+template <typename A>
+__host__ __device__ __forceinline__ int kv_sink_tiles(const A &a, int first, int tile) {
+    if (kv_sinks(a) == 0) return 0;
+    const int n = (kv_sinks(a) + tile - 1) / tile;
+    return n < first / tile ? n : first / tile;
+}
+// Tiles of an item of sequence b, the sinks' first; 0: not on the split path.
+template <typename A>
+__host__ __device__ __forceinline__ int kv_item_tiles(const A &a, int b, int &r0, int &n, int &len) {
     kv_rows(a.s, b, r0, n);
     len = kv_length(a.s, b, a.c.page_shift);
     if (n == 0 || static_cast<int64_t>(n) * a.per > a.split_cols) return 0;
-    const int t = (len - kv_first_token(a, len, n) + kKvTile - 1) / kKvTile;
-    return t > 0 ? t : 1;   // an empty item is visited, too: its output is zero
+    const int first = kv_first_token(a, len, n), t = (len - first + kKvTile - 1) / kKvTile;
+    return kv_sink_tiles(a, first, kKvTile) + (t > 0 ? t : 1);   // an empty item is visited, too: its output is zero
 }
 // Workers that share a line of this length, and where worker w's share begins (w = workers: the line's end).
 __host__ __device__ __forceinline__ int kv_workers(const KvAttend &a, int total) {
