@@ -841,6 +841,11 @@ __device__ __forceinline__ bool kv_unit(const A &a, int u, KvUnit &x) {
     }
     return true;
 }
+// Workgroups that share a line of this length.
+__device__ __forceinline__ int kv_wide_workers(const KvAttend &a, int total) {
+    const int most = total / kKvWideMinShare > 1 ? total / kKvWideMinShare : 1;
+    return a.wide_workers < most ? a.wide_workers : most;
+}
 // The tile at which a boundary `at` behind an item's begin cuts it (0 or tiles: not inside).
 __device__ __forceinline__ int kv_wide_cut(int at, int tiles) {
     const int t = at - kKvWideCost;
@@ -1362,7 +1367,8 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(A a) {
             atomicMax(&span, time);
         }
         __syncthreads();
-        if (tid == 0 && 5 * static_cast<int64_t>(span) * a.wide_workers > 6 * static_cast<int64_t>(H) * before[a.units]) jobs = 0;
+        if (tid == 0 && 5 * static_cast<int64_t>(span) * kv_wide_workers(a, H * before[a.units]) > 6 * static_cast<int64_t>(H) * before[a.units])
+            jobs = 0;
         __syncthreads();
     }
 
@@ -1374,8 +1380,7 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(A a) {
         bool whole = true, more = false;
         if (a.line) {
             const int all = __builtin_amdgcn_readfirstlane(before[a.units]), total = H * all;
-            const int most = total / kKvWideMinShare > 1 ? total / kKvWideMinShare : 1;
-            const int workers = a.wide_workers < most ? a.wide_workers : most;
+            const int workers = kv_wide_workers(a, total);
             const int whole_jobs = __builtin_amdgcn_readfirstlane(jobs);
             if (static_cast<int>(blockIdx.x) >= (whole_jobs > 0 ? whole_jobs : workers) || total == 0) return;
             // Workgroups go round the 8 XCDs; neighbours on the line, which read the same
