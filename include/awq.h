@@ -714,7 +714,7 @@ typedef struct {
  * Other arguments, results and the workspace's use as for awq_kv_attention, which is this
  * call with a view of its window.  The results with a prefix differ from those of
  * the same positions in one table by float32 roundings of the join.  The workspace then also
- * holds rows * q_heads * (dim + 2) float32.  Rows that see nothing of their sequence are
+ * holds 2 * rows * q_heads * (dim + 2) float32.  Rows that see nothing of their sequence are
  * computed against the prefix and left out of the results: padded slots cost time, not more.
  */
 size_t awq_kv_attention_workspace_size_ex(const awq_kv_cache *cache, const awq_kv_batch *batch, const awq_kv_view *view,

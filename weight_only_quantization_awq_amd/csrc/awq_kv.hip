@@ -140,13 +140,14 @@ using awq::kKvMaxCount;
 // The launches of one attention call and its workspace (byte offsets).
 struct Plan {
     bool split, wide, merge, line, wide_merge;
-    int snap, tiles_col, split_cols, workers, units, wide_workers;
-    size_t items, part_ml, part, wide_items, wide_ml, wide_part, total;
+    int snap, tiles_col, split_cols, workers, units, own_units, wide_workers;
+    size_t items, part_ml, part, wide_items, wide_ml, wide_part, own_ml, own, common_ml, common, total;
 };
 
 constexpr int kSimds = 4 * awq::kKvCus;
 
-awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, int64_t max_rows, Plan *p) {
+// prefix: the sequence of all rows over a shared prefix, or NULL.
+awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, int64_t max_rows, const awq::KvBatch *prefix, Plan *p) {
     if (q_heads < 1 || q_heads > 65535 || q_heads % c.heads != 0)
         return kv_fail(AWQ_ERR_SHAPE, "q_heads (%lld) must be a multiple of the cache's heads (%d)",
                     static_cast<long long>(q_heads), c.heads);
@@ -154,30 +155,39 @@ awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, i
     if (static_cast<int64_t>(s.T) * q_heads > kKvMaxCount) return kv_fail(AWQ_ERR_SHAPE, "rows * q_heads too large for one call");
     const int64_t per = q_heads / c.heads;
     const int64_t most = s.row_start ? (max_rows == 0 || max_rows > s.T ? s.T : max_rows) : s.even;
-    const int64_t cols = most * per, limit = awq::kv_split_cols(c.dim);
-    const int64_t tiles = (static_cast<int64_t>(s.max_pages) * (1 << c.page_shift) + awq::kKvTile - 1) / awq::kKvTile;
+    const int64_t cols = most * per, all_cols = prefix ? s.T * per : 0, limit = awq::kv_split_cols(c.dim);
+    const int64_t positions = static_cast<int64_t>(s.max_pages) << c.page_shift;
+    const int64_t all_positions = prefix ? static_cast<int64_t>(prefix->max_pages) << c.page_shift : 0;
+    auto in = [](int64_t n, int64_t size) { return (n + size - 1) / size; };
     *p = Plan{};
-    p->wide = cols > limit;
-    // Where the wide path runs, the split path is for its single tokens.
-    const int64_t need = p->wide ? per : cols;
-    p->split = need <= limit && (!p->wide || s.row_start);
+    const bool own_wide = cols > limit, all_wide = all_cols > limit, all_split = prefix && !all_wide;
+    p->wide = own_wide || all_wide;
+    // Where the sequences take the wide path, the split path is for their single tokens.
+    const int64_t need = own_wide ? per : all_split ? all_cols : cols;
+    p->split = need <= limit && (!own_wide || s.row_start);
     p->tiles_col = need <= 16 ? 1 : need <= 32 ? 2 : 4;
     // What a sequence's columns are compared with on the device is what the workspace holds for
     // each piece: one with more rows than max_rows is left out, not kept in too small a place.
-    p->split_cols = p->split ? static_cast<int>(p->wide ? 16 * p->tiles_col : need) : 0;
-    const int64_t line = s.B * static_cast<int64_t>(c.heads) * (tiles + awq::kKvItemCost);
-    const int64_t useful = (line + awq::kKvMinShare - 1) / awq::kKvMinShare;
+    p->split_cols = p->split ? static_cast<int>(own_wide ? 16 * p->tiles_col : need) : 0;
+    const int64_t own_tiles = in(positions, awq::kKvTile), all_tiles = all_split ? in(all_positions, awq::kKvTile) : 0;
+    const int64_t tiles = own_tiles > all_tiles ? own_tiles : all_tiles;
+    const int64_t line = c.heads * (s.B * (own_tiles + awq::kKvItemCost) + (all_split ? all_tiles + awq::kKvItemCost : 0));
+    if (line > kKvMaxCount) return kv_fail(AWQ_ERR_SHAPE, "batch * heads * pages too large for one call");
+    const int64_t useful = in(line, awq::kKvMinShare);
     const int64_t fill = kSimds * awq::kv_split_waves(c.dim, p->tiles_col);
     p->workers = static_cast<int>(useful < fill ? useful : fill);
     p->snap = static_cast<int>(tiles <= awq::kKvWhole ? tiles : awq::kKvSnap);
     p->merge = p->split && tiles > 2 * p->snap + 1;   // shorter items are never cut
-    const int64_t wide = awq::kv_wide_cols(c.dim);
-    p->units = static_cast<int>(s.row_start ? s.T * per / wide + s.B : s.B * ((s.even * per + wide - 1) / wide));
+    const int64_t wide = awq::kv_wide_cols(c.dim), tile = awq::kv_wide_tile(c.dim);
+    p->own_units = !own_wide ? 0 : static_cast<int>(s.row_start ? s.T * per / wide + s.B : s.B * in(s.even * per, wide));
+    const int64_t all_units = all_wide ? in(all_cols, wide) : 0;
+    p->units = static_cast<int>(p->own_units + all_units);
     const int64_t groups = static_cast<int64_t>(p->units) * c.heads;
-    const int64_t wide_tiles = (static_cast<int64_t>(s.max_pages) * (1 << c.page_shift) - 1) / awq::kv_wide_tile(c.dim) + 1;
-    const int64_t wide_line = groups * (wide_tiles + awq::kKvWideCost);
+    const int64_t own_wide_tiles = own_wide ? in(positions, tile) : 0, all_wide_tiles = all_wide ? in(all_positions, tile) : 0;
+    const int64_t wide_tiles = own_wide_tiles > all_wide_tiles ? own_wide_tiles : all_wide_tiles;
+    const int64_t wide_line = c.heads * (p->own_units * (own_wide_tiles + awq::kKvWideCost) + all_units * (all_wide_tiles + awq::kKvWideCost));
     p->line = p->wide && groups < awq::kKvLineUnits && wide_line <= kKvMaxCount;
-    const int64_t wide_useful = (wide_line + awq::kKvWideMinShare - 1) / awq::kKvWideMinShare;
+    const int64_t wide_useful = in(wide_line, awq::kKvWideMinShare);
     p->wide_workers = static_cast<int>(wide_useful < awq::kKvCus ? wide_useful : awq::kKvCus);
     p->wide_merge = p->line && wide_tiles > 2 * awq::kKvWideSnap + 1;
     size_t at = 0;
@@ -188,7 +198,7 @@ awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, i
     };
     if (p->merge) {
         const size_t n = static_cast<size_t>(p->workers) * 2 * p->split_cols;
-        p->items = take(static_cast<size_t>(s.B) * c.heads * 8);
+        p->items = take((static_cast<size_t>(s.B) + (prefix ? 1 : 0)) * c.heads * 8);
         p->part_ml = take(n * 8);
         p->part = take(n * c.dim * 4);
     }
@@ -198,73 +208,37 @@ awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, i
         p->wide_ml = take(n * 8);
         p->wide_part = take(n * c.dim * 4);
     }
+    if (prefix) {
+        const size_t heads = static_cast<size_t>(s.T) * static_cast<size_t>(q_heads);
+        p->own_ml = take(heads * 8);
+        p->own = take(heads * c.dim * 4);
+        p->common_ml = take(heads * 8);
+        p->common = take(heads * c.dim * 4);
+    }
     p->total = at;
     return AWQ_OK;
 }
 
-// The launches of one run, with its part of the workspace.
-awq_status launch(awq::KvAttend a, const Plan &p, awq_dtype t, unsigned char *ws, hipStream_t stream) {
-    a.split_cols = p.split_cols;
-    a.tiles_col = p.tiles_col;
-    a.workers = p.workers;
-    a.snap = p.snap;
-    a.units = p.units;
-    a.line = p.line;
-    a.wide_workers = p.wide_workers;
-    if (p.merge) {
-        a.items = reinterpret_cast<int2 *>(ws + p.items);
-        a.part_ml = reinterpret_cast<float *>(ws + p.part_ml);
-        a.part = reinterpret_cast<float *>(ws + p.part);
-    }
-    if (p.wide_merge) {
-        a.wide_items = reinterpret_cast<int2 *>(ws + p.wide_items);
-        a.wide_ml = reinterpret_cast<float *>(ws + p.wide_ml);
-        a.wide_part = reinterpret_cast<float *>(ws + p.wide_part);
-    }
-    hipError_t h;
-    if (a.c.dim == 64)
-        h = awq::launch_kv_attend_64(a, t, p.split, p.wide, p.merge, stream);
-    else if (a.c.dim == 128)
-        h = awq::launch_kv_attend_128(a, t, p.split, p.wide, p.merge, stream);
-    else
-        h = awq::launch_kv_attend_256(a, t, p.split, p.wide, p.merge, stream);
-    return kv_hip_status(h, "awq_kv_attention launch");
-}
-
-// A call: one run, or with a shared prefix two, one behind the other, which use the
-// same part of the workspace; what the first leaves for the second lies behind it.
-struct Call {
-    awq::KvAttend a;
-    Plan plan, first;
-    awq::KvBatch prefix_s;   // all rows as one sequence over the prefix
-    bool prefix;
-    size_t join, join_ml, total;
-};
-
-awq_status plan_call(const awq_kv_cache *cache, const awq_kv_batch *batch, const awq_kv_view *view, int64_t q_heads,
-                     int64_t max_rows, Call *x) {
-    if (!view) return kv_fail(AWQ_ERR_ARG, "view must be non-NULL");
-    awq_status e = plan(x->a.c, x->a.s, q_heads, max_rows, &x->plan);
-    if (e != AWQ_OK) return e;
-    x->total = x->plan.total;
-    x->prefix = view->prefix_len != nullptr;
-    if (!x->prefix) return AWQ_OK;
-    awq_kv_batch all = *batch;
-    all.batch = 1;
-    all.max_pages = view->prefix_pages;
-    all.row_start = nullptr;
-    all.kv_len = view->prefix_len;
-    all.block_table = view->prefix_table;
-    awq::KvCache c;
+// The prefix of a view as the kernels take it, in *all; false: refused.
+awq_status check_prefix(const awq_kv_cache *cache, const awq_kv_batch *batch, const awq_kv_view *view, awq::KvBatch *all) {
+    awq_kv_batch one = *batch;
+    one.batch = 1;
+    one.max_pages = view->prefix_pages;
+    one.row_start = nullptr;
+    one.kv_len = view->prefix_len;
+    one.block_table = view->prefix_table;
     if (view->prefix_pages < 1 || view->prefix_pages > kKvMaxCount)
         return kv_fail(AWQ_ERR_SHAPE, "prefix_pages must be >= 1 (got %lld)", static_cast<long long>(view->prefix_pages));
-    if ((e = kv_check(cache, &all, &c, &x->prefix_s, true)) != AWQ_OK) return e;
-    if ((e = plan(c, x->prefix_s, q_heads, 0, &x->first)) != AWQ_OK) return e;
-    const size_t heads = static_cast<size_t>(batch->rows) * static_cast<size_t>(q_heads);
-    x->join_ml = x->plan.total > x->first.total ? x->plan.total : x->first.total;
-    x->join = x->join_ml + (heads * 8 + 255) / 256 * 256;
-    x->total = x->join + (heads * cache->dim * 4 + 255) / 256 * 256;
-    return AWQ_OK;
+    awq::KvCache c;
+    return kv_check(cache, &one, &c, all, true);
+}
+
+awq_status plan_call(const awq::KvAttend &a, const awq_kv_cache *cache, const awq_kv_batch *batch, const awq_kv_view *view,
+                     int64_t q_heads, int64_t max_rows, awq::KvBatch *all, Plan *p) {
+    if (!view) return kv_fail(AWQ_ERR_ARG, "view must be non-NULL");
+    if (!view->prefix_len) return plan(a.c, a.s, q_heads, max_rows, nullptr, p);
+    const awq_status e = check_prefix(cache, batch, view, all);
+    return e != AWQ_OK ? e : plan(a.c, a.s, q_heads, max_rows, all, p);
 }
 
 }  // namespace
@@ -297,9 +271,13 @@ awq_status awq_kv_read(const awq_kv_cache *cache, const awq_kv_batch *batch, voi
 size_t awq_kv_attention_workspace_size_ex(const awq_kv_cache *cache, const awq_kv_batch *batch, const awq_kv_view *view,
                                           int64_t q_heads, int64_t max_rows) {
     awq::report_error(AWQ_OK, "");
-    Call x{};
-    if (kv_check(cache, batch, &x.a.c, &x.a.s, true) != AWQ_OK || plan_call(cache, batch, view, q_heads, max_rows, &x) != AWQ_OK) return 0;
-    return x.total;
+    awq::KvAttend a{};
+    awq::KvBatch all{};
+    Plan p{};
+    if (kv_check(cache, batch, &a.c, &a.s, true) != AWQ_OK ||
+        plan_call(a, cache, batch, view, q_heads, max_rows, &all, &p) != AWQ_OK)
+        return 0;
+    return p.total;
 }
 
 size_t awq_kv_attention_workspace_size(const awq_kv_cache *cache, const awq_kv_batch *batch, int64_t q_heads,
@@ -312,12 +290,13 @@ awq_status awq_kv_attention_ex(const awq_kv_cache *cache, const awq_kv_batch *ba
                                awq_dtype t, int64_t q_heads, int64_t q_stride, int64_t max_rows, float scale, int causal, void *O,
                                int64_t o_stride, float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream) {
     awq::report_error(AWQ_OK, "");
-    Call x{};
-    awq::KvAttend &a = x.a;
+    awq::KvAttend a{};
+    awq::KvBatch all{};
+    Plan p{};
     awq_status e = kv_check(cache, batch, &a.c, &a.s);
     if (e != AWQ_OK) return e;
     if (t != AWQ_BF16 && t != AWQ_F16) return kv_fail(AWQ_ERR_DTYPE, "Q must be AWQ_BF16 or AWQ_F16 (got %d)", static_cast<int>(t));
-    if ((e = plan_call(cache, batch, view, q_heads, max_rows, &x)) != AWQ_OK) return e;
+    if ((e = plan_call(a, cache, batch, view, q_heads, max_rows, &all, &p)) != AWQ_OK) return e;
     const int64_t least = q_heads * cache->dim;
     if ((e = kv_check_rows(Q, "Q", t, batch->rows, q_stride, least)) != AWQ_OK) return e;
     if ((e = kv_check_rows(O, "O", t, batch->rows, o_stride, least)) != AWQ_OK) return e;
@@ -329,17 +308,17 @@ awq_status awq_kv_attention_ex(const awq_kv_cache *cache, const awq_kv_batch *ba
     if (window > 0 && !causal) return kv_fail(AWQ_ERR_ARG, "a window needs causal = 1");
     if (sinks < 0) return kv_fail(AWQ_ERR_ARG, "sinks must be >= 0 (0: none)");
     if (sinks > 0 && window == 0) return kv_fail(AWQ_ERR_ARG, "sinks need a window");
-    if (x.prefix) {
+    if (view->prefix_len) {
         if (window > 0) return kv_fail(AWQ_ERR_ARG, "a shared prefix and a window exclude each other");
         if (!view->prefix_table || !kv_aligned(view->prefix_table, 4) || !kv_aligned(view->prefix_len, 4))
             return kv_fail(AWQ_ERR_ARG, "prefix_table and prefix_len must be non-NULL, 4-byte aligned");
     }
     if (batch->rows == 0) return AWQ_OK;
-    if (x.total > 0) {
-        if (!workspace) return kv_fail(AWQ_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", x.total);
+    if (p.total > 0) {
+        if (!workspace) return kv_fail(AWQ_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", p.total);
         if (!kv_aligned(workspace, 16)) return kv_fail(AWQ_ERR_WORKSPACE, "workspace must be 16-byte aligned");
-        if (workspace_bytes < x.total)
-            return kv_fail(AWQ_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", workspace_bytes, x.total);
+        if (workspace_bytes < p.total)
+            return kv_fail(AWQ_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", workspace_bytes, p.total);
     }
     a.Q = Q;
     a.O = O;
@@ -351,23 +330,39 @@ awq_status awq_kv_attention_ex(const awq_kv_cache *cache, const awq_kv_batch *ba
     a.scale_log2 = scale * 1.44269504088896341f;
     a.causal = causal;
     a.window = window > (int64_t(1) << 30) ? 0 : static_cast<int>(window);   // (no sequence is longer)
+    a.split_cols = p.split_cols;
+    a.tiles_col = p.tiles_col;
+    a.workers = p.workers;
+    a.snap = p.snap;
+    a.units = p.units;
+    a.line = p.line;
+    a.wide_workers = p.wide_workers;
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    auto floats = [&](size_t at) { return reinterpret_cast<float *>(ws + at); };
+    if (p.merge) {
+        a.items = reinterpret_cast<int2 *>(ws + p.items);
+        a.part_ml = floats(p.part_ml);
+        a.part = floats(p.part);
+    }
+    if (p.wide_merge) {
+        a.wide_items = reinterpret_cast<int2 *>(ws + p.wide_items);
+        a.wide_ml = floats(p.wide_ml);
+        a.wide_part = floats(p.wide_part);
+    }
     awq::KvView v{};
     v.sinks = a.window == 0 ? 0 : static_cast<int>(sinks > kKvMaxCount ? kKvMaxCount : sinks);
-    if (v.sinks > 0 || x.prefix) a.view = &v;
-    unsigned char *ws = static_cast<unsigned char *>(workspace);
-    if (x.prefix) {
-        v.join = reinterpret_cast<float *>(ws + x.join);
-        v.join_ml = reinterpret_cast<float *>(ws + x.join_ml);
-        v.shared = 1;
-        v.own = a.s;
-        awq::KvAttend first = a;
-        first.s = x.prefix_s;
-        if ((e = launch(first, x.first, t, ws, stream)) != AWQ_OK) return e;
-        v.shared = 0;
-        v.prefix_len = view->prefix_len;
-        v.prefix_most = x.prefix_s.max_pages << a.c.page_shift;
-    }
-    return launch(a, x.plan, t, ws, stream);
+    if (view->prefix_len)
+        v.prefix = {view->prefix_len, view->prefix_table, all.max_pages, p.own_units, floats(p.own), floats(p.own_ml),
+                    floats(p.common), floats(p.common_ml)};
+    if (v.sinks > 0 || view->prefix_len) a.view = &v;
+    hipError_t h;
+    if (a.c.dim == 64)
+        h = awq::launch_kv_attend_64(a, t, p.split, p.wide, p.merge, stream);
+    else if (a.c.dim == 128)
+        h = awq::launch_kv_attend_128(a, t, p.split, p.wide, p.merge, stream);
+    else
+        h = awq::launch_kv_attend_256(a, t, p.split, p.wide, p.merge, stream);
+    return kv_hip_status(h, "awq_kv_attention launch");
 }
 
 awq_status awq_kv_attention(const awq_kv_cache *cache, const awq_kv_batch *batch, const void *Q, awq_dtype t,

@@ -101,7 +101,7 @@ struct Turner {
 __device__ __forceinline__ bool row_position(const KvCache &c, const KvBatch &s, int row, int lane, int &position) {
     int b;
     if (s.row_start)
-        b = wave_sequence<1, 0>(s, row, lane);
+        b = kv_wave_sequence<1, 0>(s, row, lane);
     else
         b = row / s.even;
     int r0, n;

@@ -204,31 +204,45 @@ __device__ __forceinline__ void kv_load(const KvAttend &a, int head, int tok, in
 __device__ __forceinline__ bool kv_seen(const KvAttend &, int p, int lowest, int len) {
     return static_cast<uint32_t>(p - lowest) < static_cast<uint32_t>(len - lowest);
 }
-__device__ __forceinline__ bool kv_seen(const KvAttendView &a, int p, int lowest, int len) {
+__device__ __forceinline__ bool kv_seen(const KvAttendSinks &a, int p, int lowest, int len) {
     return (static_cast<uint32_t>(p - lowest) < static_cast<uint32_t>(len - lowest)) |
-           (static_cast<uint32_t>(p) < static_cast<uint32_t>(a.v.sinks < len ? a.v.sinks : len));
+           (static_cast<uint32_t>(p) < static_cast<uint32_t>(a.sinks < len ? a.sinks : len));
 }
 // A position as it compares with the first that a column sees: sinks lie behind all of them.
 // (A number, and opaque: joined conditions of a step's positions and columns take more scalar
 // registers than there are.)
 __device__ __forceinline__ int kv_place(const KvAttend &, int p) { return p; }
-__device__ __forceinline__ int kv_place(const KvAttendView &a, int p) {
-    int q = p < a.v.sinks ? INT32_MAX : p;
+__device__ __forceinline__ int kv_place(const KvAttendSinks &a, int p) {
+    int q = p < a.sinks ? INT32_MAX : p;
     asm("" : "+v"(q));
     return q;
 }
 // Whether one of the positions tok .. tok + tile - 1 may lie before some column's.
 __device__ __forceinline__ bool kv_some_before(const KvAttend &, int tok, int, int maxlow) { return tok < maxlow; }
-__device__ __forceinline__ bool kv_some_before(const KvAttendView &a, int tok, int tile, int maxlow) {
-    return tok < maxlow && tok + tile > a.v.sinks;
+__device__ __forceinline__ bool kv_some_before(const KvAttendSinks &a, int tok, int tile, int maxlow) {
+    return tok < maxlow && tok + tile > a.sinks;
 }
 
-// Of the rows of a run over a shared prefix: the last position that row `row` of the call sees in
-// its own sequence, -1 where it sees nothing or there is no such sequence.
-__device__ __forceinline__ int kv_own_limit(const KvAttend &, int) { return -1; }
-__device__ __forceinline__ int kv_own_limit(const KvAttendView &a, int row) {
-    const KvBatch &s = a.v.own;
-    const int b = s.row_start ? kv_unit_sequence(s, row, 1, 1, 0) : row / s.even;
+// Of the prefix's rows: the last position that row `row` of the call sees in its own sequence, -1
+// where it sees nothing or there is no such sequence.  All lanes of the wave call.
+__device__ __forceinline__ int kv_own_limit(const KvAttend &, int, int) { return -1; }
+__device__ __forceinline__ int kv_own_limit(const KvAttendPrefix &a, int row, int lane) {
+    const KvBatch &s = a.s;
+    int b;
+    if (!s.row_start) {
+        b = row / s.even;
+    } else if (s.B <= 64) {   // found among the lanes, without a load for each step
+        const int mine = lane < s.B ? kv_clamp(s.row_start[lane], 0, s.T) : INT32_MAX;
+        b = 0;
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) {
+            const int first = __shfl(mine, b + d);
+            if (first <= row) b += d;
+        }
+    } else {
+        b = kv_unit_sequence(s, row, 1, 1, 0);
+    }
+    b = b < s.B ? b : s.B - 1;
     int r0, n;
     kv_rows(s, b, r0, n);
     if (row < r0 || row >= r0 + n) return -1;
@@ -244,42 +258,17 @@ __device__ __forceinline__ int kv_wave_min(int x) {
     return __builtin_amdgcn_readfirstlane(x);
 }
 
-// Sums for the second run: of a column, and of 4 of its channels.
-__device__ __forceinline__ void kv_leave(const KvAttend &, int, int, float, float) {}
-__device__ __forceinline__ void kv_leave(const KvAttendView &a, int row, int qh, float m, float l) {
-    *reinterpret_cast<float2 *>(a.v.join_ml + 2 * (static_cast<int64_t>(row) * a.q_heads + qh)) = make_float2(m, l);
+// With a prefix, an item's sums go to memory whole: of a column, and of 4 of its channels.
+constexpr bool kv_to_sums(const KvAttend *) { return false; }
+constexpr bool kv_to_sums(const KvAttendPrefix *) { return true; }
+__device__ __forceinline__ void kv_leave(const KvAttend &, bool, int, int, float, float) {}
+__device__ __forceinline__ void kv_leave(const KvAttendPrefix &a, bool prefix, int row, int qh, float m, float l) {
+    *reinterpret_cast<float2 *>((prefix ? a.p.common_ml : a.p.own_ml) + 2 * (static_cast<int64_t>(row) * a.q_heads + qh)) = make_float2(m, l);
 }
-__device__ __forceinline__ void kv_leave4(const KvAttend &, int, int, int, floatx4) {}
-__device__ __forceinline__ void kv_leave4(const KvAttendView &a, int row, int qh, int d, floatx4 y) {
-    *reinterpret_cast<floatx4 *>(a.v.join + (static_cast<int64_t>(row) * a.q_heads + qh) * a.c.dim + d) = y;
+__device__ __forceinline__ void kv_leave4(const KvAttend &, bool, int, int, int, floatx4) {}
+__device__ __forceinline__ void kv_leave4(const KvAttendPrefix &a, bool prefix, int row, int qh, int d, floatx4 y) {
+    *reinterpret_cast<floatx4 *>((prefix ? a.p.common : a.p.own) + (static_cast<int64_t>(row) * a.q_heads + qh) * a.c.dim + d) = y;
 }
-
-// A column's sums (m, l) joined with those that the run over the shared prefix left for its row
-// and head: own *= f0 and prefix *= f1 make them one.  sees: the row sees some position (else
-// the prefix's sums mean nothing).
-struct KvJoin {
-    float f0 = 1.0f, f1 = 0.0f;
-    const float *part = nullptr;   // NULL: nothing to join
-    __device__ __forceinline__ KvJoin(const KvAttend &, int, int, bool, float &, float &) {}
-    __device__ __forceinline__ KvJoin(const KvAttendView &a, int row, int qh, bool sees, float &m, float &l) {
-        if (!a.v.join || !sees) return;
-        const int64_t at = static_cast<int64_t>(row) * a.q_heads + qh;
-        const float2 ml = *reinterpret_cast<const float2 *>(a.v.join_ml + 2 * at);
-        const float now = fmaxf(m, ml.x);
-        f0 = m == now ? 1.0f : __builtin_amdgcn_exp2f(m - now);
-        f1 = ml.x == now ? 1.0f : __builtin_amdgcn_exp2f(ml.x - now);
-        l = l * f0 + ml.y * f1;
-        m = now;
-        part = a.v.join + at * a.c.dim;
-    }
-    __device__ __forceinline__ floatx4 operator()(floatx4 y, int d) const {
-        if (!part) return y;
-        const floatx4 z = *reinterpret_cast<const floatx4 *>(part + d);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) y[r] = y[r] * f0 + z[r] * f1;
-        return y;
-    }
-};
 
 // Orders a wave's LDS accesses for its own lanes: what one lane wrote, another reads, as other
 // types (float and uint16_t, read as vectors), so nothing else keeps the compiler from moving
@@ -331,8 +320,8 @@ struct KvWave {
 
     // Returns the least of the columns' last visible positions.
     template <typename A>
-    __device__ __forceinline__ int start(const A &a, int head, int r0, int n, int len, int col0, int lane) {
-        const int kb = lane >> 4, prefix = kv_prefix(a, len);
+    __device__ __forceinline__ int start(const A &a, bool prefix, int common, int head, int r0, int n, int len, int col0, int lane) {
+        const int kb = lane >> 4;
         int least = a.causal ? len - n : len - 1;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -340,11 +329,11 @@ struct KvWave {
             const bool real = i < n;
             const T *src = static_cast<const T *>(a.Q) + (r0 + (real ? i : 0)) * a.q_stride +
                            static_cast<int64_t>(head * a.per + (c - i * a.per)) * D + 8 * kb;
-            pos[t] = real ? (a.causal && !kv_shared(a) ? len - n + i : len - 1) : -1;
-            low[t] = a.window ? len - n + i - a.window + 1 : prefix;
-            if (kv_shared(a)) {   // (what a row that sees nothing gets here is not joined)
-                const int limit = real ? kv_own_limit(a, i) : -1;
-                if (limit >= 0 && limit < pos[t]) pos[t] = limit;
+            pos[t] = real ? (a.causal && !prefix ? len - n + i : len - 1) : -1;
+            low[t] = kv_low(a, len, n, i, common);
+            if (prefix) {   // (what a row that sees nothing gets here is not joined)
+                const int limit = kv_own_limit(a, real ? i : 0, lane);
+                if (real && limit >= 0 && limit < pos[t]) pos[t] = limit;
                 const int least_here = kv_wave_min(real ? pos[t] : len - 1);
                 least = t == 0 || least_here < least ? least_here : least;
             }
@@ -527,7 +516,7 @@ struct KvWave {
 
     // Output and lse of the columns col0 .. of a sequence's rows.
     template <typename A>
-    __device__ __forceinline__ void finish(const A &a, int head, int r0, int n, int len, int col0, int lane) {
+    __device__ __forceinline__ void finish(const A &a, bool prefix, int head, int r0, int n, int col0, int lane) {
         const int kb = lane >> 4;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -535,20 +524,18 @@ struct KvWave {
             l[t] += __shfl_xor(l[t], 16);
             l[t] += __shfl_xor(l[t], 32);
             if (i >= n) continue;
-            if (kv_shared(a)) {   // sums for the second run
-                if (kb == 0) kv_leave(a, r0 + i, h, m[t], l[t]);
+            if constexpr (kv_to_sums(static_cast<const A *>(nullptr))) {
+                if (kb == 0) kv_leave(a, prefix, r0 + i, h, m[t], l[t]);
 #pragma unroll
-                for (int d = 0; d < D / 16; ++d) kv_leave4(a, r0 + i, h, 16 * d + 4 * kb, o[t][d]);
+                for (int d = 0; d < D / 16; ++d) kv_leave4(a, prefix, r0 + i, h, 16 * d + 4 * kb, o[t][d]);
                 continue;
             }
-            const KvJoin join(a, r0 + i, h, a.causal ? len - n + i >= 0 : len > 0, m[t], l[t]);
             const float inv = l[t] == 0.0f ? 0.0f : 1.0f / l[t];
             T *dst = static_cast<T *>(a.O) + (r0 + i) * a.o_stride + static_cast<int64_t>(h) * D + 4 * kb;
 #pragma unroll
-            for (int d = 0; d < D / 16; ++d) {
-                const floatx4 y = join(o[t][d], 16 * d + 4 * kb);
-                *reinterpret_cast<uint2 *>(dst + 16 * d) = pack4<T>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
-            }
+            for (int d = 0; d < D / 16; ++d)
+                *reinterpret_cast<uint2 *>(dst + 16 * d) =
+                    pack4<T>(o[t][d][0] * inv, o[t][d][1] * inv, o[t][d][2] * inv, o[t][d][3] * inv);
             if (a.lse && kb == 0)
                 a.lse[static_cast<int64_t>(r0 + i) * a.q_heads + h] = kv_lse(m[t], l[t]);
         }
@@ -594,10 +581,10 @@ struct KvLine {
     int length, upto, total;  // of one head: this lane's sequence, up to its end, all 64
 
     template <typename A>
-    __device__ __forceinline__ void load(const A &a, int c, int lane) {
+    __device__ __forceinline__ void load(const A &a, int c, int common, int lane) {
         chunk = c;
         int r0, n, len;
-        const int b = 64 * c + lane, t = b < a.s.B ? kv_item_tiles(a, b, r0, n, len) : 0;
+        const int b = 64 * c + lane, t = b < kv_count(a) ? kv_item_tiles(a, b, r0, n, len, common) : 0;
         length = t > 0 ? t + kKvItemCost : 0;
         upto = length;
 #pragma unroll
@@ -615,11 +602,11 @@ struct KvItem {
 
 // The item at x (0 <= x < the line's length), at or behind the line's present chunk.
 template <typename A>
-__device__ __forceinline__ KvItem kv_locate(const A &a, KvLine &line, int x, int lane) {
+__device__ __forceinline__ KvItem kv_locate(const A &a, KvLine &line, int x, int common, int lane) {
     const int H = a.c.heads;
-    while (x >= line.base + H * line.total && 64 * (line.chunk + 1) < a.s.B) {
+    while (x >= line.base + H * line.total && 64 * (line.chunk + 1) < kv_count(a)) {
         line.base += H * line.total;
-        line.load(a, line.chunk + 1, lane);
+        line.load(a, line.chunk + 1, common, lane);
     }
     const int y = x - line.base;
     const int k = kv_clamp(__popcll(__ballot(H * line.upto <= y)), 0, 63);
@@ -628,13 +615,12 @@ __device__ __forceinline__ KvItem kv_locate(const A &a, KvLine &line, int x, int
     length = length > 0 ? length : 1;
     KvItem it;
     it.b = 64 * line.chunk + k;
-    it.b = it.b < a.s.B ? it.b : a.s.B - 1;
+    it.b = it.b < kv_count(a) ? it.b : kv_count(a) - 1;
     it.head = kv_clamp((y - before) / length, 0, H - 1);
     it.begin = line.base + before + it.head * length;
     it.end = it.begin + length;
     it.tiles = length - kKvItemCost;
-    kv_rows(a.s, it.b, it.r0, it.n);
-    it.len = kv_length(a.s, it.b, a.c.page_shift);
+    kv_sequence(a, it.b, common, it.r0, it.n, it.len);
     return it;
 }
 
@@ -645,8 +631,9 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(kv_split_wav
     KvLine line;
     line.base = 0;
     int total = 0;
-    for (int c = (a.s.B - 1) / 64; c >= 0; --c) {   // (ends with chunk 0 loaded)
-        line.load(a, c, lane);
+    const int common = kv_common(a);
+    for (int c = (kv_count(a) - 1) / 64; c >= 0; --c) {   // (ends with chunk 0 loaded)
+        line.load(a, c, common, lane);
         total += line.total;
     }
     total *= a.c.heads;
@@ -655,19 +642,19 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(kv_split_wav
     const int x0 = kv_share(worker, total, workers), x1 = kv_share(worker + 1, total, workers);
 
     KvWave<T, D, NG, NT> w;
-    KvItem it = kv_locate(a, line, x0, lane);
+    KvItem it = kv_locate(a, line, x0, common, lane);
     int t0 = x0 == it.begin ? 0 : kv_cut(a, it.begin, it.tiles, x0);
     while (true) {
         const int t1 = x1 >= it.end ? it.tiles : kv_cut(a, it.begin, it.tiles, x1);
         if (t0 < t1) {
-            const int first = kv_first_token(a, it.len, it.n);
-            const int minpos = w.start(a, it.head, it.r0, it.n, it.len, 0, lane);
-            const int maxlow = a.window ? it.len - a.window : kv_prefix(a, it.len);
-            w.run(a, a.s.table + static_cast<int64_t>(it.b) * a.s.max_pages, it.head, t0, t1, kv_sink_tiles(a, first, kKvTile), first,
-                  kv_lowest(a, it.len, it.n), it.len, minpos, maxlow, lane, &pairs);
+            const bool prefix = kv_is_prefix(a, it.b);
+            const int before = prefix ? 0 : common, first = kv_first_token(a, it.len, it.n, before);
+            const int minpos = w.start(a, prefix, before, it.head, it.r0, it.n, it.len, 0, lane);
+            w.run(a, kv_table(a, it.b), it.head, t0, t1, kv_sink_tiles(a, first, kKvTile), first, kv_lowest(a, it.len, it.n, before),
+                  it.len, minpos, kv_low(a, it.len, it.n, it.n - 1, before), lane, &pairs);
             const bool direct = t0 == 0 && t1 == it.tiles;
             if (direct) {
-                w.finish(a, it.head, it.r0, it.n, it.len, 0, lane);
+                w.finish(a, prefix, it.head, it.r0, it.n, 0, lane);
             } else {
                 const int64_t at = kv_piece(a, worker, t0 == 0);
                 w.keep(a.part_ml + 2 * at, a.part + at * D, it.n * a.per, 0, lane);
@@ -680,33 +667,16 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(kv_split_wav
             }
         }
         if (it.end >= x1) return;
-        it = kv_locate(a, line, it.end, lane);
+        it = kv_locate(a, line, it.end, common, lane);
         t0 = 0;
     }
-}
-
-// Channels d .. d+3 of a column whose pieces have been joined: its sums for the second run
-// (shared), or its output.
-template <typename T, int D, typename A>
-__device__ __forceinline__ void kv_put4(const A &a, int row, int qh, bool sees, int d, floatx4 y, float m, float l) {
-    if (kv_shared(a)) {
-        if (d == 0) kv_leave(a, row, qh, m, l);
-        kv_leave4(a, row, qh, d, y);
-        return;
-    }
-    const KvJoin join(a, row, qh, sees, m, l);
-    y = join(y, d);
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    *reinterpret_cast<uint2 *>(static_cast<T *>(a.O) + row * a.o_stride + static_cast<int64_t>(qh) * D + d) =
-        pack4<T>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
-    if (a.lse && d == 0) a.lse[static_cast<int64_t>(row) * a.q_heads + qh] = kv_lse(m, l);
 }
 
 // Joins the pieces of CH channels of one item's column: blockIdx = (item, column, channels).
 // CH/4 threads hold the channels, and 1024/CH groups of them take every (1024/CH)th
 // piece; the groups join in LDS.
-template <typename T, int D, int CH, typename A>
-__global__ __launch_bounds__(256) void kv_merge_kernel(A a) {
+template <typename T, int D, int CH>
+__global__ __launch_bounds__(256) void kv_merge_kernel(KvAttend a) {
     constexpr int kLanes = CH / 4, kGroups = 256 / kLanes;
     const int item = blockIdx.x, col = blockIdx.y;
     int2 it = a.items[item];
@@ -757,8 +727,12 @@ __global__ __launch_bounds__(256) void kv_merge_kernel(A a) {
         if (group < half) join(mls[group + half].x, mls[group + half].y, ys[group + half][x]);
     }
     if (group != 0) return;
-    const int i = col / a.per, len = kv_length(a.s, b, a.c.page_shift);
-    kv_put4<T, D>(a, r0 + i, head * a.per + col - i * a.per, a.causal ? len - n + i >= 0 : len > 0, d, y, top, sum);
+    const int i = col / a.per, h = head * a.per + col - i * a.per;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    T *dst = static_cast<T *>(a.O) + (r0 + i) * a.o_stride + static_cast<int64_t>(h) * D + d;
+    *reinterpret_cast<uint2 *>(dst) = pack4<T>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+    if (a.lse && d == 0)
+        a.lse[static_cast<int64_t>(r0 + i) * a.q_heads + h] = kv_lse(top, sum);
 }
 
 // ---------------------------------------------------------------------------
@@ -808,27 +782,34 @@ constexpr int kv_wide_threads(int dim) { return 2 * kv_wide_cols(dim); }
 struct KvUnit {
     int b, r0, n, len, col0, t0, t1, sink_tiles, skip;
 };
+// Units of the sequences themselves; those of a prefix come behind them.
+__device__ __forceinline__ int kv_own_units(const KvAttend &a) { return a.units; }
+__device__ __forceinline__ int kv_own_units(const KvAttendPrefix &a) { return a.p.own_units; }
 template <int D, typename A>
-__device__ __forceinline__ bool kv_unit(const A &a, int u, KvUnit &x) {
+__device__ __forceinline__ bool kv_unit(const A &a, int u, int common, KvUnit &x) {
     constexpr int kCols = kv_wide_cols(D), TT = kv_wide_tile(D);
     int k;
-    if (a.s.row_start) {
+    if (u >= kv_own_units(a)) {
+        x.b = a.s.B;
+        k = u - kv_own_units(a);
+    } else if (a.s.row_start) {
         x.b = kv_unit_sequence(a.s, u, a.per, kCols, 1);
         k = u - kv_unit_first(a.s, x.b, a.per, kCols, 1);
     } else {
-        const int each = a.units / a.s.B;
+        const int each = kv_own_units(a) / a.s.B;
         x.b = u / each;
         k = u - x.b * each;
     }
-    kv_rows(a.s, x.b, x.r0, x.n);
+    if (x.b >= kv_count(a)) return false;   // (not in any launch)
+    kv_sequence(a, x.b, common, x.r0, x.n, x.len);
+    const bool prefix = kv_is_prefix(a, x.b);
     const int64_t cols = static_cast<int64_t>(x.n) * a.per;
     if (cols <= a.split_cols || k < 0 || static_cast<int64_t>(k) * kCols >= cols) return false;
     x.col0 = k * kCols;
-    x.len = kv_length(a.s, x.b, a.c.page_shift);
     const int p0 = x.len - x.n, last = static_cast<int>(cols) - 1;
     const int end = x.col0 + kCols - 1 < last ? x.col0 + kCols - 1 : last;
-    const int lo = a.window ? p0 + x.col0 / a.per - a.window + 1 : kv_prefix(a, x.len);
-    const int hi = a.causal && !kv_shared(a) ? p0 + end / a.per + 1 : x.len;
+    const int lo = kv_low(a, x.len, x.n, x.col0 / a.per, prefix ? 0 : common);
+    const int hi = a.causal && !prefix ? p0 + end / a.per + 1 : x.len;
     x.t0 = lo > 0 ? lo / TT : 0;
     x.t1 = hi > 0 ? (hi + TT - 1) / TT : 0;
     if (x.t1 <= x.t0) x.t1 = x.t0 + 1;
@@ -993,7 +974,7 @@ struct KvWideLoad {
 };
 
 template <typename T, int D, int NG, typename A>
-__device__ __forceinline__ void kv_wide_piece(const A &a, const KvUnit &unit, int head, int t0, int t1, int piece,
+__device__ __forceinline__ void kv_wide_piece(const A &a, const KvUnit &unit, int common, int head, int t0, int t1, int piece,
                                               uint4 (&ks)[2][1024], uint4 (&vs)[2][1024],
                                               float2 (&pairs)[3][NG * kv_wide_tile(D) + 1],
                                               uint32_t (&vpairs)[2][NG * kv_wide_tile(D) + 4],
@@ -1002,24 +983,26 @@ __device__ __forceinline__ void kv_wide_piece(const A &a, const KvUnit &unit, in
     constexpr int SUB = TT / 32;   // result tiles of 32 tokens x 32 columns a wave
     const int lane = threadIdx.x & 63, n32 = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r0 = unit.r0, n = unit.n, len = unit.len, p0 = len - n, lowest = kv_lowest(a, len, n);
+    const bool prefix = kv_is_prefix(a, unit.b);
+    const int before = prefix ? 0 : common;
+    const int r0 = unit.r0, n = unit.n, len = unit.len, p0 = len - n, lowest = kv_lowest(a, len, n, before);
     const int last_col = n * a.per - 1, col0 = unit.col0 + wave * 32;
-    const int32_t *table = a.s.table + static_cast<int64_t>(unit.b) * a.s.max_pages;
+    const int32_t *table = kv_table(a, unit.b);
     auto row_of = [&](int c) { return (c < last_col ? c : last_col) / a.per; };
     // where nothing is hidden from the wave's columns
     int minpos = a.causal ? p0 + row_of(col0) : len - 1;
-    const int maxlow = a.window ? p0 + row_of(col0 + 31) - a.window + 1 : kv_prefix(a, len);
+    const int maxlow = kv_low(a, len, n, row_of(col0 + 31), before);
     auto token = [&](int t) { return (t < unit.sink_tiles ? t : t + unit.skip) * TT; };
 
     // this lane's column: its queries, their sums, its visible positions
     typedef typename KvType<T>::vec8 vec8;
     const int col = col0 + n32, row = col / a.per;
     const bool real = row < n;
-    int pos = real ? (a.causal && !kv_shared(a) ? p0 + row : len - 1) : -1;
-    const int low = a.window ? p0 + row - a.window + 1 : kv_prefix(a, len);
-    if (kv_shared(a)) {   // (what a row that sees nothing gets here is not joined)
-        const int limit = real ? kv_own_limit(a, row) : -1;
-        if (limit >= 0 && limit < pos) pos = limit;
+    int pos = real ? (a.causal && !prefix ? p0 + row : len - 1) : -1;
+    const int low = kv_low(a, len, n, row, before);
+    if (prefix) {   // (what a row that sees nothing gets here is not joined)
+        const int limit = kv_own_limit(a, real ? row : 0, lane);
+        if (real && limit >= 0 && limit < pos) pos = limit;
         minpos = kv_wave_min(real ? pos : len - 1);
     }
     vec8 q[S];
@@ -1289,24 +1272,22 @@ __device__ __forceinline__ void kv_wide_piece(const A &a, const KvUnit &unit, in
             for (int e = 0; e < 4; ++e)
                 *reinterpret_cast<floatx4 *>(a.wide_part + at * D + 32 * j + 8 * e + 4 * h) =
                     floatx4{o[j][4 * e], o[j][4 * e + 1], o[j][4 * e + 2], o[j][4 * e + 3]};
-    } else if (real && kv_shared(a)) {   // sums for the second run
-        if (h == 0) kv_leave(a, r0 + row, qh, m, l);
+    } else if (real && kv_to_sums(static_cast<const A *>(nullptr))) {
+        if (h == 0) kv_leave(a, prefix, r0 + row, qh, m, l);
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                kv_leave4(a, r0 + row, qh, 32 * j + 8 * e + 4 * h, floatx4{o[j][4 * e], o[j][4 * e + 1], o[j][4 * e + 2], o[j][4 * e + 3]});
+                kv_leave4(a, prefix, r0 + row, qh, 32 * j + 8 * e + 4 * h, floatx4{o[j][4 * e], o[j][4 * e + 1], o[j][4 * e + 2], o[j][4 * e + 3]});
     } else if (real) {
-        const KvJoin join(a, r0 + row, qh, a.causal ? p0 + row >= 0 : len > 0, m, l);
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         T *dst = static_cast<T *>(a.O) + (r0 + row) * a.o_stride + static_cast<int64_t>(qh) * D + 4 * h;
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const floatx4 y = join(floatx4{o[j][4 * e], o[j][4 * e + 1], o[j][4 * e + 2], o[j][4 * e + 3]}, 32 * j + 8 * e + 4 * h);
-                *reinterpret_cast<uint2 *>(dst + 32 * j + 8 * e) = pack4<T>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
-            }
+            for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<uint2 *>(dst + 32 * j + 8 * e) = pack4<T>(
+                    o[j][4 * e] * inv, o[j][4 * e + 1] * inv, o[j][4 * e + 2] * inv, o[j][4 * e + 3] * inv);
         if (a.lse && h == 0)
             a.lse[static_cast<int64_t>(r0 + row) * a.q_heads + qh] = kv_lse(m, l);
     }
@@ -1324,11 +1305,11 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(A a) {
     __shared__ int jobs, span;                 // whole units to hand out instead of the line (0: none), and their time
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int H = a.c.heads;
+    const int H = a.c.heads, common = kv_common(a);
     if (a.line) {
         for (int i = tid; i < a.units; i += kThreads) {
             KvUnit unit;
-            before[i + 1] = kv_unit<D>(a, i, unit) ? unit.t1 - unit.t0 + kKvWideCost : 0;
+            before[i + 1] = kv_unit<D>(a, i, common, unit) ? unit.t1 - unit.t0 + kKvWideCost : 0;
         }
         if (tid == 0) before[0] = jobs = span = 0;
         __syncthreads();
@@ -1406,7 +1387,7 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(A a) {
             }
             const int item = head * all + __builtin_amdgcn_readfirstlane(before[lo]);
             const int length = __builtin_amdgcn_readfirstlane(before[lo + 1] - before[lo]), tiles = length - kKvWideCost;
-            if (length <= 0 || !kv_unit<D>(a, lo, unit)) return;   // (not unless the tables change under the call)
+            if (length <= 0 || !kv_unit<D>(a, lo, common, unit)) return;   // (not unless the tables change under the call)
             const int end = item + length;
             const int c0 = next_at < 0 ? kv_wide_cut(at - item, tiles) : 0;
             const int c1 = x1 >= end ? tiles : kv_wide_cut(x1 - item, tiles);
@@ -1427,22 +1408,22 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(A a) {
             __syncthreads();   // the piece before is done with LDS
         } else {
             head = blockIdx.x % H;
-            if (!kv_unit<D>(a, a.units - 1 - blockIdx.x / H, unit)) return;   // (the longest first)
+            if (!kv_unit<D>(a, a.units - 1 - blockIdx.x / H, common, unit)) return;   // (the longest first)
             t0 = unit.t0;
             t1 = unit.t1;
         }
-        kv_wide_piece<T, D, NG>(a, unit, head, t0, t1, whole ? -1 : piece, ks, vs, pairs, vpairs, lost);
+        kv_wide_piece<T, D, NG>(a, unit, common, head, t0, t1, whole ? -1 : piece, ks, vs, pairs, vpairs, lost);
         if (!more) return;
     }
 }
 
 // Joins the pieces of one (unit, head), blockIdx.x: D/4 threads a column.
-template <typename T, int D, typename A>
-__global__ __launch_bounds__(256) void kv_wide_merge_kernel(A a) {
+template <typename T, int D>
+__global__ __launch_bounds__(256) void kv_wide_merge_kernel(KvAttend a) {
     constexpr int kLanes = D / 4, kPer = 256 / kLanes, kCols = kv_wide_cols(D);
     const int item = blockIdx.x, u = item / a.c.heads, head = item - u * a.c.heads;
     KvUnit unit;
-    if (!kv_unit<D>(a, u, unit)) return;
+    if (!kv_unit<D>(a, u, 0, unit)) return;
     int2 it = a.wide_items[item];
     if (it.y <= 0 || it.x < 0 || it.x >= a.wide_workers) return;
     it.y = it.y < a.wide_workers - it.x ? it.y : a.wide_workers - it.x;   // (as in kv_merge_kernel)
@@ -1474,8 +1455,138 @@ __global__ __launch_bounds__(256) void kv_wide_merge_kernel(A a) {
             top = now;
         }
     }
-    kv_put4<T, D>(a, unit.r0 + row, head * a.per + col - row * a.per, a.causal ? unit.len - unit.n + row >= 0 : unit.len > 0, d, y,
-                  top, sum);
+    const int h = head * a.per + col - row * a.per;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    T *dst = static_cast<T *>(a.O) + (unit.r0 + row) * a.o_stride + static_cast<int64_t>(h) * D + d;
+    *reinterpret_cast<uint2 *>(dst) = pack4<T>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+    if (a.lse && d == 0)
+        a.lse[static_cast<int64_t>(unit.r0 + row) * a.q_heads + h] = kv_lse(top, sum);
+}
+
+// ---------------------------------------------------------------------------
+// The join of a call with a prefix: what each row and query head has got from its own sequence
+// and from the prefix, on either path, in pieces or whole.  A workgroup takes CHUNK channels of
+// 256 / (CHUNK/4) / GROUPS columns (row, query head), each with GROUPS groups of CHUNK/4 threads,
+// which take every GROUPSth piece and join in LDS.
+
+// Where the sums of one column lie: `count` pieces, the first (which begins the item) at `first`, the
+// others `step` further on each, of places of D channels; or one place in `part` (count 1, first 0).
+struct KvParts {
+    const float *ml, *part;
+    int64_t first, next;   // the first piece's place, and the second's
+    int64_t step;          // from the second on
+    int count;
+};
+template <int D>
+__device__ __forceinline__ KvParts kv_parts(const KvAttendPrefix &a, int b, int r0, int n, int row, int qh, bool prefix) {
+    const int head = qh / a.per, col = (row - r0) * a.per + (qh - head * a.per);
+    const int64_t at = static_cast<int64_t>(row) * a.q_heads + qh;
+    KvParts p = {prefix ? a.p.common_ml : a.p.own_ml, prefix ? a.p.common : a.p.own, at, at, 0, 1};
+    if (static_cast<int64_t>(n) * a.per <= a.split_cols) {
+        const int2 it = a.items ? a.items[b * a.c.heads + head] : make_int2(0, 0);
+        if (it.y > 0 && it.x >= 0 && it.x < a.workers) {
+            p.ml = a.part_ml, p.part = a.part;
+            p.first = kv_piece(a, it.x, true) + col;
+            p.next = kv_piece(a, it.x + 1, false) + col;
+            p.step = 2 * a.split_cols;
+            p.count = it.y < a.workers - it.x ? it.y : a.workers - it.x;   // (inside, should tables change under the call)
+        }
+        return p;
+    }
+    constexpr int kCols = kv_wide_cols(D);
+    int unit;
+    if (prefix)
+        unit = a.p.own_units;
+    else if (a.s.row_start)
+        unit = kv_unit_first(a.s, b, a.per, kCols, 1);
+    else
+        unit = b * (a.p.own_units / a.s.B);
+    unit += col / kCols;
+    const int2 it = a.wide_items && unit < a.units ? a.wide_items[static_cast<int64_t>(unit) * a.c.heads + head] : make_int2(0, 0);
+    if (it.y > 0 && it.x >= 0 && it.x < a.wide_workers) {
+        p.ml = a.wide_ml, p.part = a.wide_part;
+        p.first = (2 * static_cast<int64_t>(it.x) + 1) * kCols + col % kCols;
+        p.next = 2 * (static_cast<int64_t>(it.x) + 1) * kCols + col % kCols;
+        p.step = 2 * kCols;
+        p.count = it.y < a.wide_workers - it.x ? it.y : a.wide_workers - it.x;
+    }
+    return p;
+}
+
+template <typename T, int D, int CHUNK, int GROUPS>
+__global__ __launch_bounds__(256) void kv_join_kernel(KvAttendPrefix a) {
+    constexpr int kLanes = CHUNK / 4, kCols = 256 / kLanes / GROUPS;
+    const int x = threadIdx.x % kLanes, group = threadIdx.x / kLanes % GROUPS, lane = threadIdx.x & 63;
+    const int64_t column = static_cast<int64_t>(blockIdx.x) * kCols + threadIdx.x / kLanes / GROUPS;
+    const int d = blockIdx.y * CHUNK + 4 * x;
+    const bool there = column < static_cast<int64_t>(a.s.T) * a.q_heads;
+    const int row = there ? static_cast<int>(column / a.q_heads) : 0, qh = there ? static_cast<int>(column - static_cast<int64_t>(row) * a.q_heads) : 0;
+    int b = 0;
+    if (!a.s.row_start)
+        b = row / a.s.even;
+    else if (kCols == 1 || a.q_heads % kCols == 0)   // one row for the workgroup
+        b = kv_wave_sequence<1, 0>(a.s, __builtin_amdgcn_readfirstlane(row), lane);
+    else
+        b = kv_unit_sequence(a.s, row, 1, 1, 0);
+    int r0, n, len;
+    kv_sequence(static_cast<const KvAttend &>(a), b, 0, r0, n, len);
+    const bool mine = there && row >= r0 && row < r0 + n;
+    const bool sees = mine && (a.causal ? len - n + (row - r0) >= 0 : len > 0);   // (else neither has anything for it)
+    float top = -INFINITY, sum = 0.0f;
+    floatx4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto join = [&](float m, float l, floatx4 z) {
+        const float now = fmaxf(top, m);
+        const float f0 = top == now ? 1.0f : __builtin_amdgcn_exp2f(top - now);
+        const float f1 = m == now ? 1.0f : __builtin_amdgcn_exp2f(m - now);
+        sum = sum * f0 + l * f1;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y[r] = y[r] * f0 + z[r] * f1;
+        top = now;
+    };
+    if (sees) {
+        const KvParts own = kv_parts<D>(a, b, r0, n, row, qh, false), common = kv_parts<D>(a, a.s.B, 0, a.s.T, row, qh, true);
+        const int count = own.count + common.count;
+        constexpr int kAhead = 4;   // pieces in flight
+        for (int k0 = group; k0 < count; k0 += kAhead * GROUPS) {
+            float2 ml[kAhead];
+            floatx4 z[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                int k = k0 + i * GROUPS;
+                if (k >= count) break;
+                const bool second = k >= own.count;
+                k -= second ? own.count : 0;
+                const int64_t first = second ? common.first : own.first, next = second ? common.next : own.next;
+                const int64_t at = k == 0 ? first : next + (k - 1) * (second ? common.step : own.step);
+                ml[i] = *reinterpret_cast<const float2 *>((second ? common.ml : own.ml) + at * 2);
+                z[i] = *reinterpret_cast<const floatx4 *>((second ? common.part : own.part) + at * D + d);
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (k0 + i * GROUPS >= count) break;
+                join(ml[i].x, ml[i].y, z[i]);
+            }
+        }
+    }
+    if constexpr (GROUPS > 1) {
+        __shared__ floatx4 ys[256 / kLanes][kLanes];
+        __shared__ float2 mls[256 / kLanes];
+        const int mine_at = threadIdx.x / kLanes;
+        for (int half = GROUPS / 2; half > 0; half >>= 1) {
+            if (group >= half && group < 2 * half) {
+                ys[mine_at][x] = y;
+                if (x == 0) mls[mine_at] = make_float2(top, sum);
+            }
+            __syncthreads();
+            if (group < half) join(mls[mine_at + half].x, mls[mine_at + half].y, ys[mine_at + half][x]);
+        }
+        if (group != 0) return;
+    }
+    if (!mine) return;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    *reinterpret_cast<uint2 *>(static_cast<T *>(a.O) + row * a.o_stride + static_cast<int64_t>(qh) * D + d) =
+        pack4<T>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+    if (a.lse && d == 0) a.lse[column] = kv_lse(top, sum);
 }
 
 // ---------------------------------------------------------------------------
@@ -1491,27 +1602,44 @@ hipError_t kv_attend_typed(const A &a, bool run_split, bool run_wide, bool merge
         else if constexpr (D < 256)   // (awq_kv.hip takes at most 2 column tiles at 256 channels)
             hipLaunchKernelGGL((kv_split_kernel<T, D, NG, 4, A>), grid, threads, 0, st, a);
         const int64_t columns = static_cast<int64_t>(a.s.B) * a.c.heads * a.split_cols;
+        if (kv_to_sums(&a)) merge = false;   // (joined below)
         if (merge && columns <= kKvMergeFew)
-            hipLaunchKernelGGL((kv_merge_kernel<T, D, 32, A>), dim3(a.s.B * a.c.heads, a.split_cols, D / 32), dim3(256), 0, st, a);
+            hipLaunchKernelGGL((kv_merge_kernel<T, D, 32>), dim3(a.s.B * a.c.heads, a.split_cols, D / 32), dim3(256), 0, st, a);
         else if (merge)
-            hipLaunchKernelGGL((kv_merge_kernel<T, D, D, A>), dim3(a.s.B * a.c.heads, a.split_cols), dim3(256), 0, st, a);
+            hipLaunchKernelGGL((kv_merge_kernel<T, D, D>), dim3(a.s.B * a.c.heads, a.split_cols), dim3(256), 0, st, a);
     }
     if (run_wide) {
         hipLaunchKernelGGL((kv_wide_kernel<T, D, NG, A>), dim3(a.line && a.wide_workers > a.units * a.c.heads ? a.wide_workers : a.units * a.c.heads),
                            dim3(kv_wide_threads(D)), 0, st, a);
-        if (a.wide_items)
-            hipLaunchKernelGGL((kv_wide_merge_kernel<T, D, A>), dim3(a.units * a.c.heads, kv_wide_cols(D) / (1024 / D)),
+        if (a.wide_items && !kv_to_sums(&a))
+            hipLaunchKernelGGL((kv_wide_merge_kernel<T, D>), dim3(a.units * a.c.heads, kv_wide_cols(D) / (1024 / D)),
                                dim3(256), 0, st, a);
+    }
+    if constexpr (kv_to_sums(static_cast<const A *>(nullptr))) {
+        const int64_t columns = static_cast<int64_t>(a.s.T) * a.q_heads;
+        if (columns <= kKvMergeFew)
+            hipLaunchKernelGGL((kv_join_kernel<T, D, 32, 32>), dim3(columns, D / 32), dim3(256), 0, st, a);
+        else if (columns <= kKvJoinFew)
+            hipLaunchKernelGGL((kv_join_kernel<T, D, D, 1024 / D>), dim3(columns), dim3(256), 0, st, a);
+        else
+            hipLaunchKernelGGL((kv_join_kernel<T, D, D, 1>), dim3((columns + 1024 / D - 1) / (1024 / D)), dim3(256), 0, st, a);
     }
     return hipGetLastError();
 }
 
 template <int D, int NG>
 hipError_t kv_attend_group(const KvAttend &a, int type, bool run_split, bool run_wide, bool merge, hipStream_t st) {
-    if (a.view) {
-        KvAttendView v;
+    if (a.view && a.view->prefix.len) {
+        KvAttendPrefix v;
         static_cast<KvAttend &>(v) = a;
-        v.v = *a.view;
+        v.p = a.view->prefix;
+        if (type == 1) return kv_attend_typed<__bf16, D, NG>(v, run_split, run_wide, merge, st);
+        return kv_attend_typed<_Float16, D, NG>(v, run_split, run_wide, merge, st);
+    }
+    if (a.view) {
+        KvAttendSinks v;
+        static_cast<KvAttend &>(v) = a;
+        v.sinks = a.view->sinks;
         if (type == 1) return kv_attend_typed<__bf16, D, NG>(v, run_split, run_wide, merge, st);
         return kv_attend_typed<_Float16, D, NG>(v, run_split, run_wide, merge, st);
     }

@@ -77,18 +77,36 @@ __device__ __forceinline__ int kv_unit_sequence(const KvBatch &s, int u, int per
     return lo;
 }
 
-// What a call has besides, with sinks or a shared prefix.
+// kv_unit_sequence (1, SIZE, EXTRA) of a unit that is one for the wave, all of whose lanes call:
+// 64 sequences to a load, so that up to 64 cost one load's latency and not the six of a
+// search by halves (reading 4 sequences of up to 16384: 22.8 -> 21.5 us).  SIZE, EXTRA: of the
+// units (1 and 0: single rows).
+template <int SIZE = 4, int EXTRA = 2>
+__device__ __forceinline__ int kv_wave_sequence(const KvBatch &s, int unit, int lane) {
+    int lo = 0, n = s.B;
+    while (n > 1) {
+        const int step = (n + 63) >> 6, at = lane * step;
+        const int begun = __popcll(__ballot(at < n && kv_unit_first(s, lo + (at < n ? at : 0), 1, SIZE, EXTRA) <= unit));
+        const int from = begun > 0 ? (begun - 1) * step : 0;
+        lo += from;
+        n = n - from < step ? n - from : step;
+        if (begun == 0) break;   // (the first rows belong to no sequence)
+    }
+    return lo;
+}
+
+// A prefix that all sequences share is one more sequence, number B, behind the others: all rows
+// of the call over the prefix's pages.  The others begin at its end.  All sums then go to
+// memory, and one launch joins a row's own with the prefix's.
+struct KvPrefix {
+    const int32_t *len, *table;       // [1], [max_pages]
+    int max_pages, own_units;         // own_units: of the wide path, before the prefix's
+    float *own, *own_ml;              // [T][q_heads][dim] and [..][2]: sums of items that were not cut
+    float *common, *common_ml;        // the same of the prefix
+};
 struct KvView {
-    int sinks;                    // first positions that stay visible under the window
-    // A prefix that all sequences share takes two runs: first of all rows over the prefix
-    // (shared = 1: `s` is one sequence of all rows, the prefix its length and table, `own` the
-    // sequences themselves), which leaves sums in `join`; then of each sequence over its own
-    // positions, from *prefix_len on, which joins them.
-    int shared;
-    KvBatch own;
-    const int32_t *prefix_len;    // NULL: no prefix, or the first run
-    int prefix_most;              // positions that the prefix's table holds
-    float *join, *join_ml;        // [T][q_heads][dim] and [..][2]; NULL: no prefix
+    int sinks;                        // first positions that stay visible under the window
+    KvPrefix prefix;                  // len NULL: none
 };
 
 struct KvAttend {
@@ -116,24 +134,46 @@ struct KvAttend {
     const KvView *view;           // (host memory) NULL: none
 };
 
-// The arguments of a kernel with a view.  Kernels and their functions take either type, A; what
-// only a view has is a constant for KvAttend, so that calls without one pay nothing for it.
-// (One kernel for both cost them 3% on long caches, 5% at dim 256 and 23%, 4 us, on items of
-// few tiles; fields set to constants in a copy of the arguments, which is then held in registers,
-// half of that.)
-struct KvAttendView : KvAttend {
-    KvView v;
+// The arguments of the kernels with sinks, and with a shared prefix.  Kernels and their functions
+// take any of the three types, A; what only one of them has is a constant for the others, so
+// that calls without it pay nothing for it.  (One kernel for all cost calls without either 3% on
+// long caches, 5% at dim 256 and 23%, 4 us, on items of few tiles; fields set to constants in a
+// copy of the arguments, which is then held in registers, half of that.)
+struct KvAttendSinks : KvAttend {
+    int sinks;
+};
+struct KvAttendPrefix : KvAttend {
+    KvPrefix p;
 };
 __host__ __device__ __forceinline__ int kv_sinks(const KvAttend &) { return 0; }
-__host__ __device__ __forceinline__ int kv_sinks(const KvAttendView &a) { return a.v.sinks; }
-__host__ __device__ __forceinline__ bool kv_shared(const KvAttend &) { return false; }
-__host__ __device__ __forceinline__ bool kv_shared(const KvAttendView &a) { return a.v.shared != 0; }
-// Positions before this one lie in a shared prefix, which has been attended to already.
-__host__ __device__ __forceinline__ int kv_prefix(const KvAttend &, int) { return 0; }
-__host__ __device__ __forceinline__ int kv_prefix(const KvAttendView &a, int len) {
-    if (!a.v.prefix_len) return 0;
-    const int n = kv_clamp(*a.v.prefix_len, 0, a.v.prefix_most);
-    return n < len ? n : len;
+__host__ __device__ __forceinline__ int kv_sinks(const KvAttendSinks &a) { return a.sinks; }
+// Sequences, the prefix among them.
+__host__ __device__ __forceinline__ int kv_count(const KvAttend &a) { return a.s.B; }
+__host__ __device__ __forceinline__ int kv_count(const KvAttendPrefix &a) { return a.s.B + 1; }
+__host__ __device__ __forceinline__ bool kv_is_prefix(const KvAttend &, int) { return false; }
+__host__ __device__ __forceinline__ bool kv_is_prefix(const KvAttendPrefix &a, int b) { return b == a.s.B; }
+// Positions of the prefix.
+__host__ __device__ __forceinline__ int kv_common(const KvAttend &) { return 0; }
+__host__ __device__ __forceinline__ int kv_common(const KvAttendPrefix &a) {
+    return kv_clamp(*a.p.len, 0, a.p.max_pages << a.c.page_shift);
+}
+// Rows, length and pages of sequence b.
+__host__ __device__ __forceinline__ void kv_sequence(const KvAttend &a, int b, int, int &r0, int &n, int &len) {
+    kv_rows(a.s, b, r0, n);
+    len = kv_length(a.s, b, a.c.page_shift);
+}
+__host__ __device__ __forceinline__ void kv_sequence(const KvAttendPrefix &a, int b, int common, int &r0, int &n, int &len) {
+    if (b == a.s.B) {
+        r0 = 0, n = a.s.T, len = common;
+        return;
+    }
+    kv_sequence(static_cast<const KvAttend &>(a), b, common, r0, n, len);
+}
+__host__ __device__ __forceinline__ const int32_t *kv_table(const KvAttend &a, int b) {
+    return a.s.table + static_cast<int64_t>(b) * a.s.max_pages;
+}
+__host__ __device__ __forceinline__ const int32_t *kv_table(const KvAttendPrefix &a, int b) {
+    return b == a.s.B ? a.p.table : kv_table(static_cast<const KvAttend &>(a), b);
 }
 
 // A sequence's columns are its query rows x the query heads of one key head.
@@ -171,6 +211,9 @@ constexpr int kKvWhole = 6;
 // columns, dim 128, 131072 tokens: 52.5 -> 48.0 us in all; dim 256, 65536: 42.1 -> 34.0);
 // many are quicker with fewer workgroups (512 columns: 43.6 us and 44.9; 4096: 29.5 and 36.8).
 constexpr int kKvMergeFew = 256;
+// Up to so many columns (row and query head) the join of a call with a prefix gives each a
+// workgroup, whose threads share its pieces; more, which have few pieces each, share one.
+constexpr int64_t kKvJoinFew = 16384;
 // Waves of the split path that a SIMD holds at once, by the registers of a wave's
 // output (dim x 16*NT columns) and what comes with it: as many as do without spills, since
 // they hide each other's latency.  us with 1 / 2 / 3 / 4, at group 32 (the largest group has the
@@ -183,18 +226,28 @@ constexpr int kv_split_waves(int dim, int nt) {
 }
 
 // First position behind the sinks that any of a sequence's rows sees: what lies before it is
-// treated as what lies behind its length, whatever its slots hold.
-template <typename A>
-__host__ __device__ __forceinline__ int kv_lowest(const A &a, int len, int n) {
-    if (!a.window) return kv_prefix(a, len);
+// treated as what lies behind its length, whatever its slots hold.  common: positions of the
+// prefix that are not the sequence's own.
+__host__ __device__ __forceinline__ int kv_lowest(const KvAttend &a, int len, int n, int) {
+    if (!a.window) return 0;
     const int low = len - n - a.window + 1;
     return low > 0 ? low : 0;
+}
+__host__ __device__ __forceinline__ int kv_lowest(const KvAttendPrefix &, int len, int, int common) {
+    return common < len ? common : len;
+}
+// The same of the row at position len - n + i; not bounded.
+__host__ __device__ __forceinline__ int kv_low(const KvAttend &a, int len, int n, int i, int) {
+    return a.window ? len - n + i - a.window + 1 : 0;
+}
+__host__ __device__ __forceinline__ int kv_low(const KvAttendPrefix &a, int len, int n, int, int common) {
+    return kv_lowest(a, len, n, common);
 }
 
 // The split path's line (kv_attend.h).
 template <typename A>
-__host__ __device__ __forceinline__ int kv_first_token(const A &a, int len, int n) {
-    return kv_lowest(a, len, n) & ~(kKvTile - 1);
+__host__ __device__ __forceinline__ int kv_first_token(const A &a, int len, int n, int common) {
+    return kv_lowest(a, len, n, common) & ~(kKvTile - 1);
 }
 // Whole tiles of `tile` tokens before `first` (a multiple of it) that hold sinks.
 template <typename A>
@@ -205,11 +258,10 @@ __host__ __device__ __forceinline__ int kv_sink_tiles(const A &a, int first, int
 }
 // Tiles of an item of sequence b, the sinks' first; 0: not on the split path.
 template <typename A>
-__host__ __device__ __forceinline__ int kv_item_tiles(const A &a, int b, int &r0, int &n, int &len) {
-    kv_rows(a.s, b, r0, n);
-    len = kv_length(a.s, b, a.c.page_shift);
+__host__ __device__ __forceinline__ int kv_item_tiles(const A &a, int b, int &r0, int &n, int &len, int common = 0) {
+    kv_sequence(a, b, common, r0, n, len);
     if (n == 0 || static_cast<int64_t>(n) * a.per > a.split_cols) return 0;
-    const int first = kv_first_token(a, len, n), t = (len - first + kKvTile - 1) / kKvTile;
+    const int first = kv_first_token(a, len, n, kv_is_prefix(a, b) ? 0 : common), t = (len - first + kKvTile - 1) / kKvTile;
     return kv_sink_tiles(a, first, kKvTile) + (t > 0 ? t : 1);   // an empty item is visited, too: its output is zero
 }
 // Workers that share a line of this length, and where worker w's share begins (w = workers: the line's end).

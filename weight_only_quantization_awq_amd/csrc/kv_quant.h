@@ -59,24 +59,6 @@ struct Place {
     int slot;              // this lane's token within the page
 };
 
-// kv_unit_sequence (1, SIZE, EXTRA) of a unit that is one for the wave, all of whose lanes call:
-// 64 sequences to a load, so that up to 64 cost one load's latency and not the six of a
-// search by halves (reading 4 sequences of up to 16384: 22.8 -> 21.5 us).  SIZE, EXTRA: of the
-// units (1 and 0: single rows).
-template <int SIZE = 4, int EXTRA = 2>
-__device__ __forceinline__ int wave_sequence(const KvBatch &s, int unit, int lane) {
-    int lo = 0, n = s.B;
-    while (n > 1) {
-        const int step = (n + 63) >> 6, at = lane * step;
-        const int begun = __popcll(__ballot(at < n && kv_unit_first(s, lo + (at < n ? at : 0), 1, SIZE, EXTRA) <= unit));
-        const int from = begun > 0 ? (begun - 1) * step : 0;
-        lo += from;
-        n = n - from < step ? n - from : step;
-        if (begun == 0) break;   // (the first rows belong to no sequence)
-    }
-    return lo;
-}
-
 // The place of a unit's token: row first, so that its loads can leave before the page's
 // number is there.  `unit` is one for LU lanes (32 at least); all lanes of the wave call.
 template <int LU>
@@ -90,10 +72,10 @@ struct Finder {
         base = -1;
         if (s.row_start) {
             const int lane = threadIdx.x & 63, u0 = __builtin_amdgcn_readlane(unit, 0);
-            b = wave_sequence(s, u0, lane);
+            b = kv_wave_sequence(s, u0, lane);
             if constexpr (LU < 64) {
                 const int u1 = __builtin_amdgcn_readlane(unit, 32);
-                const int b1 = u1 == u0 ? b : wave_sequence(s, u1, lane);
+                const int b1 = u1 == u0 ? b : kv_wave_sequence(s, u1, lane);
                 b = lane < 32 ? b : b1;
             }
             k = unit - kv_unit_first(s, b, 1, 4, 2);
