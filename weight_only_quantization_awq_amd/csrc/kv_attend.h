@@ -1006,34 +1006,50 @@ __device__ __forceinline__ void kv_wide_piece(const A &a, const KvUnit &unit, in
         minpos = kv_wave_min(real ? pos : len - 1);
     }
     vec8 q[S];
+    // The first tile's pages, the queries, and the first tile, each asked for before the one before
+    // it is used: a piece's beginning is a chain of waits.
+    KvWideLoad<D, NG, kThreads> in;
+    in.init();
+    if (t0 < t1) {
+        in.key_page(a, table, token(t0), len);
+        in.value_pages(a, table, token(t0), len);
+    }
+    {
+        const T *src = static_cast<const T *>(a.Q) + (r0 + (real ? row : 0)) * a.q_stride +
+                       static_cast<int64_t>(head * a.per + (col - row * a.per)) * D + 8 * h;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            q[s] = vec8{};
+            if (real) q[s] = *reinterpret_cast<const vec8 *>(src + 16 * s);
+        }
+    }
+    if (t0 < t1) {
+        in.load_keys(a, head, token(t0), lowest, len);
+        in.load_values(a, head, token(t0), len);
+        in.key_page(a, table, token(t0 + 1), len);
+        in.value_pages(a, table, token(t0 + 1), len);
+    }
     // Scores x are formed relative to ref: m, but no less than -kFloorLog2, and 0 before there is one.  Where m is
     // lower, limit sends every tile through the shift to m.  (x carries 2^-24 of its distance from ref: relative
     // to an m of -1000, later scores around 0 put lse off by 1e-5; now it is 2^-24 * (|S| + kFloorLog2) at most.)
     float qs[NG], m = -INFINITY, l = 0.0f, top = -INFINITY, ref = 0.0f, limit = -INFINITY;
     floatx16 o[J];
-    {
-        const T *src = static_cast<const T *>(a.Q) + (r0 + (real ? row : 0)) * a.q_stride +
-                       static_cast<int64_t>(head * a.per + (col - row * a.per)) * D + 8 * h;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) qs[g] = 0.0f;
+    for (int g = 0; g < NG; ++g) qs[g] = 0.0f;
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            vec8 x = {};
-            if (real) x = *reinterpret_cast<const vec8 *>(src + 16 * s);
-            float sum = 0.0f;
+    for (int s = 0; s < S; ++s) {
+        float sum = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum += static_cast<float>(x[e]);
-            qs[s * NG / S] += sum;
-            if (D > 128) asm("" : "+a"(x));   // (where the output fills the other registers)
-            q[s] = x;
-        }
-#pragma unroll
-        for (int g = 0; g < NG; ++g) qs[g] += __shfl_xor(qs[g], 32);
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) o[j][r] = 0.0f;
+        for (int e = 0; e < 8; ++e) sum += static_cast<float>(q[s][e]);
+        qs[s * NG / S] += sum;
+        if (D > 128) asm("" : "+a"(q[s]));   // (where the output fills the other registers)
     }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) qs[g] += __shfl_xor(qs[g], 32);
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[j][r] = 0.0f;
 
     // Both products are kSlots MFMAs a tile, each in a slot of its own: the operand
     // of some slots on is read from LDS, one MFMA issued, and a share of the tile's
@@ -1125,8 +1141,6 @@ __device__ __forceinline__ void kv_wide_piece(const A &a, const KvUnit &unit, in
         for (int i = 0; i < kAhead; ++i) f[i] = read_key(t, i);
     };
 
-    KvWideLoad<D, NG, kThreads> in;
-    in.init();
     int t3 = t0 % 3;   // t % 3
     if (t0 < t1) {
         // keys and pairs run one tile ahead of values: K(t0), K(t0 + 1), V(t0) into LDS,
@@ -1136,12 +1150,6 @@ __device__ __forceinline__ void kv_wide_piece(const A &a, const KvUnit &unit, in
             for (int i = 0; i < in.KW; ++i) in.template unpack_key<T>(i, ks[t & 1]);
             in.template unpack_pair<T>(a, pairs[t % 3], vpairs[t & 1], lost[t % 3]);
         };
-        in.key_page(a, table, token(t0), len);
-        in.value_pages(a, table, token(t0), len);
-        in.load_keys(a, head, token(t0), lowest, len);
-        in.load_values(a, head, token(t0), len);
-        in.key_page(a, table, token(t0 + 1), len);
-        in.value_pages(a, table, token(t0 + 1), len);
         keys(t0);
         in.load_keys(a, head, token(t0 + 1), lowest, len);
         in.key_page(a, table, token(t0 + 2), len);
@@ -1620,7 +1628,7 @@ hipError_t kv_attend_typed(const A &a, bool run_split, bool run_wide, bool merge
         if (columns <= kKvMergeFew)
             hipLaunchKernelGGL((kv_join_kernel<T, D, 32, 32>), dim3(columns, D / 32), dim3(256), 0, st, a);
         else if (columns <= kKvJoinFew)
-            hipLaunchKernelGGL((kv_join_kernel<T, D, D, 1024 / D>), dim3(columns), dim3(256), 0, st, a);
+            hipLaunchKernelGGL((kv_join_kernel<T, D, D, 256 / D>), dim3((columns + 3) / 4), dim3(256), 0, st, a);
         else
             hipLaunchKernelGGL((kv_join_kernel<T, D, D, 1>), dim3((columns + 1024 / D - 1) / (1024 / D)), dim3(256), 0, st, a);
     }
