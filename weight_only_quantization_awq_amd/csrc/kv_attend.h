@@ -208,14 +208,20 @@ __device__ __forceinline__ bool kv_seen(const KvAttendSinks &a, int p, int lowes
     return (static_cast<uint32_t>(p - lowest) < static_cast<uint32_t>(len - lowest)) |
            (static_cast<uint32_t>(p) < static_cast<uint32_t>(a.sinks < len ? a.sinks : len));
 }
-// A position as it compares with the first that a column sees: sinks lie behind all of them.
-// (A number, and opaque: joined conditions of a step's positions and columns take more scalar
-// registers than there are.)
-__device__ __forceinline__ int kv_place(const KvAttend &, int p) { return p; }
-__device__ __forceinline__ int kv_place(const KvAttendSinks &a, int p) {
-    int q = p < a.sinks ? INT32_MAX : p;
-    asm("" : "+v"(q));
-    return q;
+// Which of the positions base .. base + 31 a column sees that sees low .. pos (and the sinks up to pos).
+// (As bits: a comparison for each score takes more instructions and, with a step's columns joined, more
+// scalar registers than there are.)
+__device__ __forceinline__ uint32_t kv_below(int n) { return n >= 32 ? ~0u : (1u << (n > 0 ? n : 0)) - 1u; }
+__device__ __forceinline__ uint32_t kv_visible(const KvAttend &, int base, int pos, int low) {
+    return kv_below(pos + 1 - base) & ~kv_below(low - base);
+}
+__device__ __forceinline__ uint32_t kv_visible(const KvAttendSinks &a, int base, int pos, int low) {
+    return kv_below(pos + 1 - base) & (~kv_below(low - base) | kv_below(a.sinks - base));
+}
+// x where the bit is set, else -inf.
+__device__ __forceinline__ float kv_masked(float x, uint32_t mask, int bit) {
+    const uint32_t all = static_cast<uint32_t>(__builtin_amdgcn_sbfe(static_cast<int>(mask), bit, 1));
+    return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x) & all) | (0xFF800000u & ~all));
 }
 // Whether one of the positions tok .. tok + tile - 1 may lie before some column's.
 __device__ __forceinline__ bool kv_some_before(const KvAttend &, int tok, int, int maxlow) { return tok < maxlow; }
@@ -395,17 +401,15 @@ struct KvWave {
             }
         }
         if (edge) {
+            const uint32_t there = (s.ok0 ? 0xFFFFu : 0u) | (s.ok1 ? 0xFFFF0000u : 0u);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int t = 0; t < NT; ++t) {
+                const uint32_t mask = (kv_visible(a, tok, pos[t], low[t]) & there) >> (4 * kb);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int p = tok + 16 * h + 4 * kb + r;
-                    const int place = kv_place(a, p);
-                    const bool there = h ? s.ok1 : s.ok0;
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        if (!there || p > pos[t] || place < low[t]) x[h][t][r] = -INFINITY;
-                }
+                    for (int r = 0; r < 4; ++r) x[h][t][r] = kv_masked(x[h][t][r], mask, 16 * h + r);
+            }
         }
         half8 p[NT];
 #pragma unroll
@@ -1185,13 +1189,15 @@ __device__ __forceinline__ void kv_wide_piece(const A &a, const KvUnit &unit, in
         }
         if (tok + TT - 1 > minpos || kv_some_before(a, tok, TT, maxlow) || some_gone) {
 #pragma unroll
-            for (int e = 0; e < SUB; ++e)
+            for (int e = 0; e < SUB; ++e) {
+                const uint32_t there = (gone[2 * e] ? 0u : 0xFFFFu) | (gone[2 * e + 1] ? 0u : 0xFFFF0000u);
+                const uint32_t mask = (kv_visible(a, tok + 32 * e, pos, low) & there) >> (4 * h);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const int p = tok + 32 * e + 8 * (r >> 2) + 4 * h + (r & 3);
-                    if (p > pos || kv_place(a, p) < low || gone[2 * e + (r >> 3)]) x[e][r] = -INFINITY;
+                    x[e][r] = kv_masked(x[e][r], mask, 8 * (r >> 2) + (r & 3));
                     top = e + r == 0 ? x[0][0] : fmaxf(top, x[e][r]);
                 }
+            }
         }
         if (__any(top > limit)) {
             float now = fmaxf(m, top + ref - kHeadLog2);
