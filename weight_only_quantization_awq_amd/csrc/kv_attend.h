@@ -401,14 +401,24 @@ struct KvWave {
             }
         }
         if (edge) {
-            const uint32_t there = (s.ok0 ? 0xFFFFu : 0u) | (s.ok1 ? 0xFFFF0000u : 0u);
+            if constexpr (NT > 1 || std::is_same<A, KvAttendSinks>::value) {
+                const uint32_t there = (s.ok0 ? 0xFFFFu : 0u) | (s.ok1 ? 0xFFFF0000u : 0u);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const uint32_t mask = (kv_visible(a, tok, pos[t], low[t]) & there) >> (4 * kb);
+                for (int t = 0; t < NT; ++t) {
+                    const uint32_t mask = (kv_visible(a, tok, pos[t], low[t]) & there) >> (4 * kb);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) x[h][t][r] = kv_masked(x[h][t][r], mask, 16 * h + r);
+                }
+            } else {   // (8 scores: comparisons take 2% less time where a wave waits for loads most of the time)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) x[h][t][r] = kv_masked(x[h][t][r], mask, 16 * h + r);
+                    for (int r = 0; r < 4; ++r) {
+                        const int p = tok + 16 * h + 4 * kb + r;
+                        if (!(h ? s.ok1 : s.ok0) || p > pos[0] || p < low[0]) x[h][0][r] = -INFINITY;
+                    }
             }
         }
         half8 p[NT];
