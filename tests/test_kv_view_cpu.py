@@ -90,6 +90,15 @@ def test_attention_refuses(awq, over, want):
 
 
 @built
+def test_a_prefix_of_too_many_rows_is_refused(awq):
+    """dim/4 threads to a row and query head of the join: fewer than 2^32."""
+    over = dict(q_heads=128, q_stride=16384, out_stride=16384, cache=_cache(awq, heads=1), max_rows=1)
+    for rows, want in ((1 << 20, SHAPE), ((1 << 20) - 1024, WORKSPACE)):
+        b = _batch(awq, rows=rows, batch=1024)
+        assert _call(awq, batch=b, ws_bytes=0, **PREFIX, **over) == want
+
+
+@built
 def test_no_rows_need_nothing(awq):
     none = _batch(awq, rows=0)
     assert _call(awq, batch=none, q=None, out=None, window=5, sinks=1, ws=None, ws_bytes=0) == 0

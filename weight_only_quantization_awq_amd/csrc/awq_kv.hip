@@ -153,6 +153,9 @@ awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, i
                     static_cast<long long>(q_heads), c.heads);
     if (max_rows < 0) return kv_fail(AWQ_ERR_SHAPE, "max_rows must be >= 0");
     if (static_cast<int64_t>(s.T) * q_heads > kKvMaxCount) return kv_fail(AWQ_ERR_SHAPE, "rows * q_heads too large for one call");
+    // (the join of a call with a prefix: dim/4 threads to a row and query head)
+    if (prefix && static_cast<int64_t>(s.T) * q_heads * c.dim / 4 >= int64_t(1) << 32)
+        return kv_fail(AWQ_ERR_SHAPE, "rows * q_heads too large for one call with a prefix");
     const int64_t per = q_heads / c.heads;
     const int64_t most = s.row_start ? (max_rows == 0 || max_rows > s.T ? s.T : max_rows) : s.even;
     const int64_t cols = most * per, all_cols = prefix ? s.T * per : 0, limit = awq::kv_split_cols(c.dim);

@@ -686,13 +686,14 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(kv_split_wav
     }
 }
 
-// Joins the pieces of CH channels of one item's column: blockIdx = (item, column, channels).
+// Joins the pieces of CH channels of one item's column (blockIdx.y; .z: the channels).
 // CH/4 threads hold the channels, and 1024/CH groups of them take every (1024/CH)th
 // piece; the groups join in LDS.
 template <typename T, int D, int CH>
-__global__ __launch_bounds__(256) void kv_merge_kernel(KvAttend a) {
+__device__ __forceinline__ void kv_split_join(const KvAttend &a, int item) {
     constexpr int kLanes = CH / 4, kGroups = 256 / kLanes;
-    const int item = blockIdx.x, col = blockIdx.y;
+    const int col = blockIdx.y;
+    if (col >= a.split_cols) return;
     int2 it = a.items[item];
     if (it.y <= 0 || it.x < 0 || it.x >= a.workers) return;
     it.y = it.y < a.workers - it.x ? it.y : a.workers - it.x;   // (inside, should tables change under the call)
@@ -1441,50 +1442,64 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(A a) {
     }
 }
 
-// Joins the pieces of one (unit, head), blockIdx.x: D/4 threads a column.
+// Joins the pieces of one (unit, head): D/4 threads a column, and the columns of a unit shared among
+// kKvWideJoin workgroups, which each look for the unit once.  (With a workgroup for each 1024/D of them
+// 5 ragged chunks at dim 256 took 14.0 us.)
 template <typename T, int D>
-__global__ __launch_bounds__(256) void kv_wide_merge_kernel(KvAttend a) {
+__device__ __forceinline__ void kv_wide_join(const KvAttend &a, int item) {
     constexpr int kLanes = D / 4, kPer = 256 / kLanes, kCols = kv_wide_cols(D);
-    const int item = blockIdx.x, u = item / a.c.heads, head = item - u * a.c.heads;
-    KvUnit unit;
-    if (!kv_unit<D>(a, u, 0, unit)) return;
+    if (blockIdx.y >= kKvWideJoin || blockIdx.z != 0) return;
     int2 it = a.wide_items[item];
     if (it.y <= 0 || it.x < 0 || it.x >= a.wide_workers) return;
-    it.y = it.y < a.wide_workers - it.x ? it.y : a.wide_workers - it.x;   // (as in kv_merge_kernel)
+    it.y = it.y < a.wide_workers - it.x ? it.y : a.wide_workers - it.x;   // (as in kv_split_join)
+    const int u = item / a.c.heads, head = item - u * a.c.heads;
+    KvUnit unit;
+    if (!kv_unit<D>(a, u, 0, unit)) return;
     const int d = 4 * (threadIdx.x % kLanes);
-    const int c = blockIdx.y * kPer + threadIdx.x / kLanes, col = unit.col0 + c, row = col / a.per;
-    if (row >= unit.n) return;
-    float top = -INFINITY, sum = 0.0f;
-    floatx4 y = {0.0f, 0.0f, 0.0f, 0.0f};
-    constexpr int kAhead = 4;   // pieces in flight
-    for (int k0 = 0; k0 < it.y; k0 += kAhead) {
-        float2 ml[kAhead];
-        floatx4 z[kAhead];
+    for (int c = blockIdx.y * kPer + threadIdx.x / kLanes; c < kCols; c += kKvWideJoin * kPer) {
+        const int col = unit.col0 + c, row = col / a.per;
+        if (row >= unit.n) return;
+        float top = -INFINITY, sum = 0.0f;
+        floatx4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+        constexpr int kAhead = 4;   // pieces in flight
+        for (int k0 = 0; k0 < it.y; k0 += kAhead) {
+            float2 ml[kAhead];
+            floatx4 z[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (k0 + i >= it.y) break;
-            const int64_t at = (static_cast<int64_t>(it.x + k0 + i) * 2 + (k0 + i == 0 ? 1 : 0)) * kCols + c;
-            ml[i] = *reinterpret_cast<const float2 *>(a.wide_ml + at * 2);
-            z[i] = *reinterpret_cast<const floatx4 *>(a.wide_part + at * D + d);
+            for (int i = 0; i < kAhead; ++i) {
+                if (k0 + i >= it.y) break;
+                const int64_t at = (static_cast<int64_t>(it.x + k0 + i) * 2 + (k0 + i == 0 ? 1 : 0)) * kCols + c;
+                ml[i] = *reinterpret_cast<const float2 *>(a.wide_ml + at * 2);
+                z[i] = *reinterpret_cast<const floatx4 *>(a.wide_part + at * D + d);
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (k0 + i >= it.y) break;
+                const float now = fmaxf(top, ml[i].x);
+                const float f0 = top == now ? 1.0f : __builtin_amdgcn_exp2f(top - now);
+                const float f1 = ml[i].x == now ? 1.0f : __builtin_amdgcn_exp2f(ml[i].x - now);
+                sum = sum * f0 + ml[i].y * f1;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) y[r] = y[r] * f0 + z[i][r] * f1;
+                top = now;
+            }
         }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (k0 + i >= it.y) break;
-            const float now = fmaxf(top, ml[i].x);
-            const float f0 = top == now ? 1.0f : __builtin_amdgcn_exp2f(top - now);
-            const float f1 = ml[i].x == now ? 1.0f : __builtin_amdgcn_exp2f(ml[i].x - now);
-            sum = sum * f0 + ml[i].y * f1;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) y[r] = y[r] * f0 + z[i][r] * f1;
-            top = now;
-        }
+        const int h = head * a.per + col - row * a.per;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        T *dst = static_cast<T *>(a.O) + (unit.r0 + row) * a.o_stride + static_cast<int64_t>(h) * D + d;
+        *reinterpret_cast<uint2 *>(dst) = pack4<T>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+        if (a.lse && d == 0)
+            a.lse[static_cast<int64_t>(unit.r0 + row) * a.q_heads + h] = kv_lse(top, sum);
     }
-    const int h = head * a.per + col - row * a.per;
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    T *dst = static_cast<T *>(a.O) + (unit.r0 + row) * a.o_stride + static_cast<int64_t>(h) * D + d;
-    *reinterpret_cast<uint2 *>(dst) = pack4<T>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
-    if (a.lse && d == 0)
-        a.lse[static_cast<int64_t>(unit.r0 + row) * a.q_heads + h] = kv_lse(top, sum);
+}
+
+// The pieces of both paths: blockIdx.x counts the split path's items, then the wide path's.
+template <typename T, int D, int CH>
+__global__ __launch_bounds__(256) void kv_merge_kernel(KvAttend a, int split_items) {
+    if (static_cast<int>(blockIdx.x) < split_items)
+        kv_split_join<T, D, CH>(a, blockIdx.x);
+    else
+        kv_wide_join<T, D>(a, blockIdx.x - split_items);
 }
 
 // ---------------------------------------------------------------------------
@@ -1625,24 +1640,24 @@ hipError_t kv_attend_typed(const A &a, bool run_split, bool run_wide, bool merge
             hipLaunchKernelGGL((kv_split_kernel<T, D, NG, 2, A>), grid, threads, 0, st, a);
         else if constexpr (D < 256)   // (awq_kv.hip takes at most 2 column tiles at 256 channels)
             hipLaunchKernelGGL((kv_split_kernel<T, D, NG, 4, A>), grid, threads, 0, st, a);
-        const int64_t columns = static_cast<int64_t>(a.s.B) * a.c.heads * a.split_cols;
-        if (kv_to_sums(&a)) merge = false;   // (joined below)
-        if (merge && columns <= kKvMergeFew)
-            hipLaunchKernelGGL((kv_merge_kernel<T, D, 32>), dim3(a.s.B * a.c.heads, a.split_cols, D / 32), dim3(256), 0, st, a);
-        else if (merge)
-            hipLaunchKernelGGL((kv_merge_kernel<T, D, D>), dim3(a.s.B * a.c.heads, a.split_cols), dim3(256), 0, st, a);
     }
-    if (run_wide) {
+    if (run_wide)
         hipLaunchKernelGGL((kv_wide_kernel<T, D, NG, A>), dim3(a.line && a.wide_workers > a.units * a.c.heads ? a.wide_workers : a.units * a.c.heads),
                            dim3(kv_wide_threads(D)), 0, st, a);
-        if (a.wide_items && !kv_to_sums(&a))
-            hipLaunchKernelGGL((kv_wide_merge_kernel<T, D>), dim3(a.units * a.c.heads, kv_wide_cols(D) / (1024 / D)),
-                               dim3(256), 0, st, a);
+    const int split_items = run_split && merge ? a.s.B * a.c.heads : 0, wide_items = run_wide && a.wide_items ? a.units * a.c.heads : 0;
+    if (!kv_to_sums(&a) && split_items + wide_items > 0) {
+        const int64_t columns = static_cast<int64_t>(split_items) * a.split_cols;
+        const unsigned y = split_items > 0 && (a.split_cols > kKvWideJoin || wide_items == 0) ? a.split_cols : kKvWideJoin;
+        const dim3 grid(split_items + wide_items, y, columns <= kKvMergeFew && split_items > 0 ? D / 32 : 1);
+        if (grid.z > 1)
+            hipLaunchKernelGGL((kv_merge_kernel<T, D, 32>), grid, dim3(256), 0, st, a, split_items);
+        else
+            hipLaunchKernelGGL((kv_merge_kernel<T, D, D>), grid, dim3(256), 0, st, a, split_items);
     }
     if constexpr (kv_to_sums(static_cast<const A *>(nullptr))) {
         const int64_t columns = static_cast<int64_t>(a.s.T) * a.q_heads;
         if (columns <= kKvMergeFew)
-            hipLaunchKernelGGL((kv_join_kernel<T, D, 32, 32>), dim3(columns, D / 32), dim3(256), 0, st, a);
+            hipLaunchKernelGGL((kv_join_kernel<T, D, 32, 32>), dim3(static_cast<unsigned>(columns), D / 32), dim3(256), 0, st, a);
         else if (columns <= kKvJoinFew)
             hipLaunchKernelGGL((kv_join_kernel<T, D, D, 256 / D>), dim3((columns + 3) / 4), dim3(256), 0, st, a);
         else

@@ -195,6 +195,7 @@ constexpr int kKvLineUnits = 2 * kKvCus;
 constexpr int kKvWideCost = 3;       // what a unit costs besides its tiles, in tiles
 constexpr int kKvWideMinShare = 6;   // least share of a workgroup, in tiles (12: within 1%)
 constexpr int kKvWideSnap = 1;       // tiles: pieces this short are not cut off
+constexpr int kKvWideJoin = 8;       // workgroups that join the pieces of a (unit, head)
 constexpr int kKvTile = 32;        // tokens of one step
 constexpr int kKvItemCost = 2;     // what an item costs besides its tiles, in tiles
 // Least share of a worker, in tiles: a worker's part costs as much as about 2 tiles,
