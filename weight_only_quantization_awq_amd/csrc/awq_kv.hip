@@ -188,7 +188,7 @@ awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, i
     const int64_t groups = static_cast<int64_t>(p->units) * c.heads;
     const int64_t own_wide_tiles = own_wide ? in(positions, tile) : 0, all_wide_tiles = all_wide ? in(all_positions, tile) : 0;
     const int64_t wide_tiles = own_wide_tiles > all_wide_tiles ? own_wide_tiles : all_wide_tiles;
-    const int64_t wide_line = c.heads * (p->own_units * (own_wide_tiles + awq::kKvWideCost) + all_units * (all_wide_tiles + awq::kKvWideCost));
+    const int64_t wide_line = c.heads * (p->own_units * (own_wide_tiles + awq::kv_wide_cost(c.dim)) + all_units * (all_wide_tiles + awq::kv_wide_cost(c.dim)));
     p->line = p->wide && groups < awq::kKvLineUnits && wide_line <= kKvMaxCount;
     const int64_t wide_useful = in(wide_line, awq::kKvWideMinShare);
     p->wide_workers = static_cast<int>(wide_useful < awq::kKvCus ? wide_useful : awq::kKvCus);

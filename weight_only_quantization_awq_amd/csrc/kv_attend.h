@@ -756,7 +756,7 @@ __device__ __forceinline__ void kv_split_join(const KvAttend &a, int item) {
 // A workgroup takes a unit, kv_wide_cols(D) columns of a sequence (rows x query
 // heads of one key head, 32 a wave), over the tokens they see, in tiles of
 // kv_wide_tile(D).  Where units are few, they form a line that one workgroup a CU
-// shares equally, as on the split path (a unit costs kKvWideCost besides its
+// shares equally, as on the split path (a unit costs kv_wide_cost besides its
 // tiles); else each has a workgroup of its own, the longest first.  Here the matrix
 // cores and the vector work under them bound it, so a tile is unpacked once for all
 // waves, into LDS, as 16-byte operands of 32x32x16 MFMAs in reading order (every LDS
@@ -843,8 +843,9 @@ __device__ __forceinline__ int kv_wide_workers(const KvAttend &a, int total) {
     return a.wide_workers < most ? a.wide_workers : most;
 }
 // The tile at which a boundary `at` behind an item's begin cuts it (0 or tiles: not inside).
+template <int D>
 __device__ __forceinline__ int kv_wide_cut(int at, int tiles) {
-    const int t = at - kKvWideCost;
+    const int t = at - kv_wide_cost(D);
     if (t <= kKvWideSnap) return 0;
     return tiles - t <= kKvWideSnap ? tiles : t;
 }
@@ -1334,7 +1335,7 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(A a) {
     if (a.line) {
         for (int i = tid; i < a.units; i += kThreads) {
             KvUnit unit;
-            before[i + 1] = kv_unit<D>(a, i, common, unit) ? unit.t1 - unit.t0 + kKvWideCost : 0;
+            before[i + 1] = kv_unit<D>(a, i, common, unit) ? unit.t1 - unit.t0 + kv_wide_cost(D) : 0;
         }
         if (tid == 0) before[0] = jobs = span = 0;
         __syncthreads();
@@ -1352,12 +1353,10 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(A a) {
             }
         }
         __syncthreads();
-        // Pieces cost time: their sums go through memory and a join.  Where whole units,
-        // the longest first, take at most 6/5 of the line's share, they are handed out
-        // instead: the first kKvCus to a CU each, the (kKvCus + i)th behind the
-        // (kKvCus - 1 - i)th.  (6 ragged prompts of up to 6000 tokens, 94 tiles to a CU on
-        // the line and 97 without: 278 us on the line, 263 us without; one of 2400 rows
-        // over 4096, 59 tiles and 73: 176 us both ways.)
+        // Pieces cost time: each has its own beginning, and their sums go through memory and a
+        // join.  Where whole units, the longest first, are done as soon (kv_wide_cost), they are
+        // handed out instead: the first kKvCus to a CU each, the (kKvCus + i)th behind the
+        // (kKvCus - 1 - i)th.
         auto length = [&](int i) { return before[i + 1] - before[i]; };
         for (int i = tid; i < a.units; i += kThreads) {
             const int mine = length(i);
@@ -1373,7 +1372,8 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(A a) {
             atomicMax(&span, time);
         }
         __syncthreads();
-        if (tid == 0 && 5 * static_cast<int64_t>(span) * kv_wide_workers(a, H * before[a.units]) > 6 * static_cast<int64_t>(H) * before[a.units])
+        const int line = H * before[a.units], workers = kv_wide_workers(a, line);
+        if (tid == 0 && (span - kv_wide_cost(D) - kKvWideMerge) * static_cast<int64_t>(workers) > line)
             jobs = 0;
         __syncthreads();
     }
@@ -1411,11 +1411,11 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(A a) {
                     hi = mid;
             }
             const int item = head * all + __builtin_amdgcn_readfirstlane(before[lo]);
-            const int length = __builtin_amdgcn_readfirstlane(before[lo + 1] - before[lo]), tiles = length - kKvWideCost;
+            const int length = __builtin_amdgcn_readfirstlane(before[lo + 1] - before[lo]), tiles = length - kv_wide_cost(D);
             if (length <= 0 || !kv_unit<D>(a, lo, common, unit)) return;   // (not unless the tables change under the call)
             const int end = item + length;
-            const int c0 = next_at < 0 ? kv_wide_cut(at - item, tiles) : 0;
-            const int c1 = x1 >= end ? tiles : kv_wide_cut(x1 - item, tiles);
+            const int c0 = next_at < 0 ? kv_wide_cut<D>(at - item, tiles) : 0;
+            const int c1 = x1 >= end ? tiles : kv_wide_cut<D>(x1 - item, tiles);
             whole = c0 == 0 && c1 == tiles;
             more = end < x1;
             next_at = end;
