@@ -638,8 +638,9 @@ typedef struct {
  * For each head's row x at position p, each operation rounded to float32:
  *   u = 1 / sqrt(mean x^2 + eps)   (in 64 bits, rounded once);   y = (x * u) * weight
  *   a pair (y1, y2) becomes (y1*cos - y2*sin, y2*cos + y1*sin) with p's angles.
- * Queries are rounded once more, to type t; keys are quantised from float32 (so the cache
- * holds the same as after awq_kv_append of the float32 keys).  A row at a position that
+ * Keys are quantised from these float32 values (so the cache holds the same as after
+ * awq_kv_append of the float32 keys).  Queries are within 16 * 2^-24 of the sum of the two
+ * products' sizes of the exact result (of their table and weights), rounded once more, to type t.  A row at a position that
  * cos_sin does not hold (rot > 0) gets queries of NaN and is stored as NaN.  Queries of rows
  * without a position are zero; rows that belong to no sequence are left as they were.
  */

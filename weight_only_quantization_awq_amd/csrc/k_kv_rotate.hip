@@ -6,9 +6,11 @@
 //   y = fl32(fl32(x u) w)                     (y = x where there is no weight)
 //   channels (a, b) of a pair, angle's cosine c and sine s from the table:
 //   a' = fl32(fl32(a c) - fl32(b s)),  b' = fl32(fl32(b c) + fl32(a s))
-// so what the cache holds does not depend on the order of a sum or on fused roundings: the
-// sum of squares is taken in 64 bits, where its order changes the rounded u about once in
-// 2^28 rows, and every other operation is one IEEE rounding.
+// Keys are turned by these very roundings, so what the cache holds does not depend on the order
+// of a sum or on fused operations: the sum of squares is taken in 64 bits, where its order
+// changes the rounded u about once in 2^28 rows.  Queries, which are rounded to their type next,
+// take fewer instructions: sums in float32, u (x1 (w1 c) - x2 (w2 s)), within 16 * 2^-24 of the
+// sum of the two terms' sizes; where float32's range does not hold the squares, u is taken as the keys' is.
 //
 // Work split: workgroups for keys and values come first, units of 4 aligned positions and a
 // head as in k_kv.hip (they have the more to compute), then those for queries, a wave to a
@@ -121,6 +123,84 @@ __device__ __forceinline__ bool row_position(const KvCache &c, const KvBatch &s,
     return row >= r0 && row < r0 + n;
 }
 
+// The same of queries (as the file's head says).
+template <typename T, int D>
+struct QueryTurner {
+    static constexpr int LT = D / 8;
+    typedef T vec8 __attribute__((ext_vector_type(8)));
+    float a[8], b[8];   // w1 c (w1 where nothing is rotated) and +-w2 s
+    bool norm, turned, neighbours, lost;
+    int partner;
+    double eps;
+
+    __device__ __forceinline__ void start(const KvTurn &t, int position, int w) {
+        Turner<D> x;
+        x.start(t, t.q_weight, position, w);
+        norm = x.norm, turned = x.turned, neighbours = x.neighbours, lost = x.lost, partner = x.partner, eps = x.eps;
+        const int other = w + partner - (threadIdx.x & 63);
+        float theirs[8];
+        if (norm) load8(t.q_weight + 8 * other, theirs);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            a[i] = norm ? x.weight[i] : 1.0f;
+            if (turned) {
+                b[i] = norm ? (neighbours ? x.weight[i ^ 1] : theirs[i]) * x.s[i] : x.s[i];
+                a[i] *= x.c[i];
+            }
+        }
+    }
+
+    // All lanes of the wave call.  NORM, NEIGHBOURS: as `norm` and `neighbours` say.
+    template <bool NORM, bool NEIGHBOURS>
+    __device__ __forceinline__ void turn(vec8 in, float *x) const {
+        float own[8], other[8], u = 1.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) own[i] = static_cast<float>(in[i]);
+        if constexpr (NEIGHBOURS) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) other[i] = own[i ^ 1];
+        } else {
+            constexpr int kWords = sizeof(vec8) / 4;
+            struct Words { uint32_t w[kWords]; } words = __builtin_bit_cast(Words, in);
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) words.w[i] = __shfl(words.w[i], partner);
+            const vec8 there = __builtin_bit_cast(vec8, words);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) other[i] = static_cast<float>(there[i]);
+        }
+        if constexpr (NORM) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum = fmaf(own[i], own[i], sum);
+#pragma unroll
+            for (int m = 1; m < LT; m <<= 1) sum += __shfl_xor(sum, m);
+            const float mean = fmaf(sum, 1.0f / D, static_cast<float>(eps));
+            u = __builtin_amdgcn_rsqf(mean);
+            if (__any(!(mean > 1.0e-30f && mean < 1.0e30f))) {   // (NaN, too)
+                double wide = 0.0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) wide = fma(static_cast<double>(own[i]), static_cast<double>(own[i]), wide);
+#pragma unroll
+                for (int m = 1; m < LT; m <<= 1) wide += __shfl_xor(wide, m);
+                u = inverse_root(wide * (1.0 / D) + eps);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) own[i] *= u, other[i] *= u;
+                u = 1.0f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = own[i] * a[i];
+        if (turned) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = fmaf(other[i], b[i], x[i]);
+        }
+        if constexpr (NORM) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] *= u;
+        }
+    }
+};
+
 template <typename T, int D, int GROUP>
 __global__ __launch_bounds__(kKvThreads) void kv_append_rotated_kernel(KvCache c, KvBatch s, KvTurn t, const T *Q,
                                                                        const T *__restrict__ K, const T *__restrict__ V,
@@ -129,8 +209,8 @@ __global__ __launch_bounds__(kKvThreads) void kv_append_rotated_kernel(KvCache c
                                                                        int units, int units_even, int key_groups) {
     constexpr int LT = D / 8, LU = 4 * LT, PER = kKvThreads / LU;
     __shared__ uint32_t bytes[PER][LU];
-    Turner<D> turner;
     if (static_cast<int>(blockIdx.x) < key_groups) {
+        Turner<D> turner;
         const int sub = threadIdx.x / LU, lane = threadIdx.x % LU, token = lane / LT, w = lane % LT;
         const int id = blockIdx.x * PER + sub, unit = id / c.heads, head = id - unit * c.heads;
         Finder<LU> f;
@@ -164,19 +244,28 @@ __global__ __launch_bounds__(kKvThreads) void kv_append_rotated_kernel(KvCache c
     }
     int position;
     if (!row_position(c, s, row, lane, position)) return;   // (one for the wave)
-    turner.start(t, t.q_weight, position, w);
+    QueryTurner<T, D> turner;
+    turner.start(t, position, w);
+    auto heads = [&](auto norm, auto neighbours) {
 #pragma unroll
-    for (int i = 0; i < kQueryIter; ++i) {
-        float x[8];
+        for (int i = 0; i < kQueryIter; ++i) {
+            float x[8];
+            turner.template turn<decltype(norm)::value, decltype(neighbours)::value>(in[i], x);
+            if (position < 0 || turner.lost) {   // (one for the wave)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = static_cast<float>(in[i][e]);
-        turner.turn(x);
-        if (position < 0) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+                for (int e = 0; e < 8; ++e) x[e] = position < 0 ? 0.0f : NAN;
+            }
+            if (head + i * kHeads < q_heads) store8(Qo + row * o_stride + static_cast<int64_t>(head + i * kHeads) * D + 8 * w, x);
         }
-        if (head + i * kHeads < q_heads) store8(Qo + row * o_stride + static_cast<int64_t>(head + i * kHeads) * D + 8 * w, x);
-    }
+    };
+    if (turner.norm && turner.neighbours)
+        heads(std::true_type{}, std::true_type{});
+    else if (turner.norm)
+        heads(std::true_type{}, std::false_type{});
+    else if (turner.neighbours)
+        heads(std::false_type{}, std::true_type{});
+    else
+        heads(std::false_type{}, std::false_type{});
 }
 
 template <typename T, int D, int GROUP>
