@@ -206,13 +206,16 @@ __global__ __launch_bounds__(kKvThreads) void kv_append_rotated_kernel(KvCache c
                                                                        const T *__restrict__ K, const T *__restrict__ V,
                                                                        T *Qo, int64_t q_stride, int64_t k_stride,
                                                                        int64_t v_stride, int64_t o_stride, int q_heads,
-                                                                       int units, int units_even, int key_groups) {
+                                                                       int units, int units_even, int key_groups, int apart) {
     constexpr int LT = D / 8, LU = 4 * LT, PER = kKvThreads / LU;
     __shared__ uint32_t bytes[PER][LU];
-    if (static_cast<int>(blockIdx.x) < key_groups) {
+    // every `apart`th workgroup is one for keys and values, while there are any
+    const int period = blockIdx.x / apart;
+    const bool keys_here = period < key_groups && blockIdx.x == static_cast<unsigned>(period) * apart;
+    if (keys_here) {
         Turner<D> turner;
         const int sub = threadIdx.x / LU, lane = threadIdx.x % LU, token = lane / LT, w = lane % LT;
-        const int id = blockIdx.x * PER + sub, unit = id / c.heads, head = id - unit * c.heads;
+        const int id = period * PER + sub, unit = id / c.heads, head = id - unit * c.heads;
         Finder<LU> f;
         f.row(c, s, unit, units, units_even, token);
         float k[8] = {}, v[8] = {};
@@ -229,7 +232,7 @@ __global__ __launch_bounds__(kKvThreads) void kv_append_rotated_kernel(KvCache c
     constexpr int kHeads = 64 / LT;   // of one step
     const int lane = threadIdx.x & 63, w = lane % LT;
     const int chunks = (q_heads + kQueryHeads<D> - 1) / kQueryHeads<D>;
-    const int64_t id = static_cast<int64_t>(blockIdx.x - key_groups) * (kKvThreads / 64) +
+    const int64_t id = static_cast<int64_t>(blockIdx.x - (period < key_groups ? period + 1 : key_groups)) * (kKvThreads / 64) +
                        __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t at = id / chunks;
     if (at >= s.T) return;
@@ -275,10 +278,10 @@ hipError_t append_rotated(const KvCache &c, const KvBatch &s, const KvTurn &t, c
     kv_unit_counts(s, units, even);
     const int64_t per = kKvThreads / (D / 2), keys = (static_cast<int64_t>(units) * c.heads + per - 1) / per;
     const int64_t waves = static_cast<int64_t>(s.T) * ((q_heads + kQueryHeads<D> - 1) / kQueryHeads<D>);
-    const int64_t n = keys + (waves + kKvThreads / 64 - 1) / (kKvThreads / 64);
+    const int64_t queries = (waves + kKvThreads / 64 - 1) / (kKvThreads / 64), n = keys + queries;
     hipLaunchKernelGGL((kv_append_rotated_kernel<T, D, GROUP>), dim3(static_cast<unsigned>(n)), dim3(kKvThreads), 0, st, c, s, t,
                        static_cast<const T *>(Q), static_cast<const T *>(K), static_cast<const T *>(V), static_cast<T *>(Qo), qs, ks,
-                       vs, os, q_heads, units, even, static_cast<int>(keys));
+                       vs, os, q_heads, units, even, static_cast<int>(keys), static_cast<int>(queries / keys + 1));
     return hipGetLastError();
 }
 
