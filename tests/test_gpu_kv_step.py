@@ -178,7 +178,8 @@ def check_queries(got, q, weight, cos_sin, at, eps=1e-6, interleaved=False):
     lost = ~np.isfinite(want)
     assert not np.isfinite(got[lost]).any() and np.array_equal(np.isnan(got), np.isnan(want))
     off = 16 * 2.0 ** -24 * mass
-    bad = ~(np.abs(got - want) <= off + half * (np.abs(want) + off) + small) & ~lost
+    with np.errstate(invalid="ignore"):
+        bad = ~(np.abs(got - want) <= off + half * (np.abs(want) + off) + small) & ~lost
     assert not bad.any(), (np.argwhere(bad)[:4], got[bad][:4], want[bad][:4])
 
 

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import numpy as np
 import torch
@@ -678,8 +679,7 @@ def kv_append(cache: KvCache, K: torch.Tensor, V: torch.Tensor, block_table: tor
     _kv_call(dev, _lib.awq_kv_append, c, b, k, v, _kv_type(K.dtype), k_stride, v_stride)
 
 
-@dataclass(frozen=True)
-class KvStep:
+class KvStep(NamedTuple):
     """What :func:`kv_tables` gives: a step's ``kv_len`` and ``row_start`` for the other calls, the
     free pages ``taken`` so far, and each row's ``position`` and ``slot`` (None without ``rows``)."""
     kv_len: torch.Tensor              # int32 [batch]
@@ -705,7 +705,7 @@ def kv_tables(block_table: torch.Tensor, kv_len: torch.Tensor, count: torch.Tens
     table = _kv_ints(block_table, "block_table", dev, None)
     batch, max_pages = block_table.shape
     if out is None:
-        ints = torch.empty(2 * batch + 2 + rows, dtype=torch.int32, device=dev).split((batch, batch + 1, 1, rows))
+        ints = torch.empty(2 * batch + 2 + rows, dtype=torch.int32, device=dev).split_with_sizes((batch, batch + 1, 1, rows))
         out = KvStep(ints[0], ints[1], ints[2], ints[3] if rows else None,
                      torch.empty(rows, dtype=torch.int64, device=dev) if rows else None)
         s = _KvStepC(*[x.data_ptr() for x in ints], out.slot.data_ptr() if rows else None)
