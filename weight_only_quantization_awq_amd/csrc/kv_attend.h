@@ -578,7 +578,8 @@ struct KvWave {
 // The items (sequence, head) form one line, each kKvItemCost + its tiles long,
 // which the workers (one wave each, as many as the GPU holds) share equally: ragged
 // lengths and few long sequences load the GPU evenly, and nothing but the
-// lengths on the device decides it.  A worker that holds a whole item writes
+// lengths on the device decides it.  Sinks are tiles of their own in front of an item's window;
+// a shared prefix is one more sequence.  A worker that holds a whole item writes
 // its output; the pieces of an item that a boundary cuts go to the workspace
 // and kv_merge_kernel joins them in order.  Boundaries within a.snap tiles of an
 // item's ends move there.
@@ -770,9 +771,13 @@ __device__ __forceinline__ void kv_split_join(const KvAttend &a, int item) {
 // and LDS 43%; a wave waits for operands, loads and barriers 33% of its time and for its
 // turn to issue 25%.  Two waves a SIMD beat one of 64 columns (187 and 269 us).  At dim 256 the
 // output of 32 columns fills half the registers, so a SIMD has one wave: it issues
-// (~740 instructions a tile, 32 of them MFMAs) 62% of its time and waits 29%, with no other
-// to fill in (5 ragged chunks of up to 1031 rows over 6007 tokens: 300 us; MFMA 17%, VALU
-// 36%, LDS 32%); two waves of 16 columns read every operand twice and took 337.
+// (~740 instructions a tile, 32 of them MFMAs) 63% of its time and waits 27%, with no other
+// to fill in (5 ragged chunks of up to 1031 rows over 6007 tokens: 244 us, VALU 38%); two waves of
+// 16 columns read every operand twice and took 10% longer.
+// Under a window or in a batch's chunks units have few tiles, and a piece's beginning counts: 8 us
+// until its first tile, 4.6 of them until its keys are there (a chain of row tables, page numbers and
+// loads), and 3 for its end (a prompt of 4096 under a window of 512 and 16 sinks: 40 us a unit, 31 of
+// them for 11 tiles, two to a CU one behind the other, 77 us; MFMA 27%, VALU 42%).
 
 template <typename T>
 struct KvWideType;
@@ -1443,12 +1448,13 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(A a) {
 }
 
 // Joins the pieces of one (unit, head): D/4 threads a column, and the columns of a unit shared among
-// kKvWideJoin workgroups, which each look for the unit once.  (With a workgroup for each 1024/D of them
-// 5 ragged chunks at dim 256 took 14.0 us.)
+// `shares` workgroups, which each look for the unit once: kKvWideJoin in all, at most one to each
+// 1024/D columns.  (5 ragged chunks at dim 256, 244 items: 14.0 us with 32 shares, 11.5 with 8; 128 rows over
+// 32768 tokens, 16 items of 16 pieces: a call takes 115 us with 8 and 109 with 32.)
 template <typename T, int D>
-__device__ __forceinline__ void kv_wide_join(const KvAttend &a, int item) {
+__device__ __forceinline__ void kv_wide_join(const KvAttend &a, int item, int shares) {
     constexpr int kLanes = D / 4, kPer = 256 / kLanes, kCols = kv_wide_cols(D);
-    if (blockIdx.y >= kKvWideJoin || blockIdx.z != 0) return;
+    if (static_cast<int>(blockIdx.y) >= shares || blockIdx.z != 0) return;
     int2 it = a.wide_items[item];
     if (it.y <= 0 || it.x < 0 || it.x >= a.wide_workers) return;
     it.y = it.y < a.wide_workers - it.x ? it.y : a.wide_workers - it.x;   // (as in kv_split_join)
@@ -1456,7 +1462,7 @@ __device__ __forceinline__ void kv_wide_join(const KvAttend &a, int item) {
     KvUnit unit;
     if (!kv_unit<D>(a, u, 0, unit)) return;
     const int d = 4 * (threadIdx.x % kLanes);
-    for (int c = blockIdx.y * kPer + threadIdx.x / kLanes; c < kCols; c += kKvWideJoin * kPer) {
+    for (int c = blockIdx.y * kPer + threadIdx.x / kLanes; c < kCols; c += shares * kPer) {
         const int col = unit.col0 + c, row = col / a.per;
         if (row >= unit.n) return;
         float top = -INFINITY, sum = 0.0f;
@@ -1495,11 +1501,11 @@ __device__ __forceinline__ void kv_wide_join(const KvAttend &a, int item) {
 
 // The pieces of both paths: blockIdx.x counts the split path's items, then the wide path's.
 template <typename T, int D, int CH>
-__global__ __launch_bounds__(256) void kv_merge_kernel(KvAttend a, int split_items) {
+__global__ __launch_bounds__(256) void kv_merge_kernel(KvAttend a, int split_items, int shares) {
     if (static_cast<int>(blockIdx.x) < split_items)
         kv_split_join<T, D, CH>(a, blockIdx.x);
     else
-        kv_wide_join<T, D>(a, blockIdx.x - split_items);
+        kv_wide_join<T, D>(a, blockIdx.x - split_items, shares);
 }
 
 // ---------------------------------------------------------------------------
@@ -1647,12 +1653,15 @@ hipError_t kv_attend_typed(const A &a, bool run_split, bool run_wide, bool merge
     const int split_items = run_split && merge ? a.s.B * a.c.heads : 0, wide_items = run_wide && a.wide_items ? a.units * a.c.heads : 0;
     if (!kv_to_sums(&a) && split_items + wide_items > 0) {
         const int64_t columns = static_cast<int64_t>(split_items) * a.split_cols;
-        const unsigned y = split_items > 0 && (a.split_cols > kKvWideJoin || wide_items == 0) ? a.split_cols : kKvWideJoin;
+        constexpr int kMost = kv_wide_cols(D) / (1024 / D);
+        int shares = wide_items > 0 ? (kKvWideJoin + wide_items - 1) / wide_items : 0;
+        shares = shares < kMost ? shares : kMost;
+        const unsigned y = split_items > 0 && a.split_cols > shares ? a.split_cols : shares;
         const dim3 grid(split_items + wide_items, y, columns <= kKvMergeFew && split_items > 0 ? D / 32 : 1);
         if (grid.z > 1)
-            hipLaunchKernelGGL((kv_merge_kernel<T, D, 32>), grid, dim3(256), 0, st, a, split_items);
+            hipLaunchKernelGGL((kv_merge_kernel<T, D, 32>), grid, dim3(256), 0, st, a, split_items, shares);
         else
-            hipLaunchKernelGGL((kv_merge_kernel<T, D, D>), grid, dim3(256), 0, st, a, split_items);
+            hipLaunchKernelGGL((kv_merge_kernel<T, D, D>), grid, dim3(256), 0, st, a, split_items, shares);
     }
     if constexpr (kv_to_sums(static_cast<const A *>(nullptr))) {
         const int64_t columns = static_cast<int64_t>(a.s.T) * a.q_heads;

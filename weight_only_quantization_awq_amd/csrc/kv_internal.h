@@ -189,22 +189,22 @@ constexpr int kv_wide_tile(int dim) { return 8192 / dim; }   // tokens
 constexpr int kKvCus = 256;          // a workgroup of the wide path fills a CU
 // With fewer (unit, head)s than this they may form a line; from 2 to a CU on, the
 // longest first load the GPU evenly without its pieces.  (128 rows over 32768 tokens:
-// 103 us on the line, 1044 us without; 5 ragged chunks at dim 256: 295 and 383 us; a
-// prompt of 4096, 512 units: 243 and 199 us.)
+// 109 us on the line, 1198 us without; 5 ragged chunks at dim 256: 256 and 395 us; a
+// prompt of 4096, 512 units: 243 and 184 us.)
 constexpr int kKvLineUnits = 2 * kKvCus;
-// What a piece of a unit costs besides its tiles, in tiles (13 to 15 us of a chain of waits, a tile
-// 3.3, 2.5 and 2.0), and what the join of cut units costs (its launch
-// and the sums' way through memory).  Whole units are handed out where that is no slower than the line by these: 5 ragged
-// chunks over 6007 tokens at dim 256 304 -> 258 us against costs of 3 and a line preferred up to 6/5 of
-// it, the same under a window 106 -> 96; 6 random prompts of up to 700 over 6000 at dim 64, 128 and 256
-// 200, 257 and 820 us both ways.
+// What a piece of a unit costs besides its tiles, in tiles (13 to 15 us of a chain of waits; a tile
+// takes 3.3 us at dim 64, 2.5 at 128 and 2.0 at 256), and what the join of cut units costs (its
+// launch and the sums' way through memory).  Whole units are handed out where that is no slower
+// than the line by these: 5 ragged chunks over 6007 tokens at dim 256 take 258 us, and 304 with costs
+// of 3 and the line up to 6/5 of its time; the same under a window 96 and 106; 6 random prompts of up to
+// 700 rows over 6000 at dim 64, 128 and 256 200, 257 and 820 us both ways.
 constexpr int kv_wide_cost(int dim) { return dim > 128 ? 7 : dim > 64 ? 5 : 4; }
 constexpr int kKvWideMerge = 3;
 // Least share of a workgroup, in tiles (4: 16 chunks of 64 rows over 512 tokens 43 -> 50 us; 8: one of
 // them over 1024 38 -> 58).
 constexpr int kKvWideMinShare = 6;
 constexpr int kKvWideSnap = 1;       // tiles: pieces this short are not cut off (3: prompts 2% slower)
-constexpr int kKvWideJoin = 8;       // workgroups that join the pieces of a (unit, head)
+constexpr int kKvWideJoin = 2048;    // workgroups of the join of cut units, about (kv_attend.h)
 constexpr int kKvTile = 32;        // tokens of one step
 constexpr int kKvItemCost = 2;     // what an item costs besides its tiles, in tiles
 // Least share of a worker, in tiles: a worker's part costs as much as about 2 tiles,
