@@ -25,7 +25,7 @@
 
 static size_t workspace_bytes;
 static unsigned char *const workspace = reinterpret_cast<unsigned char *>(uintptr_t(1) << 40);
-static long long kept, prefix_pieces, sink_items, walks, launched;
+static long long kept, prefix_pieces, sink_items, walks, launched, lines_apart;
 
 struct Range { const unsigned char *from, *to; };
 static std::vector<Range> ranges;
@@ -108,9 +108,11 @@ static hipError_t seen(const KvAttend &a, bool split, bool wide, bool merge) {
         own(a.part, int64_t(a.workers) * 2 * a.split_cols * D * 4);
     }
     if (a.wide_items) {
-        CHECK(wide && a.line && a.units * H < kKvLineUnits);
+        const int64_t on_line = a.units - a.view->prefix.items_from;
+        CHECK(wide && a.line && on_line > 0 && on_line * H < kKvLineUnits);
+        lines_apart += a.view->prefix.items_from > 0;
         const int64_t n = int64_t(a.wide_workers) * 2 * kv_wide_cols(a.c.dim);
-        own(a.wide_items, a.units * H * 8);
+        own(a.wide_items, on_line * H * 8);
         own(a.wide_ml, n * 8);
         own(a.wide_part, n * D * 4);
     }
@@ -237,9 +239,9 @@ static void ends() {
 
 int main() {
     std::mt19937 rng(1);
-    for (int round = 0; round < 4000; ++round) attention(rng, round);
+    for (int round = 0; round < 12000; ++round) attention(rng, round);
     ends();
-    CHECK(kept > 10000 && prefix_pieces > 1000 && sink_items > 1000 && launched > 4000);
-    std::printf("%lld walks, %lld pieces in their places, %lld of a prefix, %lld items with sinks\n", walks, kept, prefix_pieces, sink_items);
+    CHECK(kept > 10000 && prefix_pieces > 1000 && sink_items > 1000 && launched > 12000 && lines_apart > 100);
+    std::printf("%lld walks, %lld pieces in their places, %lld of a prefix, %lld items with sinks, %lld lines of a prefix alone\n", walks, kept, prefix_pieces, sink_items, lines_apart);
     return 0;
 }

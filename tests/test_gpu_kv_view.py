@@ -328,6 +328,28 @@ def test_prefix_of_a_large_batch(awq, batch, prefix):
     assert torch.equal(again[0], got) and torch.equal(again[1], lse)      # deterministic
 
 
+@pytest.mark.parametrize("dim,group,dtype", [(64, 64, "bf16"), (128, 32, "fp16"), (256, 64, "bf16")])
+def test_prefix_beside_many_sequences(awq, dim, group, dtype):
+    """So many sequences that each unit of theirs has a workgroup of its own, few of which have rows for one: the
+    prefix is shared out all the same."""
+    rng = np.random.default_rng(dim)
+    heads, page, batch, prefix = 8, 16, 70, 1500
+    counts = [1, 0, 2, 1, 3] * 14
+    counts[7], counts[33] = 90, 71
+    lengths = [int(prefix + n + rng.integers(0, 40)) for n in counts]
+    lengths[5], lengths[11] = 0, 700
+    ptable, table, n_pages = with_prefix(rng, lengths, prefix, page)
+    cache = filled(rng, n_pages, heads, dim, group, page)
+    start = np.concatenate(([0], np.cumsum(counts)))
+    q = queries(rng, (int(start[-1]), heads, dim), dtype)
+    say("prefix beside many", dim)
+    got, lse = attend(awq, q, dtype, cache, start, lengths, table, prefix=(ptable, prefix), max_rows=90)
+    rows = np.concatenate([np.arange(start[b], start[b + 1]) for b in (0, 2, 5, 7, 11, 33, 69)])     # (the oracle takes its time)
+    some, keep = np.concatenate(([0], np.cumsum([counts[b] for b in (0, 2, 5, 7, 11, 33, 69)]))), [0, 2, 5, 7, 11, 33, 69]
+    check(q[rows], dtype, cache, got[rows.tolist()], lse[rows.tolist()], some, [lengths[b] for b in keep], table[keep],
+          prefix=(ptable, prefix))
+
+
 def test_prefix_scores_far_apart(awq):
     """Either side outweighs the other by far, both ways."""
     rng = np.random.default_rng(15)

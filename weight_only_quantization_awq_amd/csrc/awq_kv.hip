@@ -139,8 +139,8 @@ using awq::kKvMaxCount;
 
 // The launches of one attention call and its workspace (byte offsets).
 struct Plan {
-    bool split, wide, merge, line, wide_merge;
-    int snap, tiles_col, split_cols, workers, units, own_units, wide_workers;
+    bool split, wide, merge, line, wide_merge, apart;
+    int snap, tiles_col, split_cols, workers, units, own_units, line_units, wide_workers;
     size_t items, part_ml, part, wide_items, wide_ml, wide_part, own_ml, own, common_ml, common, total;
 };
 
@@ -185,10 +185,16 @@ awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, i
     p->own_units = !own_wide ? 0 : static_cast<int>(s.row_start ? s.T * per / wide + s.B : s.B * in(s.even * per, wide));
     const int64_t all_units = all_wide ? in(all_cols, wide) : 0;
     p->units = static_cast<int>(p->own_units + all_units);
-    const int64_t groups = static_cast<int64_t>(p->units) * c.heads;
     const int64_t own_wide_tiles = own_wide ? in(positions, tile) : 0, all_wide_tiles = all_wide ? in(all_positions, tile) : 0;
-    const int64_t wide_tiles = own_wide_tiles > all_wide_tiles ? own_wide_tiles : all_wide_tiles;
-    const int64_t wide_line = c.heads * (p->own_units * (own_wide_tiles + awq::kv_wide_cost(c.dim)) + all_units * (all_wide_tiles + awq::kv_wide_cost(c.dim)));
+    // Where the sequences' units are too many for a line and the prefix's are not, the prefix's form
+    // one by themselves, in a launch of their own.
+    p->apart = p->own_units * c.heads >= awq::kKvLineUnits && all_units > 0 && all_units * c.heads < awq::kKvLineUnits;
+    const int64_t own_on_line = p->apart ? 0 : p->own_units;
+    p->line_units = static_cast<int>(own_on_line + all_units);
+    const int64_t groups = static_cast<int64_t>(p->line_units) * c.heads;
+    const int64_t wide_tiles = own_wide_tiles > all_wide_tiles && !p->apart ? own_wide_tiles : all_wide_tiles;
+    const int64_t wide_line = c.heads * (own_on_line * (own_wide_tiles + awq::kv_wide_cost(c.dim)) +
+                                         all_units * (all_wide_tiles + awq::kv_wide_cost(c.dim)));
     p->line = p->wide && groups < awq::kKvLineUnits && wide_line <= kKvMaxCount;
     const int64_t wide_useful = in(wide_line, awq::kKvWideMinShare);
     p->wide_workers = static_cast<int>(wide_useful < awq::kKvCus ? wide_useful : awq::kKvCus);
@@ -355,7 +361,7 @@ awq_status awq_kv_attention_ex(const awq_kv_cache *cache, const awq_kv_batch *ba
     awq::KvView v{};
     v.sinks = a.window == 0 ? 0 : static_cast<int>(sinks > kKvMaxCount ? kKvMaxCount : sinks);
     if (view->prefix_len)
-        v.prefix = {view->prefix_len, view->prefix_table, all.max_pages, p.own_units, floats(p.own), floats(p.own_ml),
+        v.prefix = {view->prefix_len, view->prefix_table, all.max_pages, p.own_units, p.apart ? p.own_units : 0, floats(p.own), floats(p.own_ml),
                     floats(p.common), floats(p.common_ml)};
     if (v.sinks > 0 || view->prefix_len) a.view = &v;
     hipError_t h;

@@ -1547,7 +1547,8 @@ __device__ __forceinline__ KvParts kv_parts(const KvAttendPrefix &a, int b, int 
     else
         unit = b * (a.p.own_units / a.s.B);
     unit += col / kCols;
-    const int2 it = a.wide_items && unit < a.units ? a.wide_items[static_cast<int64_t>(unit) * a.c.heads + head] : make_int2(0, 0);
+    const int record = unit - a.p.items_from;
+    const int2 it = a.wide_items && record >= 0 && unit < a.units ? a.wide_items[static_cast<int64_t>(record) * a.c.heads + head] : make_int2(0, 0);
     if (it.y > 0 && it.x >= 0 && it.x < a.wide_workers) {
         p.ml = a.wide_ml, p.part = a.wide_part;
         p.first = (2 * static_cast<int64_t>(it.x) + 1) * kCols + col % kCols;
@@ -1647,9 +1648,24 @@ hipError_t kv_attend_typed(const A &a, bool run_split, bool run_wide, bool merge
         else if constexpr (D < 256)   // (awq_kv.hip takes at most 2 column tiles at 256 channels)
             hipLaunchKernelGGL((kv_split_kernel<T, D, NG, 4, A>), grid, threads, 0, st, a);
     }
-    if (run_wide)
-        hipLaunchKernelGGL((kv_wide_kernel<T, D, NG, A>), dim3(a.line && a.wide_workers > a.units * a.c.heads ? a.wide_workers : a.units * a.c.heads),
-                           dim3(kv_wide_threads(D)), 0, st, a);
+    auto wide = [&](const A &b) {
+        hipLaunchKernelGGL((kv_wide_kernel<T, D, NG, A>), dim3(b.line && b.wide_workers > b.units * b.c.heads ? b.wide_workers : b.units * b.c.heads),
+                           dim3(kv_wide_threads(D)), 0, st, b);
+    };
+    if (run_wide) {
+        if constexpr (kv_to_sums(static_cast<const A *>(nullptr))) {
+            A b = a;
+            if (a.p.items_from > 0) {   // the sequences' units, many, and then the prefix's, few and long
+                b.units = a.p.own_units, b.line = 0, b.wide_items = nullptr;
+                wide(b);
+                b = a;
+                b.units = a.units - a.p.own_units, b.p.own_units = 0;
+            }
+            wide(b);
+        } else {
+            wide(a);
+        }
+    }
     const int split_items = run_split && merge ? a.s.B * a.c.heads : 0, wide_items = run_wide && a.wide_items ? a.units * a.c.heads : 0;
     if (!kv_to_sums(&a) && split_items + wide_items > 0) {
         const int64_t columns = static_cast<int64_t>(split_items) * a.split_cols;

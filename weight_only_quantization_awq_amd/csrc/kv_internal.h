@@ -101,6 +101,8 @@ __device__ __forceinline__ int kv_wave_sequence(const KvBatch &s, int unit, int 
 struct KvPrefix {
     const int32_t *len, *table;       // [1], [max_pages]
     int max_pages, own_units;         // own_units: of the wide path, before the prefix's
+    int items_from;                   // units without a place in wide_items: 0, or own_units where the prefix's
+                                      // form a line of their own in a launch of their own
     float *own, *own_ml;              // [T][q_heads][dim] and [..][2]: sums of items that were not cut
     float *common, *common_ml;        // the same of the prefix
 };
