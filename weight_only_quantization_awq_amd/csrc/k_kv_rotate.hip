@@ -12,10 +12,15 @@
 // take fewer instructions: sums in float32, u (x1 (w1 c) - x2 (w2 s)), within 16 * 2^-24 of the
 // sum of the two terms' sizes; where float32's range does not hold the squares, u is taken as the keys' is.
 //
-// Work split: workgroups for keys and values come first, units of 4 aligned positions and a
-// head as in k_kv.hip (they have the more to compute), then those for queries, a wave to a
-// row and kQueryIter * 64 / (D/8) of its heads, whose loads are all in flight while the
-// wave finds the row's sequence, position and angles.
+// Work split: units of 4 aligned positions and a head for keys and values as in k_kv.hip, and for
+// queries a wave to a row and kQueryIter * 64 / (D/8) of its heads, whose loads are all in
+// flight while the wave finds the row's sequence, position and angles.  Workgroups for keys,
+// which compute more, are spread among those for queries, which move more (first all of
+// them: 46.9 us and 45.2).
+//
+// Measured: 5 ragged bf16 chunks of up to 4099 rows, 64 query and 8 key heads of 128, with norms
+// (188 MB in and out) 45.2 us, 4.2 TB/s; vector units are busy 67% of the cycles (95% with the
+// queries' norms in 64 bits too, 49.5 us with a 64-bit root and division, 46.5 without).  One row: 4.6 us.
 #include "kv_quant.h"
 
 namespace awq {
