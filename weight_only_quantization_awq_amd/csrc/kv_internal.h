@@ -223,9 +223,12 @@ constexpr int kKvWhole = 6;
 // columns, dim 128, 131072 tokens: 52.5 -> 48.0 us in all; dim 256, 65536: 42.1 -> 34.0);
 // many are quicker with fewer workgroups (512 columns: 43.6 us and 44.9; 4096: 29.5 and 36.8).
 constexpr int kKvMergeFew = 256;
-// Up to so many columns (row and query head) the join of a call with a prefix gives each a
-// workgroup, whose threads share its pieces; more, which have few pieces each, share one.
-constexpr int64_t kKvJoinFew = 16384;
+// The join of a call with a prefix: up to kKvMergeFew columns (row and query head) are spread as above,
+// up to kKvJoinFew take a wave each, whose 256/dim groups share a column's pieces, and more take dim/4
+// threads each, since they have few pieces.  (Wave and dim/4 threads: dim 128, 4096 columns of 17 pieces:
+// 10.4 and 12.6 us; dim 64, 6336 columns of 3 pieces: 7.6 and 5.7; 32768 columns: 18.0 and 11.3 at dim 128,
+// 18.5 and 7.1 at dim 64.)
+constexpr int64_t kKvJoinFew = 4096;
 // Waves of the split path that a SIMD holds at once, by the registers of a wave's
 // output (dim x 16*NT columns) and what comes with it: as many as do without spills, since
 // they hide each other's latency.  us with 1 / 2 / 3 / 4, at group 32 (the largest group has the
