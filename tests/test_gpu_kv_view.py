@@ -350,6 +350,22 @@ def test_prefix_beside_many_sequences(awq, dim, group, dtype):
           prefix=(ptable, prefix))
 
 
+@pytest.mark.parametrize("dim,group,dtype", [(64, 64, "fp16"), (128, 128, "bf16"), (256, 32, "fp16")])
+def test_prefix_of_many_columns(awq, dim, group, dtype):
+    """So many rows and query heads that the join gives each dim/4 threads, with a last workgroup that is not full."""
+    rng = np.random.default_rng(dim + 1)
+    heads, per, page, batch, prefix = 5, 13, 32, 67, 150
+    lengths = [int(prefix + rng.integers(1, 40)) for _ in range(batch)]
+    lengths[3], lengths[9] = 0, 100
+    ptable, table, n_pages = with_prefix(rng, lengths, prefix, page)
+    cache = filled(rng, n_pages, heads, dim, group, page)
+    q = queries(rng, (batch, heads * per, dim), dtype)
+    say("prefix of many columns", dim)
+    got, lse = attend(awq, q, dtype, cache, None, lengths, table, prefix=(ptable, prefix))
+    keep = [0, 3, 9, 40, 66]
+    check(q[keep], dtype, cache, got[keep], lse[keep], None, [lengths[b] for b in keep], table[keep], prefix=(ptable, prefix))
+
+
 def test_prefix_scores_far_apart(awq):
     """Either side outweighs the other by far, both ways."""
     rng = np.random.default_rng(15)
