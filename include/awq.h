@@ -563,7 +563,8 @@ typedef struct {
  * (0 if the arguments are invalid; awq_last_error() says why). */
 size_t awq_kv_page_size(int page, int64_t heads, int dim, int group);
 
-/* What awq_kv_tables writes, in device memory, apart from the table; no output may be an input.
+/* What awq_kv_tables writes, in device memory, apart from the table; no output may share
+ * memory with an input or another output.
  *   kv_len     [batch] int32: the lengths with the step's rows.
  *   row_start  [batch + 1] int32: where each sequence's rows begin.
  *   taken      [1] int32: how many of the free pages are handed out then.

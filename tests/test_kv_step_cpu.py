@@ -191,6 +191,17 @@ def test_tables_refuse_outputs_that_are_inputs(awq, name, at):
 
 
 @built
+@pytest.mark.parametrize("over", [dict(kv_len=0x1008), dict(row_start=0x1FF4), dict(position=0x2FE8), dict(slot=0x3010), dict(kv_len=0x3FF8),
+                                  dict(row_start=0x5FFC - 8), dict(position=0x6008), dict(slot=0x7008), dict(taken=0x502C),
+                                  dict(position=0x8000 - 24)])
+def test_tables_refuse_shared_memory(awq, over):
+    """3 sequences, 4 pages each, 5 free pages, 7 rows: arrays that begin elsewhere and still share an element."""
+    c = awq._KvStepC(**{**dict(kv_len=0x6000, row_start=0x7000, taken=0x8000, position=0x9000, slot=0xA000), **over})
+    assert awq.load().awq_kv_tables(16, 3, 4, 0x1000, 0x2000, 0x3000, 5, 0x4000, 0x5000, 7, c, None) == ARG
+    assert b"share memory" in awq.load().awq_last_error()
+
+
+@built
 def test_binding_refuses_cpu_tensors_and_types(awq):
     import torch
     pages = torch.zeros(4, 2, 16 * 64 + 8 * 16, dtype=torch.uint8)

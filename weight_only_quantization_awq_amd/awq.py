@@ -697,7 +697,7 @@ def kv_tables(block_table: torch.Tensor, kv_len: torch.Tensor, count: torch.Tens
     and are written into ``block_table`` (-1 where none are left; ``taken`` of the result then
     exceeds their number).  ``rows``: with positions and slots of so many rows, -1 for those
     that belong to no sequence.  ``out``: a :class:`KvStep` to write to; none of its tensors may
-    be an input.  Everything stays on the GPU: a captured step can grow its sequences.
+    share memory with an input.  Everything stays on the GPU: a captured step can grow its sequences.
     """
     dev = block_table.device
     if dev.type != "cuda":

@@ -60,16 +60,29 @@ awq_status awq_kv_tables(int page, int64_t batch, int64_t max_pages, const int32
         return kv_fail(AWQ_ERR_ARG, "kv_len, count, free_pages and block_table must be non-NULL");
     if (!step || !step->kv_len || !step->row_start || !step->taken)
         return kv_fail(AWQ_ERR_ARG, "step and its kv_len, row_start and taken must be non-NULL");
-    const void *const in[] = {kv_len, count, free_pages, taken};
-    const void *const out[] = {step->kv_len, step->row_start, step->taken, step->position, block_table, step->slot};
-    for (const void *p : in)
-        if (!kv_aligned(p, 4)) return kv_fail(AWQ_ERR_ARG, "kv_len, count, free_pages and taken must be 4-byte aligned");
-    for (const void *p : out)
-        if (!kv_aligned(p, p == step->slot ? 8 : 4)) return kv_fail(AWQ_ERR_ARG, "outputs must be aligned to their elements");
+    struct Part {
+        const void *p;
+        int64_t n;   // elements
+        int size;
+    };
+    const Part in[] = {{kv_len, batch, 4}, {count, batch, 4}, {free_pages, n_free, 4}, {taken, 1, 4}};
+    const Part out[] = {{step->kv_len, batch, 4}, {step->row_start, batch + 1, 4}, {step->taken, 1, 4}, {step->position, rows, 4},
+                        {step->slot, rows, 8}, {block_table, batch * max_pages, 4}};
+    for (const Part &x : in)
+        if (!kv_aligned(x.p, 4)) return kv_fail(AWQ_ERR_ARG, "kv_len, count, free_pages and taken must be 4-byte aligned");
+    for (const Part &y : out)
+        if (!kv_aligned(y.p, y.size)) return kv_fail(AWQ_ERR_ARG, "outputs must be aligned to their elements");
     // workgroups read the inputs while others write the outputs
-    for (const void *p : in)
-        for (const void *q : out)
-            if (p && p == q) return kv_fail(AWQ_ERR_ARG, "no output may be an input");
+    auto meet = [](const Part &x, const Part &y) {
+        const uintptr_t x0 = reinterpret_cast<uintptr_t>(x.p), y0 = reinterpret_cast<uintptr_t>(y.p);
+        return x0 && y0 && x.n > 0 && y.n > 0 && x0 < y0 + y.n * y.size && y0 < x0 + x.n * x.size;
+    };
+    for (const Part &y : out) {
+        for (const Part &x : in)
+            if (meet(x, y)) return kv_fail(AWQ_ERR_ARG, "no output may share memory with an input");
+        for (const Part *x = out; x != &y; ++x)
+            if (meet(*x, y)) return kv_fail(AWQ_ERR_ARG, "no output may share memory with another");
+    }
     awq::KvTables a{};
     a.kv_len = kv_len, a.count = count, a.free_pages = free_pages, a.taken = taken;
     a.n_free = n_free, a.T = step->position || step->slot ? rows : 0;
