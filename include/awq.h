@@ -634,7 +634,7 @@ typedef struct {
  * awq_kv_append_rotated - normalise and rotate the rows' queries and keys, write the queries
  * and quantise keys and values into the cache, in one pass.
  *   Q, Q_out  device, [rows, q_heads, dim] of type t, rows q_stride / q_out_stride elements
- *             apart (as in awq_kv_append); Q_out may be Q.
+ *             apart (as in awq_kv_append); Q_out may be Q, and else shares no memory with Q, K and V.
  *   K, V, t   as for awq_kv_append.
  * For each head's row x at position p, each operation rounded to float32:
  *   u = 1 / sqrt(mean x^2 + eps)   (in 64 bits, rounded once);   y = (x * u) * weight

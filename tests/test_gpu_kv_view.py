@@ -366,6 +366,24 @@ def test_prefix_of_many_columns(awq, dim, group, dtype):
     check(q[keep], dtype, cache, got[keep], lse[keep], None, [lengths[b] for b in keep], table[keep], prefix=(ptable, prefix))
 
 
+@pytest.mark.parametrize("prefix,most", [(40, 2), (700, 2), (700, 40)])
+def test_prefix_beside_a_sequence_with_more_rows_than_said(awq, prefix, most):
+    """Its own rows are unspecified; all others are right, and nothing is written behind the workspace."""
+    rng = np.random.default_rng(prefix + most)
+    heads, per, dim, group, page = 2, 4, 128, 64, 16
+    counts = [1, 90, 2, 1]
+    lengths = [prefix + 33, prefix + 120, prefix + 7, prefix + 1]
+    ptable, table, n_pages = with_prefix(rng, lengths, prefix, page)
+    cache = filled(rng, n_pages, heads, dim, group, page)
+    start = np.concatenate(([0], np.cumsum(counts)))
+    q = queries(rng, (int(start[-1]) + 2, heads * per, dim), "bf16")
+    say("more rows than said", prefix, most)
+    got, lse = attend(awq, q, "bf16", cache, start, lengths, table, fill=5.0, prefix=(ptable, prefix), max_rows=most)
+    assert (got[int(start[-1]):] == 5.0).all()
+    rows, keep = [0, 91, 92, 93], [0, 2, 3]
+    check(q[rows], "bf16", cache, got[rows], lse[rows], [0, 1, 3, 4], [lengths[b] for b in keep], table[keep], prefix=(ptable, prefix))
+
+
 def test_prefix_scores_far_apart(awq):
     """Either side outweighs the other by far, both ways."""
     rng = np.random.default_rng(15)

@@ -151,6 +151,10 @@ def test_append_rotated_refuses_structs_and_sizes(awq):
     assert _rotated(awq, cache=_cache(awq, dim=96)) == SHAPE
     many = _batch(awq, rows=1 << 23, batch=1 << 20, max_pages=1)
     assert _rotated(awq, cache=_cache(awq, heads=1), batch=many, q_heads=1024, q_stride=1 << 17, out_stride=1 << 17) == SHAPE
+    # as many threads for queries as for keys, 2^32 together
+    many = _batch(awq, rows=1 << 25, batch=1, max_pages=1)
+    assert _rotated(awq, cache=_cache(awq, heads=1), batch=many, q_heads=1) == SHAPE
+    assert b"q_heads" in awq.load().awq_last_error()
     assert _rotated(awq, batch=_batch(awq, rows=0), q=None, k=None, v=None, out=None) == 0
     # nothing rotated and no norm: no table, no eps
     assert _rotated(awq, batch=_batch(awq, rows=0), rot=0, positions=0, cos_sin=None, q_weight=None, k_weight=None, eps=0.0) == 0

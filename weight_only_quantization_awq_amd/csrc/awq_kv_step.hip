@@ -35,9 +35,10 @@ awq_status awq_kv_append_rotated(const awq_kv_cache *cache, const awq_kv_batch *
         return kv_fail(AWQ_ERR_ARG, "q_weight and k_weight must be 16-byte aligned");
     if ((r.q_weight || r.k_weight) && (!(r.eps > 0.0) || !isfinite(r.eps)))
         return kv_fail(AWQ_ERR_ARG, "eps must be positive and finite (got %g)", r.eps);
-    // (a launch has fewer than 2^32 threads: a wave to 32, 16 or 8 heads of a row, and the keys' units)
+    // (a launch has fewer than 2^32 threads: up to 2^31 for the keys' units, as kv_check says, and a wave to
+    // 32, 16 or 8 query heads of a row; whole workgroups of both)
     const int64_t heads = 2048 / cache->dim, waves = batch->rows * ((q_heads + heads - 1) / heads);
-    if (waves > (int64_t(1) << 25)) return kv_fail(AWQ_ERR_SHAPE, "rows * q_heads too large for one call");
+    if (waves > (int64_t(1) << 25) - 64) return kv_fail(AWQ_ERR_SHAPE, "rows * q_heads too large for one call");
     if (s.T == 0) return AWQ_OK;
     const awq::KvTurn turn{r.cos_sin, static_cast<int>(r.positions), r.rot, r.interleaved, r.q_weight, r.k_weight, r.eps};
     return awq::kv_hip_status(awq::launch_kv_append_rotated(c, s, turn, Q, K, V, Q_out, t, static_cast<int>(q_heads), q_stride, k_stride,
