@@ -230,31 +230,50 @@ __device__ __forceinline__ bool kv_some_before(const KvAttendSinks &a, int tok, 
 }
 
 // Of the prefix's rows: the last position that row `row` of the call sees in its own sequence, -1
-// where it sees nothing or there is no such sequence.  All lanes of the wave call.
-__device__ __forceinline__ int kv_own_limit(const KvAttend &, int, int) { return -1; }
-__device__ __forceinline__ int kv_own_limit(const KvAttendPrefix &a, int row, int lane) {
-    const KvBatch &s = a.s;
-    int b;
-    if (!s.row_start) {
-        b = row / s.even;
-    } else if (s.B <= 64) {   // found among the lanes, without a load for each step
-        const int mine = lane < s.B ? kv_clamp(s.row_start[lane], 0, s.T) : INT32_MAX;
-        b = 0;
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) {
-            const int first = __shfl(mine, b + d);
-            if (first <= row) b += d;
+// where it sees nothing or there is no such sequence.  All lanes of the wave call.  What it takes
+// from memory is asked for in ask(), so that other loads can leave before limit() waits for it.
+struct KvOwn {
+    int start, len;   // of sequence `lane` (up to 63 of them), or of the row's own
+
+    __device__ __forceinline__ void ask(const KvAttend &, int, int) {}
+    __device__ __forceinline__ int limit(const KvAttend &, int, int) const { return -1; }
+    __device__ __forceinline__ void ask(const KvAttendPrefix &a, int row, int lane) {
+        const KvBatch &s = a.s;
+        if (!s.row_start) {
+            len = s.kv_len[row / s.even];
+        } else if (s.B < 64) {
+            start = lane <= s.B ? s.row_start[lane] : INT32_MAX;
+            len = lane < s.B ? s.kv_len[lane] : 0;
         }
-    } else {
-        b = kv_unit_sequence(s, row, 1, 1, 0);
     }
-    b = b < s.B ? b : s.B - 1;
-    int r0, n;
-    kv_rows(s, b, r0, n);
-    if (row < r0 || row >= r0 + n) return -1;
-    const int len = kv_length(s, b, a.c.page_shift);
-    return a.causal ? len - n + (row - r0) : len - 1;
-}
+    __device__ __forceinline__ int limit(const KvAttendPrefix &a, int row, int lane) const {
+        const KvBatch &s = a.s;
+        int r0, n, tokens = len;
+        if (!s.row_start) {
+            n = s.even;
+            r0 = row / n * n;
+        } else if (s.B < 64) {   // found among the lanes
+            const int mine = kv_clamp(start, 0, lane <= s.B ? s.T : INT32_MAX);
+            int b = 0;
+#pragma unroll
+            for (int d = 32; d > 0; d >>= 1) {
+                const int first = __shfl(mine, b + d);
+                if (first <= row) b += d;
+            }
+            b = b < s.B ? b : s.B - 1;
+            r0 = __shfl(mine, b);
+            n = __shfl(mine, b + 1) - r0;
+            tokens = __shfl(len, b);
+        } else {
+            const int b = kv_unit_sequence(s, row, 1, 1, 0);
+            kv_rows(s, b, r0, n);
+            tokens = s.kv_len[b];
+        }
+        if (row < r0 || row >= r0 + n) return -1;
+        tokens = kv_clamp(tokens, 0, s.max_pages << a.c.page_shift);
+        return a.causal ? tokens - n + (row - r0) : tokens - 1;
+    }
+};
 __device__ __forceinline__ int kv_wave_min(int x) {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -338,7 +357,9 @@ struct KvWave {
             pos[t] = real ? (a.causal && !prefix ? len - n + i : len - 1) : -1;
             low[t] = kv_low(a, len, n, i, common);
             if (prefix) {   // (what a row that sees nothing gets here is not joined)
-                const int limit = kv_own_limit(a, real ? i : 0, lane);
+                KvOwn own;
+                own.ask(a, real ? i : 0, lane);
+                const int limit = own.limit(a, real ? i : 0, lane);
                 if (real && limit >= 0 && limit < pos[t]) pos[t] = limit;
                 const int least_here = kv_wave_min(real ? pos[t] : len - 1);
                 least = t == 0 || least_here < least ? least_here : least;
@@ -1021,11 +1042,8 @@ __device__ __forceinline__ void kv_wide_piece(const A &a, const KvUnit &unit, in
     const bool real = row < n;
     int pos = real ? (a.causal && !prefix ? p0 + row : len - 1) : -1;
     const int low = kv_low(a, len, n, row, before);
-    if (prefix) {   // (what a row that sees nothing gets here is not joined)
-        const int limit = kv_own_limit(a, real ? row : 0, lane);
-        if (real && limit >= 0 && limit < pos) pos = limit;
-        minpos = kv_wave_min(real ? pos : len - 1);
-    }
+    KvOwn own;
+    if (prefix) own.ask(a, real ? row : 0, lane);
     vec8 q[S];
     // The first tile's pages, the queries, and the first tile, each asked for before the one before
     // it is used: a piece's beginning is a chain of waits.
@@ -1049,6 +1067,11 @@ __device__ __forceinline__ void kv_wide_piece(const A &a, const KvUnit &unit, in
         in.load_values(a, head, token(t0), len);
         in.key_page(a, table, token(t0 + 1), len);
         in.value_pages(a, table, token(t0 + 1), len);
+    }
+    if (prefix) {   // (what a row that sees nothing gets here is not joined)
+        const int last = own.limit(a, real ? row : 0, lane);
+        if (real && last >= 0 && last < pos) pos = last;
+        minpos = kv_wave_min(real ? pos : len - 1);
     }
     // Scores x are formed relative to ref: m, but no less than -kFloorLog2, and 0 before there is one.  Where m is
     // lower, limit sends every tile through the shift to m.  (x carries 2^-24 of its distance from ref: relative
