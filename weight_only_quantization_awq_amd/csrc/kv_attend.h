@@ -1385,25 +1385,30 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(A a) {
         // join.  Where whole units, the longest first, are done as soon (kv_wide_cost), they are
         // handed out instead: the first kKvCus to a CU each, the (kKvCus + i)th behind the
         // (kKvCus - 1 - i)th.
-        auto length = [&](int i) { return before[i + 1] - before[i]; };
-        for (int i = tid; i < a.units; i += kThreads) {
-            const int mine = length(i);
-            int rank = 0;
-            for (int j = 0; j < a.units; ++j) rank += length(j) > mine || (length(j) == mine && j < i) ? 1 : 0;
-            order[rank] = static_cast<uint16_t>(i);
-            if (mine > 0) atomicAdd(&jobs, H);
-        }
-        __syncthreads();
-        for (int i = tid; i < kKvCus; i += kThreads) {
-            const int first = kKvCus - 1 - i, second = kKvCus + i;
-            const int time = (first < jobs ? length(order[first / H]) : 0) + (second < jobs ? length(order[second / H]) : 0);
-            atomicMax(&span, time);
-        }
-        __syncthreads();
+        // (The longest is no shorter than the average, which settles it where items are few.)
         const int line = H * before[a.units], workers = kv_wide_workers(a, line);
-        if (tid == 0 && (span - kv_wide_cost(D) - kKvWideMerge) * static_cast<int64_t>(workers) > line)
-            jobs = 0;
-        __syncthreads();
+        auto sooner = [&](int time) {   // pieces than whole units
+            return (time - kv_wide_cost(D) - kKvWideMerge) * static_cast<int64_t>(workers) > line;
+        };
+        if (!sooner(line / (H * a.units))) {
+            auto length = [&](int i) { return before[i + 1] - before[i]; };
+            for (int i = tid; i < a.units; i += kThreads) {
+                const int mine = length(i);
+                int rank = 0;
+                for (int j = 0; j < a.units; ++j) rank += length(j) > mine || (length(j) == mine && j < i) ? 1 : 0;
+                order[rank] = static_cast<uint16_t>(i);
+                if (mine > 0) atomicAdd(&jobs, H);
+            }
+            __syncthreads();
+            for (int i = tid; i < kKvCus; i += kThreads) {
+                const int first = kKvCus - 1 - i, second = kKvCus + i;
+                const int time = (first < jobs ? length(order[first / H]) : 0) + (second < jobs ? length(order[second / H]) : 0);
+                atomicMax(&span, time);
+            }
+            __syncthreads();
+            if (tid == 0 && sooner(span)) jobs = 0;
+            __syncthreads();
+        }
     }
 
     // A piece at a time: unit u's tiles t0 .. t1-1 for one head.  (What the line needs is
@@ -1421,8 +1426,7 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(A a) {
             // keys, get one XCD (and its L2).
             const int xcd = blockIdx.x & 7, rest = workers & 7;
             const int worker = xcd * (workers >> 3) + (xcd < rest ? xcd : rest) + (blockIdx.x >> 3);
-            int x0 = static_cast<int>(static_cast<int64_t>(worker) * total / workers);
-            int x1 = static_cast<int>((static_cast<int64_t>(worker) + 1) * total / workers);
+            int x0 = kv_share(worker, total, workers), x1 = kv_share(worker + 1, total, workers);
             if (whole_jobs > 0) {   // this workgroup's unit, whole
                 const int u = __builtin_amdgcn_readfirstlane(order[blockIdx.x / H]);
                 x0 = (blockIdx.x % H) * all + __builtin_amdgcn_readfirstlane(before[u]);
