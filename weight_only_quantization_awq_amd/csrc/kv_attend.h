@@ -1356,7 +1356,7 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(A a) {
     __shared__ int lost[3][TT / 16 + 1];
     __shared__ int before[kKvLineUnits + 1];   // line mode: tiles (and costs) of one head of the units before
     __shared__ uint16_t order[kKvLineUnits];   // the units, longest first
-    __shared__ int jobs, span;                 // whole units to hand out instead of the line (0: none), and their time
+    __shared__ int jobs, pieces;               // items; whether the line is cut into pieces (else they are handed out whole)
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int H = a.c.heads, common = kv_common(a);
@@ -1365,12 +1365,21 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(A a) {
             KvUnit unit;
             before[i + 1] = kv_unit<D>(a, i, common, unit) ? unit.t1 - unit.t0 + kv_wide_cost(D) : 0;
         }
-        if (tid == 0) before[0] = jobs = span = 0;
+        if (tid == 0) before[0] = 0;
         __syncthreads();
+        // Pieces cost time: each has its own beginning, and their sums go through memory and a
+        // join.  Where whole units, the longest first, are done as soon (kv_wide_cost), they are
+        // handed out instead: the first kKvCus to a CU each, the (kKvCus + i)th behind the
+        // (kKvCus - 1 - i)th.  (The longest is no shorter than the average, which settles it where
+        // items are few: 2 us less.)
+        auto sooner = [&](int time, int line) {   // pieces than whole units
+            return (time - kv_wide_cost(D) - kKvWideMerge) * static_cast<int64_t>(kv_wide_workers(a, line)) > line;
+        };
         if (wave == 0) {   // prefix sums, 64 units at a time
-            int sum = 0;
+            int sum = 0, some = 0;
             for (int i = 0; i < a.units; i += 64) {
                 int v = i + lane < a.units ? before[i + lane + 1] : 0;
+                some += __popcll(__ballot(v > 0));
 #pragma unroll
                 for (int d = 1; d < 64; d <<= 1) {
                     const int up = __shfl_up(v, d);
@@ -1379,34 +1388,32 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(A a) {
                 if (i + lane < a.units) before[i + lane + 1] = sum + v;
                 sum += __builtin_amdgcn_readlane(v, 63);
             }
+            if (lane == 0) {
+                jobs = H * some;
+                pieces = some > 0 && sooner(static_cast<int>(static_cast<uint32_t>(sum) / static_cast<uint32_t>(some)), H * sum) ? 1 : 0;
+            }
         }
         __syncthreads();
-        // Pieces cost time: each has its own beginning, and their sums go through memory and a
-        // join.  Where whole units, the longest first, are done as soon (kv_wide_cost), they are
-        // handed out instead: the first kKvCus to a CU each, the (kKvCus + i)th behind the
-        // (kKvCus - 1 - i)th.
-        // (The longest is no shorter than the average, which settles it where items are few.)
-        const int line = H * before[a.units], workers = kv_wide_workers(a, line);
-        auto sooner = [&](int time) {   // pieces than whole units
-            return (time - kv_wide_cost(D) - kKvWideMerge) * static_cast<int64_t>(workers) > line;
-        };
-        if (!sooner(line / (H * a.units))) {
-            auto length = [&](int i) { return before[i + 1] - before[i]; };
+        if (!pieces) {
             for (int i = tid; i < a.units; i += kThreads) {
-                const int mine = length(i);
-                int rank = 0;
-                for (int j = 0; j < a.units; ++j) rank += length(j) > mine || (length(j) == mine && j < i) ? 1 : 0;
+                const int mine = before[i + 1] - before[i];
+                int rank = 0, from = 0;
+#pragma unroll 4
+                for (int j = 0; j < a.units; ++j) {
+                    const int to = before[j + 1], length = to - from;
+                    rank += length > mine || (length == mine && j < i) ? 1 : 0;
+                    from = to;
+                }
                 order[rank] = static_cast<uint16_t>(i);
-                if (mine > 0) atomicAdd(&jobs, H);
             }
             __syncthreads();
-            for (int i = tid; i < kKvCus; i += kThreads) {
-                const int first = kKvCus - 1 - i, second = kKvCus + i;
-                const int time = (first < jobs ? length(order[first / H]) : 0) + (second < jobs ? length(order[second / H]) : 0);
-                atomicMax(&span, time);
-            }
-            __syncthreads();
-            if (tid == 0 && sooner(span)) jobs = 0;
+            auto length = [&](int job) {
+                if (job >= jobs) return 0;
+                const int i = order[job / H];
+                return before[i + 1] - before[i];
+            };
+            for (int i = tid; i < kKvCus; i += kThreads)
+                if (sooner(length(kKvCus - 1 - i) + length(kKvCus + i), H * before[a.units])) pieces = 1;
             __syncthreads();
         }
     }
@@ -1420,7 +1427,7 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(A a) {
         if (a.line) {
             const int all = __builtin_amdgcn_readfirstlane(before[a.units]), total = H * all;
             const int workers = kv_wide_workers(a, total);
-            const int whole_jobs = __builtin_amdgcn_readfirstlane(jobs);
+            const int whole_jobs = __builtin_amdgcn_readfirstlane(pieces ? 0 : jobs);
             if (static_cast<int>(blockIdx.x) >= (whole_jobs > 0 ? whole_jobs : workers) || total == 0) return;
             // Workgroups go round the 8 XCDs; neighbours on the line, which read the same
             // keys, get one XCD (and its L2).
