@@ -641,8 +641,9 @@ typedef struct {
  *   a pair (y1, y2) becomes (y1*cos - y2*sin, y2*cos + y1*sin) with p's angles.
  * Keys are quantised from these float32 values (so the cache holds the same as after
  * awq_kv_append of the float32 keys).  Queries are within 16 * 2^-24 of the sum of the two
- * products' sizes of the exact result (of their table and weights), rounded once more, to type t.  A row at a position that
- * cos_sin does not hold (rot > 0) gets queries of NaN and is stored as NaN.  Queries of rows
+ * products' sizes of the exact result (of their table and weights) where the definition's values
+ * are in float32's normal range, and rounded once more, to type t.  A row at a position that cos_sin
+ * does not hold (rot > 0) gets queries of NaN and is stored as NaN.  Queries of rows
  * without a position are zero; rows that belong to no sequence are left as they were.
  */
 awq_status awq_kv_append_rotated(const awq_kv_cache *cache, const awq_kv_batch *batch, const awq_kv_rotation *rotation,

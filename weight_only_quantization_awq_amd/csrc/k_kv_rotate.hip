@@ -8,9 +8,11 @@
 //   a' = fl32(fl32(a c) - fl32(b s)),  b' = fl32(fl32(b c) + fl32(a s))
 // Keys are turned by these very roundings, so what the cache holds does not depend on the order
 // of a sum or on fused operations: the sum of squares is taken in 64 bits, where its order
-// changes the rounded u about once in 2^28 rows.  Queries, which are rounded to their type next,
-// take fewer instructions: sums in float32, u (x1 (w1 c) - x2 (w2 s)), within 16 * 2^-24 of the
-// sum of the two terms' sizes; where float32's range does not hold the squares, u is taken as the keys' is.
+// changes the rounded u about once in 2^28 rows.  Queries, which most callers round to 16 bits
+// next, take fewer instructions: the squares' sum and u in float32 (u as the keys' where float32's range
+// does not hold the squares) and the pair's sum in one fused operation, within 13 * 2^-24 of the sum of
+// the two terms' sizes.  Values are formed in the definition's order, so that none leaves
+// float32's range that does not leave it there (u (x1 (w1 c) - x2 (w2 s)) is no faster: 46.3 us both).
 //
 // Work split: units of 4 aligned positions and a head for keys and values as in k_kv.hip, and for
 // queries a wave to a row and kQueryIter * 64 / (D/8) of its heads, whose loads are all in
@@ -128,47 +130,30 @@ __device__ __forceinline__ bool row_position(const KvCache &c, const KvBatch &s,
     return row >= r0 && row < r0 + n;
 }
 
-// The same of queries (as the file's head says).
+// Turns queries (as the file's head says).
 template <typename T, int D>
 struct QueryTurner {
     static constexpr int LT = D / 8;
     typedef T vec8 __attribute__((ext_vector_type(8)));
-    float a[8], b[8];   // w1 c (w1 where nothing is rotated) and +-w2 s
-    bool norm, turned, neighbours, lost;
-    int partner;
-    double eps;
+    Turner<D> t;
+    float theirs[8];   // weights of the pairs' other channels (halves)
 
-    __device__ __forceinline__ void start(const KvTurn &t, int position, int w) {
-        Turner<D> x;
-        x.start(t, t.q_weight, position, w);
-        norm = x.norm, turned = x.turned, neighbours = x.neighbours, lost = x.lost, partner = x.partner, eps = x.eps;
-        const int other = w + partner - (threadIdx.x & 63);
-        float theirs[8];
-        if (norm) load8(t.q_weight + 8 * other, theirs);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            a[i] = norm ? x.weight[i] : 1.0f;
-            if (turned) {
-                b[i] = norm ? (neighbours ? x.weight[i ^ 1] : theirs[i]) * x.s[i] : x.s[i];
-                a[i] *= x.c[i];
-            }
-        }
+    __device__ __forceinline__ void start(const KvTurn &turn, int position, int w) {
+        t.start(turn, turn.q_weight, position, w);
+        if (t.norm && !t.neighbours) load8(turn.q_weight + 8 * (w + t.partner - (threadIdx.x & 63)), theirs);
     }
 
     // All lanes of the wave call.  NORM, NEIGHBOURS: as `norm` and `neighbours` say.
     template <bool NORM, bool NEIGHBOURS>
     __device__ __forceinline__ void turn(vec8 in, float *x) const {
-        float own[8], other[8], u = 1.0f;
+        float other[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) own[i] = static_cast<float>(in[i]);
-        if constexpr (NEIGHBOURS) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) other[i] = own[i ^ 1];
-        } else {
+        for (int i = 0; i < 8; ++i) x[i] = static_cast<float>(in[i]);
+        if constexpr (!NEIGHBOURS) {
             constexpr int kWords = sizeof(vec8) / 4;
             struct Words { uint32_t w[kWords]; } words = __builtin_bit_cast(Words, in);
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) words.w[i] = __shfl(words.w[i], partner);
+            for (int i = 0; i < kWords; ++i) words.w[i] = __shfl(words.w[i], t.partner);
             const vec8 there = __builtin_bit_cast(vec8, words);
 #pragma unroll
             for (int i = 0; i < 8; ++i) other[i] = static_cast<float>(there[i]);
@@ -176,32 +161,33 @@ struct QueryTurner {
         if constexpr (NORM) {
             float sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum = fmaf(own[i], own[i], sum);
+            for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
 #pragma unroll
             for (int m = 1; m < LT; m <<= 1) sum += __shfl_xor(sum, m);
-            const float mean = fmaf(sum, 1.0f / D, static_cast<float>(eps));
-            u = __builtin_amdgcn_rsqf(mean);
+            const float mean = fmaf(sum, 1.0f / D, static_cast<float>(t.eps));
+            float u = __builtin_amdgcn_rsqf(mean);
             if (__any(!(mean > 1.0e-30f && mean < 1.0e30f))) {   // (NaN, too)
                 double wide = 0.0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) wide = fma(static_cast<double>(own[i]), static_cast<double>(own[i]), wide);
+                for (int i = 0; i < 8; ++i) wide = fma(static_cast<double>(x[i]), static_cast<double>(x[i]), wide);
 #pragma unroll
                 for (int m = 1; m < LT; m <<= 1) wide += __shfl_xor(wide, m);
-                u = inverse_root(wide * (1.0 / D) + eps);
+                u = inverse_root(wide * (1.0 / D) + t.eps);
+            }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) own[i] *= u, other[i] *= u;
-                u = 1.0f;
+            for (int i = 0; i < 8; ++i) x[i] = (x[i] * u) * t.weight[i];
+            if constexpr (!NEIGHBOURS) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) other[i] = (other[i] * u) * theirs[i];
             }
         }
+        if (t.turned) {
+            if constexpr (NEIGHBOURS) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = own[i] * a[i];
-        if (turned) {
+                for (int i = 0; i < 8; ++i) other[i] = x[i ^ 1];
+            }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = fmaf(other[i], b[i], x[i]);
-        }
-        if constexpr (NORM) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] *= u;
+            for (int i = 0; i < 8; ++i) x[i] = fmaf(other[i], t.s[i], x[i] * t.c[i]);
         }
     }
 };
@@ -259,18 +245,18 @@ __global__ __launch_bounds__(kKvThreads) void kv_append_rotated_kernel(KvCache c
         for (int i = 0; i < kQueryIter; ++i) {
             float x[8];
             turner.template turn<decltype(norm)::value, decltype(neighbours)::value>(in[i], x);
-            if (position < 0 || turner.lost) {   // (one for the wave)
+            if (position < 0 || turner.t.lost) {   // (one for the wave)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = position < 0 ? 0.0f : NAN;
             }
             if (head + i * kHeads < q_heads) store8(Qo + row * o_stride + static_cast<int64_t>(head + i * kHeads) * D + 8 * w, x);
         }
     };
-    if (turner.norm && turner.neighbours)
+    if (turner.t.norm && turner.t.neighbours)
         heads(std::true_type{}, std::true_type{});
-    else if (turner.norm)
+    else if (turner.t.norm)
         heads(std::true_type{}, std::false_type{});
-    else if (turner.neighbours)
+    else if (turner.t.neighbours)
         heads(std::false_type{}, std::true_type{});
     else
         heads(std::false_type{}, std::false_type{});
