@@ -634,7 +634,10 @@ typedef struct {
  * awq_kv_append_rotated - normalise and rotate the rows' queries and keys, write the queries
  * and quantise keys and values into the cache, in one pass.
  *   Q, Q_out  device, [rows, q_heads, dim] of type t, rows q_stride / q_out_stride elements
- *             apart (as in awq_kv_append); Q_out may be Q, and else shares no memory with Q, K and V.
+ *             apart (as in awq_kv_append).  Q_out may be Q (of one row stride), and else shares no
+ *             memory with it: rows that do, or whose strides differ and would where they went on, are
+ *             refused.  Where it shares memory with K or V, they are read by a launch of their own
+ *             before.  It shares none with the other arrays.
  *   K, V, t   as for awq_kv_append.
  * For each head's row x at position p, each operation rounded to float32:
  *   u = 1 / sqrt(mean x^2 + eps)   (in 64 bits, rounded once);   y = (x * u) * weight

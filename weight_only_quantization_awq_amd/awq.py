@@ -755,7 +755,8 @@ def kv_append_rotated(cache: KvCache, Q: torch.Tensor, K: torch.Tensor, V: torch
     the weight; None leaves it.  ``cos_sin`` (float32 [positions, 2, rot/2], see
     :func:`kv_rotation_table`): the first rot channels are rotated by the row's position, in
     halves or (``interleaved``) in neighbouring pairs; None rotates nothing.  A position that
-    it does not hold gives NaN.  Returns the queries for :func:`kv_attention` (``out`` may be Q).
+    it does not hold gives NaN.  Returns the queries for :func:`kv_attention`.  ``out`` may be Q,
+    but no other tensor that shares memory with Q; K and V are read before it is written.
     """
     c, dev = _kv_pool(cache)
     rows, q_heads = Q.shape[0], Q.shape[1]

@@ -40,7 +40,13 @@ awq_status awq_kv_append_rotated(const awq_kv_cache *cache, const awq_kv_batch *
     const int64_t heads = 2048 / cache->dim, waves = batch->rows * ((q_heads + heads - 1) / heads);
     if (waves > (int64_t(1) << 25) - 64) return kv_fail(AWQ_ERR_SHAPE, "rows * q_heads too large for one call");
     if (s.T == 0) return AWQ_OK;
-    const awq::KvTurn turn{r.cos_sin, static_cast<int>(r.positions), r.rot, r.interleaved, r.q_weight, r.k_weight, r.eps};
+    // other workgroups read the queries, keys and values meanwhile
+    const int64_t size = t == AWQ_F32 ? 4 : 2, q_width = q_heads * cache->dim * size, width = cache->heads * cache->dim * size;
+    const awq::KvRowSpan out{Q_out, q_out_stride * size, q_width};
+    if (Q_out != Q && awq::kv_rows_meet(out, {Q, q_stride * size, q_width}, s.T))
+        return kv_fail(AWQ_ERR_ARG, "Q_out may be Q, but else must not share memory with it");
+    const bool keys_first = awq::kv_rows_meet(out, {K, k_stride * size, width}, s.T) || awq::kv_rows_meet(out, {V, v_stride * size, width}, s.T);
+    const awq::KvTurn turn{r.cos_sin, static_cast<int>(r.positions), r.rot, r.interleaved, r.q_weight, r.k_weight, r.eps, keys_first};
     return awq::kv_hip_status(awq::launch_kv_append_rotated(c, s, turn, Q, K, V, Q_out, t, static_cast<int>(q_heads), q_stride, k_stride,
                                                             v_stride, q_out_stride, stream),
                               "awq_kv_append_rotated launch");

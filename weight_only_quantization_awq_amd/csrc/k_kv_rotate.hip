@@ -269,10 +269,18 @@ hipError_t append_rotated(const KvCache &c, const KvBatch &s, const KvTurn &t, c
     kv_unit_counts(s, units, even);
     const int64_t per = kKvThreads / (D / 2), keys = (static_cast<int64_t>(units) * c.heads + per - 1) / per;
     const int64_t waves = static_cast<int64_t>(s.T) * ((q_heads + kQueryHeads<D> - 1) / kQueryHeads<D>);
-    const int64_t queries = (waves + kKvThreads / 64 - 1) / (kKvThreads / 64), n = keys + queries;
-    hipLaunchKernelGGL((kv_append_rotated_kernel<T, D, GROUP>), dim3(static_cast<unsigned>(n)), dim3(kKvThreads), 0, st, c, s, t,
-                       static_cast<const T *>(Q), static_cast<const T *>(K), static_cast<const T *>(V), static_cast<T *>(Qo), qs, ks,
-                       vs, os, q_heads, units, even, static_cast<int>(keys), static_cast<int>(queries / keys + 1));
+    const int64_t queries = (waves + kKvThreads / 64 - 1) / (kKvThreads / 64);
+    auto launch = [&](int64_t groups, int64_t key_groups, int64_t apart) {
+        hipLaunchKernelGGL((kv_append_rotated_kernel<T, D, GROUP>), dim3(static_cast<unsigned>(groups)), dim3(kKvThreads), 0, st, c, s, t,
+                           static_cast<const T *>(Q), static_cast<const T *>(K), static_cast<const T *>(V), static_cast<T *>(Qo), qs, ks,
+                           vs, os, q_heads, units, even, static_cast<int>(key_groups), static_cast<int>(apart));
+    };
+    if (t.keys_first) {
+        launch(keys, keys, 1);
+        launch(queries, 0, 1);
+    } else {
+        launch(keys + queries, keys, queries / keys + 1);
+    }
     return hipGetLastError();
 }
 

@@ -6,6 +6,8 @@
 
 #include "kv_internal.h"
 
+#include <numeric>
+
 namespace awq {
 
 constexpr int64_t kKvMaxCount = int64_t(1) << 30;   // rows, columns, units and tiles stay int32
@@ -25,6 +27,21 @@ bool kv_wide_type(awq_dtype t);
 
 // A tensor of `rows` rows of at least `least` elements, `stride` elements apart.
 awq_status kv_check_rows(const void *p, const char *name, awq_dtype t, int64_t rows, int64_t stride, int64_t least);
+
+// A tensor of rows, in bytes: `stride` apart, `width` of each in use.
+struct KvRowSpan {
+    const void *p;
+    int64_t stride, width;
+};
+// Whether two of them share memory.  Of one stride: exactly that.  Of two, where one begins inside the
+// other's extent: whether some multiples of the strides would bring rows of theirs together.
+inline bool kv_rows_meet(const KvRowSpan &x, const KvRowSpan &y, int64_t rows) {
+    const uint64_t x0 = reinterpret_cast<uintptr_t>(x.p), y0 = reinterpret_cast<uintptr_t>(y.p);
+    if (rows < 1 || x0 >= y0 + (rows - 1) * y.stride + y.width || y0 >= x0 + (rows - 1) * x.stride + x.width) return false;
+    if (rows == 1) return true;
+    const uint64_t each = std::gcd(x.stride, y.stride), from = (y0 % each + each - x0 % each) % each;   // y's first byte behind a row of x
+    return from < static_cast<uint64_t>(x.width) || each - from < static_cast<uint64_t>(y.width);
+}
 
 // kv_check and the keys and values of a call that writes or reads them.
 awq_status kv_check_copy(const awq_kv_cache *cache, const awq_kv_batch *batch, const void *K, const void *V, awq_dtype t,

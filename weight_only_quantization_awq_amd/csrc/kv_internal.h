@@ -307,6 +307,7 @@ struct KvTurn {
     int positions, rot, neighbours;
     const float *q_weight, *k_weight;  // [dim], NULL: no norm
     double eps;
+    bool keys_first;                   // queries are written where keys or values lie: only when those have been read
 };
 
 // A step's tables (k_kv_tables.hip).
