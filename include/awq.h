@@ -667,6 +667,8 @@ awq_status awq_kv_read(const awq_kv_cache *cache, const awq_kv_batch *batch, voi
  *   Q, O      device, [rows, q_heads, dim] of type t (AWQ_BF16 or AWQ_F16), rows
  *             q_stride / o_stride elements apart.  q_heads is a multiple of the
  *             cache's heads; query head h reads key/value head h / (q_heads/heads).
+ *             O may be Q (of one row stride), and else shares no memory with it (refused as
+ *             in awq_kv_append_rotated); nor do lse and workspace with anything.
  *   max_rows  an upper bound on any sequence's rows, known on the host; 0 means
  *             `rows`.  It chooses the kernels: with row_start it should be
  *             given.  A sequence with more rows gets them unspecified

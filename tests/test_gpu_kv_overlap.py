@@ -1,4 +1,5 @@
-"""The rotated append writing its queries where keys or values lie: as with tensors of their own, bit for bit."""
+"""The rotated append writing its queries where keys or values lie, and attention its output where its queries lie:
+as with tensors of their own, bit for bit."""
 from __future__ import annotations
 
 import numpy as np
@@ -73,3 +74,31 @@ def test_bindings_refuse_an_output_over_other_queries(awq):
         awq.kv_append_rotated(cache, q[:2], k[:2], k[:2], ints([[0], [1]]), ints([1, 1]), None, out=q[1:3])
     awq.kv_append_rotated(cache, q[:2], k[:2], k[:2], ints([[0], [1]]), ints([1, 1]), None, out=q[2:])
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dim,group", [(64, 32), (128, 128), (256, 64)])
+@pytest.mark.parametrize("view", ["plain", "sinks", "prefix"])
+def test_attention_in_place(awq, dim, group, view):
+    """Items and units whole and cut into pieces, on both paths, in slices of a fused projection."""
+    rng = np.random.default_rng(dim)
+    torch.manual_seed(dim)
+    heads, per, page = 2, 4, 16
+    lengths, counts = [3000, 17, 700, 90, 0, 2500], [300, 1, 40, 2, 1, 1]
+    table, n_pages = table_for(lengths, page, rng)
+    cache = awq.kv_cache(n_pages, heads, dim, group, page)
+    k, v = (torch.randn(sum(lengths), heads, dim, device="cuda").bfloat16() for _ in range(2))
+    t, n = ints(table), ints(lengths)
+    awq.kv_append(cache, k, v, t, n, row_start=ints(np.concatenate(([0], np.cumsum(lengths)))))
+    start = np.concatenate(([0], np.cumsum(counts)))
+    kw = dict(window=400, sinks=20) if view == "sinks" else dict(prefix=(t[0].clone(), ints([1000]))) if view == "prefix" else {}
+    x = torch.randn(sum(counts), heads * per + 3, dim, device="cuda").bfloat16()
+    for most in (300, 2):       # (2: the long ones are left as they were, without a prefix)
+        rows = list(range(sum(counts))) if most == 300 else [300, 341, 342, 343, 344]
+        q = x.clone()[:, 1:-2]
+        say("attention in place", dim, view, most)
+        want, want_lse = awq.kv_attention(q, cache, t, n, row_start=ints(start), max_rows=most, want_lse=True, out=torch.zeros_like(q), **kw)
+        got, lse = awq.kv_attention(q, cache, t, n, row_start=ints(start), max_rows=most, want_lse=True, out=q, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(got[rows], want[rows]) and torch.equal(lse[rows], want_lse[rows])
+    with pytest.raises(awq.AwqError, match="share memory"):
+        awq.kv_attention(x[:, :-3], cache, t, n, row_start=ints(start), out=x[:, 1:-2], **kw)

@@ -1,10 +1,10 @@
-"""Where the rotated append's output may lie (CPU): what is refused before any HIP call."""
+"""Where the outputs of the rotated append and of attention may lie (CPU): what is refused before any HIP call."""
 from __future__ import annotations
 
 import pytest
 
+from tests.test_kv_view_cpu import PREFIX, _call
 from tests.test_kv_step_cpu import ARG, FAKE, _batch, _rotated, awq, built  # noqa: F401  (awq: a fixture)
-
 
 HEAD, ROW = 128 * 2, 1024 * 2   # bytes of a head and of a row of 8, bf16
 
@@ -35,3 +35,11 @@ def test_a_fused_projection_a_head_further_on_is_refused(awq):
     assert _rotated(awq, q_stride=2048, out=FAKE + 5 * 2 * ROW + 7 * HEAD, out_stride=2048) == ARG
     # no rows, nothing to share
     assert _rotated(awq, batch=_batch(awq, rows=0), out=FAKE + HEAD) == 0
+
+
+@built
+@pytest.mark.parametrize("view", [{}, dict(window=5, sinks=1), PREFIX], ids=["plain", "sinks", "prefix"])
+@pytest.mark.parametrize("out,out_stride", [(FAKE + HEAD, 1024), (FAKE - HEAD, 1024), (FAKE + 5 * ROW, 1024), (FAKE, 2048), (FAKE + 16, 1024)])
+def test_attention_over_other_queries_is_refused(awq, view, out, out_stride):
+    assert _call(awq, out=out, out_stride=out_stride, **view) == ARG
+    assert b"share memory" in awq.load().awq_last_error()

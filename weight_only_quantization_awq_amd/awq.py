@@ -846,6 +846,7 @@ def kv_attention(Q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, kv_
     ``prefix`` = (table int32 [pages], length int32 [1]): the first length positions of every
     sequence (counted by ``kv_len``) lie in the table's pages instead of ``block_table``'s and are
     read once for the whole batch; not with a window.
+    ``out`` may be Q, but no other tensor that shares memory with it.
     ``workspace``: uint8 of :func:`kv_attention_workspace_size` bytes (None
     allocates it).  Returns the output like Q, and with ``want_lse`` also the
     float32 log-sum-exp [rows, q_heads] (-inf, and output 0, where a row sees

@@ -329,6 +329,10 @@ awq_status awq_kv_attention_ex(const awq_kv_cache *cache, const awq_kv_batch *ba
         if (workspace_bytes < p.total)
             return kv_fail(AWQ_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", workspace_bytes, p.total);
     }
+    // (in place, each query is read by those who write there, or by a launch before)
+    if ((O != Q || (o_stride != q_stride && batch->rows > 1)) &&
+        awq::kv_rows_meet({O, o_stride * 2, least * 2}, {Q, q_stride * 2, least * 2}, batch->rows))
+        return kv_fail(AWQ_ERR_ARG, "O may be Q, of one row stride, but else must not share memory with it");
     a.Q = Q;
     a.O = O;
     a.lse = lse;
