@@ -570,7 +570,8 @@ size_t awq_kv_page_size(int page, int64_t heads, int dim, int group);
  *   taken      [1] int32: how many of the free pages are handed out then.
  *   position   [rows] int32, slot [rows] int64: each row's position, and page*size + slot of
  *              the place where its token goes; -1 for rows that belong to no sequence (and
- *              slots on pages that do not exist).  Either may be NULL.
+ *              slots on pages that do not exist: those of negative numbers, and with
+ *              awq_kv_tables_ex those from n_pages on).  Either may be NULL.
  */
 typedef struct {
     int32_t *kv_len, *row_start, *taken, *position;
@@ -599,6 +600,13 @@ typedef struct {
 awq_status awq_kv_tables(int page, int64_t batch, int64_t max_pages, const int32_t *kv_len, const int32_t *count,
                          const int32_t *free_pages, int64_t n_free, const int32_t *taken, int32_t *block_table, int64_t rows,
                          const awq_kv_step *step, hipStream_t stream);
+
+/* awq_kv_tables_ex - awq_kv_tables with the pool's size: no slot lies on a page from n_pages
+ * (1..2^31-1) on.  Without it, and with n_pages 0, a slot lies behind the pool's end where a page
+ * number of the table or of the free pages does. */
+awq_status awq_kv_tables_ex(int page, int64_t batch, int64_t max_pages, const int32_t *kv_len, const int32_t *count,
+                            const int32_t *free_pages, int64_t n_free, const int32_t *taken, int32_t *block_table, int64_t rows,
+                            int64_t n_pages, const awq_kv_step *step, hipStream_t stream);
 
 /*
  * awq_kv_append - quantise the rows' keys and values into the cache.

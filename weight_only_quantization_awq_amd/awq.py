@@ -164,6 +164,7 @@ SIGNATURES = {
     "awq_kv_append_rotated": (_int, [_kvc, _kvb, ctypes.POINTER(_KvRotationC), _vp, _vp, _vp, _int, _i64, _i64, _i64, _i64,
                                      _vp, _i64, _vp]),
     "awq_kv_tables": (_int, [_int, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _i64, ctypes.POINTER(_KvStepC), _vp]),
+    "awq_kv_tables_ex": (_int, [_int, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _i64, _i64, ctypes.POINTER(_KvStepC), _vp]),
     "awq_kv_read": (_int, [_kvc, _kvb, _vp, _vp, _int, _i64, _i64, _vp]),
     "awq_kv_attention_workspace_size": (_sz, [_kvc, _kvb, _i64, _i64]),
     "awq_kv_attention": (_int, [_kvc, _kvb, _vp, _int, _i64, _i64, _i64, ctypes.c_float, _int, _i64, _vp, _i64, _vp,
@@ -690,13 +691,15 @@ class KvStep(NamedTuple):
 
 
 def kv_tables(block_table: torch.Tensor, kv_len: torch.Tensor, count: torch.Tensor, free_pages: torch.Tensor,
-              taken: torch.Tensor | None = None, page: int = 16, rows: int = 0, out: KvStep | None = None) -> KvStep:
+              taken: torch.Tensor | None = None, page: int = 16, rows: int = 0, out: KvStep | None = None,
+              n_pages: int = 0) -> KvStep:
     """The tables of a step in which sequence b, ``kv_len[b]`` tokens long, adds ``count[b]`` rows.
 
     The pages that new rows begin come from ``free_pages`` behind the first ``taken`` of them
     and are written into ``block_table`` (-1 where none are left; ``taken`` of the result then
     exceeds their number).  ``rows``: with positions and slots of so many rows, -1 for those
-    that belong to no sequence.  ``out``: a :class:`KvStep` to write to; none of its tensors may
+    that belong to no sequence.  A slot on a page of a negative number is -1, too, and with
+    ``n_pages`` (of the pool) one on a page from there on.  ``out``: a :class:`KvStep` to write to; none of its tensors may
     share memory with an input.  Everything stays on the GPU: a captured step can grow its sequences.
     """
     dev = block_table.device
@@ -719,9 +722,9 @@ def kv_tables(block_table: torch.Tensor, kv_len: torch.Tensor, count: torch.Tens
                      None if out.slot is None else out.slot.data_ptr())
     if free_pages.dim() != 1:
         raise ValueError("free_pages must have one dimension")
-    _kv_call(dev, _lib.awq_kv_tables, page, batch, max_pages, _kv_ints(kv_len, "kv_len", dev, (batch,)),
+    _kv_call(dev, _lib.awq_kv_tables_ex, page, batch, max_pages, _kv_ints(kv_len, "kv_len", dev, (batch,)),
              _kv_ints(count, "count", dev, (batch,)), _kv_ints(free_pages, "free_pages", dev, None), free_pages.shape[0],
-             None if taken is None else _kv_ints(taken, "taken", dev, (1,)), table, rows, s)
+             None if taken is None else _kv_ints(taken, "taken", dev, (1,)), table, rows, n_pages, s)
     return out
 
 

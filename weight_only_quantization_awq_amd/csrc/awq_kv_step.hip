@@ -55,6 +55,12 @@ awq_status awq_kv_append_rotated(const awq_kv_cache *cache, const awq_kv_batch *
 awq_status awq_kv_tables(int page, int64_t batch, int64_t max_pages, const int32_t *kv_len, const int32_t *count,
                          const int32_t *free_pages, int64_t n_free, const int32_t *taken, int32_t *block_table, int64_t rows,
                          const awq_kv_step *step, hipStream_t stream) {
+    return awq_kv_tables_ex(page, batch, max_pages, kv_len, count, free_pages, n_free, taken, block_table, rows, 0, step, stream);
+}
+
+awq_status awq_kv_tables_ex(int page, int64_t batch, int64_t max_pages, const int32_t *kv_len, const int32_t *count,
+                            const int32_t *free_pages, int64_t n_free, const int32_t *taken, int32_t *block_table, int64_t rows,
+                            int64_t n_pages, const awq_kv_step *step, hipStream_t stream) {
     awq::report_error(AWQ_OK, "");
     if (page < 16 || page > 256 || (page & (page - 1)) != 0)
         return kv_fail(AWQ_ERR_ARG, "page must be a power of two in 16..256 (got %d)", page);
@@ -67,6 +73,8 @@ awq_status awq_kv_tables(int page, int64_t batch, int64_t max_pages, const int32
         return kv_fail(AWQ_ERR_ARG, "kv_len, count, free_pages and block_table must be non-NULL");
     if (!step || !step->kv_len || !step->row_start || !step->taken)
         return kv_fail(AWQ_ERR_ARG, "step and its kv_len, row_start and taken must be non-NULL");
+    if (n_pages < 0 || n_pages > INT32_MAX)
+        return kv_fail(AWQ_ERR_SHAPE, "n_pages must be in 0..2^31-1 (got %lld)", static_cast<long long>(n_pages));
     struct Part {
         const void *p;
         int64_t n;   // elements
@@ -95,6 +103,7 @@ awq_status awq_kv_tables(int page, int64_t batch, int64_t max_pages, const int32
     a.n_free = n_free, a.T = step->position || step->slot ? rows : 0;
     a.table = block_table, a.new_len = step->kv_len, a.row_start = step->row_start, a.new_taken = step->taken;
     a.position = step->position, a.slot = step->slot;
+    a.n_pages = n_pages > 0 ? n_pages : int64_t(1) << 31;
     a.B = static_cast<int>(batch), a.max_pages = static_cast<int>(max_pages);
     while ((1 << a.page_shift) < page) ++a.page_shift;
     return awq::kv_hip_status(awq::launch_kv_tables(a, stream), "awq_kv_tables launch");

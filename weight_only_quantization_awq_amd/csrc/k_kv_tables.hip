@@ -5,7 +5,8 @@
 //   n_b = clamp(count_b, 0, cap - L_b),  L'_b = L_b + n_b,  start_b = sum_{c < b} n_c
 //   have_b = ceil(L_b / P),  need_b = ceil(L'_b / P) - have_b,  first_b = taken + sum_{c < b} need_c
 //   table[b, have_b + j] = free[first_b + j]  (-1 behind the list's end),  j < need_b
-//   row r of b: position L_b + r - start_b, slot table[b, position / P] * P + position % P
+//   row r of b: position L_b + r - start_b, slot table[b, position / P] * P + position % P (-1 where
+//   that page is none of the pool's)
 //
 // One launch.  Every workgroup forms both sums over all sequences by itself (8 bytes a
 // sequence, which the caches hold), a run of sequences to a thread, so that workgroups need
@@ -126,7 +127,7 @@ __global__ __launch_bounds__(kStepThreads) void kv_tables_kernel(KvTables a) {
                 position = len + static_cast<int>(i);
                 const int p = position >> a.page_shift, have = t.pages(len);
                 const int id = p < have ? a.table[static_cast<int64_t>(b) * a.max_pages + p] : page_of(pages + p - have);
-                if (id >= 0) slot = (static_cast<int64_t>(id) << a.page_shift) + (position & ((1 << a.page_shift) - 1));
+                if (id >= 0 && id < a.n_pages) slot = (static_cast<int64_t>(id) << a.page_shift) + (position & ((1 << a.page_shift) - 1));
             }
         }
         if (a.position) a.position[r] = position;

@@ -315,7 +315,7 @@ struct KvTables {
     const int32_t *kv_len, *count, *free_pages, *taken;
     int64_t n_free, T;
     int32_t *table, *new_len, *row_start, *new_taken, *position;
-    int64_t *slot;
+    int64_t *slot, n_pages;            // pages from n_pages on have no slots
     int B, max_pages, page_shift;
 };
 
