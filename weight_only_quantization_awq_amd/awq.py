@@ -722,7 +722,7 @@ def kv_tables(block_table: torch.Tensor, kv_len: torch.Tensor, count: torch.Tens
                      None if out.slot is None else out.slot.data_ptr())
     if free_pages.dim() != 1:
         raise ValueError("free_pages must have one dimension")
-    _kv_call(dev, load().awq_kv_tables_ex, page, batch, max_pages, _kv_ints(kv_len, "kv_len", dev, (batch,)),
+    _kv_call(dev, _lib.awq_kv_tables_ex, page, batch, max_pages, _kv_ints(kv_len, "kv_len", dev, (batch,)),
              _kv_ints(count, "count", dev, (batch,)), _kv_ints(free_pages, "free_pages", dev, None), free_pages.shape[0],
              None if taken is None else _kv_ints(taken, "taken", dev, (1,)), table, rows, n_pages, s)
     return out
