@@ -886,14 +886,16 @@ def kv_attention(Q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, kv_
     need = _kv_workspace(c, b, view, q_heads, max_rows or 0)
     if need and (workspace is None or workspace.numel() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    lse_at, ws, ws_bytes = (lse.data_ptr() if want_lse else None), *((workspace.data_ptr(), workspace.numel()) if need else (None, 0))
-    scale, causal = cache.dim ** -0.5 if scale is None else scale, 1 if causal else 0
     if view is None:
-        _kv_call(dev, _lib.awq_kv_attention, c, b, q, _KV_TYPES[dtype], q_heads, q_stride, max_rows or 0, scale, causal, window, o,
-                 o_stride, lse_at, ws, ws_bytes)
+        _kv_call(dev, _lib.awq_kv_attention, c, b, q, _KV_TYPES[dtype], q_heads, q_stride, max_rows or 0,
+                 cache.dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, o, o_stride,
+                 lse.data_ptr() if want_lse else None, workspace.data_ptr() if need else None,
+                 workspace.numel() if need else 0)
     else:
-        _kv_call(dev, _lib.awq_kv_attention_ex, c, b, view, q, _KV_TYPES[dtype], q_heads, q_stride, max_rows or 0, scale, causal, o,
-                 o_stride, lse_at, ws, ws_bytes)
+        _kv_call(dev, _lib.awq_kv_attention_ex, c, b, view, q, _KV_TYPES[dtype], q_heads, q_stride, max_rows or 0,
+                 cache.dim ** -0.5 if scale is None else scale, 1 if causal else 0, o, o_stride,
+                 lse.data_ptr() if want_lse else None, workspace.data_ptr() if need else None,
+                 workspace.numel() if need else 0)
     return (out, lse) if want_lse else out
 
 
