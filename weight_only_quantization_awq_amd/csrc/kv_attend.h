@@ -817,65 +817,6 @@ struct KvWideType<_Float16> {
 
 constexpr int kv_wide_threads(int dim) { return 2 * kv_wide_cols(dim); }
 
-// Unit u: a sequence's columns col0 .. (kv_wide_cols(D) of them at most), and the
-// tiles t0 .. t1-1 that some of them see (one at least, so that every unit is visited).
-// Tiles before sink_tiles (with sinks, t0 is 0) lie at t, the others `skip` tiles further on.
-struct KvUnit {
-    int b, r0, n, len, col0, t0, t1, sink_tiles, skip;
-};
-// Units of the sequences themselves; those of a prefix come behind them.
-__device__ __forceinline__ int kv_own_units(const KvAttend &a) { return a.units; }
-__device__ __forceinline__ int kv_own_units(const KvAttendPrefix &a) { return a.p.own_units; }
-template <int D, typename A>
-__device__ __forceinline__ bool kv_unit(const A &a, int u, int common, KvUnit &x) {
-    constexpr int kCols = kv_wide_cols(D), TT = kv_wide_tile(D);
-    int k;
-    if (u >= kv_own_units(a)) {
-        x.b = a.s.B;
-        k = u - kv_own_units(a);
-    } else if (a.s.row_start) {
-        x.b = kv_unit_sequence(a.s, u, a.per, kCols, 1);
-        k = u - kv_unit_first(a.s, x.b, a.per, kCols, 1);
-    } else {
-        const int each = kv_own_units(a) / a.s.B;
-        x.b = u / each;
-        k = u - x.b * each;
-    }
-    if (x.b >= kv_count(a)) return false;   // (not in any launch)
-    kv_sequence(a, x.b, common, x.r0, x.n, x.len);
-    const bool prefix = kv_is_prefix(a, x.b);
-    const int64_t cols = static_cast<int64_t>(x.n) * a.per;
-    if (cols <= a.split_cols || k < 0 || static_cast<int64_t>(k) * kCols >= cols) return false;
-    x.col0 = k * kCols;
-    const int p0 = x.len - x.n, last = static_cast<int>(cols) - 1;
-    const int end = x.col0 + kCols - 1 < last ? x.col0 + kCols - 1 : last;
-    const int lo = kv_low(a, x.len, x.n, x.col0 / a.per, prefix ? 0 : common);
-    const int hi = a.causal && !prefix ? p0 + end / a.per + 1 : x.len;
-    x.t0 = lo > 0 ? lo / TT : 0;
-    x.t1 = hi > 0 ? (hi + TT - 1) / TT : 0;
-    if (x.t1 <= x.t0) x.t1 = x.t0 + 1;
-    x.sink_tiles = kv_sink_tiles(a, x.t0 * TT, TT);
-    x.skip = 0;
-    if (x.sink_tiles > 0) {
-        x.skip = x.t0 - x.sink_tiles;
-        x.t1 -= x.skip;
-        x.t0 = 0;
-    }
-    return true;
-}
-// Workgroups that share a line of this length.
-__device__ __forceinline__ int kv_wide_workers(const KvAttend &a, int total) {
-    const int most = total / kKvWideMinShare > 1 ? total / kKvWideMinShare : 1;
-    return a.wide_workers < most ? a.wide_workers : most;
-}
-// The tile at which a boundary `at` behind an item's begin cuts it (0 or tiles: not inside).
-template <int D>
-__device__ __forceinline__ int kv_wide_cut(int at, int tiles) {
-    const int t = at - kv_wide_cost(D);
-    if (t <= kKvWideSnap) return 0;
-    return tiles - t <= kKvWideSnap ? tiles : t;
-}
-
 // What a thread unpacks of one tile: KW key words of one token (and one of its
 // pairs), VI pieces of 8 tokens x 2 channels of the values.
 // Everything is loaded whether the token exists or not (from page 0 where it has
@@ -1372,9 +1313,7 @@ __global__ __launch_bounds__(kv_wide_threads(D)) void kv_wide_kernel(A a) {
         // handed out instead: the first kKvCus to a CU each, the (kKvCus + i)th behind the
         // (kKvCus - 1 - i)th.  (The longest is no shorter than the average, which settles it where
         // items are few: 2 us less.)
-        auto sooner = [&](int time, int line) {   // pieces than whole units
-            return (time - kv_wide_cost(D) - kKvWideMerge) * static_cast<int64_t>(kv_wide_workers(a, line)) > line;
-        };
+        auto sooner = [&](int time, int line) { return kv_wide_sooner<D>(a, time, line); };
         if (wave == 0) {   // prefix sums, 64 units at a time
             int sum = 0, some = 0;
             for (int i = 0; i < a.units; i += 64) {
@@ -1547,51 +1486,6 @@ __global__ __launch_bounds__(256) void kv_merge_kernel(KvAttend a, int split_ite
 // and from the prefix, on either path, in pieces or whole.  A workgroup takes CHUNK channels of
 // 256 / (CHUNK/4) / GROUPS columns (row, query head), each with GROUPS groups of CHUNK/4 threads,
 // which take every GROUPSth piece and join in LDS.
-
-// Where the sums of one column lie: `count` pieces, the first (which begins the item) at `first`, the
-// others `step` further on each, of places of D channels; or one place in `part` (count 1, first 0).
-struct KvParts {
-    const float *ml, *part;
-    int64_t first, next;   // the first piece's place, and the second's
-    int64_t step;          // from the second on
-    int count;
-};
-template <int D>
-__device__ __forceinline__ KvParts kv_parts(const KvAttendPrefix &a, int b, int r0, int n, int row, int qh, bool prefix) {
-    const int head = qh / a.per, col = (row - r0) * a.per + (qh - head * a.per);
-    const int64_t at = static_cast<int64_t>(row) * a.q_heads + qh;
-    KvParts p = {prefix ? a.p.common_ml : a.p.own_ml, prefix ? a.p.common : a.p.own, at, at, 0, 1};
-    if (static_cast<int64_t>(n) * a.per <= a.split_cols) {
-        const int2 it = a.items ? a.items[b * a.c.heads + head] : make_int2(0, 0);
-        if (it.y > 0 && it.x >= 0 && it.x < a.workers) {
-            p.ml = a.part_ml, p.part = a.part;
-            p.first = kv_piece(a, it.x, true) + col;
-            p.next = kv_piece(a, it.x + 1, false) + col;
-            p.step = 2 * a.split_cols;
-            p.count = it.y < a.workers - it.x ? it.y : a.workers - it.x;   // (inside, should tables change under the call)
-        }
-        return p;
-    }
-    constexpr int kCols = kv_wide_cols(D);
-    int unit;
-    if (prefix)
-        unit = a.p.own_units;
-    else if (a.s.row_start)
-        unit = kv_unit_first(a.s, b, a.per, kCols, 1);
-    else
-        unit = b * (a.p.own_units / a.s.B);
-    unit += col / kCols;
-    const int record = unit - a.p.items_from;
-    const int2 it = a.wide_items && record >= 0 && unit < a.units ? a.wide_items[static_cast<int64_t>(record) * a.c.heads + head] : make_int2(0, 0);
-    if (it.y > 0 && it.x >= 0 && it.x < a.wide_workers) {
-        p.ml = a.wide_ml, p.part = a.wide_part;
-        p.first = (2 * static_cast<int64_t>(it.x) + 1) * kCols + col % kCols;
-        p.next = 2 * (static_cast<int64_t>(it.x) + 1) * kCols + col % kCols;
-        p.step = 2 * kCols;
-        p.count = it.y < a.wide_workers - it.x ? it.y : a.wide_workers - it.x;
-    }
-    return p;
-}
 
 template <typename T, int D, int CHUNK, int GROUPS>
 __global__ __launch_bounds__(256) void kv_join_kernel(KvAttendPrefix a) {
