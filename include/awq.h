@@ -730,7 +730,11 @@ typedef struct {
  * Other arguments, results and the workspace's use as for awq_kv_attention, which is this
  * call with a view of its window.  The results with a prefix differ from those of
  * the same positions in one table by float32 roundings of the join.  The workspace then also
- * holds 2 * rows * q_heads * (dim + 2) float32.  Rows that see nothing of their sequence are
+ * holds 2 * rows * q_heads * (dim + 2) float32, and places as large as the prefix's columns for the
+ * pieces of all (up to about 70 MB more; the size function counts all of it).  A prefix pays where its
+ * reading and products outweigh a second set of launches and sums: from about 8 sequences behind 32768
+ * positions, 32 behind 8192 or 128 behind 2048 on (single tokens, 8 heads of 128; with fewer or smaller
+ * heads from more on); below that, one table with the shared pages in each row is up to three times as fast.  Rows that see nothing of their sequence are
  * computed against the prefix and left out of the results: padded slots cost time, not more.
  */
 size_t awq_kv_attention_workspace_size_ex(const awq_kv_cache *cache, const awq_kv_batch *batch, const awq_kv_view *view,

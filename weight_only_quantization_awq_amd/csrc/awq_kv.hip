@@ -166,6 +166,11 @@ awq_status plan(const awq::KvCache &c, const awq::KvBatch &s, int64_t q_heads, i
     const bool own_wide = cols > limit, all_wide = all_cols > limit, all_split = prefix && !all_wide;
     p->wide = own_wide || all_wide;
     // Where the sequences take the wide path, the split path is for their single tokens.
+    // With a prefix whose columns take it, one launch serves its items and the sequences', with the
+    // column tiles that the prefix needs.  (That costs where own parts are long: single tokens, 32 query
+    // heads on 8 of dim 128, 4096 positions of their own behind 512, us of a call: 8 sequences, two tiles, 27;
+    // 9, four tiles, 43; 16 66; 17, whose prefix takes the wide path and whose own items one tile, 57; over one
+    // table 21, 21, 29 and 29.)
     const int64_t need = own_wide ? per : all_split ? all_cols : cols;
     p->split = need <= limit && (!own_wide || s.row_start);
     p->tiles_col = need <= 16 ? 1 : need <= 32 ? 2 : 4;

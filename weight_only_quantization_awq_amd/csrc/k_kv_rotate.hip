@@ -21,8 +21,8 @@
 // them: 46.9 us and 45.2).
 //
 // Measured: 5 ragged bf16 chunks of up to 4099 rows, 64 query and 8 key heads of 128, with norms
-// (188 MB in and out) 45.2 us, 4.2 TB/s; vector units are busy 67% of the cycles (95% with the
-// queries' norms in 64 bits too, 49.5 us with a 64-bit root and division, 46.5 without).  One row: 4.6 us.
+// (188 MB in and out) 44.9 us, 4.2 TB/s; vector units are busy 71% of the cycles (95% with the
+// queries' norms in 64 bits too, 49.5 us with a 64-bit root and division, 46.5 without).  One row: 4.5 us.
 #include "kv_quant.h"
 
 namespace awq {

@@ -225,9 +225,18 @@ constexpr int kKvWhole = 6;
 constexpr int kKvMergeFew = 256;
 // The join of a call with a prefix: up to kKvMergeFew columns (row and query head) are spread as above,
 // up to kKvJoinFew take a wave each, whose 256/dim groups share a column's pieces, and more take dim/4
-// threads each, since they have few pieces.  (Wave and dim/4 threads: dim 128, 4096 columns of 17 pieces:
-// 10.4 and 12.6 us; dim 64, 6336 columns of 3 pieces: 7.6 and 5.7; 32768 columns: 18.0 and 11.3 at dim 128,
-// 18.5 and 7.1 at dim 64.)
+// threads each.  What decides is the pieces of a column: n columns have up to 65536/n of the prefix's
+// (32768/n at dim 256, where the two forms are one), as many as share the line's 256 workgroups, but
+// behind a short prefix fewer, which the host does not know.  Wave and dim/4 threads, us:
+//   columns of      3 pieces             8                    16
+//   dim 64   2048   4.6  4.6             4.7  5.5             5.5  7.2
+//            4096   4.8  4.6             5.8  5.8             7.1  7.9
+//            8192   7.3  4.6             8.4  6.6
+//   dim 128  2048   4.6  4.6             4.9  4.9             6.2  6.7
+//            4096   5.1  4.5             6.4  5.2             9.0  8.5 (64 rows over 16384 positions: 10.4 12.6)
+//            8192   7.7  5.0             9.4  8.1
+// So the wave is the quicker one for many pieces, which there are up to about the bound, and costs up to 1.2 us
+// at it behind short prefixes.
 constexpr int64_t kKvJoinFew = 4096;
 // Waves of the split path that a SIMD holds at once, by the registers of a wave's
 // output (dim x 16*NT columns) and what comes with it: as many as do without spills, since
