@@ -642,10 +642,9 @@ typedef struct {
  * awq_kv_append_rotated - normalise and rotate the rows' queries and keys, write the queries
  * and quantise keys and values into the cache, in one pass.
  *   Q, Q_out  device, [rows, q_heads, dim] of type t, rows q_stride / q_out_stride elements
- *             apart (as in awq_kv_append).  Q_out may be Q (of one row stride), and else shares no
- *             memory with it: rows that do, or whose strides differ and would where they went on, are
- *             refused.  Where it shares memory with K or V, they are read by a launch of their own
- *             before.  It shares none with the other arrays.
+ *             apart (as in awq_kv_append).  Q_out may be Q (of one row stride), and is else refused
+ *             where a row of it shares memory with one of Q.  Where it shares memory with K or V, they
+ *             are read by a launch of their own before.  It shares none with the other arrays.
  *   K, V, t   as for awq_kv_append.
  * For each head's row x at position p, each operation rounded to float32:
  *   u = 1 / sqrt(mean x^2 + eps)   (in 64 bits, rounded once);   y = (x * u) * weight
@@ -675,8 +674,8 @@ awq_status awq_kv_read(const awq_kv_cache *cache, const awq_kv_batch *batch, voi
  *   Q, O      device, [rows, q_heads, dim] of type t (AWQ_BF16 or AWQ_F16), rows
  *             q_stride / o_stride elements apart.  q_heads is a multiple of the
  *             cache's heads; query head h reads key/value head h / (q_heads/heads).
- *             O may be Q (of one row stride), and else shares no memory with it (refused as
- *             in awq_kv_append_rotated); nor do lse and workspace with anything.
+ *             O may be Q (of one row stride), and is else refused where it shares memory with
+ *             it; lse and workspace share none with anything.
  *   max_rows  an upper bound on any sequence's rows, known on the host; 0 means
  *             `rows`.  It chooses the kernels: with row_start it should be
  *             given.  A sequence with more rows gets them unspecified

@@ -33,14 +33,25 @@ struct KvRowSpan {
     const void *p;
     int64_t stride, width;
 };
-// Whether two of them share memory.  Of one stride: exactly that.  Of two, where one begins inside the
-// other's extent: whether some multiples of the strides would bring rows of theirs together.
+// Whether two of them share memory.  (Row by row only where the strides differ and their greatest
+// common divisor does not settle it, inside the memory that both extend over.)
 inline bool kv_rows_meet(const KvRowSpan &x, const KvRowSpan &y, int64_t rows) {
     const uint64_t x0 = reinterpret_cast<uintptr_t>(x.p), y0 = reinterpret_cast<uintptr_t>(y.p);
     if (rows < 1 || x0 >= y0 + (rows - 1) * y.stride + y.width || y0 >= x0 + (rows - 1) * x.stride + x.width) return false;
     if (rows == 1) return true;
-    const uint64_t each = std::gcd(x.stride, y.stride), from = (y0 % each + each - x0 % each) % each;   // y's first byte behind a row of x
-    return from < static_cast<uint64_t>(x.width) || each - from < static_cast<uint64_t>(y.width);
+    const int64_t each = std::gcd(x.stride, y.stride), ahead = static_cast<int64_t>(y0 - x0);   // (they meet, so it fits)
+    const int64_t from = (ahead % each + each) % each;   // y's first byte behind a row of x, in the finest order of both
+    if (from >= x.width && each - from >= y.width) return false;
+    if (x.stride == y.stride) return true;
+    const int64_t first = ahead - x.width < 0 ? 0 : (ahead - x.width) / x.stride;
+    for (int64_t i = first; i < rows; ++i) {
+        const int64_t at = i * x.stride - ahead;   // behind y's first byte
+        if (at >= (rows - 1) * y.stride + y.width) return false;
+        if (at < 0 ? at + x.width > 0 : at / y.stride < rows && at % y.stride < y.width) return true;
+        const int64_t next = at < 0 ? 0 : at / y.stride + 1;   // the first row of y that begins behind it
+        if (next < rows && next * y.stride < at + x.width) return true;
+    }
+    return false;
 }
 
 // kv_check and the keys and values of a call that writes or reads them.
