@@ -154,3 +154,12 @@ def test_nan_in_a_prefix_and_beside_it_on_the_wide_path(awq, dim, group, dtype, 
     pos = torch.arange(160, 200)
     assert lost[4, :, 0].tolist() == ((pos >= 178) if causal else pos >= 0).tolist()
     assert lost[3, :, 1].tolist() == ((torch.arange(88, 128) >= 99) if causal else pos >= 0).tolist()
+
+
+@pytest.mark.parametrize("view", [dict(prefix=333), dict(window=20, sinks=3)], ids=["prefix", "sinks"])
+def test_tens_of_thousands_of_sequences(awq, view):
+    rng = np.random.default_rng(2)
+    lengths = [int(view.get("prefix", 0) + x) for x in rng.integers(1, 90, 1 << 16)]
+    count_check(awq, "bf16", 64, 32, 4, 1, 16, lengths, [1] * len(lengths), **view)
+    few = lengths[:1 << 13]
+    count_check(awq, "fp16", 128, 64, 4, 1, 16, few, [1, 2, 0, 3] * (len(few) // 4), most=3, **view)

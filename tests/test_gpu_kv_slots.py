@@ -69,3 +69,32 @@ def test_a_step_has_the_slots_that_append_writes(awq):
     assert sorted(y for y in slots if y >= 0) == written and slots.count(-1) > 4
     with pytest.raises(awq.AwqError, match="n_pages"):
         awq.kv_tables(table, s.kv_len, s.kv_len, free, page=page, n_pages=-1)
+
+
+@pytest.mark.parametrize("batch,rows", [(1 << 21, 5000), (1 << 20, 1 << 21), (100003, 77)])
+def test_tables_of_the_largest_batches(awq, batch, rows):
+    """The definitions for all sequences at once; half of the pages that they need, some behind the pool's end."""
+    rng = np.random.default_rng(rows)
+    page, most, n_pages = 16, 4, 900
+    kv_len, count = rng.integers(0, 50, batch), rng.integers(0, 3, batch)
+    count[rng.integers(0, batch, 50)] = 1000
+    n = np.clip(count, 0, page * most - kv_len)
+    now, have = kv_len + n, -(-kv_len // page)
+    need = -(-now // page) - have
+    free, table = rng.integers(0, 1000, int(need.sum()) // 2), rng.integers(0, 1000, (batch, most))
+    dev = ints(table)
+    say("tables", batch, rows)
+    got = awq.kv_tables(dev, ints(kv_len), ints(count), ints(free), page=page, rows=rows, n_pages=n_pages)
+    torch.cuda.synchronize()
+    j = np.arange(most) - have[:, None]
+    which = (np.cumsum(need) - need)[:, None] + j
+    want = np.where((j >= 0) & (j < need[:, None]), np.where(which < len(free), free[np.clip(which, 0, len(free) - 1)], -1), table)
+    start = np.concatenate(([0], np.cumsum(n)))
+    r = np.arange(rows)
+    b = np.minimum(np.searchsorted(start[1:], r, side="right"), batch - 1)
+    position = np.where(r < start[-1], kv_len[b] + r - start[b], -1)
+    pg = want[b, np.maximum(position, 0) // page]
+    slot = np.where((position >= 0) & (pg >= 0) & (pg < n_pages), pg * page + position % page, -1)
+    for name, x, y in (("table", dev, want), ("kv_len", got.kv_len, now), ("row_start", got.row_start, start),
+                       ("taken", got.taken, [need.sum()]), ("position", got.position, position), ("slot", got.slot, slot)):
+        assert np.array_equal(x.cpu().numpy(), y), name
