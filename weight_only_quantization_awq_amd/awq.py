@@ -731,6 +731,8 @@ def kv_tables(block_table: torch.Tensor, kv_len: torch.Tensor, count: torch.Tens
 def kv_rotation_table(positions: int, rot: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
     """Cosines and sines [positions, 2, rot/2] of the angles p * base^(-2i/rot), taken in 64 bits and
     rounded once to float32 (for :func:`kv_append_rotated`; scaled frequencies are a table of one's own)."""
+    if rot < 0 or rot % 2:
+        raise ValueError(f"rot must be even (got {rot})")
     freq = base ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
     angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * freq
     return torch.stack((angle.cos(), angle.sin()), 1).float()
